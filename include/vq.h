@@ -56,6 +56,7 @@
 #ifndef VQ_H
 #define VQ_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -362,6 +363,95 @@ vq_status vq_kivi_unpack_dequant(const uint32_t *k_packed, const void *k_scale, 
  */
 vq_status vq_qjl_encode(const void *x_f16, int N, int D, const void *s_f16, int m, uint32_t *packed,
                         void *norms_f16, vq_stream_t stream);
+
+/*
+ * A paged key/value cache - the tier in front of the codecs: a prompt's chunks
+ * and the tokens of each step are written into pages, attention reads the
+ * pages, and blocks read back contiguous go to the flush calls above.
+ *   k_pages, v_pages [num_pages, Hkv, page_size, D], k_exp, v_exp
+ *     [num_pages, Hkv, page_size] uint8, device; page_size 16, 32, 64, 128 or
+ *     256, D = 128, fewer than 2^31 rows in all.
+ *   cache_dtype VQ_F16 or VQ_BF16: 16-bit entries, k_exp and v_exp NULL.
+ *   cache_dtype VQ_E4M3: 8-bit codes, value = code * 2^(exp - 127): the
+ *     exponent of a token and head is the least e in [-32, 64] with
+ *     max|x| <= 448 * 2^e (0 for a zero row), stored as e + 127, and the codes
+ *     are x * 2^-e rounded to nearest even (saturated).
+ *   block_table [B, max_pages] int32, device: page block_table[b][j / page_size]
+ *     holds token j of sequence b.  Entries of pages that a call reads no token
+ *     of may hold anything (a window's pages can be given back).  A page that
+ *     is read but is not in [0, num_pages) sets VQ_DEVERR_BAD_OFFSET; its
+ *     tokens read as zeros (vq_paged_gather) or leave the outputs that see them
+ *     unspecified (vq_paged_attend).
+ * Tensors of [T, H, D] with strides: element strides of token and head, both
+ * multiples of 8 and at least D, the D entries of a head contiguous.
+ */
+#define VQ_F16 0
+#define VQ_BF16 1
+#define VQ_E4M3 2
+
+/*
+ * vq_paged_append - writes the keys and values of T new tokens into the cache,
+ * quantising them if it is an 8-bit cache.
+ *   k_in, v_in [T, Hkv, D] of in_dtype (VQ_F16 or VQ_BF16; a 16-bit cache has the
+ *     same type), strided.
+ *   slots [T] int64, device: token t goes to page slots[t] / page_size, place
+ *     slots[t] % page_size; a negative slot is a padding token, not written; a
+ *     slot past the pool is not written and sets VQ_DEVERR_BAD_OFFSET.  Two
+ *     tokens with one slot leave either of them (or parts of both).
+ */
+vq_status vq_paged_append(const void *k_in, long long k_stride_t, long long k_stride_h, const void *v_in,
+                          long long v_stride_t, long long v_stride_h, int in_dtype, int T, const int64_t *slots,
+                          void *k_pages, void *v_pages, uint8_t *k_exp, uint8_t *v_exp, int cache_dtype,
+                          int num_pages, int Hkv, int page_size, int D, vq_stream_t stream);
+
+/*
+ * vq_paged_gather - reads S_out tokens of every sequence back: k_out, v_out
+ * [B, Hkv, S_out, D] (either may be NULL) get tokens first[b] + i (first NULL:
+ * i) of sequence b, zeros where that is negative or not below lens[b].
+ *   out_dtype VQ_F16 or VQ_BF16; a 16-bit cache has the same type.  From an
+ *     8-bit cache: code * 2^(exp - 127) rounded once.
+ *   lens, first [B] int32, device.
+ * The layout is the one vq_rvq_encode_pack, vq_kivi_quant_pack and
+ * vq_flush_decode take.
+ */
+vq_status vq_paged_gather(const void *k_pages, const void *v_pages, const uint8_t *k_exp, const uint8_t *v_exp,
+                          int cache_dtype, int num_pages, int Hkv, int page_size, int D, const int32_t *block_table,
+                          int max_pages, const int32_t *lens, const int32_t *first, int B, int S_out, int out_dtype,
+                          void *k_out, void *v_out, vq_stream_t stream);
+
+/*
+ * vq_paged_attend - attention of the new tokens of B sequences over their
+ * pages, one token each (decode), a chunk of a prompt each, or any mix.
+ *   q [T, Hq, D] of q_dtype (VQ_F16 or VQ_BF16; a 16-bit cache has the same
+ *     type), strided: the new tokens of all sequences one after another.
+ *   cu_q [B + 1] int32, device: sequence b has tokens [cu_q[b], cu_q[b + 1]) of
+ *     q, n_b of them, at most max_q (more set VQ_DEVERR_BAD_OFFSET, and the
+ *     tokens past max_q are left out).
+ *   lens [B] int32, device: tokens of sequence b in the cache, the new ones
+ *     (already written) included.
+ * Token i of sequence b is at position p = lens[b] - n_b + i and sees the keys
+ * j <= p that satisfy: window == 0, or j > p - window, or j < sinks.
+ *   out[t][hq] = sum_j softmax_j(scale * q[t][hq] . k_j) v_j over them, kv head
+ *   hq / (Hq / Hkv); zeros if there is none.  out [T, Hq, D] of q_dtype,
+ *   contiguous; tokens of no sequence are not written.
+ * Scores, softmax and sums are held in 32 bits; the softmax weights enter the
+ * value product as 16-bit numbers (fp16 over an 8-bit cache, else the cache's
+ * type), half a step of rounding each.  Keys that no new token of a sequence
+ * sees may hold anything, infinities and NaN among it.  A visible entry must be
+ * finite: one that is not may reach the outputs of tokens that do not see it.
+ *   workspace: device memory of at least the size that
+ *     vq_paged_attend_workspace reports on the current device, 256-byte
+ *     aligned, not shared by calls in flight at the same time.
+ * Hq = GQ * Hkv with GQ from 1 to 16.  Results do not depend on the order in
+ * which blocks run.
+ */
+vq_status vq_paged_attend_workspace(int T, int B, int Hq, int Hkv, int max_q, size_t *bytes);
+vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_stride_h, int q_dtype,
+                          const void *k_pages, const void *v_pages, const uint8_t *k_exp, const uint8_t *v_exp,
+                          int cache_dtype, int num_pages, int Hkv, int page_size, int D, const int32_t *block_table,
+                          int max_pages, const int32_t *cu_q, const int32_t *lens, int T, int B, int Hq, int max_q,
+                          int window, int sinks, float scale, void *out, void *workspace, size_t workspace_bytes,
+                          vq_stream_t stream);
 
 /*
  * vq_device_error - waits for `stream`, then reads and clears the library's

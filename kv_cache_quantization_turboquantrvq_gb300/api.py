@@ -31,7 +31,9 @@ EXPORTED = ("vq_status_str", "vq_version", "vq_rvq_codebook", "vq_rvq_encode_pac
             "vq_rvq_unpack_dequant", "vq_kivi_quant_pack", "vq_kivi_unpack_dequant",
             "vq_device_error", "vq_rvq_attend_workspace", "vq_rvq_attend", "vq_rvq_attend_noalloc",
             "vq_rvq_encode_pack_rs", "vq_rvq_unpack_dequant_rs", "vq_rvq_attend_rs",
-            "vq_kivi_attend_workspace", "vq_kivi_attend", "vq_qjl_encode", "vq_flush_decode")
+            "vq_kivi_attend_workspace", "vq_kivi_attend", "vq_qjl_encode", "vq_flush_decode",
+            "vq_paged_append", "vq_paged_gather", "vq_paged_attend_workspace", "vq_paged_attend")
+VQ_F16, VQ_BF16, VQ_E4M3 = 0, 1, 2
 VQ_ATTEND_SCRATCH_BYTES = 16 * 1024 * 1024
 
 
@@ -73,6 +75,12 @@ def lib():
     L.vq_qjl_encode.argtypes = [P, I, I, P, I, P, P, P]
     L.vq_flush_decode.argtypes = [P, P, I, I, I, I, I, P, I, I, P, P, P, P, P, P, P, I, I,
                                   P, P, P, P, P, P, P, P, P, I, P]
+    Q = ctypes.c_longlong
+    L.vq_paged_append.argtypes = [P, Q, Q, P, Q, Q, I, I, P, P, P, P, P, I, I, I, I, I, P]
+    L.vq_paged_gather.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, P, I, I, I, P, P, P]
+    L.vq_paged_attend_workspace.argtypes = [I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
+    L.vq_paged_attend.argtypes = [P, Q, Q, I, P, P, P, P, I, I, I, I, I, P, I, P, P, I, I, I, I, I, I,
+                                  ctypes.c_float, P, P, ctypes.c_size_t, P]
     for name in EXPORTED[2:]:
         getattr(L, name).restype = I
     _lib = L
@@ -413,4 +421,163 @@ def vq_flush_decode(k, v, residual_length: int, dst_off=None, S_dst=None, rvq=No
                                  _ptr(g("v_packed")), _ptr(g("v_scale")), _ptr(g("v_zero")),
                                  _ptr(g("k_win")), _ptr(g("v_win")), _ptr(win_off), R_cap, _stream(stream)),
            "vq_flush_decode")
+    return out
+
+
+def _dtype_code(dtype) -> int:
+    """VQ_F16, VQ_BF16 or VQ_E4M3 of a torch dtype (ValueError for others)."""
+    import torch
+    code = {torch.float16: VQ_F16, torch.bfloat16: VQ_BF16, torch.float8_e4m3fn: VQ_E4M3}.get(dtype)
+    if code is None:
+        raise ValueError("dtype %s: float16, bfloat16 or float8_e4m3fn" % dtype)
+    return code
+
+
+def _typed(t, dtype, shape, what):
+    """Raise ValueError unless t is a contiguous CUDA tensor of this dtype and shape."""
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s: a contiguous CUDA tensor %s of %s" % (what, tuple(shape), dtype))
+
+
+def _rows_view(t, heads, what):
+    """Checks a [T, heads, 128] view whose last dimension is contiguous."""
+    if not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError("%s: a CUDA tensor [tokens, %d, D] with contiguous rows" % (what, heads))
+
+
+def _use(stream, *tensors):
+    """Tensors allocated here for a call on another stream than the current one stay
+    reserved until that stream is done with them."""
+    if stream is not None and hasattr(stream, "cuda_stream"):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def paged_cache(num_pages: int, Hkv: int, page_size: int, dtype, device="cuda", D: int = 128) -> dict:
+    """An empty paged cache: k_pages, v_pages [num_pages, Hkv, page_size, D] of
+    dtype (float16, bfloat16 or float8_e4m3fn) and, for float8_e4m3fn, k_exp, v_exp
+    [num_pages, Hkv, page_size] uint8 (None otherwise)."""
+    import torch
+    shape = (num_pages, Hkv, page_size, D)
+    c = {x + "_pages": torch.zeros(shape, dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype,
+                                   device=device).view(dtype) for x in "kv"}
+    q = _dtype_code(dtype) == VQ_E4M3
+    for x in "kv":
+        c[x + "_exp"] = torch.full(shape[:3], 127, dtype=torch.uint8, device=device) if q else None
+    return c
+
+
+def _cache_args(cache):
+    """(k, v, k_exp, v_exp, dtype, num_pages, Hkv, page_size, D) of a cache dict."""
+    import torch
+    k, v = cache["k_pages"], cache["v_pages"]
+    if k.dim() != 4:
+        raise ValueError("k_pages: [num_pages, Hkv, page_size, D]")
+    code = _dtype_code(k.dtype)
+    _typed(k, k.dtype, k.shape, "k_pages")
+    _typed(v, k.dtype, k.shape, "v_pages")
+    ke, ve = cache.get("k_exp"), cache.get("v_exp")
+    if code == VQ_E4M3:
+        if ke is None or ve is None:
+            raise ValueError("a float8_e4m3fn cache has k_exp and v_exp")
+        _typed(ke, torch.uint8, k.shape[:3], "k_exp")
+        _typed(ve, torch.uint8, k.shape[:3], "v_exp")
+    else:
+        ke = ve = None
+    return (_ptr(k), _ptr(v), _ptr(ke), _ptr(ve), code) + tuple(k.shape)
+
+
+def vq_paged_append(k, v, cache: dict, slots, stream=None) -> dict:
+    """Write the keys and values k, v [T, Hkv, 128] (fp16 or bf16, rows may be
+    strided) of new tokens into the paged cache at slots [T] int64 (page *
+    page_size + place; negative: not written).  Returns the cache."""
+    import torch
+    args = _cache_args(cache)
+    T = k.shape[0]
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v: the same shape and dtype")
+    _rows_view(k, args[6], "k")
+    _rows_view(v, args[6], "v")
+    _typed(slots, torch.int64, (T,), "slots")
+    if k.shape[2] != args[8]:
+        raise ValueError("k: head width %d" % args[8])
+    _check(lib().vq_paged_append(_ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1),
+                                 _dtype_code(k.dtype), T, _ptr(slots), *args, _stream(stream)), "vq_paged_append")
+    return cache
+
+
+def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtype=None, k_out=None, v_out=None,
+                    want_k=True, want_v=True, stream=None):
+    """Read tokens first[b] + [0, S_out) of every sequence back: (k, v)
+    [B, Hkv, S_out, 128] of dtype (the cache's; float16 by default from an 8-bit
+    cache), zeros past lens[b].  block_table [B, max_pages], lens and first [B] int32."""
+    import torch
+    args = _cache_args(cache)
+    B, max_pages = block_table.shape
+    _typed(block_table, torch.int32, (B, max_pages), "block_table")
+    _typed(lens, torch.int32, (B,), "lens")
+    if first is not None:
+        _typed(first, torch.int32, (B,), "first")
+    if dtype is None:
+        dtype = torch.float16 if args[4] == VQ_E4M3 else cache["k_pages"].dtype
+    shape = (B, args[6], S_out, args[8])
+    dev = block_table.device
+    made = []
+    if want_k and k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+        made.append(k_out)
+    if want_v and v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+        made.append(v_out)
+    for t, want in ((k_out, want_k), (v_out, want_v)):
+        if want:
+            _typed(t, dtype, shape, "k_out, v_out")
+    _check(lib().vq_paged_gather(*args, _ptr(block_table), max_pages, _ptr(lens), _ptr(first), B, S_out,
+                                 _dtype_code(dtype), _ptr(k_out) if want_k else None,
+                                 _ptr(v_out) if want_v else None, _stream(stream)), "vq_paged_gather")
+    _use(stream, *made)
+    return (k_out if want_k else None), (v_out if want_v else None)
+
+
+def vq_paged_attend_workspace(T: int, B: int, Hq: int, Hkv: int, max_q: int) -> int:
+    """Workspace bytes vq_paged_attend needs for these shapes on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(lib().vq_paged_attend_workspace(T, B, Hq, Hkv, max_q, ctypes.byref(n)), "vq_paged_attend_workspace")
+    return int(n.value)
+
+
+def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q: int, window: int = 0, sinks: int = 0,
+                    out=None, workspace=None, stream=None):
+    """Attention of new tokens q [T, Hq, 128] (rows may be strided) over a paged
+    cache.  Sequence b has tokens cu_q[b] .. cu_q[b + 1] - 1 (at most max_q), the
+    last of them at position lens[b] - 1; each sees the keys up to its own
+    position, with a window those of the last `window` positions and the first
+    `sinks`.  cu_q [B + 1], lens [B], block_table [B, max_pages] int32.  Returns
+    [T, Hq, 128] of q's dtype; the workspace (uint8) is allocated when not given."""
+    import torch
+    args = _cache_args(cache)
+    B, max_pages = block_table.shape
+    T, Hq, _ = q.shape
+    _rows_view(q, Hq, "q")
+    if q.shape[2] != args[8]:
+        raise ValueError("q: head width %d" % args[8])
+    _typed(block_table, torch.int32, (B, max_pages), "block_table")
+    _typed(cu_q, torch.int32, (B + 1,), "cu_q")
+    _typed(lens, torch.int32, (B,), "lens")
+    made = []
+    if out is None:
+        out = torch.empty((T, Hq, args[8]), dtype=q.dtype, device=q.device)
+        made.append(out)
+    else:
+        _typed(out, q.dtype, (T, Hq, args[8]), "out")
+    if workspace is None:
+        workspace = torch.empty(max(vq_paged_attend_workspace(T, B, Hq, args[6], max_q), 16), dtype=torch.uint8,
+                                device=q.device)
+        made.append(workspace)
+    _check(lib().vq_paged_attend(_ptr(q), q.stride(0), q.stride(1), _dtype_code(q.dtype), *args, _ptr(block_table),
+                                 max_pages, _ptr(cu_q), _ptr(lens), T, B, Hq, max_q, window, sinks, float(scale),
+                                 _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                 _stream(stream)), "vq_paged_attend")
+    _use(stream, *made)
     return out

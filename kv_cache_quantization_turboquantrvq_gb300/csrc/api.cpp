@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "launch.h"
+#include "paged.h"
 #include "vq.h"
 
 namespace vq {
@@ -913,8 +914,11 @@ vq_status vq_device_error(vq_stream_t stream, int *code_out)
     if (gen_take_device_error(&e, s) != cudaSuccess) return VQ_ERR_CUDA;
     if (qjl_take_device_error(&f, s) != cudaSuccess) return VQ_ERR_CUDA;
     if (flush_take_device_error(&g, s) != cudaSuccess) return VQ_ERR_CUDA;
-    *code_out = (int)(a | b | c | d | e | f | g);
-    return (a | b | c | d | e | f | g) ? VQ_ERR_DEVICE : VQ_OK;
+    unsigned h = 0, i = 0;
+    if (paged_cache_take_device_error(&h, s) != cudaSuccess) return VQ_ERR_CUDA;
+    if (paged_attend_take_device_error(&i, s) != cudaSuccess) return VQ_ERR_CUDA;
+    *code_out = (int)(a | b | c | d | e | f | g | h | i);
+    return *code_out ? VQ_ERR_DEVICE : VQ_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,63 @@
+// paged_dev.cuh - device helpers of the paged-cache operators: e4m3 codes,
+// powers of two, the walk over a launch's units of work.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "device_common.cuh"
+#include "paged.h"
+
+namespace vq {
+namespace {
+
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Two e4m3 codes (bits 0-7 and 8-15) as an fp16 pair; exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ long long pg_first_unit(const PgPlanHead &h, int c) { return h.total * c / h.g; }
+
+// What of an entry's keys its rows see together: [lo, hi) and the first `sink` keys.
+struct PgView {
+    int hi, lo, sink;
+    __device__ __forceinline__ void set(const PgEntry &e, int window, int sinks)
+    {
+        hi = e.hi;
+        lo = window > 0 ? max(0, e.p0 - window + 1) : 0;
+        sink = window > 0 ? min(sinks, hi) : 0;
+    }
+    // some / every key of [k0, k1) is seen by some row
+    __device__ __forceinline__ bool any(int k0, int k1) const { return k0 < hi && (k1 > lo || k0 < sink); }
+    __device__ __forceinline__ bool one(int k) const { return k < hi && (k >= lo || k < sink); }
+};
+
+__device__ __forceinline__ PgEntry pg_entry(const PgEntry *e)
+{
+    const int4 a = __ldg(reinterpret_cast<const int4 *>(e)), b = __ldg(reinterpret_cast<const int4 *>(e) + 1);
+    PgEntry r;
+    r.b = a.x; r.tok0 = a.y; r.nt = a.z; r.p0 = a.w;
+    r.hi = b.x; r.nsink = b.y; r.tl = b.z; r.ntiles = b.w;
+    return r;
+}
+
+// first key of tile t of an entry
+__device__ __forceinline__ int pg_tile_key(const PgEntry &e, int t)
+{
+    return (t < e.nsink ? t : e.tl + (t - e.nsink)) * PG_TILE;
+}
+
+}  // namespace
+}  // namespace vq

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "launch.h"
+#include "paged.h"
 
 namespace vq {
 
@@ -69,6 +70,21 @@ bool encode_tmap_words(CUtensorMap *map, const void *base, uint64_t rows, uint32
                                                         : CU_TENSOR_MAP_SWIZZLE_NONE;
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), gd, gs, bx, es,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+bool encode_tmap_pages(CUtensorMap *map, const void *base, uint64_t rows, int elem_bytes, uint32_t box_rows)
+{
+    EncodeTiled fn = encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t gd[2] = {128, rows};
+    const cuuint64_t gs[1] = {(cuuint64_t)128 * elem_bytes};
+    const cuuint32_t bx[2] = {128u / (cuuint32_t)elem_bytes, box_rows};  // 128 bytes a row
+    const cuuint32_t es[2] = {1, 1};
+    const CUresult r = fn(map, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                          const_cast<void *>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
