@@ -917,7 +917,9 @@ vq_status vq_device_error(vq_stream_t stream, int *code_out)
     unsigned h = 0, i = 0;
     if (paged_cache_take_device_error(&h, s) != cudaSuccess) return VQ_ERR_CUDA;
     if (paged_attend_take_device_error(&i, s) != cudaSuccess) return VQ_ERR_CUDA;
-    *code_out = (int)(a | b | c | d | e | f | g | h | i);
+    unsigned j = 0;
+    if (paged_chunk_take_device_error(&j, s) != cudaSuccess) return VQ_ERR_CUDA;
+    *code_out = (int)(a | b | c | d | e | f | g | h | i | j);
     return *code_out ? VQ_ERR_DEVICE : VQ_OK;
 }
 

@@ -99,6 +99,8 @@ constexpr int PG_PART = 2 + 128; // floats of a row's partial result: max, sum, 
 
 cudaError_t launch_paged_plan(const PagedAttendParams &p, cudaStream_t stream);
 cudaError_t launch_paged_small(const PagedAttendParams &p, int q_dtype, int cache_dtype, cudaStream_t stream);
+cudaError_t launch_paged_large(const PagedAttendParams &p, int q_dtype, int cache_dtype, cudaStream_t stream);
+cudaError_t paged_chunk_take_device_error(unsigned *bits, cudaStream_t stream);
 cudaError_t launch_paged_combine(const PagedAttendParams &p, int q_dtype, bool large, cudaStream_t stream);
 cudaError_t paged_attend_take_device_error(unsigned *bits, cudaStream_t stream);
 

@@ -120,9 +120,9 @@ Layout layout(size_t at, int cap, int G, int rows)
 }
 
 struct AttendPlan {
-    int small_rows, small_cap, small_tq, G;
+    int small_rows, small_cap, small_tq, large_cap, large_tq, G;
     size_t bytes;
-    Layout s;
+    Layout s, l;
 };
 
 vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, AttendPlan &pl)
@@ -133,11 +133,20 @@ vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, AttendPlan &pl)
     if ((long long)T * Hq >= (1LL << 31) || B > (1 << 20)) return VQ_ERR_UNSUPPORTED;
     std::memset(&pl, 0, sizeof(pl));
     pl.G = sm_count();
-    pl.small_rows = 0x7fffffff;
-    pl.small_tq = gq ? PG_SROWS / gq : PG_SROWS;
-    pl.small_cap = (T + pl.small_tq - 1) / pl.small_tq + B;
+    if (T == 0 || B == 0 || gq == 0) return VQ_OK;
+    // Sequences with at most 16 query rows per kv head go to the small kernel,
+    // longer chunks to the tensor-memory kernel.  A call whose bounds leave one
+    // kind only (max_q short, or every sequence at max_q) launches one kernel.
+    pl.small_tq = PG_SROWS / gq;
+    pl.large_tq = 2 * (128 / gq);
+    const bool large = (long long)max_q * gq > PG_SROWS;
+    const bool small = !large || (long long)B * max_q > T;
+    pl.small_rows = small ? PG_SROWS : 0;
+    if (small) pl.small_cap = B;
+    if (large) pl.large_cap = (T + pl.large_tq - 1) / pl.large_tq + B;
     pl.s = layout(0, pl.small_cap, pl.G, PG_SROWS);
-    pl.bytes = pl.s.end;
+    pl.l = layout(pl.s.end, pl.large_cap, pl.G, PG_LROWS);
+    pl.bytes = pl.l.end;
     return VQ_OK;
 }
 
@@ -306,10 +315,13 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
     p.qscale = (float)((double)scale * 1.4426950408889634);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     place(p.small, ws, pl.s, pl.small_cap, pl.G, pl.small_tq);
+    place(p.large, ws, pl.l, pl.large_cap, pl.G, pl.large_tq);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_paged_plan(p, s);
-    if (e == cudaSuccess) e = launch_paged_small(p, q_dtype, cache_dtype, s);
-    if (e == cudaSuccess) e = launch_paged_combine(p, q_dtype, false, s);
+    if (e == cudaSuccess && pl.large_cap) e = launch_paged_large(p, q_dtype, cache_dtype, s);
+    if (e == cudaSuccess && pl.small_cap) e = launch_paged_small(p, q_dtype, cache_dtype, s);
+    if (e == cudaSuccess && pl.large_cap) e = launch_paged_combine(p, q_dtype, true, s);
+    if (e == cudaSuccess && pl.small_cap) e = launch_paged_combine(p, q_dtype, false, s);
     return status_of(e);
 }
 

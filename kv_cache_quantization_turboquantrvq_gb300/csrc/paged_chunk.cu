@@ -1,0 +1,707 @@
+// paged_chunk.cu - attention of chunks of new tokens over a paged key/value
+// cache on the 5th-generation tensor cores (sm_103a).  Formulas, plan and the
+// merge of partial results: paged_attend.cu.
+//
+// Both products are matrix products with enough rows to fill the tensor cores,
+// so they bound the kernel.  An item is 256 query rows of one kv head (all GQ
+// query heads of up to 2 * floor(128 / GQ) tokens, so a key tile is read once
+// for all of them) against a run of 128-key tiles, in two tiles of 128 rows
+// that share every key and value tile: while the tensor cores work for one,
+// the other's softmax runs.  Tensor memory holds both score tiles and both
+// outputs (4 x 128 columns); the weights, rounded to 16 bits, overwrite the
+// scores they came from and enter the second product from there, so scores and
+// weights never leave the SM.
+//
+// Roles (one CTA per SM): two groups of 4 softmax warps, a thread per query
+// row; one warp that streams queries, keys and values by TMA (a box per page);
+// one thread that issues tcgen05.mma.  With an 8-bit cache four more warps
+// turn the codes into 16-bit operands in shared memory (exact) and put the
+// exponents where the softmax reads them.
+//
+// The output is rescaled only when a row's maximum grew by more than 2^LAG
+// (the softmax warps do it in tensor memory between two products), so weights
+// reach up to 2^(OFF + LAG) and nearly no tile pays for it.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "device_common.cuh"
+#include "paged.h"
+#include "paged_dev.cuh"
+#include "tcgen05.cuh"
+
+namespace vq {
+
+namespace {
+
+VQ_DEFINE_ERROR_WORD(g_pk_err);
+
+constexpr int D = 128;
+constexpr float NEG_INF = -__builtin_huge_valf();
+constexpr float OFF = 7.0f, LAG = 8.0f;
+constexpr int TILE_B = PG_TILE * D * 2;  // a 16-bit tile of 128 rows: two halves of 64 columns
+constexpr int HALF_B = TILE_B / 2;
+constexpr int RAW_B = PG_TILE * D;       // a tile of codes
+
+template <bool Q8> struct CkShape {
+    static constexpr int STAGES = Q8 ? 3 : 5;   // 16-bit key / value tiles
+    static constexpr int RAW = Q8 ? 3 : 0;      // tiles of codes in flight
+    static constexpr int META = Q8 ? 2 : 0;     // key tiles whose exponents are unpacked
+    static constexpr int WARPS = Q8 ? 16 : 12;
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int BARS = 2 + 2 * STAGES + 6 + 2 * RAW + 2 * META + 1;
+    static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + RAW * 2 * PG_TILE +
+                                META * 3 * PG_TILE * 4 + 8 * BARS + 16;
+};
+static_assert(CkShape<false>::SMEM <= 232448 && CkShape<true>::SMEM <= 232448, "shared memory of one CTA");
+
+// Operand B of the value product: rows are keys (K), 64-column halves side by
+// side (N contiguous): 128-byte swizzle, 8-key groups 1024 bytes apart, the
+// halves HALF_B apart.
+__device__ __forceinline__ uint64_t ck_desc_v(uint32_t saddr)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(HALF_B >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Instruction descriptor: fp32 accumulator, M = N = 128, both operands fp16 or
+// both bf16; `b_mn`: B has its N dimension contiguous.
+__host__ __device__ constexpr uint32_t ck_idesc(bool bf16, bool b_mn)
+{
+    return qt_idesc(128) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+
+// D += A B with A (16-bit pairs) in tensor memory.
+__device__ __forceinline__ void ck_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+}
+
+__device__ __forceinline__ void ck_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void ck_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void ck_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// L2 policy of the cache's tiles: other CTAs read them too.
+__device__ __forceinline__ uint64_t ck_policy()
+{
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
+template <class T> __device__ __forceinline__ uint32_t ck_pack(float a, float b);
+template <> __device__ __forceinline__ uint32_t ck_pack<__half>(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <> __device__ __forceinline__ uint32_t ck_pack<__nv_bfloat16>(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <class T> __device__ __forceinline__ uint32_t ck_codes(uint32_t two);
+template <> __device__ __forceinline__ uint32_t ck_codes<__half>(uint32_t two) { return e4m3x2_to_f16x2(two); }
+template <> __device__ __forceinline__ uint32_t ck_codes<__nv_bfloat16>(uint32_t two)
+{
+    const uint32_t h2 = e4m3x2_to_f16x2(two);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+    return ck_pack<__nv_bfloat16>(f.x, f.y);
+}
+
+// One CTA's share as runs of tiles of one item each.
+struct Run {
+    PgEntry e;
+    int ei, h, t0, tn, left;
+    bool first;  // the CTA's first run
+    __device__ __forceinline__ void start(const PgPlan &pl, const PgPlanHead &head, int c)
+    {
+        const int4 at = __ldg(pl.ctab + c);
+        ei = at.x;
+        h = at.y;
+        t0 = at.z;
+        left = (int)(pg_first_unit(head, c + 1) - pg_first_unit(head, c));
+        e = pg_entry(pl.ent + ei);
+        tn = min(e.ntiles, t0 + left);
+        first = true;
+    }
+    __device__ __forceinline__ bool next(const PgPlan &pl, int Hkv)
+    {
+        left -= tn - t0;
+        if (left <= 0) return false;
+        if (++h == Hkv) {
+            h = 0;
+            ++ei;
+            e = pg_entry(pl.ent + ei);
+        }
+        t0 = 0;
+        tn = min(e.ntiles, left);
+        first = false;
+        return true;
+    }
+};
+
+// Position in a ring of N barriers: slot and the parity of its current pass.
+template <int N> struct Ring {
+    int s = 0;
+    uint32_t par = 0;
+    __device__ __forceinline__ void step()
+    {
+        if (++s == N) {
+            s = 0;
+            par ^= 1u;
+        }
+    }
+};
+
+template <class T, bool Q8>
+__global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(const __grid_constant__ PagedAttendParams p)
+{
+    using C = CkShape<Q8>;
+    using TV = typename std::conditional<Q8, __half, T>::type;  // weights and values
+    constexpr int STAGES = C::STAGES;
+    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value, BFV = std::is_same<TV, __nv_bfloat16>::value;
+    const PgPlanHead head = *p.large.head;
+    if ((int)blockIdx.x >= head.g) return;
+
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    unsigned char *sq = smem_1k(smem_raw);                  // two query tiles
+    unsigned char *skv = sq + 2 * TILE_B;                   // key / value tiles
+    unsigned char *sraw = skv + STAGES * TILE_B;            // tiles of codes
+    unsigned char *sexp = sraw + C::RAW * RAW_B;            // [RAW][2][128] exponents (of key tiles)
+    float *smeta = reinterpret_cast<float *>(sexp + C::RAW * 2 * PG_TILE);  // [META][3][128]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smeta + C::META * 3 * PG_TILE);
+    uint64_t *q_full = bars, *q_empty = bars + 1, *kv_full = bars + 2, *kv_empty = kv_full + STAGES;
+    uint64_t *s_full = kv_empty + STAGES, *p_full = s_full + 2, *o_full = p_full + 2;
+    uint64_t *raw_full = o_full + 2, *raw_empty = raw_full + C::RAW;
+    uint64_t *meta_full = raw_empty + C::RAW, *meta_empty = meta_full + C::META;
+    uint64_t *drain = meta_empty + C::META;
+    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(drain + 1);
+    volatile uint32_t *abort_flag = tslot + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tqt = 128 / p.GQ;  // tokens of one query tile
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&kv_full[s], Q8 ? 4 : 1);
+            mbar_init(&kv_empty[s], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&s_full[w], 1);
+            mbar_init(&p_full[w], 4);
+            mbar_init(&o_full[w], 1);
+        }
+        for (int s = 0; s < C::RAW; ++s) {
+            mbar_init(&raw_full[s], 1);
+            mbar_init(&raw_empty[s], 4);
+        }
+        for (int s = 0; s < C::META; ++s) {
+            mbar_init(&meta_full[s], 4);
+            mbar_init(&meta_empty[s], 8);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(const_cast<uint32_t *>(tslot), 512);
+    qt_fence_before();
+    __syncthreads();
+    qt_fence_after();
+    const uint32_t tmem = *tslot;  // scores at 0, 128; outputs at 256, 384
+
+    // Bounded wait; gives up (and makes every role give up) after the limit.
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        for (;;) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > MBAR_TIMEOUT_NS) {
+                atomicOr(&g_pk_err, (unsigned)VQ_DEVERR_WAIT_TIMEOUT);
+                *abort_flag = 1u;
+                return false;
+            }
+        }
+    };
+
+    Run r;
+    r.start(p.large, head, blockIdx.x);
+
+    if (warp == 8) {
+        // ------------------------------------------------ copies (TMA)
+        const int box = min(1 << p.c.page_shift, PG_TILE), nbox = PG_TILE / box;
+        const int rows_all = p.c.num_pages * p.c.Hkv << p.c.page_shift;  // no box holds this row: reads zeros
+        const uint64_t pol = ck_policy();
+        Ring<STAGES> kv;
+        Ring<C::RAW ? C::RAW : 1> raw;
+        uint32_t qpar = 0;
+        int tiles = 0;  // tiles copied
+        bool ok = true;
+        do {
+            if (!r.first) {
+                ok = __all_sync(FULL_MASK, wait(q_empty, qpar));
+                qpar ^= 1u;
+                if (!ok) break;
+            }
+            if (lane == 0) {
+                // tokens past the chunk bring other sequences' rows, past the tensor zeros: never used
+                const int nq = r.e.nt > tqt ? 2 : 1;
+                mbar_arrive_expect_tx(q_full, (uint32_t)(nq * 2 * tqt * p.GQ * 128));
+                for (int w = 0; w < nq; ++w)
+                    for (int hf = 0; hf < 2; ++hf)
+                        tma_load_3d(sq + w * TILE_B + hf * HALF_B, &p.tmq, 64 * hf, r.h * p.GQ, r.e.tok0 + w * tqt, q_full, pol);
+            }
+            PgView view;
+            view.set(r.e, p.window, p.sinks);
+            for (int t = r.t0; t < r.tn && ok; ++t) {
+                const int k0 = pg_tile_key(r.e, t) + lane * box;
+                int row = rows_all;
+                bool held = false;
+                if (lane < nbox && view.any(k0, k0 + box)) {
+                    const int lp = k0 >> p.c.page_shift;
+                    const int page = lp < p.max_pages ? __ldg(p.table + (long long)r.e.b * p.max_pages + lp) : -1;
+                    held = page >= 0 && page < p.c.num_pages;
+                    if (held) row = ((page * p.c.Hkv + r.h) << p.c.page_shift) + (k0 & ((1 << p.c.page_shift) - 1));
+                    else atomicOr(&g_pk_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+                }
+                for (int part = 0; part < 2; ++part) {  // keys, values
+                    const CUtensorMap *map = part ? &p.tmv : &p.tmk;
+                    if constexpr (Q8) {
+                        if (tiles >= C::RAW && !__all_sync(FULL_MASK, wait(&raw_empty[raw.s], raw.par ^ 1u))) {
+                            ok = false;
+                            break;
+                        }
+                        // a key tile brings the exponents of keys and values
+                        const unsigned n = part ? 0u : (unsigned)__popc(__ballot_sync(FULL_MASK, held));
+                        if (lane == 0) mbar_arrive_expect_tx(&raw_full[raw.s], RAW_B + n * 2 * box);
+                        __syncwarp();
+                        if (lane < nbox) {
+                            tma_load_2d(sraw + raw.s * RAW_B + lane * box * 128, map, 0, row, &raw_full[raw.s], pol);
+                            if (held && part == 0) {
+                                unsigned char *x = sexp + raw.s * 2 * PG_TILE + lane * box;
+                                bulk_g2s(x, p.c.ke + row, box, &raw_full[raw.s], pol);
+                                bulk_g2s(x + PG_TILE, p.c.ve + row, box, &raw_full[raw.s], pol);
+                            }
+                        }
+                        raw.step();
+                    } else {
+                        if (tiles >= STAGES && !__all_sync(FULL_MASK, wait(&kv_empty[kv.s], kv.par ^ 1u))) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&kv_full[kv.s], TILE_B);
+                        __syncwarp();
+                        if (lane < nbox) {
+                            unsigned char *dst = skv + kv.s * TILE_B + lane * box * 128;
+                            tma_load_2d(dst, map, 0, row, &kv_full[kv.s], pol);
+                            tma_load_2d(dst + HALF_B, map, 64, row, &kv_full[kv.s], pol);
+                        }
+                        kv.step();
+                    }
+                    ++tiles;
+                }
+            }
+        } while (ok && r.next(p.large, p.Hkv));
+        // every copy has landed before the CTA may exit
+        if constexpr (Q8) {
+            for (int k = 0; k < C::RAW && k < tiles; ++k) {
+                const int j = tiles - 1 - k;
+                (void)mbar_wait_bounded(&raw_full[j % C::RAW], (uint32_t)(j / C::RAW) & 1u);
+            }
+        } else {
+            for (int k = 0; k < STAGES && k < tiles; ++k) {
+                const int j = tiles - 1 - k;
+                (void)mbar_wait_bounded(&kv_full[j % STAGES], (uint32_t)(j / STAGES) & 1u);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ------------------------------------------------ products (one thread)
+        if (lane == 0) {
+            constexpr uint32_t ID_S = ck_idesc(BF, false), ID_O = ck_idesc(BFV, true);
+            const uint32_t aq = smem_u32(sq), akv = smem_u32(skv);
+            Ring<STAGES> ks, vs;  // slot of the next key tile and of the next value tile
+            vs.step();
+            uint32_t qpar = 0, ppar[2] = {0, 0};
+            bool ok = true;
+            auto scores = [&](int w, int slot) {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t o = (kk >> 2) * HALF_B + (kk & 3) * 32;
+                    qt_mma(tmem + 128 * w, qt_desc(aq + w * TILE_B + o), qt_desc(akv + slot * TILE_B + o), ID_S, kk ? 1u : 0u);
+                }
+                qt_commit(&s_full[w]);
+            };
+            auto values = [&](int w, int slot, bool acc) {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    ck_mma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * kk, ck_desc_v(akv + slot * TILE_B + kk * 2048), ID_O,
+                              (acc || kk) ? 1u : 0u);
+            };
+            do {
+                const int nq = r.e.nt > tqt ? 2 : 1;
+                ok = wait(q_full, qpar) && wait(&kv_full[ks.s], ks.par);
+                qpar ^= 1u;
+                if (!ok) break;
+                qt_fence_after();
+                for (int w = 0; w < nq; ++w) scores(w, ks.s);
+                qt_commit(&kv_empty[ks.s]);
+                ks.step();
+                ks.step();
+                for (int t = r.t0; t < r.tn && ok; ++t) {
+                    const bool last = t + 1 == r.tn;
+                    ok = wait(&kv_full[vs.s], vs.par);
+                    for (int w = 0; w < nq && ok; ++w) {
+                        ok = wait(&p_full[w], ppar[w]);
+                        ppar[w] ^= 1u;
+                        if (!ok) break;
+                        qt_fence_after();
+                        values(w, vs.s, t > r.t0);
+                        if (w == nq - 1) qt_commit(&kv_empty[vs.s]);
+                        if (last) {
+                            qt_commit(&o_full[w]);
+                        } else {
+                            if (w == 0) {
+                                ok = wait(&kv_full[ks.s], ks.par);
+                                if (!ok) break;
+                                qt_fence_after();
+                            }
+                            scores(w, ks.s);
+                        }
+                    }
+                    if (!ok) break;
+                    if (!last) qt_commit(&kv_empty[ks.s]);
+                    // (after the last scores of the run the queries may be replaced)
+                    if (t + 2 == r.tn || (last && r.tn - r.t0 == 1)) qt_commit(q_empty);
+                    vs.step();
+                    vs.step();
+                    if (!last) {
+                        ks.step();
+                        ks.step();
+                    }
+                }
+            } while (ok && r.next(p.large, p.Hkv));
+            qt_commit(drain);  // every product is done before shared and tensor memory are given up
+            (void)mbar_wait_bounded(drain, 0u);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ------------------------------------------------ softmax: a thread per query row
+        const int w = warp >> 2;
+        const int row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
+        const int tok_in = row / p.GQ, g = row % p.GQ;
+        uint32_t spar = 0, opar = 0;
+        Ring<STAGES> vs;  // (16-bit cache) slot of the next value tile
+        vs.step();
+        Ring<C::META ? C::META : 1> mt;
+        bool ok = true;
+        do {
+            const int nq = r.e.nt > tqt ? 2 : 1;
+            if (w >= nq) {  // this half has no rows in the item
+                if constexpr (Q8) {
+                    for (int t = r.t0; t < r.tn && ok; ++t) {
+                        ok = __all_sync(FULL_MASK, wait(&meta_full[mt.s], mt.par));  // (not ahead of its tile)
+                        if (lane == 0) mbar_arrive(&meta_empty[mt.s]);
+                        mt.step();
+                    }
+                    if (!ok) break;
+                }
+                continue;
+            }
+            PgView view;
+            view.set(r.e, p.window, p.sinks);
+            const int tok = w * tqt + tok_in;
+            const bool mine = tok_in < tqt && tok < r.e.nt;
+            const int pos = mine ? r.e.p0 + tok : -1;
+            const int low = p.window > 0 ? pos - p.window + 1 : 0;
+            const int pos_a = r.e.p0 + w * tqt, pos_z = r.e.p0 + min(r.e.nt, (w + 1) * tqt) - 1;  // this tile's tokens
+            float m = NEG_INF, l = 0.0f;
+            for (int t = r.t0; t < r.tn; ++t) {
+                const int k0 = pg_tile_key(r.e, t);
+                const bool whole = k0 + PG_TILE <= pos_a + 1 &&
+                                   (p.window == 0 || k0 > pos_z - p.window || k0 + PG_TILE <= view.sink);
+                ok = __all_sync(FULL_MASK, wait(&s_full[w], spar));
+                spar ^= 1u;
+                if (!ok) break;
+                if constexpr (Q8) {
+                    ok = __all_sync(FULL_MASK, wait(&meta_full[mt.s], mt.par));
+                    if (!ok) break;
+                }
+                qt_fence_after();
+                const float *ma = smeta + mt.s * 3 * PG_TILE;
+                // score c of this row in the softmax's units (base 2), masked
+                auto value = [&](uint32_t raw, int c) {
+                    float x = __uint_as_float(raw);
+                    if constexpr (Q8) x = fmaf(x, ma[c], ma[PG_TILE + c]);
+                    else x *= p.qscale;
+                    if (!whole) {
+                        const int k = k0 + c;
+                        x = k <= pos && (k >= low || k < view.sink) ? x : NEG_INF;
+                    }
+                    return x;
+                };
+                float mx = NEG_INF;
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t x[32];
+                    qt_ld32(ts + 32 * b, x);
+                    qt_wait_ld();
+                    qt_hold(x);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, value(x[j], 32 * b + j));
+                }
+                const bool grow = mx - OFF > m + LAG;
+                if (__any_sync(FULL_MASK, grow)) {
+                    const float f = grow ? ex2(m - (mx - OFF)) : 1.0f;
+                    if (grow) m = mx - OFF;
+                    l *= f;
+                    if (t > r.t0) {  // the previous value product is done: its scores came after it
+#pragma unroll 1
+                        for (int b = 0; b < 4; ++b) {
+                            uint32_t x[32];
+                            qt_ld32(to + 32 * b, x);
+                            qt_wait_ld();
+                            qt_hold(x);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+                            ck_st32(to + 32 * b, x);
+                        }
+                    }
+                }
+                const float ms = m > NEG_INF ? m : 0.0f;
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t x[32], pk[16];
+                    qt_ld32(ts + 32 * b, x);
+                    qt_wait_ld();
+                    qt_hold(x);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const int c = 32 * b + j;
+                        const float a = ex2(value(x[j], c) - ms), z = ex2(value(x[j + 1], c + 1) - ms);
+                        if constexpr (Q8) {
+                            sum[0] = fmaf(a, ma[2 * PG_TILE + c], sum[0]);
+                            sum[1] = fmaf(z, ma[2 * PG_TILE + c + 1], sum[1]);
+                        } else {
+                            sum[0] += a;
+                            sum[1] += z;
+                        }
+                        pk[j >> 1] = ck_pack<TV>(a, z);
+                    }
+                    ck_st16(ts + 16 * b, pk);  // over scores that were read
+                }
+                l += sum[0] + sum[1];
+                if constexpr (Q8) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&meta_empty[mt.s]);
+                    mt.step();
+                } else {
+                    // values of keys that no row sees may hold anything: zero
+                    // them before the product (the second half's comes later)
+                    if (w == 0 && (k0 + PG_TILE > view.hi || (k0 < view.lo && k0 + PG_TILE > view.sink))) {
+                        ok = __all_sync(FULL_MASK, wait(&kv_full[vs.s], vs.par));
+                        if (!ok) break;
+                        if (!view.one(k0 + row)) {
+                            uint4 *z = reinterpret_cast<uint4 *>(skv + vs.s * TILE_B + row * 128);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                z[j] = make_uint4(0u, 0u, 0u, 0u);
+                                z[HALF_B / 16 + j] = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                        }
+                        fence_proxy_async_smem();
+                    }
+                }
+                vs.step();
+                vs.step();
+                ck_wait_st();
+                qt_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[w]);
+            }
+            if (!ok) break;
+            ok = __all_sync(FULL_MASK, wait(&o_full[w], opar));
+            opar ^= 1u;
+            if (!ok) break;
+            qt_fence_after();
+            const bool split = r.t0 > 0 || r.tn < r.e.ntiles;
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            float *part = p.large.part + (size_t)(2 * blockIdx.x + (r.first && r.t0 > 0 ? 0 : 1)) * (PG_LROWS * PG_PART);
+            if (split && mine) {
+                part[128 * w + row] = m;
+                part[PG_LROWS + 128 * w + row] = l;
+            }
+            float4 *po = reinterpret_cast<float4 *>(part + 2 * PG_LROWS + (size_t)(128 * w + row) * D);
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) +
+                                                   ((size_t)(r.e.tok0 + tok) * p.Hq + (size_t)r.h * p.GQ + g) * D);
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                uint32_t x[32];
+                qt_ld32(to + 32 * b, x);
+                qt_wait_ld();
+                qt_hold(x);
+                if (!mine) continue;
+                if (split) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        po[8 * b + j] = make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]),
+                                                    __uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            y[i] = ck_pack<T>(__uint_as_float(x[8 * j + 2 * i]) * inv, __uint_as_float(x[8 * j + 2 * i + 1]) * inv);
+                        out[4 * b + j] = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+            }
+            qt_fence_before();  // (ordered before the next run's products by p_full)
+        } while (r.next(p.large, p.Hkv));
+    } else if (Q8 && warp >= 12) {
+        // ------------------------------------------------ codes to 16-bit operands
+        const int j = threadIdx.x - 12 * 32;
+        Ring<C::RAW ? C::RAW : 1> raw;
+        Ring<STAGES> kv;
+        Ring<C::META ? C::META : 1> mt;
+        int tiles = 0, keys = 0;
+        bool ok = true;
+        do {
+            PgView view;
+            view.set(r.e, p.window, p.sinks);
+            for (int t = r.t0; t < r.tn && ok; ++t) {
+                const int k0 = pg_tile_key(r.e, t);
+                const bool edge = k0 + PG_TILE > view.hi || (k0 < view.lo && k0 + PG_TILE > view.sink);
+                for (int part = 0; part < 2; ++part) {
+                    ok = __all_sync(FULL_MASK, wait(&raw_full[raw.s], raw.par));
+                    if (ok && tiles >= STAGES) ok = __all_sync(FULL_MASK, wait(&kv_empty[kv.s], kv.par ^ 1u));
+                    if (ok && part == 0 && keys >= C::META) ok = __all_sync(FULL_MASK, wait(&meta_empty[mt.s], mt.par ^ 1u));
+                    if (!ok) break;
+                    if (part == 0) {
+                        // this key's factors: scores * a + b, weights / 2^b
+                        const unsigned char *x = sexp + raw.s * 2 * PG_TILE;
+                        const int a = (int)x[j] - 127, b = (int)x[PG_TILE + j] - 127;
+                        float *ma = smeta + mt.s * 3 * PG_TILE;
+                        ma[j] = p.qscale * pow2f(max(a, -126));
+                        ma[PG_TILE + j] = (float)b;
+                        ma[2 * PG_TILE + j] = pow2f(max(-b, -126));
+                    }
+                    const unsigned char *src = sraw + raw.s * RAW_B;
+                    unsigned char *dst = skv + kv.s * TILE_B;
+#pragma unroll 2
+                    for (int i = 0; i < 8; ++i) {
+                        const int id = j + 128 * i, row = id >> 3, c = id & 7;
+                        uint4 v = *reinterpret_cast<const uint4 *>(src + swz128(row, c));
+                        if (edge && part == 1 && !view.one(k0 + row)) v = make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            o[2 * q] = part ? ck_codes<TV>(in[q] & 0xffffu) : ck_codes<T>(in[q] & 0xffffu);
+                            o[2 * q + 1] = part ? ck_codes<TV>(in[q] >> 16) : ck_codes<T>(in[q] >> 16);
+                        }
+                        unsigned char *d = dst + (c >> 2) * HALF_B;
+                        *reinterpret_cast<uint4 *>(d + swz128(row, 2 * (c & 3))) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(d + swz128(row, 2 * (c & 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&raw_empty[raw.s]);
+                        mbar_arrive(&kv_full[kv.s]);
+                        if (part == 0) mbar_arrive(&meta_full[mt.s]);
+                    }
+                    raw.step();
+                    kv.step();
+                    ++tiles;
+                    if (part == 0) {
+                        mt.step();
+                        ++keys;
+                    }
+                }
+            }
+        } while (ok && r.next(p.large, p.Hkv));
+    }
+
+    qt_fence_before();
+    __syncthreads();
+    qt_fence_after();
+    if (warp == 9) tmem_free(tmem, 512);
+}
+
+template <class T, bool Q8>
+cudaError_t launch_chunk(const PagedAttendParams &p, cudaStream_t stream)
+{
+    auto kern = paged_chunk_kernel<T, Q8>;
+    constexpr int smem = CkShape<Q8>::SMEM;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<p.large.G, CkShape<Q8>::THREADS, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_large(const PagedAttendParams &p0, int q_dtype, int cache_dtype, cudaStream_t stream)
+{
+    PagedAttendParams p = p0;
+    const bool q8 = cache_dtype == VQ_E4M3;
+    const uint64_t rows = ((uint64_t)p.c.num_pages * p.c.Hkv) << p.c.page_shift;
+    const uint32_t box = 1u << p.c.page_shift < (unsigned)PG_TILE ? 1u << p.c.page_shift : (unsigned)PG_TILE;
+    if (!encode_tmap_pages(&p.tmk, p.c.k, rows, q8 ? 1 : 2, box) || !encode_tmap_pages(&p.tmv, p.c.v, rows, q8 ? 1 : 2, box))
+        return cudaErrorInvalidValue;
+    // queries: boxes of 64 columns, the heads of a kv head, the tokens of a tile
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.Hq, (uint64_t)p.T};
+    const uint64_t strides[2] = {(uint64_t)(p.Hq > 1 ? p.qsh : D) * 2, (uint64_t)(p.T > 1 ? p.qst : (long long)p.Hq * D) * 2};
+    const uint32_t qbox[3] = {64u, (uint32_t)p.GQ, (uint32_t)(128 / p.GQ)};
+    if (!encode_tmap_f16(&p.tmq, p.q, 3, dims, strides, qbox, true, true)) return cudaErrorInvalidValue;
+    if (q_dtype == VQ_F16) return q8 ? launch_chunk<__half, true>(p, stream) : launch_chunk<__half, false>(p, stream);
+    return q8 ? launch_chunk<__nv_bfloat16, true>(p, stream) : launch_chunk<__nv_bfloat16, false>(p, stream);
+}
+
+cudaError_t paged_chunk_take_device_error(unsigned *bits, cudaStream_t stream)
+{
+    *bits = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_pk_err, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) return e;
+    if (*bits) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbolAsync(g_pk_err, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, stream);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    }
+    return e;
+}
+
+}  // namespace vq
