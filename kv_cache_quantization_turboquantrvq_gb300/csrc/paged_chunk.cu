@@ -50,6 +50,10 @@ template <bool Q8> struct CkShape {
     static constexpr int META = Q8 ? 2 : 0;     // key tiles whose exponents are unpacked
     static constexpr int WARPS = Q8 ? 16 : 12;
     static constexpr int THREADS = 32 * WARPS;
+    // registers a thread: at launch, the softmax warps, warps 8-11, warps 12-15;
+    // the shares of all warps add up to the launch's at most
+    static constexpr int REGS = Q8 ? 128 : 168, R_SOFT = Q8 ? 184 : 208, R_CTL = Q8 ? 72 : 88, R_CONV = 72;
+    static_assert(256 * R_SOFT + 128 * R_CTL + (Q8 ? 128 * R_CONV : 0) <= THREADS * REGS, "registers of one CTA");
     static constexpr int BARS = 2 + 2 * STAGES + 6 + 2 * RAW + 2 * META + 1;
     static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + RAW * 2 * PG_TILE +
                                 META * 3 * PG_TILE * 4 + 8 * BARS + 16;
@@ -91,18 +95,6 @@ __device__ __forceinline__ void ck_st16(uint32_t taddr, const uint32_t (&r)[16])
         : "memory");
 }
 
-__device__ __forceinline__ void ck_st32(uint32_t taddr, const uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
 __device__ __forceinline__ void ck_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // L2 policy of the cache's tiles: other CTAs read them too.
@@ -112,6 +104,28 @@ __device__ __forceinline__ uint64_t ck_policy()
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
     return pol;
 }
+
+// 16 consecutive fp32 columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void ck_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void ck_hold16(uint32_t (&r)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[j])::"memory");
+}
+
+__device__ __forceinline__ float2 ck_f2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
+
+template <int N> __device__ __forceinline__ void ck_reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void ck_reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <class T> __device__ __forceinline__ uint32_t ck_pack(float a, float b);
 template <> __device__ __forceinline__ uint32_t ck_pack<__half>(float a, float b)
@@ -254,6 +268,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     Run r;
     r.start(p.large, head, blockIdx.x);
 
+    if (warp >= 8 && warp < 12) {
+    ck_reg_dec<C::R_CTL>();
     if (warp == 8) {
         // ------------------------------------------------ copies (TMA)
         const int box = min(1 << p.c.page_shift, PG_TILE), nbox = PG_TILE / box;
@@ -412,13 +428,16 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
             (void)mbar_wait_bounded(drain, 0u);
         }
         __syncwarp();
+    }
     } else if (warp < 8) {
+        ck_reg_inc<C::R_SOFT>();
         // ------------------------------------------------ softmax: a thread per query row
         const int w = warp >> 2;
         const int row = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
         const int tok_in = row / p.GQ, g = row % p.GQ;
+        const float qabs = fabsf(p.qscale);
         uint32_t spar = 0, opar = 0;
         Ring<STAGES> vs;  // (16-bit cache) slot of the next value tile
         vs.step();
@@ -457,28 +476,49 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     if (!ok) break;
                 }
                 qt_fence_after();
-                const float *ma = smeta + mt.s * 3 * PG_TILE;
-                // score c of this row in the softmax's units (base 2), masked
-                auto value = [&](uint32_t raw, int c) {
-                    float x = __uint_as_float(raw);
-                    if constexpr (Q8) x = fmaf(x, ma[c], ma[PG_TILE + c]);
-                    else x *= p.qscale;
-                    if (!whole) {
-                        const int k = k0 + c;
-                        x = k <= pos && (k >= low || k < view.sink) ? x : NEG_INF;
-                    }
-                    return x;
-                };
-                float mx = NEG_INF;
-#pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t x[32];
-                    qt_ld32(ts + 32 * b, x);
-                    qt_wait_ld();
-                    qt_hold(x);
+                // all scores of the row into registers
+                uint32_t x[4][32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, value(x[j], 32 * b + j));
+                for (int b = 0; b < 4; ++b) qt_ld32(ts + 32 * b, x[b]);
+                qt_wait_ld();
+#pragma unroll
+                for (int b = 0; b < 4; ++b) qt_hold(x[b]);
+                const float *ma = smeta + mt.s * 3 * PG_TILE;
+                if constexpr (Q8) {
+                    // 2^a and the scale, plus the value's exponent, key by key
+#pragma unroll
+                    for (int c = 0; c < PG_TILE; c += 4) {
+                        const float4 fa = *reinterpret_cast<const float4 *>(ma + c);
+                        const float4 fb = *reinterpret_cast<const float4 *>(ma + PG_TILE + c);
+                        uint32_t *y = &x[c >> 5][c & 31];
+                        const float2 u = __ffma2_rn(ck_f2(y[0], y[1]), make_float2(fa.x, fa.y), make_float2(fb.x, fb.y));
+                        const float2 v = __ffma2_rn(ck_f2(y[2], y[3]), make_float2(fa.z, fa.w), make_float2(fb.z, fb.w));
+                        y[0] = __float_as_uint(u.x);
+                        y[1] = __float_as_uint(u.y);
+                        y[2] = __float_as_uint(v.x);
+                        y[3] = __float_as_uint(v.y);
+                    }
+                } else if (p.qscale < 0.0f) {  // (the products below take |scale|)
+#pragma unroll
+                    for (int c = 0; c < PG_TILE; ++c) x[c >> 5][c & 31] ^= 0x80000000u;
                 }
+                if (!whole) {
+                    const int hi = pos - k0, lo = low - k0, sink = view.sink - k0;
+#pragma unroll
+                    for (int c = 0; c < PG_TILE; ++c)
+                        if (c > hi || (c < lo && c >= sink)) x[c >> 5][c & 31] = 0xff800000u;
+                }
+                float mx4[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    float y = fmaxf(__uint_as_float(x[b][0]), __uint_as_float(x[b][1]));
+#pragma unroll
+                    for (int j = 2; j < 32; j += 2)
+                        y = fmaxf(fmaxf(y, __uint_as_float(x[b][j])), __uint_as_float(x[b][j + 1]));
+                    mx4[b] = y;
+                }
+                float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                if constexpr (!Q8) mx *= qabs;
                 const bool grow = mx - OFF > m + LAG;
                 if (__any_sync(FULL_MASK, grow)) {
                     const float f = grow ? ex2(m - (mx - OFF)) : 1.0f;
@@ -486,41 +526,37 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     l *= f;
                     if (t > r.t0) {  // the previous value product is done: its scores came after it
 #pragma unroll 1
-                        for (int b = 0; b < 4; ++b) {
-                            uint32_t x[32];
-                            qt_ld32(to + 32 * b, x);
+                        for (int b = 0; b < 8; ++b) {
+                            uint32_t y[16];
+                            ck_ld16(to + 16 * b, y);
                             qt_wait_ld();
-                            qt_hold(x);
+                            ck_hold16(y);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-                            ck_st32(to + 32 * b, x);
+                            for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                            ck_st16(to + 16 * b, y);
                         }
                     }
                 }
                 const float ms = m > NEG_INF ? m : 0.0f;
-                float sum[2] = {0.0f, 0.0f};
-#pragma unroll 1
+                const float2 neg = make_float2(-ms, -ms), mul = make_float2(qabs, qabs);
+                float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    uint32_t x[32], pk[16];
-                    qt_ld32(ts + 32 * b, x);
-                    qt_wait_ld();
-                    qt_hold(x);
+                    uint32_t pk[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const int c = 32 * b + j;
-                        const float a = ex2(value(x[j], c) - ms), z = ex2(value(x[j + 1], c + 1) - ms);
-                        if constexpr (Q8) {
-                            sum[0] = fmaf(a, ma[2 * PG_TILE + c], sum[0]);
-                            sum[1] = fmaf(z, ma[2 * PG_TILE + c + 1], sum[1]);
-                        } else {
-                            sum[0] += a;
-                            sum[1] += z;
-                        }
-                        pk[j >> 1] = ck_pack<TV>(a, z);
+                        const float2 y = ck_f2(x[b][j], x[b][j + 1]);
+                        const float2 u = Q8 ? __fadd2_rn(y, neg) : __ffma2_rn(y, mul, neg);
+                        const float2 e = make_float2(ex2(u.x), ex2(u.y));
+                        if constexpr (Q8)
+                            sum2 = __ffma2_rn(e, *reinterpret_cast<const float2 *>(ma + 2 * PG_TILE + 32 * b + j), sum2);
+                        else
+                            sum2 = __fadd2_rn(sum2, e);
+                        pk[j >> 1] = ck_pack<TV>(e.x, e.y);
                     }
                     ck_st16(ts + 16 * b, pk);  // over scores that were read
                 }
-                l += sum[0] + sum[1];
+                l += sum2.x + sum2.y;
                 if constexpr (Q8) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&meta_empty[mt.s]);
@@ -589,7 +625,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
             }
             qt_fence_before();  // (ordered before the next run's products by p_full)
         } while (r.next(p.large, p.Hkv));
-    } else if (Q8 && warp >= 12) {
+    } else if constexpr (Q8) {
+        ck_reg_dec<C::R_CONV>();
         // ------------------------------------------------ codes to 16-bit operands
         const int j = threadIdx.x - 12 * 32;
         Ring<C::RAW ? C::RAW : 1> raw;
@@ -667,6 +704,11 @@ cudaError_t launch_chunk(const PagedAttendParams &p, cudaStream_t stream)
     constexpr int smem = CkShape<Q8>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    // the warps trade registers inside the launch's share: never start with fewer
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, kern);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs != CkShape<Q8>::REGS) return cudaErrorLaunchOutOfResources;
     kern<<<p.large.G, CkShape<Q8>::THREADS, smem, stream>>>(p);
     return cudaGetLastError();
 }
