@@ -124,6 +124,9 @@ __device__ __forceinline__ void ck_hold16(uint32_t (&r)[16])
 
 __device__ __forceinline__ float2 ck_f2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
 
+// A word with its n lowest bits set (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t ck_below(int n) { return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u; }
+
 template <int N> __device__ __forceinline__ void ck_reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void ck_reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -503,10 +506,15 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     for (int c = 0; c < PG_TILE; ++c) x[c >> 5][c & 31] ^= 0x80000000u;
                 }
                 if (!whole) {
-                    const int hi = pos - k0, lo = low - k0, sink = view.sink - k0;
+                    // bit c of word b: key k0 + 32 b + c is seen (words, not
+                    // comparisons key by key: those became branches)
+                    const int hi = pos - k0 + 1, lo = low - k0, sink = view.sink - k0;
 #pragma unroll
-                    for (int c = 0; c < PG_TILE; ++c)
-                        if (c > hi || (c < lo && c >= sink)) x[c >> 5][c & 31] = 0xff800000u;
+                    for (int b = 0; b < 4; ++b) {
+                        const uint32_t see = ck_below(hi - 32 * b) & (~ck_below(lo - 32 * b) | ck_below(sink - 32 * b));
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[b][j] = (see >> j) & 1u ? x[b][j] : 0xff800000u;
+                    }
                 }
                 float mx4[4];
 #pragma unroll
