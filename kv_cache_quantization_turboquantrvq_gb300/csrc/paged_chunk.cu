@@ -6,11 +6,14 @@
 // so they bound the kernel.  An item is 256 query rows of one kv head (all GQ
 // query heads of up to 2 * floor(128 / GQ) tokens, so a key tile is read once
 // for all of them) against a run of 128-key tiles, in two tiles of 128 rows
-// that share every key and value tile: while the tensor cores work for one,
-// the other's softmax runs.  Tensor memory holds both score tiles and both
-// outputs (4 x 128 columns); the weights, rounded to 16 bits, overwrite the
-// scores they came from and enter the second product from there, so scores and
-// weights never leave the SM.
+// that share every key and value tile.  Tensor memory holds one score tile
+// (128 columns), the weights of both tiles as 16-bit pairs (2 x 64) and both
+// outputs (2 x 128): a score tile is copied to registers as soon as it is there
+// and its place goes to the other tile's next scores, so that the next product
+// never waits for a softmax (with a score tile of its own each, whose place the
+// weights took over, the chain scores - softmax - values - next scores bound the
+// kernel: 1.98 us for two tiles of 128 x 128, of which the products are 1.07).
+// Scores and weights never leave the SM.
 //
 // Roles (one CTA per SM): two groups of 4 softmax warps, a thread per query
 // row; one warp that streams queries, keys and values by TMA (a box per page);
@@ -45,7 +48,7 @@ constexpr int HALF_B = TILE_B / 2;
 constexpr int RAW_B = PG_TILE * D;       // a tile of codes
 
 template <bool Q8> struct CkShape {
-    static constexpr int STAGES = Q8 ? 3 : 5;   // 16-bit key / value tiles
+    static constexpr int STAGES = Q8 ? 3 : 4;   // 16-bit key / value tiles
     static constexpr int RAW = Q8 ? 3 : 0;      // tiles of codes in flight
     static constexpr int META = Q8 ? 2 : 0;     // key tiles whose exponents are unpacked
     static constexpr int WARPS = Q8 ? 16 : 12;
@@ -54,8 +57,9 @@ template <bool Q8> struct CkShape {
     // the shares of all warps add up to the launch's at most
     static constexpr int REGS = Q8 ? 128 : 168, R_SOFT = Q8 ? 184 : 208, R_CTL = Q8 ? 72 : 88, R_CONV = 72;
     static_assert(256 * R_SOFT + 128 * R_CTL + (Q8 ? 128 * R_CONV : 0) <= THREADS * REGS, "registers of one CTA");
-    static constexpr int BARS = 2 + 2 * STAGES + 6 + 2 * RAW + 2 * META + 1;
-    static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + RAW * 2 * PG_TILE +
+    static constexpr int BARS = 2 + 2 * STAGES + 7 + 2 * RAW + 2 * META + 1;
+    static constexpr int OUTB = Q8 ? 32 : 128;  // bytes a row that a softmax warp lays out at a time for its stores
+    static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + 8 * 32 * OUTB + RAW * 2 * PG_TILE +
                                 META * 3 * PG_TILE * 4 + 8 * BARS + 16;
 };
 static_assert(CkShape<false>::SMEM <= 232448 && CkShape<true>::SMEM <= 232448, "shared memory of one CTA");
@@ -76,13 +80,80 @@ __host__ __device__ constexpr uint32_t ck_idesc(bool bf16, bool b_mn)
     return qt_idesc(128) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u);
 }
 
-// D += A B with A (16-bit pairs) in tensor memory.
-__device__ __forceinline__ void ck_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
+// The products of one 128 x 128 x 128 tile, eight K = 16 steps, by one elected
+// thread of the (whole, converged) warp.  One block of PTX each, so that the
+// operands' addresses stay in uniform registers: issued one by one from a
+// branch on the lane number, an instruction took 107 cycles to issue where the
+// tensor core needs 64.  `bar` (shared) gets an arrival when they are done.
+
+// D = A B, both from shared memory, rows of 64 entries: steps 32 bytes apart,
+// the second half of K HALF_B further.
+__device__ __forceinline__ void ck_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t bar)
+{
+    static_assert(HALF_B == 16384, "the descriptors' steps below");
+    asm volatile(
+        "{\n\t.reg .pred q, f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 t, 1, 0;\n\tsetp.ne.b32 f, 0, 0;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\tadd.s64 a4, %1, 1024;\n\t"
+        "add.s64 a5, %1, 1026;\n\tadd.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\tadd.s64 b4, %2, 1024;\n\t"
+        "add.s64 b5, %2, 1026;\n\tadd.s64 b6, %2, 1028;\n\tadd.s64 b7, %2, 1030;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, t;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(bar)
+        : "memory");
+}
+
+// D (+)= A B with A (16-bit pairs) in tensor memory, 8 columns a step, and B's
+// rows (keys) 2048 bytes a step; acc 0: D is overwritten.
+__device__ __forceinline__ void ck_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t bar)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+        "{\n\t.reg .pred q, f, t;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
+        ".reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 t, 1, 0;\n\tsetp.ne.b32 f, %4, 0;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 32;\n\t"
+        "add.s32 a5, %1, 40;\n\tadd.s32 a6, %1, 48;\n\tadd.s32 a7, %1, 56;\n\t"
+        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\t"
+        "add.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(bar)
+        : "memory");
+}
+
+// An arrival on `bar` when every product that this warp's elected thread issued
+// is done.
+__device__ __forceinline__ void ck_commit(uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+// One lane of the (whole, converged) warp: the same each time.
+__device__ __forceinline__ bool ck_elect()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));
+    return e != 0;
 }
 
 __device__ __forceinline__ void ck_st16(uint32_t taddr, const uint32_t (&r)[16])
@@ -210,12 +281,13 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     unsigned char *sq = smem_1k(smem_raw);                  // two query tiles
     unsigned char *skv = sq + 2 * TILE_B;                   // key / value tiles
     unsigned char *sraw = skv + STAGES * TILE_B;            // tiles of codes
-    unsigned char *sexp = sraw + C::RAW * RAW_B;            // [RAW][2][128] exponents (of key tiles)
+    unsigned char *sout = sraw + C::RAW * RAW_B;            // [8 warps][32 rows][OUTB]
+    unsigned char *sexp = sout + 8 * 32 * C::OUTB;          // [RAW][2][128] exponents (of key tiles)
     float *smeta = reinterpret_cast<float *>(sexp + C::RAW * 2 * PG_TILE);  // [META][3][128]
     uint64_t *bars = reinterpret_cast<uint64_t *>(smeta + C::META * 3 * PG_TILE);
     uint64_t *q_full = bars, *q_empty = bars + 1, *kv_full = bars + 2, *kv_empty = kv_full + STAGES;
-    uint64_t *s_full = kv_empty + STAGES, *p_full = s_full + 2, *o_full = p_full + 2;
-    uint64_t *raw_full = o_full + 2, *raw_empty = raw_full + C::RAW;
+    uint64_t *s_full = kv_empty + STAGES, *p_full = s_full + 2, *pv_done = p_full + 2, *s_free = pv_done + 2;
+    uint64_t *raw_full = s_free + 1, *raw_empty = raw_full + C::RAW;
     uint64_t *meta_full = raw_empty + C::RAW, *meta_empty = meta_full + C::META;
     uint64_t *drain = meta_empty + C::META;
     volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(drain + 1);
@@ -233,8 +305,9 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         for (int w = 0; w < 2; ++w) {
             mbar_init(&s_full[w], 1);
             mbar_init(&p_full[w], 4);
-            mbar_init(&o_full[w], 1);
+            mbar_init(&pv_done[w], 1);
         }
+        mbar_init(s_free, 4);
         for (int s = 0; s < C::RAW; ++s) {
             mbar_init(&raw_full[s], 1);
             mbar_init(&raw_empty[s], 4);
@@ -251,7 +324,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     qt_fence_before();
     __syncthreads();
     qt_fence_after();
-    const uint32_t tmem = *tslot;  // scores at 0, 128; outputs at 256, 384
+    const uint32_t tmem = *tslot;  // scores at 0, weights at 128 and 192, outputs at 256 and 384
 
     // Bounded wait; gives up (and makes every role give up) after the limit.
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -289,7 +362,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 qpar ^= 1u;
                 if (!ok) break;
             }
-            if (lane == 0) {
+            if (ck_elect()) {
                 // tokens past the chunk bring other sequences' rows, past the tensor zeros: never used
                 const int nq = r.e.nt > tqt ? 2 : 1;
                 mbar_arrive_expect_tx(q_full, (uint32_t)(nq * 2 * tqt * p.GQ * 128));
@@ -299,19 +372,27 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
             }
             PgView view;
             view.set(r.e, p.window, p.sinks);
-            for (int t = r.t0; t < r.tn && ok; ++t) {
-                const int k0 = pg_tile_key(r.e, t) + lane * box;
-                int row = rows_all;
-                bool held = false;
-                if (lane < nbox && view.any(k0, k0 + box)) {
-                    const int lp = k0 >> p.c.page_shift;
-                    const int page = lp < p.max_pages ? __ldg(p.table + (long long)r.e.b * p.max_pages + lp) : -1;
-                    held = page >= 0 && page < p.c.num_pages;
-                    if (held) row = ((page * p.c.Hkv + r.h) << p.c.page_shift) + (k0 & ((1 << p.c.page_shift) - 1));
-                    else atomicOr(&g_pk_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+            int row = rows_all, prow = rows_all;  // of this tile and of the one before
+            bool held = false;
+            // in the order of use: keys of tile t + 1, then values of tile t
+            for (int t = r.t0; t <= r.tn && ok; ++t) {
+                prow = row;
+                row = rows_all;
+                held = false;
+                if (t < r.tn) {
+                    const int k0 = pg_tile_key(r.e, t) + lane * box;
+                    if (lane < nbox && view.any(k0, k0 + box)) {
+                        const int lp = k0 >> p.c.page_shift;
+                        const int page = lp < p.max_pages ? __ldg(p.table + (long long)r.e.b * p.max_pages + lp) : -1;
+                        held = page >= 0 && page < p.c.num_pages;
+                        if (held) row = ((page * p.c.Hkv + r.h) << p.c.page_shift) + (k0 & ((1 << p.c.page_shift) - 1));
+                        else atomicOr(&g_pk_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+                    }
                 }
                 for (int part = 0; part < 2; ++part) {  // keys, values
+                    if (part == 0 ? t == r.tn : t == r.t0) continue;
                     const CUtensorMap *map = part ? &p.tmv : &p.tmk;
+                    const int at = part ? prow : row;
                     if constexpr (Q8) {
                         if (tiles >= C::RAW && !__all_sync(FULL_MASK, wait(&raw_empty[raw.s], raw.par ^ 1u))) {
                             ok = false;
@@ -319,14 +400,16 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                         }
                         // a key tile brings the exponents of keys and values
                         const unsigned n = part ? 0u : (unsigned)__popc(__ballot_sync(FULL_MASK, held));
-                        if (lane == 0) mbar_arrive_expect_tx(&raw_full[raw.s], RAW_B + n * 2 * box);
-                        __syncwarp();
-                        if (lane < nbox) {
-                            tma_load_2d(sraw + raw.s * RAW_B + lane * box * 128, map, 0, row, &raw_full[raw.s], pol);
-                            if (held && part == 0) {
-                                unsigned char *x = sexp + raw.s * 2 * PG_TILE + lane * box;
-                                bulk_g2s(x, p.c.ke + row, box, &raw_full[raw.s], pol);
-                                bulk_g2s(x + PG_TILE, p.c.ve + row, box, &raw_full[raw.s], pol);
+                        if (ck_elect()) mbar_arrive_expect_tx(&raw_full[raw.s], RAW_B + n * 2 * box);
+                        for (int i = 0; i < nbox; ++i) {
+                            const int rw = __shfl_sync(FULL_MASK, at, i);
+                            if (ck_elect()) {
+                                tma_load_2d(sraw + raw.s * RAW_B + i * box * 128, map, 0, rw, &raw_full[raw.s], pol);
+                                if (part == 0 && rw != rows_all) {
+                                    unsigned char *x = sexp + raw.s * 2 * PG_TILE + i * box;
+                                    bulk_g2s(x, p.c.ke + rw, box, &raw_full[raw.s], pol);
+                                    bulk_g2s(x + PG_TILE, p.c.ve + rw, box, &raw_full[raw.s], pol);
+                                }
                             }
                         }
                         raw.step();
@@ -335,12 +418,14 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                             ok = false;
                             break;
                         }
-                        if (lane == 0) mbar_arrive_expect_tx(&kv_full[kv.s], TILE_B);
-                        __syncwarp();
-                        if (lane < nbox) {
-                            unsigned char *dst = skv + kv.s * TILE_B + lane * box * 128;
-                            tma_load_2d(dst, map, 0, row, &kv_full[kv.s], pol);
-                            tma_load_2d(dst + HALF_B, map, 64, row, &kv_full[kv.s], pol);
+                        if (ck_elect()) mbar_arrive_expect_tx(&kv_full[kv.s], TILE_B);
+                        for (int i = 0; i < nbox; ++i) {
+                            const int rw = __shfl_sync(FULL_MASK, at, i);
+                            if (ck_elect()) {
+                                unsigned char *dst = skv + kv.s * TILE_B + i * box * 128;
+                                tma_load_2d(dst, map, 0, rw, &kv_full[kv.s], pol);
+                                tma_load_2d(dst + HALF_B, map, 64, rw, &kv_full[kv.s], pol);
+                            }
                         }
                         kv.step();
                     }
@@ -362,74 +447,65 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         }
         __syncwarp();
     } else if (warp == 9) {
-        // ------------------------------------------------ products (one thread)
-        if (lane == 0) {
-            constexpr uint32_t ID_S = ck_idesc(BF, false), ID_O = ck_idesc(BFV, true);
-            const uint32_t aq = smem_u32(sq), akv = smem_u32(skv);
-            Ring<STAGES> ks, vs;  // slot of the next key tile and of the next value tile
-            vs.step();
-            uint32_t qpar = 0, ppar[2] = {0, 0};
-            bool ok = true;
-            auto scores = [&](int w, int slot) {
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t o = (kk >> 2) * HALF_B + (kk & 3) * 32;
-                    qt_mma(tmem + 128 * w, qt_desc(aq + w * TILE_B + o), qt_desc(akv + slot * TILE_B + o), ID_S, kk ? 1u : 0u);
+        // ------------------------------------------------ products (the whole warp
+        // keeps the order, an elected thread issues)
+        constexpr uint32_t ID_S = ck_idesc(BF, false), ID_O = ck_idesc(BFV, true);
+        const uint64_t dq = qt_desc(smem_u32(sq)), dk = qt_desc(smem_u32(skv)), dv = ck_desc_v(smem_u32(skv));
+        const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
+        Ring<STAGES> kv;
+        uint32_t qpar = 0, ppar[2] = {0, 0}, fpar = 1;  // (the score tile is free at first)
+        bool ok = true;
+        auto await = [&](uint64_t *bar, uint32_t parity) { ok = ok && __all_sync(FULL_MASK, wait(bar, parity)); };
+        auto scores = [&](int w, int slot) {  // into the score tile, once its last use was copied out
+            await(s_free, fpar);
+            fpar ^= 1u;
+            if (!ok) return;
+            qt_fence_after();
+            ck_mma_ss(tm, dq + w * (TILE_B >> 4), dk + slot * (TILE_B >> 4), ID_S, smem_u32(&s_full[w]));
+        };
+        auto values = [&](int w, int slot, bool acc) {
+            await(&p_full[w], ppar[w]);
+            ppar[w] ^= 1u;
+            if (!ok) return;
+            qt_fence_after();
+            ck_mma_ts(tm + 256 + 128 * w, tm + 128 + 64 * w, dv + slot * (TILE_B >> 4), ID_O, acc ? 1u : 0u,
+                      smem_u32(&pv_done[w]));
+        };
+        do {
+            const bool two = r.e.nt > tqt;
+            await(q_full, qpar);
+            await(&kv_full[kv.s], kv.par);
+            qpar ^= 1u;
+            scores(0, kv.s);
+            if (two) scores(1, kv.s);
+            if (!ok) break;
+            ck_commit(&kv_empty[kv.s]);
+            if (r.tn - r.t0 == 1) ck_commit(q_empty);  // (the run's last scores: the queries may be replaced)
+            kv.step();
+            for (int t = r.t0; t < r.tn && ok; ++t) {
+                const bool last = t + 1 == r.tn;
+                const Ring<STAGES> k = kv;
+                if (!last) {
+                    await(&kv_full[k.s], k.par);
+                    scores(0, k.s);
+                    kv.step();
                 }
-                qt_commit(&s_full[w]);
-            };
-            auto values = [&](int w, int slot, bool acc) {
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    ck_mma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * kk, ck_desc_v(akv + slot * TILE_B + kk * 2048), ID_O,
-                              (acc || kk) ? 1u : 0u);
-            };
-            do {
-                const int nq = r.e.nt > tqt ? 2 : 1;
-                ok = wait(q_full, qpar) && wait(&kv_full[ks.s], ks.par);
-                qpar ^= 1u;
+                await(&kv_full[kv.s], kv.par);
+                values(0, kv.s, t > r.t0);
+                if (two && !last) scores(1, k.s);
                 if (!ok) break;
-                qt_fence_after();
-                for (int w = 0; w < nq; ++w) scores(w, ks.s);
-                qt_commit(&kv_empty[ks.s]);
-                ks.step();
-                ks.step();
-                for (int t = r.t0; t < r.tn && ok; ++t) {
-                    const bool last = t + 1 == r.tn;
-                    ok = wait(&kv_full[vs.s], vs.par);
-                    for (int w = 0; w < nq && ok; ++w) {
-                        ok = wait(&p_full[w], ppar[w]);
-                        ppar[w] ^= 1u;
-                        if (!ok) break;
-                        qt_fence_after();
-                        values(w, vs.s, t > r.t0);
-                        if (w == nq - 1) qt_commit(&kv_empty[vs.s]);
-                        if (last) {
-                            qt_commit(&o_full[w]);
-                        } else {
-                            if (w == 0) {
-                                ok = wait(&kv_full[ks.s], ks.par);
-                                if (!ok) break;
-                                qt_fence_after();
-                            }
-                            scores(w, ks.s);
-                        }
-                    }
-                    if (!ok) break;
-                    if (!last) qt_commit(&kv_empty[ks.s]);
-                    // (after the last scores of the run the queries may be replaced)
-                    if (t + 2 == r.tn || (last && r.tn - r.t0 == 1)) qt_commit(q_empty);
-                    vs.step();
-                    vs.step();
-                    if (!last) {
-                        ks.step();
-                        ks.step();
-                    }
+                if (!last) {
+                    ck_commit(&kv_empty[k.s]);
+                    if (t + 2 == r.tn) ck_commit(q_empty);
                 }
-            } while (ok && r.next(p.large, p.Hkv));
-            qt_commit(drain);  // every product is done before shared and tensor memory are given up
-            (void)mbar_wait_bounded(drain, 0u);
-        }
+                if (two) values(1, kv.s, t > r.t0);
+                if (!ok) break;
+                ck_commit(&kv_empty[kv.s]);
+                kv.step();
+            }
+        } while (ok && r.next(p.large, p.Hkv));
+        ck_commit(drain);  // every product is done before shared and tensor memory are given up
+        (void)mbar_wait_bounded(drain, 0u);
         __syncwarp();
     }
     } else if (warp < 8) {
@@ -438,12 +514,12 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         const int w = warp >> 2;
         const int row = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
-        const int tok_in = row / p.GQ, g = row % p.GQ;
+        const uint32_t ts = tmem + lanes, tp = tmem + lanes + 128 + 64 * w, to = tmem + lanes + 256 + 128 * w;
+        unsigned char *so = sout + warp * 32 * C::OUTB;
+        const int tok_in = row / p.GQ;
         const float qabs = fabsf(p.qscale);
-        uint32_t spar = 0, opar = 0;
-        Ring<STAGES> vs;  // (16-bit cache) slot of the next value tile
-        vs.step();
+        uint32_t spar = 0, vpar = 0;
+        Ring<STAGES> vs;  // (16-bit cache) slot of the next tile that the products take
         Ring<C::META ? C::META : 1> mt;
         bool ok = true;
         do {
@@ -467,8 +543,10 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
             const int low = p.window > 0 ? pos - p.window + 1 : 0;
             const int pos_a = r.e.p0 + w * tqt, pos_z = r.e.p0 + min(r.e.nt, (w + 1) * tqt) - 1;  // this tile's tokens
             float m = NEG_INF, l = 0.0f;
+            vs.step();
             for (int t = r.t0; t < r.tn; ++t) {
                 const int k0 = pg_tile_key(r.e, t);
+                if (t + 1 < r.tn) vs.step();  // now at the values of tile t
                 const bool whole = k0 + PG_TILE <= pos_a + 1 &&
                                    (p.window == 0 || k0 > pos_z - p.window || k0 + PG_TILE <= view.sink);
                 ok = __all_sync(FULL_MASK, wait(&s_full[w], spar));
@@ -486,6 +564,9 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 qt_wait_ld();
 #pragma unroll
                 for (int b = 0; b < 4; ++b) qt_hold(x[b]);
+                qt_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free);
                 const float *ma = smeta + mt.s * 3 * PG_TILE;
                 if constexpr (Q8) {
                     // 2^a and the scale, plus the value's exponent, key by key
@@ -528,11 +609,17 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 if constexpr (!Q8) mx *= qabs;
                 const bool grow = mx - OFF > m + LAG;
+                if (t > r.t0) {  // the last weights are used up, the output holds their product
+                    ok = __all_sync(FULL_MASK, wait(&pv_done[w], vpar));
+                    vpar ^= 1u;
+                    if (!ok) break;
+                    qt_fence_after();
+                }
                 if (__any_sync(FULL_MASK, grow)) {
                     const float f = grow ? ex2(m - (mx - OFF)) : 1.0f;
                     if (grow) m = mx - OFF;
                     l *= f;
-                    if (t > r.t0) {  // the previous value product is done: its scores came after it
+                    if (t > r.t0) {
 #pragma unroll 1
                         for (int b = 0; b < 8; ++b) {
                             uint32_t y[16];
@@ -562,7 +649,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                             sum2 = __fadd2_rn(sum2, e);
                         pk[j >> 1] = ck_pack<TV>(e.x, e.y);
                     }
-                    ck_st16(ts + 16 * b, pk);  // over scores that were read
+                    ck_st16(tp + 16 * b, pk);
                 }
                 l += sum2.x + sum2.y;
                 if constexpr (Q8) {
@@ -587,15 +674,14 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     }
                 }
                 vs.step();
-                vs.step();
                 ck_wait_st();
                 qt_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[w]);
             }
             if (!ok) break;
-            ok = __all_sync(FULL_MASK, wait(&o_full[w], opar));
-            opar ^= 1u;
+            ok = __all_sync(FULL_MASK, wait(&pv_done[w], vpar));
+            vpar ^= 1u;
             if (!ok) break;
             qt_fence_after();
             const bool split = r.t0 > 0 || r.tn < r.e.ntiles;
@@ -605,29 +691,63 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 part[128 * w + row] = m;
                 part[PG_LROWS + 128 * w + row] = l;
             }
-            float4 *po = reinterpret_cast<float4 *>(part + 2 * PG_LROWS + (size_t)(128 * w + row) * D);
-            uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) +
-                                                   ((size_t)(r.e.tok0 + tok) * p.Hq + (size_t)r.h * p.GQ + g) * D);
+            // A thread holds a row; stores of one row by many lanes fill whole
+            // sectors, so the warp passes each OUTB bytes of its 32 rows through
+            // shared memory (16-byte pieces exchanged against bank conflicts).
+            constexpr int PIECES = C::OUTB / 16, SWZ = PIECES - 1;
+            const int r4 = lane / PIECES, pc = lane % PIECES;  // row (of 32 / PIECES at a time) and piece of a store
+            auto put = [&](int i, uint4 v) { *reinterpret_cast<uint4 *>(so + lane * C::OUTB + ((i ^ (lane & SWZ)) << 4)) = v; };
+            auto get = [&](int rr) { return *reinterpret_cast<const uint4 *>(so + rr * C::OUTB + ((pc ^ (rr & SWZ)) << 4)); };
+            constexpr int COLS = C::OUTB / 4;  // columns of a block (half as many registers again for 16-bit rows)
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                uint32_t x[32];
-                qt_ld32(to + 32 * b, x);
+            for (int b = 0; b < D / COLS; ++b) {
+                uint32_t y[COLS < 16 ? 16 : COLS];
+                if constexpr (COLS == 32) qt_ld32(to + COLS * b, y);
+                else ck_ld16(to + (COLS * b & ~15), y);
                 qt_wait_ld();
-                qt_hold(x);
-                if (!mine) continue;
+                if constexpr (COLS == 32) qt_hold(y);
+                else ck_hold16(y);
+                const int o = COLS < 16 && (b & 1) ? COLS : 0;
                 if (split) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        po[8 * b + j] = make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]),
-                                                    __uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3]));
+                    for (int i = 0; i < PIECES; ++i) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] = o ? y[(COLS + 4 * i + j) % (COLS < 16 ? 16 : COLS)] : y[4 * i + j];
+                        put(i, make_uint4(v[0], v[1], v[2], v[3]));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int rr = r4; rr < 32; rr += 32 / PIECES)
+                        *reinterpret_cast<uint4 *>(part + 2 * PG_LROWS + (size_t)(128 * w + 32 * (warp & 3) + rr) * D + COLS * b +
+                                                   4 * pc) = get(rr);
+                    __syncwarp();
                 } else {
+                    // half a block of 16-bit output; two blocks make OUTB bytes
+                    const int half = (b & 1) * (PIECES / 2);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t y[4];
+                    for (int i = 0; i < PIECES / 2; ++i) {
+                        uint32_t v[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            y[i] = ck_pack<T>(__uint_as_float(x[8 * j + 2 * i]) * inv, __uint_as_float(x[8 * j + 2 * i + 1]) * inv);
-                        out[4 * b + j] = make_uint4(y[0], y[1], y[2], y[3]);
+                        for (int j = 0; j < 4; ++j) {
+                            const int c = 8 * i + 2 * j;
+                            const uint32_t lo = o ? y[(COLS + c) % (COLS < 16 ? 16 : COLS)] : y[c];
+                            const uint32_t hi = o ? y[(COLS + c + 1) % (COLS < 16 ? 16 : COLS)] : y[c + 1];
+                            v[j] = ck_pack<T>(__uint_as_float(lo) * inv, __uint_as_float(hi) * inv);
+                        }
+                        put(half + i, make_uint4(v[0], v[1], v[2], v[3]));
+                    }
+                    if (b & 1) {
+                        __syncwarp();
+#pragma unroll
+                        for (int rr = r4; rr < 32; rr += 32 / PIECES) {
+                            const int q = 32 * (warp & 3) + rr, qt = q / p.GQ, tk = w * tqt + qt;
+                            if (qt < tqt && tk < r.e.nt)
+                                *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) +
+                                                           ((size_t)(r.e.tok0 + tk) * p.Hq + (size_t)r.h * p.GQ + q % p.GQ) * D +
+                                                           2 * COLS * (b >> 1) + 8 * pc) = get(rr);
+                        }
+                        __syncwarp();
                     }
                 }
             }
@@ -645,10 +765,11 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         do {
             PgView view;
             view.set(r.e, p.window, p.sinks);
-            for (int t = r.t0; t < r.tn && ok; ++t) {
-                const int k0 = pg_tile_key(r.e, t);
-                const bool edge = k0 + PG_TILE > view.hi || (k0 < view.lo && k0 + PG_TILE > view.sink);
-                for (int part = 0; part < 2; ++part) {
+            for (int u = r.t0; u <= r.tn && ok; ++u) {
+                for (int part = 0; part < 2; ++part) {  // keys of tile u, values of the tile before
+                    if (part == 0 ? u == r.tn : u == r.t0) continue;
+                    const int k0 = pg_tile_key(r.e, part ? u - 1 : u);
+                    const bool edge = k0 + PG_TILE > view.hi || (k0 < view.lo && k0 + PG_TILE > view.sink);
                     ok = __all_sync(FULL_MASK, wait(&raw_full[raw.s], raw.par));
                     if (ok && tiles >= STAGES) ok = __all_sync(FULL_MASK, wait(&kv_empty[kv.s], kv.par ^ 1u));
                     if (ok && part == 0 && keys >= C::META) ok = __all_sync(FULL_MASK, wait(&meta_empty[mt.s], mt.par ^ 1u));
