@@ -17,7 +17,8 @@
 //
 // Roles (one CTA per SM): two groups of 4 softmax warps, a thread per query
 // row; one warp that streams queries, keys and values by TMA (a box per page);
-// one thread that issues tcgen05.mma.  With an 8-bit cache four more warps
+// two warps that issue tcgen05.mma, one for scores, one for values.  With an
+// 8-bit cache four more warps
 // turn the codes into 16-bit operands in shared memory (exact) and put the
 // exponents where the softmax reads them.
 //
@@ -57,7 +58,7 @@ template <bool Q8> struct CkShape {
     // the shares of all warps add up to the launch's at most
     static constexpr int REGS = Q8 ? 128 : 168, R_SOFT = Q8 ? 184 : 208, R_CTL = Q8 ? 72 : 88, R_CONV = 72;
     static_assert(256 * R_SOFT + 128 * R_CTL + (Q8 ? 128 * R_CONV : 0) <= THREADS * REGS, "registers of one CTA");
-    static constexpr int BARS = 2 + 2 * STAGES + 7 + 2 * RAW + 2 * META + 1;
+    static constexpr int BARS = 2 + 2 * STAGES + 7 + 2 * RAW + 2 * META + 2;
     static constexpr int OUTB = Q8 ? 32 : 128;  // bytes a row that a softmax warp lays out at a time for its stores
     static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + 8 * 32 * OUTB + RAW * 2 * PG_TILE +
                                 META * 3 * PG_TILE * 4 + 8 * BARS + 16;
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     uint64_t *raw_full = s_free + 1, *raw_empty = raw_full + C::RAW;
     uint64_t *meta_full = raw_empty + C::RAW, *meta_empty = meta_full + C::META;
     uint64_t *drain = meta_empty + C::META;
-    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(drain + 1);
+    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(drain + 2);
     volatile uint32_t *abort_flag = tslot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -316,7 +317,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
             mbar_init(&meta_full[s], 4);
             mbar_init(&meta_empty[s], 8);
         }
-        mbar_init(drain, 1);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -446,66 +448,65 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
             }
         }
         __syncwarp();
-    } else if (warp == 9) {
-        // ------------------------------------------------ products (the whole warp
-        // keeps the order, an elected thread issues)
+    } else if (warp == 9 || warp == 10) {
+        // ------------------------------------------------ products: warp 9 the
+        // scores, warp 10 the values, so that neither's waits hold the other up
+        // (one warp for both spent 3600 cycles a tile on waits and issues alone)
         constexpr uint32_t ID_S = ck_idesc(BF, false), ID_O = ck_idesc(BFV, true);
         const uint64_t dq = qt_desc(smem_u32(sq)), dk = qt_desc(smem_u32(skv)), dv = ck_desc_v(smem_u32(skv));
         const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
         Ring<STAGES> kv;
-        uint32_t qpar = 0, ppar[2] = {0, 0}, fpar = 1;  // (the score tile is free at first)
         bool ok = true;
         auto await = [&](uint64_t *bar, uint32_t parity) { ok = ok && __all_sync(FULL_MASK, wait(bar, parity)); };
-        auto scores = [&](int w, int slot) {  // into the score tile, once its last use was copied out
-            await(s_free, fpar);
-            fpar ^= 1u;
-            if (!ok) return;
-            qt_fence_after();
-            ck_mma_ss(tm, dq + w * (TILE_B >> 4), dk + slot * (TILE_B >> 4), ID_S, smem_u32(&s_full[w]));
-        };
-        auto values = [&](int w, int slot, bool acc) {
-            await(&p_full[w], ppar[w]);
-            ppar[w] ^= 1u;
-            if (!ok) return;
-            qt_fence_after();
-            ck_mma_ts(tm + 256 + 128 * w, tm + 128 + 64 * w, dv + slot * (TILE_B >> 4), ID_O, acc ? 1u : 0u,
-                      smem_u32(&pv_done[w]));
-        };
-        do {
-            const bool two = r.e.nt > tqt;
-            await(q_full, qpar);
-            await(&kv_full[kv.s], kv.par);
-            qpar ^= 1u;
-            scores(0, kv.s);
-            if (two) scores(1, kv.s);
-            if (!ok) break;
-            ck_commit(&kv_empty[kv.s]);
-            if (r.tn - r.t0 == 1) ck_commit(q_empty);  // (the run's last scores: the queries may be replaced)
-            kv.step();
-            for (int t = r.t0; t < r.tn && ok; ++t) {
-                const bool last = t + 1 == r.tn;
-                const Ring<STAGES> k = kv;
-                if (!last) {
-                    await(&kv_full[k.s], k.par);
-                    scores(0, k.s);
+        if (warp == 9) {
+            uint32_t qpar = 0, fpar = 1;  // (the score tile is free at first)
+            do {
+                const bool two = r.e.nt > tqt;
+                await(q_full, qpar);
+                qpar ^= 1u;
+                for (int t = r.t0; t < r.tn && ok; ++t) {
+                    await(&kv_full[kv.s], kv.par);
+                    for (int w = 0; w < (two ? 2 : 1); ++w) {
+                        await(s_free, fpar);  // the score tile's last use was copied out
+                        fpar ^= 1u;
+                        if (!ok) break;
+                        qt_fence_after();
+                        ck_mma_ss(tm, dq + w * (TILE_B >> 4), dk + kv.s * (TILE_B >> 4), ID_S, smem_u32(&s_full[w]));
+                    }
+                    if (!ok) break;
+                    ck_commit(&kv_empty[kv.s]);
+                    kv.step();
+                    if (t > r.t0) kv.step();  // (values of tile t - 1 lie between)
+                }
+                if (!ok) break;
+                ck_commit(q_empty);  // the queries may be replaced
+                kv.step();
+            } while (r.next(p.large, p.Hkv));
+        } else {
+            uint32_t ppar[2] = {0, 0};
+            do {
+                const bool two = r.e.nt > tqt;
+                kv.step();
+                for (int t = r.t0; t < r.tn && ok; ++t) {
+                    if (t + 1 < r.tn) kv.step();  // (keys of tile t + 1 come first)
+                    await(&kv_full[kv.s], kv.par);
+                    for (int w = 0; w < (two ? 2 : 1); ++w) {
+                        await(&p_full[w], ppar[w]);
+                        ppar[w] ^= 1u;
+                        if (!ok) break;
+                        qt_fence_after();
+                        ck_mma_ts(tm + 256 + 128 * w, tm + 128 + 64 * w, dv + kv.s * (TILE_B >> 4), ID_O, t > r.t0 ? 1u : 0u,
+                                  smem_u32(&pv_done[w]));
+                    }
+                    if (!ok) break;
+                    ck_commit(&kv_empty[kv.s]);
                     kv.step();
                 }
-                await(&kv_full[kv.s], kv.par);
-                values(0, kv.s, t > r.t0);
-                if (two && !last) scores(1, k.s);
-                if (!ok) break;
-                if (!last) {
-                    ck_commit(&kv_empty[k.s]);
-                    if (t + 2 == r.tn) ck_commit(q_empty);
-                }
-                if (two) values(1, kv.s, t > r.t0);
-                if (!ok) break;
-                ck_commit(&kv_empty[kv.s]);
-                kv.step();
-            }
-        } while (ok && r.next(p.large, p.Hkv));
-        ck_commit(drain);  // every product is done before shared and tensor memory are given up
-        (void)mbar_wait_bounded(drain, 0u);
+            } while (ok && r.next(p.large, p.Hkv));
+        }
+        // every product is done before shared and tensor memory are given up
+        ck_commit(&drain[warp - 9]);
+        (void)mbar_wait_bounded(&drain[warp - 9], 0u);
         __syncwarp();
     }
     } else if (warp < 8) {
@@ -599,13 +600,12 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 }
                 float mx4[4];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float y = fmaxf(__uint_as_float(x[b][0]), __uint_as_float(x[b][1]));
+                for (int b = 0; b < 4; ++b) mx4[b] = fmaxf(__uint_as_float(x[b][0]), __uint_as_float(x[b][1]));
 #pragma unroll
-                    for (int j = 2; j < 32; j += 2)
-                        y = fmaxf(fmaxf(y, __uint_as_float(x[b][j])), __uint_as_float(x[b][j + 1]));
-                    mx4[b] = y;
-                }
+                for (int j = 2; j < 32; j += 2)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        mx4[b] = fmaxf(fmaxf(mx4[b], __uint_as_float(x[b][j])), __uint_as_float(x[b][j + 1]));
                 float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 if constexpr (!Q8) mx *= qabs;
                 const bool grow = mx - OFF > m + LAG;
