@@ -315,7 +315,7 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
     p.qscale = (float)((double)scale * 1.4426950408889634);
     // (scale 0: any factor that makes every finite score vanish, so that the
     // mask's -inf times it stays -inf)
-    if (p.qscale == 0.0f) p.qscale = 1e-37f;
+    if (p.qscale == 0.0f) p.qscale = 1e-30f;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     place(p.small, ws, pl.s, pl.small_cap, pl.G, pl.small_tq);
     place(p.large, ws, pl.l, pl.large_cap, pl.G, pl.large_tq);

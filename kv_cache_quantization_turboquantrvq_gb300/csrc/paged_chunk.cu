@@ -18,9 +18,19 @@
 // Roles (one CTA per SM): two groups of 4 softmax warps, a thread per query
 // row; one warp that streams queries, keys and values by TMA (a box per page);
 // two warps that issue tcgen05.mma, one for scores, one for values.  With an
-// 8-bit cache four more warps
-// turn the codes into 16-bit operands in shared memory (exact) and put the
-// exponents where the softmax reads them.
+// 8-bit cache four more warps turn the codes into 16-bit operands in shared
+// memory.
+//
+// 8-bit cache.  A factor per key inside the softmax (2 x 128 numbers a tile to
+// every thread) cost more than the softmax itself: 1306 us against 830 for the
+// same chunk over a 16-bit cache.  So the exponents are split in a tile's largest
+// among the keys that are seen, A of keys and B of values, and each key's rest:
+// the operands are code * 2^(a - A) and code * 2^(b - B), and a tile's two
+// exponents act once per score: t = scale 2^A (q . K') + B, w = 2^(t - M) with M
+// the running maximum of t, out = sum w V' / sum w 2^-B.  The operands are exact
+// but for the smallest entries of rows more than 2^15 below the tile's largest
+// (fp16; off by 2^-25 2^A, 2^-33 of the largest row: less than the 32-bit sums
+// of that row's own products), so no weight or value leaves its type's range.
 //
 // The output is rescaled only when a row's maximum grew by more than 2^LAG
 // (the softmax warps do it in tensor memory between two products), so weights
@@ -61,7 +71,7 @@ template <bool Q8> struct CkShape {
     static constexpr int BARS = 2 + 2 * STAGES + 7 + 2 * RAW + 2 * META + 2;
     static constexpr int OUTB = Q8 ? 32 : 128;  // bytes a row that a softmax warp lays out at a time for its stores
     static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + 8 * 32 * OUTB + RAW * 2 * PG_TILE +
-                                META * 3 * PG_TILE * 4 + 8 * BARS + 16;
+                                META * 16 + 8 * BARS + 16;
 };
 static_assert(CkShape<false>::SMEM <= 232448 && CkShape<true>::SMEM <= 232448, "shared memory of one CTA");
 
@@ -214,13 +224,49 @@ template <> __device__ __forceinline__ uint32_t ck_pack<__nv_bfloat16>(float a, 
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <class T> __device__ __forceinline__ uint32_t ck_codes(uint32_t two);
-template <> __device__ __forceinline__ uint32_t ck_codes<__half>(uint32_t two) { return e4m3x2_to_f16x2(two); }
-template <> __device__ __forceinline__ uint32_t ck_codes<__nv_bfloat16>(uint32_t two)
+// 2^e (e <= 0) twice, as what ck_operand multiplies codes by; 0 where T's range ends.
+template <class T> __device__ __forceinline__ uint32_t ck_factor(int e);
+template <> __device__ __forceinline__ uint32_t ck_factor<__half>(int e)
 {
-    const uint32_t h2 = e4m3x2_to_f16x2(two);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-    return ck_pack<__nv_bfloat16>(f.x, f.y);
+    e = min(e, 0);
+    return 0x00010001u * (e >= -14 ? (uint32_t)(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u);
+}
+template <> __device__ __forceinline__ uint32_t ck_factor<__nv_bfloat16>(int e)
+{
+    // (2^120 of it turns the code's bits, moved to a bf16's place, into its value)
+    return 0x00010001u * ((uint32_t)(120 + 127 + max(min(e, 0), -240)) << 7);
+}
+
+// Four codes times a factor as two pairs of T.
+template <class T> __device__ __forceinline__ void ck_operand(uint32_t four, uint32_t f, uint32_t &lo, uint32_t &hi);
+template <>
+__device__ __forceinline__ void ck_operand<__half>(uint32_t four, uint32_t f, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t a = e4m3x2_to_f16x2(four & 0xffffu), b = e4m3x2_to_f16x2(four >> 16);
+    const __half2 g = *reinterpret_cast<const __half2 *>(&f);
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&a), g), y = __hmul2(*reinterpret_cast<const __half2 *>(&b), g);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+template <>
+__device__ __forceinline__ void ck_operand<__nv_bfloat16>(uint32_t four, uint32_t f, uint32_t &lo, uint32_t &hi)
+{
+    // sign, exponent and fraction of a code in a bf16's places: value * 2^-120,
+    // subnormal codes as subnormal bf16 (the product takes those)
+    const uint32_t h0 = __byte_perm(four, 0u, 0x1404), h1 = __byte_perm(four, 0u, 0x3424);
+    const uint32_t a = ((h0 >> 4) & 0x07f007f0u) | (h0 & 0x80008000u), b = ((h1 >> 4) & 0x07f007f0u) | (h1 & 0x80008000u);
+    const __nv_bfloat162 g = *reinterpret_cast<const __nv_bfloat162 *>(&f);
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), g);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&b), g);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
+// Largest of the bytes that the lanes of a warp hold.
+__device__ __forceinline__ uint32_t ck_top(uint32_t four)
+{
+    four = __vmaxu4(four, four >> 16);
+    return __reduce_max_sync(FULL_MASK, max(four & 0xffu, (four >> 8) & 0xffu));
 }
 
 // One CTA's share as runs of tiles of one item each.
@@ -284,8 +330,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     unsigned char *sraw = skv + STAGES * TILE_B;            // tiles of codes
     unsigned char *sout = sraw + C::RAW * RAW_B;            // [8 warps][32 rows][OUTB]
     unsigned char *sexp = sout + 8 * 32 * C::OUTB;          // [RAW][2][128] exponents (of key tiles)
-    float *smeta = reinterpret_cast<float *>(sexp + C::RAW * 2 * PG_TILE);  // [META][3][128]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smeta + C::META * 3 * PG_TILE);
+    float4 *smeta = reinterpret_cast<float4 *>(sexp + C::RAW * 2 * PG_TILE);  // [META] |scale| 2^A, B, 2^-B
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smeta + C::META);
     uint64_t *q_full = bars, *q_empty = bars + 1, *kv_full = bars + 2, *kv_empty = kv_full + STAGES;
     uint64_t *s_full = kv_empty + STAGES, *p_full = s_full + 2, *pv_done = p_full + 2, *s_free = pv_done + 2;
     uint64_t *raw_full = s_free + 1, *raw_empty = raw_full + C::RAW;
@@ -568,22 +614,18 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 qt_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free);
-                const float *ma = smeta + mt.s * 3 * PG_TILE;
+                // t = score * mul + add, in base 2
+                float mul = qabs, add = 0.0f, back = 1.0f;
                 if constexpr (Q8) {
-                    // 2^a and the scale, plus the value's exponent, key by key
-#pragma unroll
-                    for (int c = 0; c < PG_TILE; c += 4) {
-                        const float4 fa = *reinterpret_cast<const float4 *>(ma + c);
-                        const float4 fb = *reinterpret_cast<const float4 *>(ma + PG_TILE + c);
-                        uint32_t *y = &x[c >> 5][c & 31];
-                        const float2 u = __ffma2_rn(ck_f2(y[0], y[1]), make_float2(fa.x, fa.y), make_float2(fb.x, fb.y));
-                        const float2 v = __ffma2_rn(ck_f2(y[2], y[3]), make_float2(fa.z, fa.w), make_float2(fb.z, fb.w));
-                        y[0] = __float_as_uint(u.x);
-                        y[1] = __float_as_uint(u.y);
-                        y[2] = __float_as_uint(v.x);
-                        y[3] = __float_as_uint(v.y);
-                    }
-                } else if (p.qscale < 0.0f) {  // (the products below take |scale|)
+                    const float4 f = smeta[mt.s];
+                    mul = f.x;
+                    add = f.y;
+                    back = f.z;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&meta_empty[mt.s]);
+                    mt.step();
+                }
+                if (p.qscale < 0.0f) {  // (mul is |scale|)
 #pragma unroll
                     for (int c = 0; c < PG_TILE; ++c) x[c >> 5][c & 31] ^= 0x80000000u;
                 }
@@ -607,19 +649,19 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     for (int b = 0; b < 4; ++b)
                         mx4[b] = fmaxf(fmaxf(mx4[b], __uint_as_float(x[b][j])), __uint_as_float(x[b][j + 1]));
                 float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                if constexpr (!Q8) mx *= qabs;
+                mx = Q8 ? fmaf(mx, mul, add) : mx * mul;
                 const bool grow = mx - OFF > m + LAG;
-                if (t > r.t0) {  // the last weights are used up, the output holds their product
-                    ok = __all_sync(FULL_MASK, wait(&pv_done[w], vpar));
-                    vpar ^= 1u;
-                    if (!ok) break;
-                    qt_fence_after();
-                }
+                bool used = t == r.t0;  // the last weights are used up, the output holds their product
                 if (__any_sync(FULL_MASK, grow)) {
                     const float f = grow ? ex2(m - (mx - OFF)) : 1.0f;
                     if (grow) m = mx - OFF;
                     l *= f;
-                    if (t > r.t0) {
+                    if (!used) {
+                        ok = __all_sync(FULL_MASK, wait(&pv_done[w], vpar));
+                        vpar ^= 1u;
+                        if (!ok) break;
+                        used = true;
+                        qt_fence_after();
 #pragma unroll 1
                         for (int b = 0; b < 8; ++b) {
                             uint32_t y[16];
@@ -633,30 +675,29 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     }
                 }
                 const float ms = m > NEG_INF ? m : 0.0f;
-                const float2 neg = make_float2(-ms, -ms), mul = make_float2(qabs, qabs);
+                const float2 neg = make_float2(add - ms, add - ms), mul2 = make_float2(mul, mul);
                 float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float2 y = ck_f2(x[b][j], x[b][j + 1]);
-                        const float2 u = Q8 ? __fadd2_rn(y, neg) : __ffma2_rn(y, mul, neg);
+                        const float2 u = __ffma2_rn(ck_f2(x[b][j], x[b][j + 1]), mul2, neg);
                         const float2 e = make_float2(ex2(u.x), ex2(u.y));
-                        if constexpr (Q8)
-                            sum2 = __ffma2_rn(e, *reinterpret_cast<const float2 *>(ma + 2 * PG_TILE + 32 * b + j), sum2);
-                        else
-                            sum2 = __fadd2_rn(sum2, e);
+                        sum2 = __fadd2_rn(sum2, e);
                         pk[j >> 1] = ck_pack<TV>(e.x, e.y);
+                    }
+                    if (b == 0 && !used) {
+                        ok = __all_sync(FULL_MASK, wait(&pv_done[w], vpar));
+                        vpar ^= 1u;
+                        if (!ok) break;
+                        qt_fence_after();
                     }
                     ck_st16(tp + 16 * b, pk);
                 }
-                l += sum2.x + sum2.y;
-                if constexpr (Q8) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&meta_empty[mt.s]);
-                    mt.step();
-                } else {
+                if (!ok) break;
+                l = fmaf(sum2.x + sum2.y, back, l);
+                if constexpr (!Q8) {
                     // values of keys that no row sees may hold anything: zero
                     // them before the product (the second half's comes later)
                     if (w == 0 && (k0 + PG_TILE > view.hi || (k0 < view.lo && k0 + PG_TILE > view.sink))) {
@@ -761,6 +802,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         Ring<STAGES> kv;
         Ring<C::META ? C::META : 1> mt;
         int tiles = 0, keys = 0;
+        uint32_t vtop0 = 0, vtop1 = 0;  // exponents of the values to come: of tile u - 1, of tile u
+        uint64_t vrow0 = 0, vrow1 = 0;
         bool ok = true;
         do {
             PgView view;
@@ -774,33 +817,57 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     if (ok && tiles >= STAGES) ok = __all_sync(FULL_MASK, wait(&kv_empty[kv.s], kv.par ^ 1u));
                     if (ok && part == 0 && keys >= C::META) ok = __all_sync(FULL_MASK, wait(&meta_empty[mt.s], mt.par ^ 1u));
                     if (!ok) break;
+                    // rows of this thread: j / 8 + 16 i
+                    uint32_t top;         // the tile's largest exponent
+                    uint64_t rows = 0;    // this thread's rows' exponents, a byte each
                     if (part == 0) {
-                        // this key's factors: scores * a + b, weights / 2^b
-                        const unsigned char *x = sexp + raw.s * 2 * PG_TILE;
-                        const int a = (int)x[j] - 127, b = (int)x[PG_TILE + j] - 127;
-                        float *ma = smeta + mt.s * 3 * PG_TILE;
-                        ma[j] = p.qscale * pow2f(max(a, -126));
-                        ma[PG_TILE + j] = (float)b;
-                        ma[2 * PG_TILE + j] = pow2f(max(-b, -126));
-                    }
-                    const unsigned char *src = sraw + raw.s * RAW_B;
-                    unsigned char *dst = skv + kv.s * TILE_B;
-#pragma unroll 2
-                    for (int i = 0; i < 8; ++i) {
-                        const int id = j + 128 * i, row = id >> 3, c = id & 7;
-                        uint4 v = *reinterpret_cast<const uint4 *>(src + swz128(row, c));
-                        if (edge && part == 1 && !view.one(k0 + row)) v = make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                        uint32_t o[8];
+                        const uint32_t *e4 = reinterpret_cast<const uint32_t *>(sexp + raw.s * 2 * PG_TILE) + lane;
+                        uint32_t see = 0xffffffffu;  // of this lane's four keys
+                        if (edge) {
+                            see = 0u;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            o[2 * q] = part ? ck_codes<TV>(in[q] & 0xffffu) : ck_codes<T>(in[q] & 0xffffu);
-                            o[2 * q + 1] = part ? ck_codes<TV>(in[q] >> 16) : ck_codes<T>(in[q] >> 16);
+                            for (int i = 0; i < 4; ++i) see |= view.one(k0 + 4 * lane + i) ? 0xffu << (8 * i) : 0u;
                         }
-                        unsigned char *d = dst + (c >> 2) * HALF_B;
-                        *reinterpret_cast<uint4 *>(d + swz128(row, 2 * (c & 3))) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(d + swz128(row, 2 * (c & 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                        top = max(ck_top(e4[0] & see), 87u);  // (at least 2^-40: the factors below stay normal)
+                        vtop1 = max(ck_top(e4[PG_TILE / 4] & see), 87u);
+                        const unsigned char *ex = sexp + raw.s * 2 * PG_TILE + (j >> 3);
+                        vrow1 = 0;
+#pragma unroll 2
+                        for (int i = 7; i >= 0; --i) {
+                            rows = rows << 8 | ex[16 * i];
+                            vrow1 = vrow1 << 8 | ex[PG_TILE + 16 * i];
+                        }
+                        if (j == 0) {
+                            const int A = (int)top - 127, B = (int)vtop1 - 127;
+                            smeta[mt.s] = make_float4(fabsf(p.qscale) * pow2f(min(A, 127)), (float)B, pow2f(max(-B, -126)), 0.0f);
+                        }
+                    } else {
+                        top = vtop0;
+                        rows = vrow0;
                     }
+                    // (short loops: unrolled in full, the warps' code no longer
+                    // fitted the instruction caches, 1832 us for the chunk of 4096)
+                    const unsigned char *src = sraw + raw.s * RAW_B + swz128(j >> 3, j & 7);  // 16 rows on: the same swizzle
+                    unsigned char *dst = skv + kv.s * TILE_B + ((j & 7) >> 2) * HALF_B;
+                    const uint32_t d0 = swz128(j >> 3, 2 * (j & 3)), d1 = swz128(j >> 3, 2 * (j & 3) + 1);
+                    auto convert = [&](auto tag, bool zero_hidden) {
+                        using X = decltype(tag);
+#pragma unroll 2
+                        for (int i = 0; i < 8; ++i, rows >>= 8) {
+                            uint4 v = *reinterpret_cast<const uint4 *>(src + 2048 * i);
+                            if (zero_hidden && !view.one(k0 + (j >> 3) + 16 * i)) v = make_uint4(0u, 0u, 0u, 0u);
+                            const uint32_t f = ck_factor<X>((int)((uint32_t)rows & 0xffu) - (int)top);
+                            uint4 lo, hi;
+                            ck_operand<X>(v.x, f, lo.x, lo.y);
+                            ck_operand<X>(v.y, f, lo.z, lo.w);
+                            ck_operand<X>(v.z, f, hi.x, hi.y);
+                            ck_operand<X>(v.w, f, hi.z, hi.w);
+                            *reinterpret_cast<uint4 *>(dst + d0 + 2048 * i) = lo;
+                            *reinterpret_cast<uint4 *>(dst + d1 + 2048 * i) = hi;
+                        }
+                    };
+                    if (part == 0) convert(T(), false);
+                    else convert(TV(), edge);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -816,6 +883,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                         ++keys;
                     }
                 }
+                vtop0 = vtop1;
+                vrow0 = vrow1;
             }
         } while (ok && r.next(p.large, p.Hkv));
     }
