@@ -849,7 +849,10 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     // fitted the instruction caches, 1832 us for the chunk of 4096)
                     const unsigned char *src = sraw + raw.s * RAW_B + swz128(j >> 3, j & 7);  // 16 rows on: the same swizzle
                     unsigned char *dst = skv + kv.s * TILE_B + ((j & 7) >> 2) * HALF_B;
-                    const uint32_t d0 = swz128(j >> 3, 2 * (j & 3)), d1 = swz128(j >> 3, 2 * (j & 3) + 1);
+                    // eight lanes hold a row; the upper four store their second half
+                    // first, so that the eight fill all banks
+                    const bool odd = (j & 4) != 0;
+                    const uint32_t d0 = swz128(j >> 3, 2 * (j & 3) + odd), d1 = swz128(j >> 3, 2 * (j & 3) + !odd);
                     auto convert = [&](auto tag, bool zero_hidden) {
                         using X = decltype(tag);
 #pragma unroll 2
@@ -857,13 +860,13 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                             uint4 v = *reinterpret_cast<const uint4 *>(src + 2048 * i);
                             if (zero_hidden && !view.one(k0 + (j >> 3) + 16 * i)) v = make_uint4(0u, 0u, 0u, 0u);
                             const uint32_t f = ck_factor<X>((int)((uint32_t)rows & 0xffu) - (int)top);
-                            uint4 lo, hi;
-                            ck_operand<X>(v.x, f, lo.x, lo.y);
-                            ck_operand<X>(v.y, f, lo.z, lo.w);
-                            ck_operand<X>(v.z, f, hi.x, hi.y);
-                            ck_operand<X>(v.w, f, hi.z, hi.w);
-                            *reinterpret_cast<uint4 *>(dst + d0 + 2048 * i) = lo;
-                            *reinterpret_cast<uint4 *>(dst + d1 + 2048 * i) = hi;
+                            uint4 x0, x1;
+                            ck_operand<X>(odd ? v.z : v.x, f, x0.x, x0.y);
+                            ck_operand<X>(odd ? v.w : v.y, f, x0.z, x0.w);
+                            ck_operand<X>(odd ? v.x : v.z, f, x1.x, x1.y);
+                            ck_operand<X>(odd ? v.y : v.w, f, x1.z, x1.w);
+                            *reinterpret_cast<uint4 *>(dst + d0 + 2048 * i) = x0;
+                            *reinterpret_cast<uint4 *>(dst + d1 + 2048 * i) = x1;
                         }
                     };
                     if (part == 0) convert(T(), false);
