@@ -66,14 +66,14 @@ struct PgEntry {     // 32 bytes, read as two int4
     int ntiles;      // tiles of the entry (at least 1)
 };
 struct PgPlanHead {
-    long long total;  // units
-    int nent, g;      // entries, CTAs with work
-    int pad[4];
+    long long q;  // units of a CTA, the first `rem` of the `g` CTAs with work take one more
+    int rem, g;
 };
 // One class of entries (small: few rows; large: tensor-memory tiles): device arrays.
 struct PgPlan {
     PgPlanHead *head;
     int4 *ctab;        // [G] where each CTA starts: entry, head, tile
+    int4 *cmb;         // [G] what is merged at its start: parts (0: nothing), first token, tokens, head
     PgEntry *ent;
     long long *base;   // first unit of each entry
     float *part;       // [G][2] partial slots

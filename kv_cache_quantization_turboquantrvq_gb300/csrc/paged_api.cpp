@@ -103,7 +103,7 @@ vq_status status_of(cudaError_t e) { return e == cudaSuccess ? VQ_OK : VQ_ERR_CU
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-    size_t head, ctab, ent, base, part, end;
+    size_t head, ctab, cmb, ent, base, part, end;
 };
 
 // One class of entries from byte `at`; cap 0: the class is not used.
@@ -112,7 +112,8 @@ Layout layout(size_t at, int cap, int G, int rows)
     Layout l;
     l.head = at;
     l.ctab = l.head + up(sizeof(PgPlanHead));
-    l.ent = l.ctab + up(cap ? sizeof(int4) * G : 0);
+    l.cmb = l.ctab + up(cap ? sizeof(int4) * G : 0);
+    l.ent = l.cmb + up(cap ? sizeof(int4) * G : 0);
     l.base = l.ent + up(sizeof(PgEntry) * (size_t)cap);
     l.part = l.base + up(sizeof(long long) * (size_t)cap);
     l.end = l.part + up(cap ? sizeof(float) * 2 * (size_t)G * rows * PG_PART : 0);
@@ -137,11 +138,14 @@ vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, AttendPlan &pl)
     // Sequences with at most 16 query rows per kv head go to the small kernel,
     // longer chunks to the tensor-memory kernel.  A call whose bounds leave one
     // kind only (max_q short, or every sequence at max_q) launches one kernel.
+    // The small kernel has a form for 8 rows, which is taken where it does: in
+    // a call that launches the large kernel too, 9 to 16 rows go there.
     pl.small_tq = PG_SROWS / gq;
     pl.large_tq = 2 * (128 / gq);
     const bool large = (long long)max_q * gq > PG_SROWS;
     const bool small = !large || (long long)B * max_q > T;
-    pl.small_rows = small ? PG_SROWS : 0;
+    const bool narrow = large ? gq <= PG_SROWS / 2 : (long long)max_q * gq <= PG_SROWS / 2;
+    pl.small_rows = !small ? 0 : narrow ? PG_SROWS / 2 : PG_SROWS;
     if (small) pl.small_cap = B;
     if (large) pl.large_cap = (T + pl.large_tq - 1) / pl.large_tq + B;
     pl.s = layout(0, pl.small_cap, pl.G, PG_SROWS);
@@ -154,6 +158,7 @@ void place(PgPlan &d, unsigned char *ws, const Layout &l, int cap, int G, int tq
 {
     d.head = reinterpret_cast<PgPlanHead *>(ws + l.head);
     d.ctab = reinterpret_cast<int4 *>(ws + l.ctab);
+    d.cmb = reinterpret_cast<int4 *>(ws + l.cmb);
     d.ent = reinterpret_cast<PgEntry *>(ws + l.ent);
     d.base = reinterpret_cast<long long *>(ws + l.base);
     d.part = reinterpret_cast<float *>(ws + l.part);

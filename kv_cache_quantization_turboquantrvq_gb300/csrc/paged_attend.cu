@@ -21,6 +21,7 @@
 #include "device_common.cuh"
 #include "paged.h"
 #include "paged_dev.cuh"
+#include "tcgen05.cuh"
 
 namespace vq {
 
@@ -143,9 +144,9 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
         }
         __syncthreads();
         PgPlanHead h;
-        h.total = total;
-        h.nent = nent;
         h.g = (int)min((long long)pl.G, total);
+        h.q = h.g ? total / h.g : 0;
+        h.rem = h.g ? (int)(total % h.g) : 0;
         if (threadIdx.x == 0) *pl.head = h;
         for (int c = threadIdx.x; c < h.g; c += PLAN_THREADS) {
             const long long u = pg_first_unit(h, c);
@@ -156,14 +157,23 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
                 else z = m - 1;
             }
             const int r = (int)(u - pl.base[a]), nt = pl.ent[a].ntiles;
-            pl.ctab[c] = make_int4(a, r / nt, r % nt, 0);
+            const int head_ = r / nt, t = r % nt;
+            pl.ctab[c] = make_int4(a, head_, t, 0);
+            // the merge at this CTA's start: of the item it enters in its
+            // middle, if no earlier CTA does so
+            int parts = 0;
+            if (t > 0 && t <= u - pg_first_unit(h, c - 1)) {
+                parts = 2;
+                while (c + parts - 1 < h.g && pg_first_unit(h, c + parts - 1) < u - t + nt) ++parts;
+            }
+            pl.cmb[c] = make_int4(parts, pl.ent[a].tok0, pl.ent[a].nt, head_);
         }
     }
 }
 
 // ------------------------------------------------------- the merge of parts
 
-constexpr int CB_ROWS = 16;  // rows of one combine CTA
+constexpr int CB_ROWS = 8;   // rows of one combine CTA, a warp each
 
 template <class T> __device__ __forceinline__ uint2 pack4(float4 v);
 template <> __device__ __forceinline__ uint2 pack4<__half>(float4 v)
@@ -177,89 +187,96 @@ template <> __device__ __forceinline__ uint2 pack4<__nv_bfloat16>(float4 v)
     return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-// CTA c merges the item that c enters in its middle, if no earlier CTA does
-// so: its parts are the second slot of CTA c - 1 and the first slots of c,
-// c + 1, ..., in that order on every run.
+// Block c merges the item that CTA c enters in its middle, if no earlier CTA
+// does so: its parts are the second slot of CTA c - 1 and the first slots of c,
+// c + 1, ..., in that order on every run.  A warp takes a row.
 template <class T, int ROWS, int HALF>
-__global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constant__ PagedAttendParams p)
+__global__ void __launch_bounds__(32 * CB_ROWS) paged_combine_kernel(const __grid_constant__ PagedAttendParams p)
 {
     const PgPlan &pl = HALF ? p.large : p.small;
-    const PgPlanHead h = *pl.head;
     const int c = blockIdx.x;
-    if (c == 0 || c >= h.g) return;
-    const int4 at = pl.ctab[c];
-    const long long u = pg_first_unit(h, c);
-    if (at.z == 0 || at.z > u - pg_first_unit(h, c - 1)) return;
-    const PgEntry e = pl.ent[at.x];
-    const long long end = u - at.z + e.ntiles;
-    int parts = 2;
-    while (c + parts - 1 < h.g && pg_first_unit(h, c + parts - 1) < end) ++parts;
+    if (c >= pl.head->g) return;
+    const int4 at = pl.cmb[c];
+    const int parts = at.x;
+    if (parts == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int RT = HALF ? 128 : ROWS;  // rows of one tile of queries
     const int tqt = RT / p.GQ;
     const size_t slot = (size_t)ROWS * PG_PART;
-    for (int i = warp; i < CB_ROWS; i += 4) {
-        const int r = blockIdx.y * CB_ROWS + i;
-        const int tok = (r / RT) * tqt + (r % RT) / p.GQ, g = (r % RT) % p.GQ;
-        if (r % RT >= tqt * p.GQ || tok >= e.nt) continue;
-        float M = NEG_INF;
-        for (int k = lane; k < parts; k += 32) {
-            const float *s = pl.part + (size_t)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c + k - 1)) * slot;
-            M = fmaxf(M, s[r]);
-        }
+    const int r = blockIdx.y * CB_ROWS + warp;
+    const int tok = (r / RT) * tqt + (r % RT) / p.GQ, g = (r % RT) % p.GQ;
+    if (r % RT >= tqt * p.GQ || tok >= at.z) return;
+    auto at_part = [&](int k) { return pl.part + (size_t)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c + k - 1)) * slot; };
+    float M = NEG_INF;
+    for (int k = lane; k < parts; k += 32) M = fmaxf(M, at_part(k)[r]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
-        float L = 0.0f;
-        float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (M > NEG_INF) {
-            for (int k = 0; k < parts; ++k) {
-                const float *s = pl.part + (size_t)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c + k - 1)) * slot;
-                const float f = ex2(s[r] - M);
-                const float4 o = *reinterpret_cast<const float4 *>(s + 2 * ROWS + (size_t)r * D + 4 * lane);
-                L = fmaf(s[ROWS + r], f, L);
-                O.x = fmaf(o.x, f, O.x);
-                O.y = fmaf(o.y, f, O.y);
-                O.z = fmaf(o.z, f, O.z);
-                O.w = fmaf(o.w, f, O.w);
-            }
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
+    float L = 0.0f;
+    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (M > NEG_INF) {
+#pragma unroll 4
+        for (int k = 0; k < parts; ++k) {
+            const float *s = at_part(k);
+            const float f = ex2(s[r] - M);
+            const float4 o = *reinterpret_cast<const float4 *>(s + 2 * ROWS + (size_t)r * D + 4 * lane);
+            L = fmaf(s[ROWS + r], f, L);
+            O.x = fmaf(o.x, f, O.x);
+            O.y = fmaf(o.y, f, O.y);
+            O.z = fmaf(o.z, f, O.z);
+            O.w = fmaf(o.w, f, O.w);
         }
-        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-        O.x *= inv; O.y *= inv; O.z *= inv; O.w *= inv;
-        T *dst = static_cast<T *>(p.out) + ((size_t)(e.tok0 + tok) * p.Hq + (size_t)at.y * p.GQ + g) * D + 4 * lane;
-        *reinterpret_cast<uint2 *>(dst) = pack4<T>(O);
     }
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    O.x *= inv; O.y *= inv; O.z *= inv; O.w *= inv;
+    T *dst = static_cast<T *>(p.out) + ((size_t)(at.y + tok) * p.Hq + (size_t)at.w * p.GQ + g) * D + 4 * lane;
+    *reinterpret_cast<uint2 *>(dst) = pack4<T>(O);
 }
 
 // --------------------------------------------------------- the small kernel
 //
-// One CTA of 8 warps per SM.  A tile of 128 keys is cut into 16 keys for each
-// warp; a warp streams its own 16-key blocks of keys and values by TMA through
-// a ring of its own (no barrier between warps in the loop) and keeps the
-// running maximum, sum and output of all 16 rows (new tokens x query heads of
-// the kv head, so the cache is read once for all of them) in registers.  Both
-// products are 16 x 8 x 16 mma.sync: HBM bounds this kernel, and a tile of 128
-// tensor-memory rows would be mostly padding.  The order of the 128
-// coordinates in the score product is free as long as both operands share it:
-// each lane takes 16 consecutive bytes of its key's row per load, for fp16 and
-// for codes alike.  The walk over the units continues across items, so the
-// copies of the next item are in flight while an item's warps are merged.
-constexpr int SM_WARPS = 8;
-constexpr int KB = 16;  // keys of a warp's block
+// HBM bounds this kernel: every visible key and value is read once per kv head
+// for all of its query rows (at most 8 NT).  One CTA per SM: two warps copy
+// tiles of 128 keys (one the keys, one the values) into a ring by TMA, a box
+// per page; the others compute, each on 16 of a tile's keys with a running
+// maximum, sum and output of its own in registers, in groups of 8 that take the
+// tiles in turn.  What bounds a warp is the latency of its chain (wait, scores,
+// maximum, weights, product), so the copies' page lookups and waits are not in
+// it, and two groups hide one another's (8-bit cache: 350 -> ? us).
+//
+// Both products are 16 x 8 x 16 mma.sync with the cache as the 16-row operand:
+// S^T = K Q^T and O^T += V^T W^T, the query rows in the 8-wide dimension, where
+// little is padding (a tile of 128 tensor-memory rows would be mostly padding).
+// The order of the 128 coordinates in the score product is free as long as both
+// operands share it: a lane takes 16 consecutive bytes of a cache row per load,
+// for 16-bit entries and for codes alike.
+constexpr int KB = 16;         // keys of a warp's block
 constexpr float OFF = 7.0f;    // weights reach up to 2^(OFF + LAG): fp16 stays normal down to 2^-14
 constexpr float LAG = 8.0f;    // the maximum is only followed when it grew by more than this
 
-constexpr int MROW = D + 4;    // row of the merge buffers (floats)
+constexpr int SM_HALF = PG_TILE * 128;  // 128-byte columns of a 16-bit tile
 
-template <bool Q8> struct SmTile {
+template <bool Q8, int NT> struct SmShape {
     static constexpr int ROW = Q8 ? 128 : 256;            // bytes of a cache row
-    static constexpr int KV = KB * ROW;                   // keys, or values, of a block
-    static constexpr int STAGE = 2 * KV;                  // keys, values
-    static constexpr int STAGES = Q8 ? 5 : 3;
-    static constexpr int EXP = Q8 ? 2 * KB : 0;           // exponents of a block
-    static constexpr int MERGE = 4 * 16 * MROW * 4;       // four warps' outputs; maxima and sums in the padding
-    static constexpr int SMEM = 1024 + SM_WARPS * STAGES * (STAGE + EXP + 8) + MERGE;
+    static constexpr int KV = PG_TILE * ROW;              // keys, or values, of a tile
+    static constexpr int STAGE = 2 * KV;
+    static constexpr int STAGES = Q8 ? 6 : 3;
+    static constexpr int EXP = Q8 ? 2 * PG_TILE : 0;      // exponents of a tile
+    // Groups of 8 warps: two over codes, which take more work a byte.  A warp
+    // waits only for its own group's tiles, so a ring slot has to come back to
+    // the same group: another group's pass in between would be taken for the
+    // next one (the parity of a barrier tells two passes apart, not three).
+    static constexpr int GROUPS = NT == 1 && Q8 ? 2 : 1;
+    static_assert(STAGES % GROUPS == 0, "a slot belongs to one group");
+    static constexpr int WARPS = 8 * GROUPS;              // that compute
+    static constexpr int THREADS = 32 * (WARPS + 2);
+    static constexpr int ROWS = 8 * NT;
+    static constexpr int MBUF = NT == 1 ? 4 : 2;          // buffers that the warps' outputs are summed in
+    static constexpr int MROW = D + 4;                    // row of a buffer (floats)
+    static constexpr int SMEM = 1024 + STAGES * (STAGE + EXP + 16) + MBUF * ROWS * MROW * 4 + WARPS * ROWS * 8;
 };
-static_assert(SmTile<false>::SMEM <= 232448 && SmTile<true>::SMEM <= 232448, "shared memory of one CTA");
+static_assert(SmShape<false, 1>::SMEM <= 232448 && SmShape<true, 1>::SMEM <= 232448 &&
+                  SmShape<false, 2>::SMEM <= 232448 && SmShape<true, 2>::SMEM <= 232448,
+              "shared memory of one CTA");
 
 __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4])
 {
@@ -267,6 +284,14 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4])
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
+}
+
+// 8 x 8 matrix of 16-bit elements, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 template <class T>
@@ -313,391 +338,382 @@ template <> __device__ __forceinline__ uint32_t codes2<__nv_bfloat16>(uint32_t t
     return pack2<__nv_bfloat16>(f.x, f.y);
 }
 
-// The walk of one warp over its CTA's units: the item (entry, head), the tile,
-// and the units left.
-struct Walk {
-    PgEntry e;
-    PgView v;
-    int ei, h, t, left;
-    __device__ __forceinline__ void load(const PagedAttendParams &p)
-    {
-        e = pg_entry(p.small.ent + ei);
-        v.set(e, p.window, p.sinks);
-    }
-    __device__ __forceinline__ bool next(const PagedAttendParams &p)  // false: no unit left
-    {
-        if (--left <= 0) return false;
-        if (++t == e.ntiles) {
-            t = 0;
-            if (++h == p.Hkv) {
-                h = 0;
-                ++ei;
-                load(p);
-            }
-        }
-        return true;
-    }
-};
-
 // T: query and output type; Q8: e4m3 cache (values are then taken as fp16)
-template <class T, bool Q8>
-__global__ void __launch_bounds__(SM_WARPS * 32, 1) paged_small_kernel(const __grid_constant__ PagedAttendParams p)
+template <class T, bool Q8, int NT>
+__global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kernel(const __grid_constant__ PagedAttendParams p)
 {
-    using L = SmTile<Q8>;
+    using L = SmShape<Q8, NT>;
     using TV = typename std::conditional<Q8, __half, T>::type;  // operand type of the value product
     extern __shared__ __align__(128) unsigned char smem_raw[];
     unsigned char *stages = smem_1k(smem_raw);
-    float *merge = reinterpret_cast<float *>(stages + SM_WARPS * L::STAGES * L::STAGE);
-    unsigned char *exps = reinterpret_cast<unsigned char *>(merge + 4 * 16 * MROW);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(exps + SM_WARPS * L::STAGES * L::EXP);
-    // maximum (and, one further, sum) of row r of warp w, in the padding of the merge buffers
-    auto stat = [&](int w, int r) -> float * { return merge + ((w & 3) * 16 + r) * MROW + D + 2 * (w >> 2); };
+    float *merge = reinterpret_cast<float *>(stages + L::STAGES * L::STAGE);
+    float2 *stat = reinterpret_cast<float2 *>(merge + L::MBUF * L::ROWS * L::MROW);  // [warp][row] maximum, sum
+    unsigned char *exps = reinterpret_cast<unsigned char *>(stat + L::WARPS * L::ROWS);
+    uint64_t *full = reinterpret_cast<uint64_t *>(exps + L::STAGES * L::EXP), *empty = full + L::STAGES;
 
     const PgPlanHead head = *p.small.head;
     const int c = blockIdx.x;
     if (c >= head.g) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g8 = lane >> 2, t4 = lane & 3;
-    unsigned char *my_st = stages + warp * L::STAGES * L::STAGE;
-    unsigned char *my_exp = exps + warp * L::STAGES * L::EXP;
-    uint64_t *my_bar = bars + warp * L::STAGES;
-    if (lane == 0) {
-        for (int s = 0; s < L::STAGES; ++s) mbar_init(&my_bar[s], 1);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::STAGES; ++s) {
+            mbar_init(&full[s], 2);
+            mbar_init(&empty[s], 8);
+        }
         fence_mbar_init();
     }
-    __syncwarp();
+    __syncthreads();
 
-    Walk co;  // what is computed
-    {
-        const int4 at = p.small.ctab[c];
-        co.ei = at.x;
-        co.h = at.y;
-        co.t = at.z;
-        co.left = (int)(pg_first_unit(head, c + 1) - pg_first_unit(head, c));
-        co.load(p);
-    }
-    Walk is = co;  // what is copied
-    bool more = true;
-    int issued = 0, taken = 0;
-    const uint64_t pol = l2_policy_evict_first();
-    const int rows_all = p.c.num_pages * p.c.Hkv << p.c.page_shift;  // a row that no box holds: reads zeros
-    auto issue = [&]() {  // the next block with a visible key, if any
-        while (more) {
-            const int k0 = pg_tile_key(is.e, is.t) + KB * warp;
-            const bool see = is.v.any(k0, k0 + KB);
-            if (see && lane == 0) {
-                const int lp = k0 >> p.c.page_shift;
-                int page = lp < p.max_pages ? __ldg(p.table + (long long)is.e.b * p.max_pages + lp) : -1;
-                if (page < 0 || page >= p.c.num_pages) {
-                    atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
-                    page = -1;
+    PgRun r;
+    r.start(p.small, head, c);
+    PgRing<L::STAGES> ring;
+
+    if (warp >= L::WARPS) {
+        // ------------------------------------------------ copies: keys, values
+        const bool val = warp > L::WARPS;
+        const CUtensorMap *map = val ? &p.tmv : &p.tmk;
+        const uint8_t *ex = val ? p.c.ve : p.c.ke;
+        const int box = min(1 << p.c.page_shift, PG_TILE), nbox = PG_TILE / box;
+        const uint64_t pol = l2_policy_evict_first();
+        int tiles = 0;
+        bool ok = true;
+        do {
+            PgView view;
+            view.set(r.e, p.window, p.sinks);
+            // a lane per box: its page is looked up one tile ahead
+            auto row_of = [&](int t) -> int {  // -1: nothing to copy, -2: no such page
+                if (t >= r.tn || lane >= nbox) return -1;
+                const int k = pg_tile_key(r.e, t) + lane * box;
+                if (!view.any(k, k + box)) return -1;
+                const int lp = k >> p.c.page_shift;
+                const int page = lp < p.max_pages ? __ldg(p.table + (long long)r.e.b * p.max_pages + lp) : -1;
+                if (page < 0 || page >= p.c.num_pages) return -2;
+                return ((page * p.c.Hkv + r.h) << p.c.page_shift) + (k & ((1 << p.c.page_shift) - 1));
+            };
+            int next = row_of(r.t0);
+            for (int t = r.t0; t < r.tn && ok; ++t) {
+                const int row = next;
+                next = row_of(t + 1);
+                if (row < -1) atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+                if (tiles >= L::STAGES) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&empty[ring.s], ring.par ^ 1u));
+                if (!ok) {
+                    if (lane == 0) atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_WAIT_TIMEOUT);
+                    break;
                 }
-                const int row = page < 0 ? rows_all
-                                         : ((page * p.c.Hkv + is.h) << p.c.page_shift) + (k0 & ((1 << p.c.page_shift) - 1));
-                const int st = issued % L::STAGES;
-                unsigned char *dst = my_st + st * L::STAGE;
-                uint64_t *bar = &my_bar[st];
-                if constexpr (Q8) {
-                    mbar_arrive_expect_tx(bar, 2 * L::KV + (page < 0 ? 0 : 2 * KB));
-                    tma_load_2d(dst, &p.tmk, 0, row, bar, pol);
-                    tma_load_2d(dst + L::KV, &p.tmv, 0, row, bar, pol);
-                    if (page >= 0) {
-                        bulk_g2s(my_exp + st * L::EXP, p.c.ke + row, KB, bar, pol);
-                        bulk_g2s(my_exp + st * L::EXP + KB, p.c.ve + row, KB, bar, pol);
+                // boxes of a missing page are left as they are: reported, their
+                // keys' scores are not specified
+                const unsigned held = __ballot_sync(FULL_MASK, row >= 0);
+                unsigned char *dst = stages + ring.s * L::STAGE + (val ? L::KV : 0);
+                unsigned char *dx = exps + ring.s * L::EXP + (val ? PG_TILE : 0);
+                uint64_t *bar = &full[ring.s];
+                if (elect_lane()) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(held) * box * (L::ROW + (Q8 ? 1 : 0))));
+                for (int i = 0; i < nbox; ++i) {
+                    if (!((held >> i) & 1u)) continue;
+                    const int rw = __shfl_sync(FULL_MASK, row, i);
+                    if (elect_lane()) {
+                        tma_load_2d(dst + i * box * 128, map, 0, rw, bar, pol);
+                        if constexpr (Q8) bulk_g2s(dx + i * box, ex + rw, box, bar, pol);
+                        else tma_load_2d(dst + SM_HALF + i * box * 128, map, 64, rw, bar, pol);
                     }
-                } else {
-                    mbar_arrive_expect_tx(bar, 2 * L::KV);
-                    tma_load_2d(dst, &p.tmk, 0, row, bar, pol);
-                    tma_load_2d(dst + L::KV / 2, &p.tmk, 64, row, bar, pol);
-                    tma_load_2d(dst + L::KV, &p.tmv, 0, row, bar, pol);
-                    tma_load_2d(dst + L::KV + L::KV / 2, &p.tmv, 64, row, bar, pol);
                 }
+                ring.step();
+                ++tiles;
             }
-            more = is.next(p);
-            if (see) {
-                ++issued;
-                return;
-            }
+        } while (ok && r.next(p.small, p.Hkv));
+        // every copy has landed before the CTA may exit
+        for (int k = 0; k < L::STAGES && k < tiles; ++k) {
+            const int j = tiles - 1 - k;
+            (void)mbar_wait_bounded(&full[j % L::STAGES], (uint32_t)(j / L::STAGES) & 1u);
         }
-    };
-    for (int s = 0; s < L::STAGES; ++s) issue();
+        return;
+    }
 
-    bool ok = true, first_item = true;
-    for (;;) {
-        // ---- one item, or the part of it in this CTA's share
-        const PgEntry e = co.e;
-        const PgView v = co.v;
-        const int h = co.h, t0 = co.t;
-        const int tn = min(e.ntiles, t0 + co.left);
+    // ---------------------------------------------------- scores, softmax, values
+    const int group = warp >> 3, g8 = lane >> 2, t4 = lane & 3;
+    const int kw = KB * (warp & 7);  // this warp's keys of a tile
+    int tile = 0;                    // tiles of this CTA so far: group g takes those with tile mod GROUPS == g
+    bool ok = true;
+    do {
+        const PgEntry &e = r.e;
+        PgView v;
+        v.set(e, p.window, p.sinks);
         const int rows = e.nt * p.GQ;
-        // query fragments: lane's rows g8, g8 + 8; its run of coordinates per
-        // 16 bytes of cache row (8 entries or 16 codes) at run t4 + 4 q
-        constexpr int RUN = Q8 ? 16 : 8;
-        uint32_t qf[2][16];
+        // query fragments: row 8 nt + g8 of the item; this lane's coordinates
+        // are those of its 16-byte pieces of a cache row (8 entries or 16 codes)
+        uint32_t qf[NT][16];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = g8 + 8 * r;
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = 8 * nt + g8;
             const bool in = row < rows;
             const T *src = static_cast<const T *>(p.q);
-            if (in) src += (e.tok0 + row / p.GQ) * p.qst + ((long long)h * p.GQ + row % p.GQ) * p.qsh;
+            if (in) src += (e.tok0 + row / p.GQ) * p.qst + ((long long)r.h * p.GQ + row % p.GQ) * p.qsh;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                // the j-th 8 coordinates of this lane
-                const int d = RUN == 8 ? 8 * (t4 + 4 * j) : 16 * (t4 + 4 * (j >> 1)) + 8 * (j & 1);
+                const int d = Q8 ? 16 * (t4 + 4 * (j >> 1)) + 8 * (j & 1) : 8 * (t4 + 4 * j);
                 const uint4 w = in ? __ldg(reinterpret_cast<const uint4 *>(src + d)) : make_uint4(0u, 0u, 0u, 0u);
-                qf[r][4 * j] = w.x;
-                qf[r][4 * j + 1] = w.y;
-                qf[r][4 * j + 2] = w.z;
-                qf[r][4 * j + 3] = w.w;
+                qf[nt][4 * j] = w.x;
+                qf[nt][4 * j + 1] = w.y;
+                qf[nt][4 * j + 2] = w.z;
+                qf[nt][4 * j + 3] = w.w;
             }
         }
-        // visible keys of this lane's two rows: j <= pos, and the window
-        int pos[2], low[2];
+        // the rows of this lane's results are 8 nt + 2 t4 + {0, 1}; their
+        // visible keys: j <= pos, and the window
+        int pos[2 * NT], low[2 * NT];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = g8 + 8 * r;
-            pos[r] = row < rows ? e.p0 + row / p.GQ : -1;
-            low[r] = p.window > 0 ? pos[r] - p.window + 1 : 0;
+        for (int i = 0; i < 2 * NT; ++i) {
+            const int row = 8 * (i >> 1) + 2 * t4 + (i & 1);
+            pos[i] = row < rows ? e.p0 + row / p.GQ : -1;
+            low[i] = p.window > 0 ? pos[i] - p.window + 1 : 0;
         }
         const int lo_all = p.window > 0 ? e.p0 + e.nt - p.window : 0;  // the last row's first key in the window
-        float m[2] = {NEG_INF, NEG_INF}, l[2] = {0.0f, 0.0f};
-        float o[16][4];
+        float m[2 * NT], l[2 * NT], o[NT][8][4];
 #pragma unroll
-        for (int n = 0; n < 16; ++n)
+        for (int i = 0; i < 2 * NT; ++i) {
+            m[i] = NEG_INF;
+            l[i] = 0.0f;
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[n][j] = 0.0f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[nt][n][j] = 0.0f;
 
-        for (int t = t0; t < tn; ++t) {
-            const int k0 = pg_tile_key(e, t) + KB * warp;
-            if (!v.any(k0, k0 + KB) || !ok) continue;
-            const int st = taken % L::STAGES;
-            if (!__all_sync(FULL_MASK, mbar_wait_bounded(&my_bar[st], (uint32_t)(taken / L::STAGES) & 1u))) {
+        for (int t = r.t0; t < r.tn; ++t, ++tile, ring.step()) {
+            if (L::GROUPS > 1 && (tile & 1) != group) continue;
+            if (!ok) continue;
+            if (!__all_sync(FULL_MASK, mbar_wait_bounded(&full[ring.s], ring.par))) {
                 if (lane == 0) atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_WAIT_TIMEOUT);
                 ok = false;
                 continue;
             }
-            const unsigned char *sb = my_st + st * L::STAGE;
-            // ---- scores: S[row][key], two blocks of 8 keys
-            float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+            const int k0 = pg_tile_key(e, t) + kw;
+            if (v.any(k0, k0 + KB)) {
+                const unsigned char *sb = stages + ring.s * L::STAGE + kw * 128;
+                // ---- scores: S^T[key][row]; this lane's keys are g8 and g8 + 8
+                float s[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                const int key = 8 * nt + g8;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[nt][j] = 0.0f;
                 if constexpr (Q8) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(sb + swz128(key, t4 + 4 * q));
-                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                        const uint4 wa = *reinterpret_cast<const uint4 *>(sb + swz128(g8, t4 + 4 * q));
+                        const uint4 wb = *reinterpret_cast<const uint4 *>(sb + swz128(g8 + 8, t4 + 4 * q));
+                        const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xb[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int i = 8 * q + 2 * j;  // pairs 2 i, 2 i + 1 of the lane's coordinates
-                            mma16<T>(s[nt], qf[0][i], qf[1][i], qf[0][i + 1], qf[1][i + 1], codes2<T>(x[j] & 0xffffu),
-                                     codes2<T>(x[j] >> 16));
+                            const uint32_t a0 = codes2<T>(xa[j] & 0xffffu), a1 = codes2<T>(xb[j] & 0xffffu);
+                            const uint32_t a2 = codes2<T>(xa[j] >> 16), a3 = codes2<T>(xb[j] >> 16);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16<T>(s[nt], a0, a1, a2, a3, qf[nt][8 * q + 2 * j], qf[nt][8 * q + 2 * j + 1]);
                         }
                     }
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(sb + (q >> 1) * (L::KV / 2) +
-                                                                         swz128(key, t4 + 4 * (q & 1)));
-                        mma16<T>(s[nt], qf[0][4 * q], qf[1][4 * q], qf[0][4 * q + 1], qf[1][4 * q + 1], w.x, w.y);
-                        mma16<T>(s[nt], qf[0][4 * q + 2], qf[1][4 * q + 2], qf[0][4 * q + 3], qf[1][4 * q + 3], w.z, w.w);
-                    }
-                }
-            }
-            // ---- scale, mask: this lane's keys are 8 nt + 2 t4 + {0, 1}
-            float vb[2][2];  // 2^-b of the lane's keys' values (8-bit cache)
-            const bool whole = k0 + KB <= e.p0 + 1 && (p.window == 0 || k0 >= lo_all || k0 + KB <= v.sink);
+                        const unsigned char *h = sb + (q >> 1) * SM_HALF;
+                        const uint4 wa = *reinterpret_cast<const uint4 *>(h + swz128(g8, t4 + 4 * (q & 1)));
+                        const uint4 wb = *reinterpret_cast<const uint4 *>(h + swz128(g8 + 8, t4 + 4 * (q & 1)));
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float a = p.qscale, b = 0.0f;
-                    if constexpr (Q8) {
-                        const int key = 8 * nt + 2 * t4 + j;
-                        const int be = (int)my_exp[st * L::EXP + KB + key] - 127;
-                        a *= pow2f(max((int)my_exp[st * L::EXP + key] - 127, -126));
-                        b = (float)be;
-                        vb[nt][j] = pow2f(max(-be, -126));
-                    }
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float &x = s[nt][2 * r + j];
-                        x = fmaf(x, a, b);
-                        if (!whole) {
-                            const int k = k0 + 8 * nt + 2 * t4 + j;
-                            const bool in = k <= pos[r] && (k >= low[r] || k < v.sink);
-                            x = in ? x : NEG_INF;
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16<T>(s[nt], wa.x, wb.x, wa.y, wb.y, qf[nt][4 * q], qf[nt][4 * q + 1]);
+                            mma16<T>(s[nt], wa.z, wb.z, wa.w, wb.w, qf[nt][4 * q + 2], qf[nt][4 * q + 3]);
                         }
                     }
                 }
-            }
-            // ---- softmax: the four lanes of a row share its maximum
-            uint32_t pf[4];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float x = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-                x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, 2));
-                if (x - OFF > m[r] + LAG) {  // the same for the row's four lanes
-                    const float f = ex2(m[r] - (x - OFF));
-                    m[r] = x - OFF;
-                    l[r] *= f;
-#pragma unroll
-                    for (int n = 0; n < 16; ++n) {
-                        o[n][2 * r] *= f;
-                        o[n][2 * r + 1] *= f;
-                    }
-                }
-                const float mm = m[r] > NEG_INF ? m[r] : 0.0f;
-                float w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = ex2(s[i >> 1][2 * r + (i & 1)] - mm);
+                // ---- scale, mask
+                const bool whole = k0 + KB <= e.p0 + 1 && (p.window == 0 || k0 >= lo_all || k0 + KB <= v.sink);
+                float fa[2] = {p.qscale, p.qscale}, fb[2] = {0.0f, 0.0f}, back[2] = {1.0f, 1.0f};
                 if constexpr (Q8) {
-                    l[r] += w[0] * vb[0][0] + w[1] * vb[0][1] + (w[2] * vb[1][0] + w[3] * vb[1][1]);
-                } else {
-                    l[r] += (w[0] + w[1]) + (w[2] + w[3]);
-                }
-                pf[r] = pack2<TV>(w[0], w[1]);
-                pf[r + 2] = pack2<TV>(w[2], w[3]);
-            }
-            // ---- values: keys that no row sees may hold anything, their
-            // entries are masked out of the operand
-            uint32_t ka = 0xffffffffu, kb = 0xffffffffu;
-            if (!whole) {
-                const int k = k0 + 2 * t4;
-                ka = (v.one(k) ? 0x0000ffffu : 0u) | (v.one(k + 1) ? 0xffff0000u : 0u);
-                kb = (v.one(k + 8) ? 0x0000ffffu : 0u) | (v.one(k + 9) ? 0xffff0000u : 0u);
-            }
-            const uint32_t vbase = smem_u32(sb) + L::KV;
-            const int vkey = (lane & 7) + 8 * ((lane >> 3) & 1), vc = lane >> 4;
-            if constexpr (Q8) {
-                // 16 columns of codes at a time: a transposed 16-bit element is
-                // the pair of codes of columns 2 g8, 2 g8 + 1
 #pragma unroll
-                for (int n = 0; n < 8; n += 2) {
-                    uint32_t x[4];
-                    ldsm_x4_t(vbase + swz128(vkey, n + vc), x);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint32_t lo = __byte_perm(x[2 * q], 0u, 0x3120), hi = __byte_perm(x[2 * q + 1], 0u, 0x3120);
-                        const int nn = 2 * (n + q);
-                        mma16<TV>(o[nn], pf[0], pf[1], pf[2], pf[3], codes2<TV>(lo & 0xffffu) & ka,
-                                  codes2<TV>(hi & 0xffffu) & kb);
-                        mma16<TV>(o[nn + 1], pf[0], pf[1], pf[2], pf[3], codes2<TV>(lo >> 16) & ka,
-                                  codes2<TV>(hi >> 16) & kb);
+                    for (int i = 0; i < 2; ++i) {
+                        const unsigned char *x = exps + ring.s * L::EXP + kw + g8 + 8 * i;
+                        const int a = (int)x[0] - 127, b = (int)x[PG_TILE] - 127;
+                        fa[i] *= pow2f(max(a, -126));
+                        fb[i] = (float)b;
+                        back[i] = pow2f(max(-b, -126));
                     }
                 }
-            } else {
+                uint32_t pf[NT][2];
 #pragma unroll
-                for (int n = 0; n < 16; n += 2) {
-                    uint32_t x[4];
-                    ldsm_x4_t(vbase + (n >> 3) * (L::KV / 2) + swz128(vkey, (n & 7) + vc), x);
-                    mma16<TV>(o[n], pf[0], pf[1], pf[2], pf[3], x[0] & ka, x[1] & kb);
-                    mma16<TV>(o[n + 1], pf[0], pf[1], pf[2], pf[3], x[2] & ka, x[3] & kb);
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[nt][j] = Q8 ? fmaf(s[nt][j], fa[j >> 1], fb[j >> 1]) : s[nt][j] * fa[0];
+                    if (!whole) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int k = k0 + g8 + 8 * (j >> 1), i = 2 * nt + (j & 1);
+                            const bool in = k <= pos[i] && (k >= low[i] || k < v.sink);
+                            s[nt][j] = in ? s[nt][j] : NEG_INF;
+                        }
+                    }
+                    // ---- softmax: a row's 16 scores lie in the 8 lanes of one t4
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float x = fmaxf(s[nt][i], s[nt][i + 2]);
+#pragma unroll
+                        for (int sh = 4; sh <= 16; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, sh));
+                        float &mi = m[2 * nt + i];
+                        if (x - OFF > mi + LAG) {
+                            const float f = ex2(mi - (x - OFF));
+                            mi = x - OFF;
+                            l[2 * nt + i] *= f;
+#pragma unroll
+                            for (int n = 0; n < 8; ++n) {
+                                o[nt][n][i] *= f;
+                                o[nt][n][i + 2] *= f;
+                            }
+                        }
+                    }
+                    const float ma = m[2 * nt] > NEG_INF ? m[2 * nt] : 0.0f, mb = m[2 * nt + 1] > NEG_INF ? m[2 * nt + 1] : 0.0f;
+                    const float w0 = ex2(s[nt][0] - ma), w1 = ex2(s[nt][1] - mb), w2 = ex2(s[nt][2] - ma),
+                                w3 = ex2(s[nt][3] - mb);
+                    if constexpr (Q8) {
+                        l[2 * nt] = fmaf(w0, back[0], fmaf(w2, back[1], l[2 * nt]));
+                        l[2 * nt + 1] = fmaf(w1, back[0], fmaf(w3, back[1], l[2 * nt + 1]));
+                    } else {
+                        l[2 * nt] += w0 + w2;
+                        l[2 * nt + 1] += w1 + w3;
+                    }
+                    // W^T as the second operand: [key][row] to [row][key pairs]
+                    pf[nt][0] = transpose8(pack2<TV>(w0, w1));
+                    pf[nt][1] = transpose8(pack2<TV>(w2, w3));
+                }
+                // ---- values: keys that no row sees may hold anything, their
+                // entries are masked out of the operand
+                uint32_t ka = 0xffffffffu, kb = 0xffffffffu;
+                if (!whole) {
+                    const int k = k0 + 2 * t4;
+                    ka = (v.one(k) ? 0x0000ffffu : 0u) | (v.one(k + 1) ? 0xffff0000u : 0u);
+                    kb = (v.one(k + 8) ? 0x0000ffffu : 0u) | (v.one(k + 9) ? 0xffff0000u : 0u);
+                }
+                const uint32_t vbase = smem_u32(sb) + L::KV;
+                if constexpr (Q8) {
+                    // 16 columns of codes at a time: a transposed 16-bit element is
+                    // the pair of codes of columns 2 g8, 2 g8 + 1, which become
+                    // rows g8 and g8 + 8 of the operand
+                    const int vkey = (lane & 7) + 8 * ((lane >> 3) & 1), vc = lane >> 4;
+#pragma unroll
+                    for (int n = 0; n < 8; n += 2) {
+                        uint32_t x[4];
+                        ldsm_x4_t(vbase + swz128(vkey, n + vc), x);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t lo = __byte_perm(x[2 * q], 0u, 0x3120), hi = __byte_perm(x[2 * q + 1], 0u, 0x3120);
+                            const uint32_t a0 = codes2<TV>(lo & 0xffffu) & ka, a1 = codes2<TV>(lo >> 16) & ka;
+                            const uint32_t a2 = codes2<TV>(hi & 0xffffu) & kb, a3 = codes2<TV>(hi >> 16) & kb;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma16<TV>(o[nt][n + q], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                        }
+                    }
+                } else {
+                    const int vkey = (lane & 7) + 8 * (lane >> 4), vc = (lane >> 3) & 1;
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        uint32_t x[4];
+                        ldsm_x4_t(vbase + (n >> 2) * SM_HALF + swz128(vkey, 2 * (n & 3) + vc), x);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16<TV>(o[nt][n], x[0] & ka, x[1] & ka, x[2] & kb, x[3] & kb, pf[nt][0], pf[nt][1]);
+                    }
                 }
             }
+            fence_proxy_async_smem();  // the tile was read; a copy may overwrite it
             __syncwarp();
-            fence_proxy_async_smem();
-            ++taken;
-            issue();
+            if (lane == 0) mbar_arrive(&empty[ring.s]);
         }
 
-        // ---- merge the warps: common maximum, then outputs in two rounds of
-        // four buffers
+        // ---- merge the warps: common maximum, then the outputs, MBUF at a time
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(FULL_MASK, l[r], 1);
-            l[r] += __shfl_xor_sync(FULL_MASK, l[r], 2);
-        }
-        __syncthreads();  // the previous item's merge has been read
-        if (t4 == 0) {
-            *reinterpret_cast<float2 *>(stat(warp, g8)) = make_float2(m[0], l[0]);
-            *reinterpret_cast<float2 *>(stat(warp, g8 + 8)) = make_float2(m[1], l[1]);
-        }
-        __syncthreads();
-        float f[2];
+        for (int i = 0; i < 2 * NT; ++i)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+            for (int sh = 4; sh <= 16; sh <<= 1) l[i] += __shfl_xor_sync(FULL_MASK, l[i], sh);
+        bar_compute<L::WARPS * 32>();  // the previous item's merge has been read
+        if (g8 == 0) {
+#pragma unroll
+            for (int i = 0; i < 2 * NT; ++i)
+                stat[warp * L::ROWS + 8 * (i >> 1) + 2 * t4 + (i & 1)] = make_float2(m[i], l[i]);
+        }
+        bar_compute<L::WARPS * 32>();
+        float f[2 * NT];
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) {
             float M = NEG_INF;
 #pragma unroll
-            for (int w = 0; w < SM_WARPS; ++w) M = fmaxf(M, *stat(w, g8 + 8 * r));
-            f[r] = m[r] > NEG_INF ? ex2(m[r] - M) : 0.0f;
+            for (int w = 0; w < L::WARPS; ++w) M = fmaxf(M, stat[w * L::ROWS + 8 * (i >> 1) + 2 * t4 + (i & 1)].x);
+            f[i] = m[i] > NEG_INF ? ex2(m[i] - M) : 0.0f;
         }
-        float *mine = merge + (warp & 3) * 16 * MROW;
+        float *mine = merge + (warp % L::MBUF) * L::ROWS * L::MROW;
+#pragma unroll 1
+        for (int round = 0; round < L::WARPS / L::MBUF; ++round) {
+            if (warp / L::MBUF == round) {
 #pragma unroll
-        for (int round = 0; round < 2; ++round) {
-            if ((warp >> 2) == round) {
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int n = 0; n < 16; ++n) {
-                    // columns of this accumulator: 8 n + 2 t4 + {0, 1}, or with codes
-                    // 16 (n / 2) + 4 t4 + (n mod 2) + {0, 2}
-                    const int d0 = Q8 ? 16 * (n >> 1) + 4 * t4 + (n & 1) : 8 * n + 2 * t4, d1 = d0 + (Q8 ? 2 : 1);
-                    float *a = mine + g8 * MROW, *b = a + 8 * MROW;
-                    if (round == 0) {
-                        a[d0] = o[n][0] * f[0];
-                        a[d1] = o[n][1] * f[0];
-                        b[d0] = o[n][2] * f[1];
-                        b[d1] = o[n][3] * f[1];
-                    } else {
-                        a[d0] += o[n][0] * f[0];
-                        a[d1] += o[n][1] * f[0];
-                        b[d0] += o[n][2] * f[1];
-                        b[d1] += o[n][3] * f[1];
-                    }
-                }
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            // coordinate: 16 n + g8 (+ 8), with codes 16 n + 2 g8 (+ 1)
+                            const int d = 16 * n + (Q8 ? 2 * g8 + (j >> 1) : g8 + 8 * (j >> 1));
+                            float *a = mine + (8 * nt + 2 * t4 + (j & 1)) * L::MROW + d;
+                            const float x = o[nt][n][j] * f[2 * nt + (j & 1)];
+                            *a = round == 0 ? x : *a + x;
+                        }
             }
-            __syncthreads();
+            bar_compute<L::WARPS * 32>();
         }
-        const bool split = t0 > 0 || tn < e.ntiles;
-        float *part = p.small.part + (size_t)(2 * c + (first_item && t0 > 0 ? 0 : 1)) * (PG_SROWS * PG_PART);
-        for (int r = warp; r < rows; r += SM_WARPS) {  // a warp writes a row
+        const bool split = r.t0 > 0 || r.tn < e.ntiles;
+        float *part = p.small.part + (size_t)(2 * c + (r.first && r.t0 > 0 ? 0 : 1)) * (PG_SROWS * PG_PART);
+        for (int row = warp; row < rows; row += L::WARPS) {  // a warp writes a row
             float M = NEG_INF, Ls = 0.0f;
 #pragma unroll
-            for (int w = 0; w < SM_WARPS; ++w) M = fmaxf(M, *stat(w, r));
+            for (int w = 0; w < L::WARPS; ++w) M = fmaxf(M, stat[w * L::ROWS + row].x);
             if (M > NEG_INF) {
 #pragma unroll
-                for (int w = 0; w < SM_WARPS; ++w) Ls += stat(w, r)[1] * ex2(*stat(w, r) - M);
+                for (int w = 0; w < L::WARPS; ++w) Ls += stat[w * L::ROWS + row].y * ex2(stat[w * L::ROWS + row].x - M);
             }
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float4 y = *reinterpret_cast<const float4 *>(merge + (w * 16 + r) * MROW + 4 * lane);
+            for (int w = 0; w < L::MBUF; ++w) {
+                const float4 y = *reinterpret_cast<const float4 *>(merge + (w * L::ROWS + row) * L::MROW + 4 * lane);
                 x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
             }
             if (split) {
                 if (lane == 0) {
-                    part[r] = M;
-                    part[PG_SROWS + r] = Ls;
+                    part[row] = M;
+                    part[PG_SROWS + row] = Ls;
                 }
-                *reinterpret_cast<float4 *>(part + 2 * PG_SROWS + r * D + 4 * lane) = x;
+                *reinterpret_cast<float4 *>(part + 2 * PG_SROWS + row * D + 4 * lane) = x;
             } else {
                 const float inv = Ls > 0.0f ? 1.0f / Ls : 0.0f;
                 x.x *= inv; x.y *= inv; x.z *= inv; x.w *= inv;
                 T *dst = static_cast<T *>(p.out) +
-                         ((size_t)(e.tok0 + r / p.GQ) * p.Hq + (size_t)h * p.GQ + r % p.GQ) * D + 4 * lane;
+                         ((size_t)(e.tok0 + row / p.GQ) * p.Hq + (size_t)r.h * p.GQ + row % p.GQ) * D + 4 * lane;
                 *reinterpret_cast<uint2 *>(dst) = pack4<T>(x);
             }
         }
-        first_item = false;
-        co.t = tn - 1;
-        co.left -= tn - t0 - 1;
-        if (!co.next(p)) break;
-    }
-    if (!ok) {  // a copy did not land in time: wait (bounded) for the others before the memory is given up
-        for (; taken < issued; ++taken)
-            (void)mbar_wait_bounded(&my_bar[taken % L::STAGES], (uint32_t)(taken / L::STAGES) & 1u);
-    }
+    } while (r.next(p.small, p.Hkv));
+}
+
+template <class T, bool Q8, int NT>
+cudaError_t launch_small(const PagedAttendParams &p, cudaStream_t stream)
+{
+    auto kern = paged_small_kernel<T, Q8, NT>;
+    constexpr int smem = SmShape<Q8, NT>::SMEM;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<p.small.G, SmShape<Q8, NT>::THREADS, smem, stream>>>(p);
+    return cudaGetLastError();
 }
 
 template <class T, bool Q8>
-cudaError_t launch_small(const PagedAttendParams &p, cudaStream_t stream)
+cudaError_t dispatch_small(const PagedAttendParams &p, cudaStream_t stream)
 {
-    auto kern = paged_small_kernel<T, Q8>;
-    constexpr int smem = SmTile<Q8>::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    kern<<<p.small.G, SM_WARPS * 32, smem, stream>>>(p);
-    return cudaGetLastError();
+    return p.small_rows <= 8 ? launch_small<T, Q8, 1>(p, stream) : launch_small<T, Q8, 2>(p, stream);
 }
 
 }  // namespace
@@ -713,21 +729,22 @@ cudaError_t launch_paged_small(const PagedAttendParams &p0, int q_dtype, int cac
     PagedAttendParams p = p0;
     const bool q8 = cache_dtype == VQ_E4M3;
     const uint64_t rows = ((uint64_t)p.c.num_pages * p.c.Hkv) << p.c.page_shift;
-    if (!encode_tmap_pages(&p.tmk, p.c.k, rows, q8 ? 1 : 2, KB) || !encode_tmap_pages(&p.tmv, p.c.v, rows, q8 ? 1 : 2, KB))
+    const uint32_t box = 1u << p.c.page_shift < (unsigned)PG_TILE ? 1u << p.c.page_shift : (unsigned)PG_TILE;
+    if (!encode_tmap_pages(&p.tmk, p.c.k, rows, q8 ? 1 : 2, box) || !encode_tmap_pages(&p.tmv, p.c.v, rows, q8 ? 1 : 2, box))
         return cudaErrorInvalidValue;
-    if (q_dtype == VQ_F16) return q8 ? launch_small<__half, true>(p, stream) : launch_small<__half, false>(p, stream);
-    return q8 ? launch_small<__nv_bfloat16, true>(p, stream) : launch_small<__nv_bfloat16, false>(p, stream);
+    if (q_dtype == VQ_F16) return q8 ? dispatch_small<__half, true>(p, stream) : dispatch_small<__half, false>(p, stream);
+    return q8 ? dispatch_small<__nv_bfloat16, true>(p, stream) : dispatch_small<__nv_bfloat16, false>(p, stream);
 }
 
 cudaError_t launch_paged_combine(const PagedAttendParams &p, int q_dtype, bool large, cudaStream_t stream)
 {
     const dim3 grid(large ? p.large.G : p.small.G, (large ? PG_LROWS : PG_SROWS) / CB_ROWS);
     if (q_dtype == VQ_F16) {
-        if (large) paged_combine_kernel<__half, PG_LROWS, 1><<<grid, 128, 0, stream>>>(p);
-        else paged_combine_kernel<__half, PG_SROWS, 0><<<grid, 128, 0, stream>>>(p);
+        if (large) paged_combine_kernel<__half, PG_LROWS, 1><<<grid, 32 * CB_ROWS, 0, stream>>>(p);
+        else paged_combine_kernel<__half, PG_SROWS, 0><<<grid, 32 * CB_ROWS, 0, stream>>>(p);
     } else {
-        if (large) paged_combine_kernel<__nv_bfloat16, PG_LROWS, 1><<<grid, 128, 0, stream>>>(p);
-        else paged_combine_kernel<__nv_bfloat16, PG_SROWS, 0><<<grid, 128, 0, stream>>>(p);
+        if (large) paged_combine_kernel<__nv_bfloat16, PG_LROWS, 1><<<grid, 32 * CB_ROWS, 0, stream>>>(p);
+        else paged_combine_kernel<__nv_bfloat16, PG_SROWS, 0><<<grid, 32 * CB_ROWS, 0, stream>>>(p);
     }
     return cudaGetLastError();
 }

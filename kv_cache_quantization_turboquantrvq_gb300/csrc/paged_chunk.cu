@@ -159,14 +159,6 @@ __device__ __forceinline__ void ck_commit(uint64_t *bar)
         : "memory");
 }
 
-// One lane of the (whole, converged) warp: the same each time.
-__device__ __forceinline__ bool ck_elect()
-{
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));
-    return e != 0;
-}
-
 __device__ __forceinline__ void ck_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
@@ -269,51 +261,6 @@ __device__ __forceinline__ uint32_t ck_top(uint32_t four)
     return __reduce_max_sync(FULL_MASK, max(four & 0xffu, (four >> 8) & 0xffu));
 }
 
-// One CTA's share as runs of tiles of one item each.
-struct Run {
-    PgEntry e;
-    int ei, h, t0, tn, left;
-    bool first;  // the CTA's first run
-    __device__ __forceinline__ void start(const PgPlan &pl, const PgPlanHead &head, int c)
-    {
-        const int4 at = __ldg(pl.ctab + c);
-        ei = at.x;
-        h = at.y;
-        t0 = at.z;
-        left = (int)(pg_first_unit(head, c + 1) - pg_first_unit(head, c));
-        e = pg_entry(pl.ent + ei);
-        tn = min(e.ntiles, t0 + left);
-        first = true;
-    }
-    __device__ __forceinline__ bool next(const PgPlan &pl, int Hkv)
-    {
-        left -= tn - t0;
-        if (left <= 0) return false;
-        if (++h == Hkv) {
-            h = 0;
-            ++ei;
-            e = pg_entry(pl.ent + ei);
-        }
-        t0 = 0;
-        tn = min(e.ntiles, left);
-        first = false;
-        return true;
-    }
-};
-
-// Position in a ring of N barriers: slot and the parity of its current pass.
-template <int N> struct Ring {
-    int s = 0;
-    uint32_t par = 0;
-    __device__ __forceinline__ void step()
-    {
-        if (++s == N) {
-            s = 0;
-            par ^= 1u;
-        }
-    }
-};
-
 template <class T, bool Q8>
 __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(const __grid_constant__ PagedAttendParams p)
 {
@@ -389,7 +336,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         }
     };
 
-    Run r;
+    PgRun r;
     r.start(p.large, head, blockIdx.x);
 
     if (warp >= 8 && warp < 12) {
@@ -399,8 +346,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         const int box = min(1 << p.c.page_shift, PG_TILE), nbox = PG_TILE / box;
         const int rows_all = p.c.num_pages * p.c.Hkv << p.c.page_shift;  // no box holds this row: reads zeros
         const uint64_t pol = ck_policy();
-        Ring<STAGES> kv;
-        Ring<C::RAW ? C::RAW : 1> raw;
+        PgRing<STAGES> kv;
+        PgRing<C::RAW ? C::RAW : 1> raw;
         uint32_t qpar = 0;
         int tiles = 0;  // tiles copied
         bool ok = true;
@@ -410,7 +357,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 qpar ^= 1u;
                 if (!ok) break;
             }
-            if (ck_elect()) {
+            if (elect_lane()) {
                 // tokens past the chunk bring other sequences' rows, past the tensor zeros: never used
                 const int nq = r.e.nt > tqt ? 2 : 1;
                 mbar_arrive_expect_tx(q_full, (uint32_t)(nq * 2 * tqt * p.GQ * 128));
@@ -448,10 +395,10 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                         }
                         // a key tile brings the exponents of keys and values
                         const unsigned n = part ? 0u : (unsigned)__popc(__ballot_sync(FULL_MASK, held));
-                        if (ck_elect()) mbar_arrive_expect_tx(&raw_full[raw.s], RAW_B + n * 2 * box);
+                        if (elect_lane()) mbar_arrive_expect_tx(&raw_full[raw.s], RAW_B + n * 2 * box);
                         for (int i = 0; i < nbox; ++i) {
                             const int rw = __shfl_sync(FULL_MASK, at, i);
-                            if (ck_elect()) {
+                            if (elect_lane()) {
                                 tma_load_2d(sraw + raw.s * RAW_B + i * box * 128, map, 0, rw, &raw_full[raw.s], pol);
                                 if (part == 0 && rw != rows_all) {
                                     unsigned char *x = sexp + raw.s * 2 * PG_TILE + i * box;
@@ -466,10 +413,10 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                             ok = false;
                             break;
                         }
-                        if (ck_elect()) mbar_arrive_expect_tx(&kv_full[kv.s], TILE_B);
+                        if (elect_lane()) mbar_arrive_expect_tx(&kv_full[kv.s], TILE_B);
                         for (int i = 0; i < nbox; ++i) {
                             const int rw = __shfl_sync(FULL_MASK, at, i);
-                            if (ck_elect()) {
+                            if (elect_lane()) {
                                 unsigned char *dst = skv + kv.s * TILE_B + i * box * 128;
                                 tma_load_2d(dst, map, 0, rw, &kv_full[kv.s], pol);
                                 tma_load_2d(dst + HALF_B, map, 64, rw, &kv_full[kv.s], pol);
@@ -501,13 +448,20 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         constexpr uint32_t ID_S = ck_idesc(BF, false), ID_O = ck_idesc(BFV, true);
         const uint64_t dq = qt_desc(smem_u32(sq)), dk = qt_desc(smem_u32(skv)), dv = ck_desc_v(smem_u32(skv));
         const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
-        Ring<STAGES> kv;
+        PgRing<STAGES> kv;
         bool ok = true;
         auto await = [&](uint64_t *bar, uint32_t parity) { ok = ok && __all_sync(FULL_MASK, wait(bar, parity)); };
         if (warp == 9) {
             uint32_t qpar = 0, fpar = 1;  // (the score tile is free at first)
+            int tiles = 0;                // of the ring, keys and values
             do {
                 const bool two = r.e.nt > tqt;
+                // A run's first keys may follow values in their slot: those must
+                // have come and gone, or their pass would be taken for this one
+                // (a barrier's parity tells two passes apart, not three).  Later
+                // keys follow keys, or (codes) come in order.
+                if (!Q8 && tiles >= STAGES) await(&kv_empty[kv.s], kv.par ^ 1u);
+                tiles += 2 * (r.tn - r.t0);
                 await(q_full, qpar);
                 qpar ^= 1u;
                 for (int t = r.t0; t < r.tn && ok; ++t) {
@@ -566,8 +520,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         const int tok_in = row / p.GQ;
         const float qabs = fabsf(p.qscale);
         uint32_t spar = 0, vpar = 0;
-        Ring<STAGES> vs;  // (16-bit cache) slot of the next tile that the products take
-        Ring<C::META ? C::META : 1> mt;
+        PgRing<STAGES> vs;  // (16-bit cache) slot of the next tile that the products take
+        PgRing<C::META ? C::META : 1> mt;
         bool ok = true;
         do {
             const int nq = r.e.nt > tqt ? 2 : 1;
@@ -798,9 +752,9 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         ck_reg_dec<C::R_CONV>();
         // ------------------------------------------------ codes to 16-bit operands
         const int j = threadIdx.x - 12 * 32;
-        Ring<C::RAW ? C::RAW : 1> raw;
-        Ring<STAGES> kv;
-        Ring<C::META ? C::META : 1> mt;
+        PgRing<C::RAW ? C::RAW : 1> raw;
+        PgRing<STAGES> kv;
+        PgRing<C::META ? C::META : 1> mt;
         int tiles = 0, keys = 0;
         uint32_t vtop0 = 0, vtop1 = 0;  // exponents of the values to come: of tile u - 1, of tile u
         uint64_t vrow0 = 0, vrow1 = 0;

@@ -28,7 +28,23 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-__device__ __forceinline__ long long pg_first_unit(const PgPlanHead &h, int c) { return h.total * c / h.g; }
+// One lane of the (whole, converged) warp, the same each time.  Copies and
+// products issued under it keep their operands in uniform registers.
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+// First unit of CTA c: an even share, the first `rem` CTAs take one more.
+__device__ __forceinline__ long long pg_first_unit(const PgPlanHead &h, int c) { return h.q * c + min(c, h.rem); }
+
+// Barrier of the first THREADS threads of the CTA.
+template <int THREADS> __device__ __forceinline__ void bar_compute()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
 
 // What of an entry's keys its rows see together: [lo, hi) and the first `sink` keys.
 struct PgView {
@@ -58,6 +74,51 @@ __device__ __forceinline__ int pg_tile_key(const PgEntry &e, int t)
 {
     return (t < e.nsink ? t : e.tl + (t - e.nsink)) * PG_TILE;
 }
+
+// One CTA's share as runs of tiles of one item each.
+struct PgRun {
+    PgEntry e;
+    int ei, h, t0, tn, left;
+    bool first;  // the CTA's first run
+    __device__ __forceinline__ void start(const PgPlan &pl, const PgPlanHead &head, int c)
+    {
+        const int4 at = __ldg(pl.ctab + c);
+        ei = at.x;
+        h = at.y;
+        t0 = at.z;
+        left = (int)(pg_first_unit(head, c + 1) - pg_first_unit(head, c));
+        e = pg_entry(pl.ent + ei);
+        tn = min(e.ntiles, t0 + left);
+        first = true;
+    }
+    __device__ __forceinline__ bool next(const PgPlan &pl, int Hkv)
+    {
+        left -= tn - t0;
+        if (left <= 0) return false;
+        if (++h == Hkv) {
+            h = 0;
+            ++ei;
+            e = pg_entry(pl.ent + ei);
+        }
+        t0 = 0;
+        tn = min(e.ntiles, left);
+        first = false;
+        return true;
+    }
+};
+
+// Position in a ring of N barriers: slot and the parity of its current pass.
+template <int N> struct PgRing {
+    int s = 0;
+    uint32_t par = 0;
+    __device__ __forceinline__ void step()
+    {
+        if (++s == N) {
+            s = 0;
+            par ^= 1u;
+        }
+    }
+};
 
 }  // namespace
 }  // namespace vq

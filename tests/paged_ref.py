@@ -81,12 +81,12 @@ def attend(q, k, v, table, cu, lens, scale, window, sinks, w_step):
             pg = table[b].long()[j // PS]
             kk, vv = k[pg, :, j % PS], v[pg, :, j % PS]  # [n, Hkv, D]
             t = int(cu[b]) + i
-            for h in range(Hq):
-                kh, vh = kk[:, h // G], vv[:, h // G]
-                s = kh @ q[t, h] * scale
-                w = torch.softmax(s, 0)
-                out[t, h] = w @ vh
-                d = 2.0 ** -24 * 140 * float((kh.abs() @ q[t, h].abs()).max()) * abs(scale) + 2.0 ** -20
-                small = len(j) * 2.0 ** -32 * vh.abs().max(0).values
-                bound[t, h] = (w_step + 2 * math.expm1(d) + len(j) ** 0.5 * 2.0 ** -22) * (w @ vh.abs()) + small
+            kh, vh = kk.transpose(0, 1), vv.transpose(0, 1)  # [Hkv, n, D]
+            qt = q[t].view(Hkv, G, D).transpose(1, 2)        # [Hkv, D, G]
+            w = torch.softmax(kh @ qt * scale, 1).transpose(1, 2)
+            out[t] = (w @ vh).reshape(Hq, D)
+            d = 2.0 ** -24 * 140 * (kh.abs() @ qt.abs()).amax(1) * abs(scale) + 2.0 ** -20  # [Hkv, G]
+            small = len(j) * 2.0 ** -32 * vh.abs().amax(1, keepdim=True)
+            u = w_step + 2 * torch.expm1(d) + len(j) ** 0.5 * 2.0 ** -22
+            bound[t] = (u[..., None] * (w @ vh.abs()) + small).reshape(Hq, D)
     return out, bound

@@ -299,6 +299,23 @@ def test_one_long_sequence_is_split_and_joined(vq, dtype, cache):
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("GQ", [2, 12])
+def test_many_tiles_for_every_block(vq, dtype, cache, GQ):
+    """Single tokens with far more key tiles than blocks: the rings of copies
+    come round many times, across items (8 and 16 row forms)."""
+    news, lens = [1] * 40, [1500 + 61 * i for i in range(40)]
+    _check(vq, _case(vq, news, lens, 8 if GQ == 2 else 4, GQ, 64, dtype, cache, seed=35))
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+def test_many_chunk_tiles_for_every_block(vq, dtype, cache):
+    """Chunks with several items and many tiles for every block, among them
+    items of one query tile and of two."""
+    news, lens = [33, 70, 1, 200, 130, 64], [2100, 3000, 900, 2500, 130, 1900]
+    _check(vq, _case(vq, news, lens, 8, 4, 128, dtype, cache, seed=36))
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
 def test_scores_far_apart(vq, dtype, cache):
     """Large scores (one key takes nearly all weight, the maximum moves often), a
     negative scale, and scale 0 (plain means)."""
