@@ -5,7 +5,7 @@
 
 #include <cstdint>
 #include <cuda.h>
-#include <cuda_runtime_api.h>
+#include <cuda_runtime.h>
 
 #include "launch.h"
 
@@ -65,14 +65,14 @@ struct PgEntry {     // 32 bytes, read as two int4
     int tl;          // first tile after those
     int ntiles;      // tiles of the entry (at least 1)
 };
-struct PgPlanHead {
-    long long q;  // units of a CTA, the first `rem` of the `g` CTAs with work take one more
-    int rem, g;
+struct PgStart {     // where a CTA starts: 48 bytes, read as three int4
+    int ei, h, t;    // entry, kv head, tile
+    int left;        // units of the CTA (0: nothing to do)
+    PgEntry e;       // entry ei
 };
 // One class of entries (small: few rows; large: tensor-memory tiles): device arrays.
 struct PgPlan {
-    PgPlanHead *head;
-    int4 *ctab;        // [G] where each CTA starts: entry, head, tile
+    PgStart *start;    // [G]
     int4 *cmb;         // [G] what is merged at its start: parts (0: nothing), first token, tokens, head
     PgEntry *ent;
     long long *base;   // first unit of each entry
@@ -91,17 +91,36 @@ struct PagedAttendParams {
     int window, sinks;           // window 0: all earlier keys
     int small_rows;              // sequences with at most this many query rows per kv head are small
     float qscale;                // softmax scale * log2(e)
-    PgPlan small, large;
+    PgPlan small, large;         // cap 0: the class is not used
 };
 constexpr int PG_SROWS = 16;     // rows of a small item
 constexpr int PG_LROWS = 256;    // rows of a large item (two tensor-memory tiles)
 constexpr int PG_PART = 2 + 128; // floats of a row's partial result: max, sum, output
 
+
+// A launch that may start while the kernel before it in the stream still runs
+// (it waits for that kernel's results by itself, pg_wait()).
+template <class... A, class... B>
+cudaError_t launch_early(void (*kern)(A...), dim3 grid, int threads, int smem, cudaStream_t stream, const B &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 cudaError_t launch_paged_plan(const PagedAttendParams &p, cudaStream_t stream);
 cudaError_t launch_paged_small(const PagedAttendParams &p, int q_dtype, int cache_dtype, cudaStream_t stream);
 cudaError_t launch_paged_large(const PagedAttendParams &p, int q_dtype, int cache_dtype, cudaStream_t stream);
 cudaError_t paged_chunk_take_device_error(unsigned *bits, cudaStream_t stream);
-cudaError_t launch_paged_combine(const PagedAttendParams &p, int q_dtype, bool large, cudaStream_t stream);
+cudaError_t launch_paged_combine(const PagedAttendParams &p, int q_dtype, cudaStream_t stream);
 cudaError_t paged_attend_take_device_error(unsigned *bits, cudaStream_t stream);
 
 // Tensor map of pages [rows, 128]: 16-bit boxes of 64 columns, 8-bit boxes of

@@ -103,16 +103,15 @@ vq_status status_of(cudaError_t e) { return e == cudaSuccess ? VQ_OK : VQ_ERR_CU
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-    size_t head, ctab, cmb, ent, base, part, end;
+    size_t start, cmb, ent, base, part, end;
 };
 
 // One class of entries from byte `at`; cap 0: the class is not used.
 Layout layout(size_t at, int cap, int G, int rows)
 {
     Layout l;
-    l.head = at;
-    l.ctab = l.head + up(sizeof(PgPlanHead));
-    l.cmb = l.ctab + up(cap ? sizeof(int4) * G : 0);
+    l.start = at;
+    l.cmb = l.start + up(cap ? sizeof(PgStart) * G : 0);
     l.ent = l.cmb + up(cap ? sizeof(int4) * G : 0);
     l.base = l.ent + up(sizeof(PgEntry) * (size_t)cap);
     l.part = l.base + up(sizeof(long long) * (size_t)cap);
@@ -156,8 +155,7 @@ vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, AttendPlan &pl)
 
 void place(PgPlan &d, unsigned char *ws, const Layout &l, int cap, int G, int tq)
 {
-    d.head = reinterpret_cast<PgPlanHead *>(ws + l.head);
-    d.ctab = reinterpret_cast<int4 *>(ws + l.ctab);
+    d.start = reinterpret_cast<PgStart *>(ws + l.start);
     d.cmb = reinterpret_cast<int4 *>(ws + l.cmb);
     d.ent = reinterpret_cast<PgEntry *>(ws + l.ent);
     d.base = reinterpret_cast<long long *>(ws + l.base);
@@ -328,8 +326,7 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
     cudaError_t e = launch_paged_plan(p, s);
     if (e == cudaSuccess && pl.large_cap) e = launch_paged_large(p, q_dtype, cache_dtype, s);
     if (e == cudaSuccess && pl.small_cap) e = launch_paged_small(p, q_dtype, cache_dtype, s);
-    if (e == cudaSuccess && pl.large_cap) e = launch_paged_combine(p, q_dtype, true, s);
-    if (e == cudaSuccess && pl.small_cap) e = launch_paged_combine(p, q_dtype, false, s);
+    if (e == cudaSuccess) e = launch_paged_combine(p, q_dtype, s);
     return status_of(e);
 }
 

@@ -35,6 +35,7 @@ constexpr float NEG_INF = -__builtin_huge_valf();
 // ---------------------------------------------------------------- the plan
 
 constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_KEPT = 1024;  // entries whose sums stay in shared memory
 
 // Exclusive sum over the block; `total` gets the sum of all.
 __device__ __forceinline__ long long block_scan(long long v, long long *ws, long long &total)
@@ -87,6 +88,11 @@ __device__ __forceinline__ PgEntry make_entry(const PagedAttendParams &p, int b,
 __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __grid_constant__ PagedAttendParams p)
 {
     __shared__ long long ws[32];
+    // units before, and tiles of, the first entries of each class (later ones
+    // are read back from memory)
+    __shared__ long long s_base[2][PLAN_KEPT];
+    __shared__ int s_nt[2][PLAN_KEPT];
+    pg_go();
     const int lane = threadIdx.x & 31;
     const int cap_len = (int)min((long long)p.max_pages << p.c.page_shift, 0x7fffffffLL);
     long long carry = 0;  // entries so far: small in the low half, large in the high one
@@ -112,8 +118,14 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
         // sequences of one entry write it themselves, a warp writes those of more
         auto put = [&](int b_, int start_, int n_, int len_, bool large_, int first_, int i) {
             const PgPlan &pl = large_ ? p.large : p.small;
-            if (first_ + i < pl.cap) pl.ent[first_ + i] = make_entry(p, b_, start_, n_, len_, pl.tq, i);
-            else atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+            const int at = first_ + i;
+            if (at >= pl.cap) {
+                atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+                return;
+            }
+            const PgEntry e = make_entry(p, b_, start_, n_, len_, pl.tq, i);
+            pl.ent[at] = e;
+            if (at < PLAN_KEPT) s_nt[large_][at] = e.ntiles;
         };
         if (cnt == 1) put(b, start, n, len, large, first, 0);
         unsigned many = __ballot_sync(FULL_MASK, cnt > 1);
@@ -128,45 +140,57 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
         }
     }
     __syncthreads();
-#pragma unroll
     for (int k = 0; k < 2; ++k) {
         const PgPlan &pl = k ? p.large : p.small;
         if (pl.cap == 0) continue;
         const int nent = min(pl.cap, (int)(k ? carry >> 32 : carry & 0xffffffffLL));
+        auto tiles = [&](int i) { return i < PLAN_KEPT ? s_nt[k][i] : pl.ent[i].ntiles; };
+        auto base = [&](int i) { return i < PLAN_KEPT ? s_base[k][i] : pl.base[i]; };
         long long total = 0;
         for (int i0 = 0; i0 < nent; i0 += PLAN_THREADS) {
             const int i = i0 + threadIdx.x;
-            const long long u = i < nent ? (long long)pl.ent[i].ntiles * p.Hkv : 0;
+            const long long u = i < nent ? (long long)tiles(i) * p.Hkv : 0;
             long long all;
             const long long before = block_scan(u, ws, all);
-            if (i < nent) pl.base[i] = total + before;
+            if (i < nent) {
+                if (i < PLAN_KEPT) s_base[k][i] = total + before;
+                else pl.base[i] = total + before;
+            }
             total += all;
         }
         __syncthreads();
-        PgPlanHead h;
-        h.g = (int)min((long long)pl.G, total);
-        h.q = h.g ? total / h.g : 0;
-        h.rem = h.g ? (int)(total % h.g) : 0;
-        if (threadIdx.x == 0) *pl.head = h;
-        for (int c = threadIdx.x; c < h.g; c += PLAN_THREADS) {
-            const long long u = pg_first_unit(h, c);
-            int a = 0, z = nent - 1;  // the last entry that starts at or before u
-            while (a < z) {
-                const int m = (a + z + 1) >> 1;
-                if (pl.base[m] <= u) a = m;
-                else z = m - 1;
+        // even shares: the first `rem` CTAs take one unit more
+        const int g = (int)min((long long)pl.G, total);
+        const long long q = g ? total / g : 0;
+        const int rem = g ? (int)(total - q * g) : 0;
+        auto unit = [&](int c) { return q * c + min(c, rem); };
+        for (int c = threadIdx.x; c < pl.G; c += PLAN_THREADS) {
+            PgStart st = {};
+            int4 m = make_int4(0, 0, 0, 0);
+            if (c < g) {
+                const long long u = unit(c);
+                int a = 0, z = nent - 1;  // the last entry that starts at or before u
+                while (a < z) {
+                    const int mid = (a + z + 1) >> 1;
+                    if (base(mid) <= u) a = mid;
+                    else z = mid - 1;
+                }
+                st.e = pl.ent[a];
+                const int r = (int)(u - base(a)), nt = st.e.ntiles;
+                st.ei = a;
+                st.h = r / nt;
+                st.t = r - st.h * nt;
+                st.left = (int)(unit(c + 1) - u);
+                // the merge at this CTA's start: of the item it enters in its
+                // middle, if no earlier CTA does so
+                if (st.t > 0 && st.t <= u - unit(c - 1)) {
+                    int parts = 2;
+                    while (c + parts - 1 < g && unit(c + parts - 1) < u - st.t + nt) ++parts;
+                    m = make_int4(parts, st.e.tok0, st.e.nt, st.h);
+                }
             }
-            const int r = (int)(u - pl.base[a]), nt = pl.ent[a].ntiles;
-            const int head_ = r / nt, t = r % nt;
-            pl.ctab[c] = make_int4(a, head_, t, 0);
-            // the merge at this CTA's start: of the item it enters in its
-            // middle, if no earlier CTA does so
-            int parts = 0;
-            if (t > 0 && t <= u - pg_first_unit(h, c - 1)) {
-                parts = 2;
-                while (c + parts - 1 < h.g && pg_first_unit(h, c + parts - 1) < u - t + nt) ++parts;
-            }
-            pl.cmb[c] = make_int4(parts, pl.ent[a].tok0, pl.ent[a].nt, head_);
+            pl.start[c] = st;
+            pl.cmb[c] = m;
         }
     }
 }
@@ -189,26 +213,34 @@ template <> __device__ __forceinline__ uint2 pack4<__nv_bfloat16>(float4 v)
 
 // Block c merges the item that CTA c enters in its middle, if no earlier CTA
 // does so: its parts are the second slot of CTA c - 1 and the first slots of c,
-// c + 1, ..., in that order on every run.  A warp takes a row.
-template <class T, int ROWS, int HALF>
+// c + 1, ..., in that order on every run.  A warp takes a row; the blocks of
+// large items come first, then those of small ones.
+template <class T>
 __global__ void __launch_bounds__(32 * CB_ROWS) paged_combine_kernel(const __grid_constant__ PagedAttendParams p)
 {
-    const PgPlan &pl = HALF ? p.large : p.small;
+    pg_wait();
+    constexpr int LARGE = PG_LROWS / CB_ROWS;
+    const int first_small = p.large.cap ? LARGE : 0;
+    const bool large = (int)blockIdx.y < first_small;
+    const PgPlan &pl = large ? p.large : p.small;
     const int c = blockIdx.x;
-    if (c >= pl.head->g) return;
     const int4 at = pl.cmb[c];
     const int parts = at.x;
     if (parts == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int RT = HALF ? 128 : ROWS;  // rows of one tile of queries
+    const int ROWS = large ? PG_LROWS : PG_SROWS, RT = large ? 128 : PG_SROWS;  // rows of a slot, of a query tile
     const int tqt = RT / p.GQ;
     const size_t slot = (size_t)ROWS * PG_PART;
-    const int r = blockIdx.y * CB_ROWS + warp;
-    const int tok = (r / RT) * tqt + (r % RT) / p.GQ, g = (r % RT) % p.GQ;
-    if (r % RT >= tqt * p.GQ || tok >= at.z) return;
-    auto at_part = [&](int k) { return pl.part + (size_t)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c + k - 1)) * slot; };
+    const int r = ((int)blockIdx.y - (large ? 0 : first_small)) * CB_ROWS + warp;
+    const int half = r >= RT ? 1 : 0, rr = r - half * RT;
+    const int tok = half * tqt + rr / p.GQ, g = rr % p.GQ;
+    if (rr >= tqt * p.GQ || tok >= at.z) return;
+    const float *first = pl.part + (size_t)(2 * c - 1) * slot;
+    auto at_part = [&](int k) { return first + (size_t)(2 * k - (k > 0 ? 1 : 0)) * slot; };
+    // (a lane past the last part takes the last once more: a loop that left lanes
+    // out by its bound was seen to read past it, see the test of 119 parts)
     float M = NEG_INF;
-    for (int k = lane; k < parts; k += 32) M = fmaxf(M, at_part(k)[r]);
+    for (int k = 0; k < parts; k += 32) M = fmaxf(M, at_part(min(k + lane, parts - 1))[r]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
     float L = 0.0f;
@@ -328,14 +360,15 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, fl
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A pair of e4m3 codes as a pair of T (exact: both types hold every code).
-template <class T> __device__ __forceinline__ uint32_t codes2(uint32_t two);
-template <> __device__ __forceinline__ uint32_t codes2<__half>(uint32_t two) { return e4m3x2_to_f16x2(two); }
-template <> __device__ __forceinline__ uint32_t codes2<__nv_bfloat16>(uint32_t two)
+// Four e4m3 codes as two pairs of T (exact: both types hold every code).
+template <class T> __device__ __forceinline__ void codes4(uint32_t four, uint32_t &lo, uint32_t &hi);
+template <> __device__ __forceinline__ void codes4<__half>(uint32_t four, uint32_t &lo, uint32_t &hi)
 {
-    const uint32_t h2 = e4m3x2_to_f16x2(two);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-    return pack2<__nv_bfloat16>(f.x, f.y);
+    e4m3x4_to_f16x4(four, lo, hi);
+}
+template <> __device__ __forceinline__ void codes4<__nv_bfloat16>(uint32_t four, uint32_t &lo, uint32_t &hi)
+{
+    e4m3x4_to_bf16x4(four, 0x7b807b80u, lo, hi);  // 2^120
 }
 
 // T: query and output type; Q8: e4m3 cache (values are then taken as fp16)
@@ -351,9 +384,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
     unsigned char *exps = reinterpret_cast<unsigned char *>(stat + L::WARPS * L::ROWS);
     uint64_t *full = reinterpret_cast<uint64_t *>(exps + L::STAGES * L::EXP), *empty = full + L::STAGES;
 
-    const PgPlanHead head = *p.small.head;
     const int c = blockIdx.x;
-    if (c >= head.g) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::STAGES; ++s) {
@@ -363,9 +394,16 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
         fence_mbar_init();
     }
     __syncthreads();
-
+    // Alone, this kernel follows the plan: wait for it.  After the large kernel
+    // it starts when that one's CTAs run, which had waited for the plan; it then
+    // waits at its end, so that the merge after it comes after both.
+    if (p.large.cap == 0) pg_wait();
+    pg_go();
     PgRun r;
-    r.start(p.small, head, c);
+    if (!r.start(p.small, c)) {
+        if (p.large.cap != 0) pg_wait();
+        return;
+    }
     PgRing<L::STAGES> ring;
 
     if (warp >= L::WARPS) {
@@ -425,6 +463,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
             const int j = tiles - 1 - k;
             (void)mbar_wait_bounded(&full[j % L::STAGES], (uint32_t)(j / L::STAGES) & 1u);
         }
+        if (p.large.cap != 0) pg_wait();
         return;
     }
 
@@ -505,8 +544,9 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                         const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xb[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const uint32_t a0 = codes2<T>(xa[j] & 0xffffu), a1 = codes2<T>(xb[j] & 0xffffu);
-                            const uint32_t a2 = codes2<T>(xa[j] >> 16), a3 = codes2<T>(xb[j] >> 16);
+                            uint32_t a0, a1, a2, a3;
+                            codes4<T>(xa[j], a0, a2);
+                            codes4<T>(xb[j], a1, a3);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
                                 mma16<T>(s[nt], a0, a1, a2, a3, qf[nt][8 * q + 2 * j], qf[nt][8 * q + 2 * j + 1]);
@@ -603,9 +643,12 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                         ldsm_x4_t(vbase + swz128(vkey, n + vc), x);
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const uint32_t lo = __byte_perm(x[2 * q], 0u, 0x3120), hi = __byte_perm(x[2 * q + 1], 0u, 0x3120);
-                            const uint32_t a0 = codes2<TV>(lo & 0xffffu) & ka, a1 = codes2<TV>(lo >> 16) & ka;
-                            const uint32_t a2 = codes2<TV>(hi & 0xffffu) & kb, a3 = codes2<TV>(hi >> 16) & kb;
+                            // (a hidden key's codes become zero: the halves of x are keys here)
+                            const uint32_t lo = __byte_perm(x[2 * q] & ka, 0u, 0x3120);
+                            const uint32_t hi = __byte_perm(x[2 * q + 1] & kb, 0u, 0x3120);
+                            uint32_t a0, a1, a2, a3;
+                            codes4<TV>(lo, a0, a1);
+                            codes4<TV>(hi, a2, a3);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) mma16<TV>(o[nt][n + q], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
                         }
@@ -697,6 +740,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
             }
         }
     } while (r.next(p.small, p.Hkv));
+    if (p.large.cap != 0) pg_wait();
 }
 
 template <class T, bool Q8, int NT>
@@ -706,8 +750,7 @@ cudaError_t launch_small(const PagedAttendParams &p, cudaStream_t stream)
     constexpr int smem = SmShape<Q8, NT>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<p.small.G, SmShape<Q8, NT>::THREADS, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(kern, dim3(p.small.G), SmShape<Q8, NT>::THREADS, smem, stream, p);
 }
 
 template <class T, bool Q8>
@@ -736,17 +779,12 @@ cudaError_t launch_paged_small(const PagedAttendParams &p0, int q_dtype, int cac
     return q8 ? dispatch_small<__nv_bfloat16, true>(p, stream) : dispatch_small<__nv_bfloat16, false>(p, stream);
 }
 
-cudaError_t launch_paged_combine(const PagedAttendParams &p, int q_dtype, bool large, cudaStream_t stream)
+cudaError_t launch_paged_combine(const PagedAttendParams &p, int q_dtype, cudaStream_t stream)
 {
-    const dim3 grid(large ? p.large.G : p.small.G, (large ? PG_LROWS : PG_SROWS) / CB_ROWS);
-    if (q_dtype == VQ_F16) {
-        if (large) paged_combine_kernel<__half, PG_LROWS, 1><<<grid, 32 * CB_ROWS, 0, stream>>>(p);
-        else paged_combine_kernel<__half, PG_SROWS, 0><<<grid, 32 * CB_ROWS, 0, stream>>>(p);
-    } else {
-        if (large) paged_combine_kernel<__nv_bfloat16, PG_LROWS, 1><<<grid, 32 * CB_ROWS, 0, stream>>>(p);
-        else paged_combine_kernel<__nv_bfloat16, PG_SROWS, 0><<<grid, 32 * CB_ROWS, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
+    const dim3 grid(p.large.cap ? p.large.G : p.small.G,
+                    ((p.large.cap ? PG_LROWS : 0) + (p.small.cap ? PG_SROWS : 0)) / CB_ROWS);
+    return launch_early(q_dtype == VQ_F16 ? paged_combine_kernel<__half> : paged_combine_kernel<__nv_bfloat16>, grid,
+                        32 * CB_ROWS, 0, stream, p);
 }
 
 cudaError_t paged_attend_take_device_error(unsigned *bits, cudaStream_t stream)

@@ -25,7 +25,6 @@ namespace {
 
 VQ_DEFINE_ERROR_WORD(g_pc_err);
 
-constexpr int D = 128;
 constexpr int THREADS = 256;
 
 template <class T> struct Pair;

@@ -234,7 +234,8 @@ template <class T> __device__ __forceinline__ void ck_operand(uint32_t four, uin
 template <>
 __device__ __forceinline__ void ck_operand<__half>(uint32_t four, uint32_t f, uint32_t &lo, uint32_t &hi)
 {
-    const uint32_t a = e4m3x2_to_f16x2(four & 0xffffu), b = e4m3x2_to_f16x2(four >> 16);
+    uint32_t a, b;
+    e4m3x4_to_f16x4(four, a, b);
     const __half2 g = *reinterpret_cast<const __half2 *>(&f);
     const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&a), g), y = __hmul2(*reinterpret_cast<const __half2 *>(&b), g);
     lo = *reinterpret_cast<const uint32_t *>(&x);
@@ -243,15 +244,7 @@ __device__ __forceinline__ void ck_operand<__half>(uint32_t four, uint32_t f, ui
 template <>
 __device__ __forceinline__ void ck_operand<__nv_bfloat16>(uint32_t four, uint32_t f, uint32_t &lo, uint32_t &hi)
 {
-    // sign, exponent and fraction of a code in a bf16's places: value * 2^-120,
-    // subnormal codes as subnormal bf16 (the product takes those)
-    const uint32_t h0 = __byte_perm(four, 0u, 0x1404), h1 = __byte_perm(four, 0u, 0x3424);
-    const uint32_t a = ((h0 >> 4) & 0x07f007f0u) | (h0 & 0x80008000u), b = ((h1 >> 4) & 0x07f007f0u) | (h1 & 0x80008000u);
-    const __nv_bfloat162 g = *reinterpret_cast<const __nv_bfloat162 *>(&f);
-    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), g);
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&b), g);
-    lo = *reinterpret_cast<const uint32_t *>(&x);
-    hi = *reinterpret_cast<const uint32_t *>(&y);
+    e4m3x4_to_bf16x4(four, f, lo, hi);
 }
 
 // Largest of the bytes that the lanes of a warp hold.
@@ -268,9 +261,6 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     using TV = typename std::conditional<Q8, __half, T>::type;  // weights and values
     constexpr int STAGES = C::STAGES;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value, BFV = std::is_same<TV, __nv_bfloat16>::value;
-    const PgPlanHead head = *p.large.head;
-    if ((int)blockIdx.x >= head.g) return;
-
     extern __shared__ __align__(128) unsigned char smem_raw[];
     unsigned char *sq = smem_1k(smem_raw);                  // two query tiles
     unsigned char *skv = sq + 2 * TILE_B;                   // key / value tiles
@@ -315,6 +305,10 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         *abort_flag = 0u;
         fence_mbar_init();
     }
+    pg_wait();  // for the plan
+    pg_go();
+    PgRun r;
+    if (!r.start(p.large, blockIdx.x)) return;  // the whole CTA
     if (warp == 9) tmem_alloc(const_cast<uint32_t *>(tslot), 512);
     qt_fence_before();
     __syncthreads();
@@ -335,9 +329,6 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
             }
         }
     };
-
-    PgRun r;
-    r.start(p.large, head, blockIdx.x);
 
     if (warp >= 8 && warp < 12) {
     ck_reg_dec<C::R_CTL>();
@@ -864,8 +855,7 @@ cudaError_t launch_chunk(const PagedAttendParams &p, cudaStream_t stream)
     e = cudaFuncGetAttributes(&at, kern);
     if (e != cudaSuccess) return e;
     if (at.numRegs != CkShape<Q8>::REGS) return cudaErrorLaunchOutOfResources;
-    kern<<<p.large.G, CkShape<Q8>::THREADS, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(kern, dim3(p.large.G), CkShape<Q8>::THREADS, smem, stream, p);
 }
 
 }  // namespace

@@ -2,6 +2,7 @@
 // powers of two, the walk over a launch's units of work.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "device_common.cuh"
@@ -21,6 +22,28 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)
     return r;
 }
 
+// Four codes as two fp16 pairs; exact.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+}
+
+// Four codes as two bf16 pairs times f / 2^120 (a bf16 twice): sign, exponent
+// and fraction moved to a bf16's places give value * 2^-120, subnormal codes as
+// subnormal bf16, which the product takes.
+__device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t four, uint32_t f, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t h0 = __byte_perm(four, 0u, 0x1404), h1 = __byte_perm(four, 0u, 0x3424);
+    const uint32_t a = ((h0 >> 4) & 0x07f007f0u) | (h0 & 0x80008000u), b = ((h1 >> 4) & 0x07f007f0u) | (h1 & 0x80008000u);
+    const __nv_bfloat162 g = *reinterpret_cast<const __nv_bfloat162 *>(&f);
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), g);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&b), g);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -37,8 +60,11 @@ __device__ __forceinline__ bool elect_lane()
     return e != 0;
 }
 
-// First unit of CTA c: an even share, the first `rem` CTAs take one more.
-__device__ __forceinline__ long long pg_first_unit(const PgPlanHead &h, int c) { return h.q * c + min(c, h.rem); }
+// Programmatic launch order: pg_wait() until the kernel before in the stream is
+// complete and its writes are seen, pg_go() lets the next one start early (it
+// takes the SMs as they become free).
+__device__ __forceinline__ void pg_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pg_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Barrier of the first THREADS threads of the CTA.
 template <int THREADS> __device__ __forceinline__ void bar_compute()
@@ -62,7 +88,7 @@ struct PgView {
 
 __device__ __forceinline__ PgEntry pg_entry(const PgEntry *e)
 {
-    const int4 a = __ldg(reinterpret_cast<const int4 *>(e)), b = __ldg(reinterpret_cast<const int4 *>(e) + 1);
+    const int4 a = *reinterpret_cast<const int4 *>(e), b = *(reinterpret_cast<const int4 *>(e) + 1);
     PgEntry r;
     r.b = a.x; r.tok0 = a.y; r.nt = a.z; r.p0 = a.w;
     r.hi = b.x; r.nsink = b.y; r.tl = b.z; r.ntiles = b.w;
@@ -80,16 +106,17 @@ struct PgRun {
     PgEntry e;
     int ei, h, t0, tn, left;
     bool first;  // the CTA's first run
-    __device__ __forceinline__ void start(const PgPlan &pl, const PgPlanHead &head, int c)
+    __device__ __forceinline__ bool start(const PgPlan &pl, int c)  // false: nothing to do
     {
-        const int4 at = __ldg(pl.ctab + c);
+        const int4 at = *reinterpret_cast<const int4 *>(pl.start + c);
+        e = pg_entry(&pl.start[c].e);
         ei = at.x;
         h = at.y;
         t0 = at.z;
-        left = (int)(pg_first_unit(head, c + 1) - pg_first_unit(head, c));
-        e = pg_entry(pl.ent + ei);
+        left = at.w;
         tn = min(e.ntiles, t0 + left);
         first = true;
+        return left > 0;
     }
     __device__ __forceinline__ bool next(const PgPlan &pl, int Hkv)
     {

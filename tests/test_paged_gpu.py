@@ -292,7 +292,8 @@ def test_window_and_first_tokens(vq, dtype, cache, window, sinks):
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
 def test_one_long_sequence_is_split_and_joined(vq, dtype, cache):
-    """One sequence over every CTA, single token and chunk, with and without window."""
+    """One sequence over every CTA, single token and chunk, with and without
+    window (71, 80 and 119 parts to join)."""
     _check(vq, _case(vq, [1], [9001], 1, 4, 64, dtype, cache, seed=31))
     _check(vq, _case(vq, [3], [5003], 2, 5, 16, dtype, cache, seed=32))
     _check(vq, _case(vq, [1], [20000], 1, 8, 128, dtype, cache, window=15000, sinks=4, seed=33))
