@@ -424,10 +424,17 @@ def vq_flush_decode(k, v, residual_length: int, dst_off=None, S_dst=None, rvq=No
     return out
 
 
+# The paged calls run once per layer and step, so the checks below are written to
+# cost little: plain comparisons, no copies, the stream's handle without an object.
+_DTYPE_CODES: dict = {}
+
+
 def _dtype_code(dtype) -> int:
     """VQ_F16, VQ_BF16 or VQ_E4M3 of a torch dtype (ValueError for others)."""
-    import torch
-    code = {torch.float16: VQ_F16, torch.bfloat16: VQ_BF16, torch.float8_e4m3fn: VQ_E4M3}.get(dtype)
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.float16: VQ_F16, torch.bfloat16: VQ_BF16, torch.float8_e4m3fn: VQ_E4M3})
+    code = _DTYPE_CODES.get(dtype)
     if code is None:
         raise ValueError("dtype %s: float16, bfloat16 or float8_e4m3fn" % dtype)
     return code
@@ -435,14 +442,29 @@ def _dtype_code(dtype) -> int:
 
 def _typed(t, dtype, shape, what):
     """Raise ValueError unless t is a contiguous CUDA tensor of this dtype and shape."""
-    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s: a contiguous CUDA tensor %s of %s" % (what, tuple(shape), dtype))
+    return t.data_ptr()
 
 
-def _rows_view(t, heads, what):
-    """Checks a [T, heads, 128] view whose last dimension is contiguous."""
-    if not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError("%s: a CUDA tensor [tokens, %d, D] with contiguous rows" % (what, heads))
+def _rows_view(t, heads, D, what):
+    """(address, token stride, head stride) of a [T, heads, D] view whose rows are contiguous."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D or not t.is_cuda:
+        raise ValueError("%s: a CUDA tensor [tokens, %d, %d]" % (what, heads, D))
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError("%s: the entries of a head have to be contiguous" % what)
+    return t.data_ptr(), st[0], st[1]
+
+
+def _raw_stream(stream, t):
+    """The handle of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(t.device.index) if raw is not None else torch.cuda.current_stream().cuda_stream
 
 
 def _use(stream, *tensors):
@@ -470,22 +492,20 @@ def paged_cache(num_pages: int, Hkv: int, page_size: int, dtype, device="cuda", 
 
 def _cache_args(cache):
     """(k, v, k_exp, v_exp, dtype, num_pages, Hkv, page_size, D) of a cache dict."""
-    import torch
     k, v = cache["k_pages"], cache["v_pages"]
-    if k.dim() != 4:
+    dtype, shape = k.dtype, k.shape
+    code = _dtype_code(dtype)
+    if len(shape) != 4:
         raise ValueError("k_pages: [num_pages, Hkv, page_size, D]")
-    code = _dtype_code(k.dtype)
-    _typed(k, k.dtype, k.shape, "k_pages")
-    _typed(v, k.dtype, k.shape, "v_pages")
-    ke, ve = cache.get("k_exp"), cache.get("v_exp")
+    kp, vp = _typed(k, dtype, shape, "k_pages"), _typed(v, dtype, shape, "v_pages")
+    ke = ve = None
     if code == VQ_E4M3:
+        import torch
+        ke, ve = cache.get("k_exp"), cache.get("v_exp")
         if ke is None or ve is None:
             raise ValueError("a float8_e4m3fn cache has k_exp and v_exp")
-        _typed(ke, torch.uint8, k.shape[:3], "k_exp")
-        _typed(ve, torch.uint8, k.shape[:3], "v_exp")
-    else:
-        ke = ve = None
-    return (_ptr(k), _ptr(v), _ptr(ke), _ptr(ve), code) + tuple(k.shape)
+        ke, ve = _typed(ke, torch.uint8, shape[:3], "k_exp"), _typed(ve, torch.uint8, shape[:3], "v_exp")
+    return (kp, vp, ke, ve, code, *shape)
 
 
 def vq_paged_append(k, v, cache: dict, slots, stream=None) -> dict:
@@ -495,15 +515,11 @@ def vq_paged_append(k, v, cache: dict, slots, stream=None) -> dict:
     import torch
     args = _cache_args(cache)
     T = k.shape[0]
-    if k.shape != v.shape or k.dtype != v.dtype:
-        raise ValueError("k and v: the same shape and dtype")
-    _rows_view(k, args[6], "k")
-    _rows_view(v, args[6], "v")
-    _typed(slots, torch.int64, (T,), "slots")
-    if k.shape[2] != args[8]:
-        raise ValueError("k: head width %d" % args[8])
-    _check(lib().vq_paged_append(_ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1),
-                                 _dtype_code(k.dtype), T, _ptr(slots), *args, _stream(stream)), "vq_paged_append")
+    if k.dtype != v.dtype or v.shape[0] != T:
+        raise ValueError("k and v: the same tokens and dtype")
+    views = _rows_view(k, args[6], args[8], "k") + _rows_view(v, args[6], args[8], "v")
+    _check(lib().vq_paged_append(*views, _dtype_code(k.dtype), T, _typed(slots, torch.int64, (T,), "slots"), *args,
+                                 _raw_stream(stream, k)), "vq_paged_append")
     return cache
 
 
@@ -514,30 +530,30 @@ def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtyp
     cache), zeros past lens[b].  block_table [B, max_pages], lens and first [B] int32."""
     import torch
     args = _cache_args(cache)
+    i32 = torch.int32
     B, max_pages = block_table.shape
-    _typed(block_table, torch.int32, (B, max_pages), "block_table")
-    _typed(lens, torch.int32, (B,), "lens")
-    if first is not None:
-        _typed(first, torch.int32, (B,), "first")
+    table = _typed(block_table, i32, (B, max_pages), "block_table")
     if dtype is None:
         dtype = torch.float16 if args[4] == VQ_E4M3 else cache["k_pages"].dtype
     shape = (B, args[6], S_out, args[8])
     dev = block_table.device
     made = []
-    if want_k and k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=dev)
-        made.append(k_out)
-    if want_v and v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=dev)
-        made.append(v_out)
-    for t, want in ((k_out, want_k), (v_out, want_v)):
-        if want:
-            _typed(t, dtype, shape, "k_out, v_out")
-    _check(lib().vq_paged_gather(*args, _ptr(block_table), max_pages, _ptr(lens), _ptr(first), B, S_out,
-                                 _dtype_code(dtype), _ptr(k_out) if want_k else None,
-                                 _ptr(v_out) if want_v else None, _stream(stream)), "vq_paged_gather")
+    ptrs = [None, None]
+    outs = [k_out if want_k else None, v_out if want_v else None]
+    for i, want in enumerate((want_k, want_v)):
+        if not want:
+            continue
+        if outs[i] is None:
+            outs[i] = torch.empty(shape, dtype=dtype, device=dev)
+            made.append(outs[i])
+            ptrs[i] = outs[i].data_ptr()
+        else:
+            ptrs[i] = _typed(outs[i], dtype, shape, "k_out, v_out")
+    _check(lib().vq_paged_gather(*args, table, max_pages, _typed(lens, i32, (B,), "lens"),
+                                 None if first is None else _typed(first, i32, (B,), "first"), B, S_out,
+                                 _dtype_code(dtype), *ptrs, _raw_stream(stream, block_table)), "vq_paged_gather")
     _use(stream, *made)
-    return (k_out if want_k else None), (v_out if want_v else None)
+    return outs[0], outs[1]
 
 
 def vq_paged_attend_workspace(T: int, B: int, Hq: int, Hkv: int, max_q: int) -> int:
@@ -545,6 +561,9 @@ def vq_paged_attend_workspace(T: int, B: int, Hq: int, Hkv: int, max_q: int) -> 
     n = ctypes.c_size_t(0)
     _check(lib().vq_paged_attend_workspace(T, B, Hq, Hkv, max_q, ctypes.byref(n)), "vq_paged_attend_workspace")
     return int(n.value)
+
+
+_workspace_bytes: dict = {}  # sizes by shape and device: the call's own arithmetic, repeated every step
 
 
 def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q: int, window: int = 0, sinks: int = 0,
@@ -557,27 +576,33 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
     [T, Hq, 128] of q's dtype; the workspace (uint8) is allocated when not given."""
     import torch
     args = _cache_args(cache)
+    i32 = torch.int32
     B, max_pages = block_table.shape
     T, Hq, _ = q.shape
-    _rows_view(q, Hq, "q")
-    if q.shape[2] != args[8]:
-        raise ValueError("q: head width %d" % args[8])
-    _typed(block_table, torch.int32, (B, max_pages), "block_table")
-    _typed(cu_q, torch.int32, (B + 1,), "cu_q")
-    _typed(lens, torch.int32, (B,), "lens")
+    D, dtype, dev = args[8], q.dtype, q.device
+    view = _rows_view(q, Hq, D, "q")
+    table = _typed(block_table, i32, (B, max_pages), "block_table")
+    cu, ln = _typed(cu_q, i32, (B + 1,), "cu_q"), _typed(lens, i32, (B,), "lens")
     made = []
     if out is None:
-        out = torch.empty((T, Hq, args[8]), dtype=q.dtype, device=q.device)
+        out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
         made.append(out)
+        po = out.data_ptr()
     else:
-        _typed(out, q.dtype, (T, Hq, args[8]), "out")
+        po = _typed(out, dtype, (T, Hq, D), "out")
     if workspace is None:
-        workspace = torch.empty(max(vq_paged_attend_workspace(T, B, Hq, args[6], max_q), 16), dtype=torch.uint8,
-                                device=q.device)
+        key = (T, B, Hq, args[6], max_q, dev.index)
+        wb = _workspace_bytes.get(key)
+        if wb is None:
+            if len(_workspace_bytes) > 4096:
+                _workspace_bytes.clear()
+            wb = _workspace_bytes[key] = vq_paged_attend_workspace(T, B, Hq, args[6], max_q)
+        workspace = torch.empty(max(wb, 16), dtype=torch.uint8, device=dev)
         made.append(workspace)
-    _check(lib().vq_paged_attend(_ptr(q), q.stride(0), q.stride(1), _dtype_code(q.dtype), *args, _ptr(block_table),
-                                 max_pages, _ptr(cu_q), _ptr(lens), T, B, Hq, max_q, window, sinks, float(scale),
-                                 _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                 _stream(stream)), "vq_paged_attend")
-    _use(stream, *made)
+    else:
+        wb = workspace.numel() * workspace.element_size()
+    _check(lib().vq_paged_attend(*view, _dtype_code(dtype), *args, table, max_pages, cu, ln, T, B, Hq, max_q, window, sinks,
+                                 scale, po, workspace.data_ptr(), wb, _raw_stream(stream, q)), "vq_paged_attend")
+    if stream is not None:
+        _use(stream, *made)
     return out
