@@ -323,7 +323,8 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
     place(p.small, ws, pl.s, pl.small_cap, pl.G, pl.small_tq);
     place(p.large, ws, pl.l, pl.large_cap, pl.G, pl.large_tq);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_paged_plan(p, s);
+    // (a call of small sequences alone: its kernel makes the plan)
+    cudaError_t e = pl.large_cap ? launch_paged_plan(p, s) : cudaSuccess;
     if (e == cudaSuccess && pl.large_cap) e = launch_paged_large(p, q_dtype, cache_dtype, s);
     if (e == cudaSuccess && pl.small_cap) e = launch_paged_small(p, q_dtype, cache_dtype, s);
     if (e == cudaSuccess) e = launch_paged_combine(p, q_dtype, s);

@@ -83,6 +83,42 @@ __device__ __forceinline__ PgEntry make_entry(const PagedAttendParams &p, int b,
     return e;
 }
 
+// The first query token, the number of new tokens and the length of sequence b,
+// within the buffers whatever the numbers given; false: more tokens than max_q.
+__device__ __forceinline__ bool sequence(const PagedAttendParams &p, int b, int &start, int &n, int &len)
+{
+    const int cap = (int)min((long long)p.max_pages << p.c.page_shift, 0x7fffffffLL);
+    start = min(max(__ldg(p.cu + b), 0), p.T);
+    n = min(max(__ldg(p.cu + b + 1), start), p.T) - start;
+    len = min(max(__ldg(p.lens + b), 0), cap);
+    const bool ok = n <= p.max_q;
+    n = min(n, p.max_q);
+    return ok;
+}
+
+// Even shares of the units: the first `rem` of `g` CTAs take one more than q.
+struct Shares {
+    long long q;
+    int g, rem;
+    __device__ __forceinline__ void set(long long total, int G)
+    {
+        g = (int)min((long long)G, total);
+        q = g ? total / g : 0;
+        rem = g ? (int)(total - q * g) : 0;
+    }
+    __device__ __forceinline__ long long first(int c) const { return q * c + min(c, rem); }
+    // what is merged where CTA c starts, in tile t of nt of an item: the item it
+    // enters in its middle, if no earlier CTA does so
+    __device__ __forceinline__ int parts(int c, int t, int nt) const
+    {
+        const long long u = first(c);
+        if (t == 0 || t > u - first(c - 1)) return 0;
+        int n = 2;
+        while (c + n - 1 < g && first(c + n - 1) < u - t + nt) ++n;
+        return n;
+    }
+};
+
 // One CTA: entries of both classes in the order of the sequences, the units
 // before each, and where each CTA of the attention kernels starts.
 __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __grid_constant__ PagedAttendParams p)
@@ -94,20 +130,11 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
     __shared__ int s_nt[2][PLAN_KEPT];
     pg_go();
     const int lane = threadIdx.x & 31;
-    const int cap_len = (int)min((long long)p.max_pages << p.c.page_shift, 0x7fffffffLL);
     long long carry = 0;  // entries so far: small in the low half, large in the high one
     for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
         const int b = b0 + threadIdx.x;
         int start = 0, n = 0, len = 0;
-        if (b < p.B) {
-            start = min(max(p.cu[b], 0), p.T);
-            n = min(max(p.cu[b + 1], start), p.T) - start;
-            len = min(max(p.lens[b], 0), cap_len);
-            if (n > p.max_q) {
-                atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
-                n = p.max_q;
-            }
-        }
+        if (b < p.B && !sequence(p, b, start, n, len)) atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
         const bool large = n * p.GQ > p.small_rows;
         const int tq = large ? p.large.tq : p.small.tq;
         const int cnt = (n + tq - 1) / tq;
@@ -159,16 +186,13 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
             total += all;
         }
         __syncthreads();
-        // even shares: the first `rem` CTAs take one unit more
-        const int g = (int)min((long long)pl.G, total);
-        const long long q = g ? total / g : 0;
-        const int rem = g ? (int)(total - q * g) : 0;
-        auto unit = [&](int c) { return q * c + min(c, rem); };
+        Shares sh;
+        sh.set(total, pl.G);
         for (int c = threadIdx.x; c < pl.G; c += PLAN_THREADS) {
             PgStart st = {};
             int4 m = make_int4(0, 0, 0, 0);
-            if (c < g) {
-                const long long u = unit(c);
+            if (c < sh.g) {
+                const long long u = sh.first(c);
                 int a = 0, z = nent - 1;  // the last entry that starts at or before u
                 while (a < z) {
                     const int mid = (a + z + 1) >> 1;
@@ -180,14 +204,8 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
                 st.ei = a;
                 st.h = r / nt;
                 st.t = r - st.h * nt;
-                st.left = (int)(unit(c + 1) - u);
-                // the merge at this CTA's start: of the item it enters in its
-                // middle, if no earlier CTA does so
-                if (st.t > 0 && st.t <= u - unit(c - 1)) {
-                    int parts = 2;
-                    while (c + parts - 1 < g && unit(c + parts - 1) < u - st.t + nt) ++parts;
-                    m = make_int4(parts, st.e.tok0, st.e.nt, st.h);
-                }
+                st.left = (int)(sh.first(c + 1) - u);
+                m = make_int4(sh.parts(c, st.t, nt), st.e.tok0, st.e.nt, st.h);
             }
             pl.start[c] = st;
             pl.cmb[c] = m;
@@ -237,25 +255,36 @@ __global__ void __launch_bounds__(32 * CB_ROWS) paged_combine_kernel(const __gri
     if (rr >= tqt * p.GQ || tok >= at.z) return;
     const float *first = pl.part + (size_t)(2 * c - 1) * slot;
     auto at_part = [&](int k) { return first + (size_t)(2 * k - (k > 0 ? 1 : 0)) * slot; };
-    // (a lane past the last part takes the last once more: a loop that left lanes
-    // out by its bound was seen to read past it, see the test of 119 parts)
-    float M = NEG_INF;
-    for (int k = 0; k < parts; k += 32) M = fmaxf(M, at_part(min(k + lane, parts - 1))[r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
-    float L = 0.0f;
+    // eight parts' loads in flight at a time, the maximum followed online
+    float M = NEG_INF, L = 0.0f;
     float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (M > NEG_INF) {
-#pragma unroll 4
-        for (int k = 0; k < parts; ++k) {
-            const float *s = at_part(k);
-            const float f = ex2(s[r] - M);
-            const float4 o = *reinterpret_cast<const float4 *>(s + 2 * ROWS + (size_t)r * D + 4 * lane);
-            L = fmaf(s[ROWS + r], f, L);
-            O.x = fmaf(o.x, f, O.x);
-            O.y = fmaf(o.y, f, O.y);
-            O.z = fmaf(o.z, f, O.z);
-            O.w = fmaf(o.w, f, O.w);
+    constexpr int NP = 8;
+    for (int k0 = 0; k0 < parts; k0 += NP) {
+        float m[NP], l[NP];
+        float4 o[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const float *s = at_part(min(k0 + i, parts - 1));
+            m[i] = s[r];
+            l[i] = s[ROWS + r];
+            o[i] = *reinterpret_cast<const float4 *>(s + 2 * ROWS + (size_t)r * D + 4 * lane);
+        }
+        float N = M;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) N = fmaxf(N, m[i]);
+        if (N == NEG_INF) continue;  // nothing seen so far
+        const float f0 = ex2(M - N);
+        M = N;
+        L *= f0;
+        O.x *= f0; O.y *= f0; O.z *= f0; O.w *= f0;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const float f = k0 + i < parts ? ex2(m[i] - N) : 0.0f;
+            L = fmaf(l[i], f, L);
+            O.x = fmaf(o[i].x, f, O.x);
+            O.y = fmaf(o[i].y, f, O.y);
+            O.z = fmaf(o[i].z, f, O.z);
+            O.w = fmaf(o[i].w, f, O.w);
         }
     }
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
@@ -371,6 +400,71 @@ template <> __device__ __forceinline__ void codes4<__nv_bfloat16>(uint32_t four,
     e4m3x4_to_bf16x4(four, 0x7b807b80u, lo, hi);  // 2^120
 }
 
+// The plan of a call whose sequences are all small, made by every CTA for itself
+// (a kernel for it cost a launch, 4 us before the first copy): the start of CTA c
+// into `ws` as a PgStart, what is merged there into the plan's cmb.  Entries are
+// the sequences with new tokens, `ei` the sequence.
+template <int THREADS> __device__ __forceinline__ void own_plan(const PagedAttendParams &p, int c, long long *ws)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    PgStart *out = reinterpret_cast<PgStart *>(ws);
+    long long *sums = ws + 8;
+    const int per = (p.B + THREADS - 1) / THREADS, b0 = threadIdx.x * per, b1 = min(b0 + per, p.B);
+    long long mine = 0;
+    bool fits = true;
+    for (int b = b0; b < b1; ++b) {
+        int start, n, len;
+        fits = sequence(p, b, start, n, len) && fits;
+        if (n > 0) mine += (long long)make_entry(p, b, start, n, len, p.small.tq, 0).ntiles * p.Hkv;
+    }
+    if (!fits && c == 0) atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+    long long x = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const long long y = __shfl_up_sync(FULL_MASK, x, s);
+        if (lane >= s) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    if (threadIdx.x == 0) out->left = 0;
+    __syncthreads();
+    long long base = x - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) base += sums[w];
+        total += sums[w];
+    }
+    Shares sh;
+    sh.set(total, p.small.G);
+    int4 m = make_int4(0, 0, 0, 0);
+    if (c < sh.g) {
+        const long long u = sh.first(c);
+        if (u >= base && u < base + mine) {  // one thread: the share starts in its sequences
+            for (int b = b0; b < b1; ++b) {
+                int start, n, len;
+                (void)sequence(p, b, start, n, len);
+                if (n == 0) continue;
+                const PgEntry e = make_entry(p, b, start, n, len, p.small.tq, 0);
+                if (u < base + (long long)e.ntiles * p.Hkv) {
+                    PgStart st;
+                    const int r = (int)(u - base);
+                    st.ei = b;
+                    st.h = r / e.ntiles;
+                    st.t = r - st.h * e.ntiles;
+                    st.left = (int)(sh.first(c + 1) - u);
+                    st.e = e;
+                    *out = st;
+                    p.small.cmb[c] = make_int4(sh.parts(c, st.t, e.ntiles), e.tok0, e.nt, st.h);
+                    break;
+                }
+                base += (long long)e.ntiles * p.Hkv;
+            }
+        }
+    } else if (threadIdx.x == 0) {
+        p.small.cmb[c] = m;
+    }
+    __syncthreads();
+}
+
 // T: query and output type; Q8: e4m3 cache (values are then taken as fp16)
 template <class T, bool Q8, int NT>
 __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kernel(const __grid_constant__ PagedAttendParams p)
@@ -394,16 +488,38 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
         fence_mbar_init();
     }
     __syncthreads();
-    // Alone, this kernel follows the plan: wait for it.  After the large kernel
-    // it starts when that one's CTAs run, which had waited for the plan; it then
-    // waits at its end, so that the merge after it comes after both.
-    if (p.large.cap == 0) pg_wait();
+    // Alone, this kernel makes its own plan.  After the large kernel it has that
+    // of the plan kernel: it starts when the large kernel's CTAs run, which had
+    // waited for the plan, and waits at its end, so that the merge after it comes
+    // after both.
+    const bool alone = p.large.cap == 0;
     pg_go();
     PgRun r;
-    if (!r.start(p.small, c)) {
-        if (p.large.cap != 0) pg_wait();
+    if (alone) {
+        own_plan<L::THREADS>(p, c, reinterpret_cast<long long *>(merge));
+        r.start(*reinterpret_cast<const PgStart *>(merge));
+        __syncthreads();
+    } else {
+        r.start(p.small.start[c]);
+    }
+    if (r.left <= 0) {
+        if (!alone) pg_wait();
         return;
     }
+    // the next entry: in a plan's list, or the next sequence with new tokens
+    auto step = [&](PgRun &x) {
+        ++x.ei;
+        if (!alone) {
+            x.e = pg_entry(p.small.ent + x.ei);
+            return;
+        }
+        int start = 0, n = 0, len = 0;
+        for (; x.ei < p.B; ++x.ei) {
+            (void)sequence(p, x.ei, start, n, len);
+            if (n > 0) break;
+        }
+        x.e = make_entry(p, x.ei, start, n, len, p.small.tq, 0);
+    };
     PgRing<L::STAGES> ring;
 
     if (warp >= L::WARPS) {
@@ -457,13 +573,13 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                 ring.step();
                 ++tiles;
             }
-        } while (ok && r.next(p.small, p.Hkv));
+        } while (ok && r.next(p.Hkv, step));
         // every copy has landed before the CTA may exit
         for (int k = 0; k < L::STAGES && k < tiles; ++k) {
             const int j = tiles - 1 - k;
             (void)mbar_wait_bounded(&full[j % L::STAGES], (uint32_t)(j / L::STAGES) & 1u);
         }
-        if (p.large.cap != 0) pg_wait();
+        if (!alone) pg_wait();
         return;
     }
 
@@ -739,8 +855,8 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                 *reinterpret_cast<uint2 *>(dst) = pack4<T>(x);
             }
         }
-    } while (r.next(p.small, p.Hkv));
-    if (p.large.cap != 0) pg_wait();
+    } while (r.next(p.Hkv, step));
+    if (!alone) pg_wait();
 }
 
 template <class T, bool Q8, int NT>
@@ -750,7 +866,9 @@ cudaError_t launch_small(const PagedAttendParams &p, cudaStream_t stream)
     constexpr int smem = SmShape<Q8, NT>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_early(kern, dim3(p.small.G), SmShape<Q8, NT>::THREADS, smem, stream, p);
+    if (p.large.cap != 0) return launch_early(kern, dim3(p.small.G), SmShape<Q8, NT>::THREADS, smem, stream, p);
+    kern<<<p.small.G, SmShape<Q8, NT>::THREADS, smem, stream>>>(p);  // the call's first kernel
+    return cudaGetLastError();
 }
 
 template <class T, bool Q8>

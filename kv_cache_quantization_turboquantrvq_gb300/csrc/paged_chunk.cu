@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     pg_wait();  // for the plan
     pg_go();
     PgRun r;
-    if (!r.start(p.large, blockIdx.x)) return;  // the whole CTA
+    r.start(p.large.start[blockIdx.x]);
+    if (r.left <= 0) return;  // the whole CTA
     if (warp == 9) tmem_alloc(const_cast<uint32_t *>(tslot), 512);
     qt_fence_before();
     __syncthreads();

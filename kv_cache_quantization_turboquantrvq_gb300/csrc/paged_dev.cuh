@@ -106,31 +106,33 @@ struct PgRun {
     PgEntry e;
     int ei, h, t0, tn, left;
     bool first;  // the CTA's first run
-    __device__ __forceinline__ bool start(const PgPlan &pl, int c)  // false: nothing to do
+    __device__ __forceinline__ void start(const PgStart &s)
     {
-        const int4 at = *reinterpret_cast<const int4 *>(pl.start + c);
-        e = pg_entry(&pl.start[c].e);
+        const int4 at = *reinterpret_cast<const int4 *>(&s);
+        e = pg_entry(&s.e);
         ei = at.x;
         h = at.y;
         t0 = at.z;
-        left = at.w;
+        left = at.w;  // 0: nothing to do
         tn = min(e.ntiles, t0 + left);
         first = true;
-        return left > 0;
     }
-    __device__ __forceinline__ bool next(const PgPlan &pl, int Hkv)
+    template <class F> __device__ __forceinline__ bool next(int Hkv, F &&step)  // step: to the next entry
     {
         left -= tn - t0;
         if (left <= 0) return false;
         if (++h == Hkv) {
             h = 0;
-            ++ei;
-            e = pg_entry(pl.ent + ei);
+            step(*this);
         }
         t0 = 0;
         tn = min(e.ntiles, left);
         first = false;
         return true;
+    }
+    __device__ __forceinline__ bool next(const PgPlan &pl, int Hkv)
+    {
+        return next(Hkv, [&](PgRun &r) { r.e = pg_entry(pl.ent + ++r.ei); });
     }
 };
 
