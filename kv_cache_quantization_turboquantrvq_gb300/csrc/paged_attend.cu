@@ -215,7 +215,9 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
 
 // ------------------------------------------------------- the merge of parts
 
-constexpr int CB_ROWS = 8;   // rows of one combine CTA, a warp each
+constexpr int CB_WARPS = 8;
+constexpr int CB_LARGE = 4;  // rows of a warp: large items (few parts, many rows)
+static_assert(PG_LROWS % (CB_WARPS * CB_LARGE) == 0 && PG_SROWS % CB_WARPS == 0, "whole blocks");
 
 template <class T> __device__ __forceinline__ uint2 pack4(float4 v);
 template <> __device__ __forceinline__ uint2 pack4<__half>(float4 v)
@@ -229,68 +231,91 @@ template <> __device__ __forceinline__ uint2 pack4<__nv_bfloat16>(float4 v)
     return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-// Block c merges the item that CTA c enters in its middle, if no earlier CTA
-// does so: its parts are the second slot of CTA c - 1 and the first slots of c,
-// c + 1, ..., in that order on every run.  A warp takes a row; the blocks of
-// large items come first, then those of small ones.
-template <class T>
-__global__ void __launch_bounds__(32 * CB_ROWS) paged_combine_kernel(const __grid_constant__ PagedAttendParams p)
+// Rows r0, r0 + 1, ..., R of them, of the item merged where CTA c starts, by one
+// warp: its parts are the second slot of CTA c - 1 and the first slots of c,
+// c + 1, ..., taken in that order on every run, NP at a time with all loads in
+// flight (8 of 512 bytes a warp), the maximum followed online.
+template <class T, int ROWS, int RT, int R, int NP>
+__device__ __forceinline__ void merge_rows(const PagedAttendParams &p, const float *parts_base, int c, int4 at, int r0)
 {
-    pg_wait();
-    constexpr int LARGE = PG_LROWS / CB_ROWS;
-    const int first_small = p.large.cap ? LARGE : 0;
-    const bool large = (int)blockIdx.y < first_small;
-    const PgPlan &pl = large ? p.large : p.small;
-    const int c = blockIdx.x;
-    const int4 at = pl.cmb[c];
-    const int parts = at.x;
-    if (parts == 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ROWS = large ? PG_LROWS : PG_SROWS, RT = large ? 128 : PG_SROWS;  // rows of a slot, of a query tile
-    const int tqt = RT / p.GQ;
-    const size_t slot = (size_t)ROWS * PG_PART;
-    const int r = ((int)blockIdx.y - (large ? 0 : first_small)) * CB_ROWS + warp;
-    const int half = r >= RT ? 1 : 0, rr = r - half * RT;
-    const int tok = half * tqt + rr / p.GQ, g = rr % p.GQ;
-    if (rr >= tqt * p.GQ || tok >= at.z) return;
-    const float *first = pl.part + (size_t)(2 * c - 1) * slot;
-    auto at_part = [&](int k) { return first + (size_t)(2 * k - (k > 0 ? 1 : 0)) * slot; };
-    // eight parts' loads in flight at a time, the maximum followed online
-    float M = NEG_INF, L = 0.0f;
-    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    constexpr int NP = 8;
+    const int lane = threadIdx.x & 31, parts = at.x;
+    const int tqt = RT / p.GQ;  // tokens of a query tile of RT rows
+    constexpr size_t SLOT = (size_t)ROWS * PG_PART;
+    const float *first = parts_base + (size_t)(2 * c - 1) * SLOT;
+    float M[R], L[R];
+    float4 O[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        M[j] = NEG_INF;
+        L[j] = 0.0f;
+        O[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
     for (int k0 = 0; k0 < parts; k0 += NP) {
-        float m[NP], l[NP];
-        float4 o[NP];
+        float m[R][NP], l[R][NP];
+        float4 o[R][NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const float *s = at_part(min(k0 + i, parts - 1));
-            m[i] = s[r];
-            l[i] = s[ROWS + r];
-            o[i] = *reinterpret_cast<const float4 *>(s + 2 * ROWS + (size_t)r * D + 4 * lane);
+            const int k = min(k0 + i, parts - 1);
+            const float *s = first + (size_t)(2 * k - (k > 0 ? 1 : 0)) * SLOT + r0;
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                m[j][i] = s[j];
+                l[j][i] = s[ROWS + j];
+                o[j][i] = *reinterpret_cast<const float4 *>(s - r0 + 2 * ROWS + (size_t)(r0 + j) * D + 4 * lane);
+            }
         }
-        float N = M;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) N = fmaxf(N, m[i]);
-        if (N == NEG_INF) continue;  // nothing seen so far
-        const float f0 = ex2(M - N);
-        M = N;
-        L *= f0;
-        O.x *= f0; O.y *= f0; O.z *= f0; O.w *= f0;
+        for (int j = 0; j < R; ++j) {
+            float N = M[j];
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const float f = k0 + i < parts ? ex2(m[i] - N) : 0.0f;
-            L = fmaf(l[i], f, L);
-            O.x = fmaf(o[i].x, f, O.x);
-            O.y = fmaf(o[i].y, f, O.y);
-            O.z = fmaf(o[i].z, f, O.z);
-            O.w = fmaf(o[i].w, f, O.w);
+            for (int i = 0; i < NP; ++i) N = fmaxf(N, m[j][i]);
+            if (N == NEG_INF) continue;  // nothing seen so far
+            const float f0 = ex2(M[j] - N);
+            M[j] = N;
+            L[j] *= f0;
+            O[j].x *= f0; O[j].y *= f0; O[j].z *= f0; O[j].w *= f0;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const float f = k0 + i < parts ? ex2(m[j][i] - N) : 0.0f;
+                L[j] = fmaf(l[j][i], f, L[j]);
+                O[j].x = fmaf(o[j][i].x, f, O[j].x);
+                O[j].y = fmaf(o[j][i].y, f, O[j].y);
+                O[j].z = fmaf(o[j][i].z, f, O[j].z);
+                O[j].w = fmaf(o[j][i].w, f, O[j].w);
+            }
         }
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    O.x *= inv; O.y *= inv; O.z *= inv; O.w *= inv;
-    T *dst = static_cast<T *>(p.out) + ((size_t)(at.y + tok) * p.Hq + (size_t)at.w * p.GQ + g) * D + 4 * lane;
-    *reinterpret_cast<uint2 *>(dst) = pack4<T>(O);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const int r = r0 + j, half = r / RT, rr = r % RT;
+        const int tok = half * tqt + rr / p.GQ, g = rr % p.GQ;
+        if (rr >= tqt * p.GQ || tok >= at.z) continue;  // a row of no token
+        const float inv = L[j] > 0.0f ? 1.0f / L[j] : 0.0f;
+        T *dst = static_cast<T *>(p.out) + ((size_t)(at.y + tok) * p.Hq + (size_t)at.w * p.GQ + g) * D + 4 * lane;
+        *reinterpret_cast<uint2 *>(dst) =
+            pack4<T>(make_float4(O[j].x * inv, O[j].y * inv, O[j].z * inv, O[j].w * inv));
+    }
+}
+
+// Blocks x: the CTAs at whose start an item may have to be merged; blocks y: rows
+// of large items, then of small ones.
+template <class T>
+__global__ void __launch_bounds__(32 * CB_WARPS) paged_combine_kernel(const __grid_constant__ PagedAttendParams p)
+{
+    pg_wait();
+    const int first_small = p.large.cap ? PG_LROWS / (CB_WARPS * CB_LARGE) : 0;
+    const int c = blockIdx.x, y = blockIdx.y, warp = threadIdx.x >> 5;
+    if (y < first_small) {
+        const int4 at = p.large.cmb[c];
+        const int r0 = (y * CB_WARPS + warp) * CB_LARGE, tqt = 128 / p.GQ;
+        // (rows past the item's tokens come in whole query tiles, or at its end)
+        if (at.x > 0 && (r0 < 128 ? r0 / p.GQ < at.z : tqt + (r0 - 128) / p.GQ < at.z))
+            merge_rows<T, PG_LROWS, 128, CB_LARGE, 2>(p, p.large.part, c, at, r0);
+    } else {
+        const int4 at = p.small.cmb[c];
+        const int r0 = (y - first_small) * CB_WARPS + warp;
+        if (at.x > 0 && r0 < at.z * p.GQ) merge_rows<T, PG_SROWS, PG_SROWS, 1, 8>(p, p.small.part, c, at, r0);
+    }
 }
 
 // --------------------------------------------------------- the small kernel
@@ -900,9 +925,9 @@ cudaError_t launch_paged_small(const PagedAttendParams &p0, int q_dtype, int cac
 cudaError_t launch_paged_combine(const PagedAttendParams &p, int q_dtype, cudaStream_t stream)
 {
     const dim3 grid(p.large.cap ? p.large.G : p.small.G,
-                    ((p.large.cap ? PG_LROWS : 0) + (p.small.cap ? PG_SROWS : 0)) / CB_ROWS);
+                    (p.large.cap ? PG_LROWS / (CB_WARPS * CB_LARGE) : 0) + (p.small.cap ? PG_SROWS / CB_WARPS : 0));
     return launch_early(q_dtype == VQ_F16 ? paged_combine_kernel<__half> : paged_combine_kernel<__nv_bfloat16>, grid,
-                        32 * CB_ROWS, 0, stream, p);
+                        32 * CB_WARPS, 0, stream, p);
 }
 
 cudaError_t paged_attend_take_device_error(unsigned *bits, cudaStream_t stream)

@@ -15,6 +15,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "paged.h"
 #include "paged_dev.cuh"
@@ -47,104 +49,161 @@ __device__ __forceinline__ int row_exponent(uint32_t bits)
     return bits == 0u ? 0 : min(max(e, PG_EMIN), PG_EMAX);
 }
 
-template <class T, bool E4M3>
+// R rows (token, head) a group of 16 lanes, all of their loads in flight at once.
+template <class T, bool E4M3, int R>
 __global__ void __launch_bounds__(THREADS) paged_append_kernel(const __grid_constant__ PagedAppendParams p)
 {
     using T2 = typename Pair<T>::type;
     const int lane = threadIdx.x & 15;
-    const long long row = (long long)blockIdx.x * (THREADS / 16) + (threadIdx.x >> 4);  // (token, head)
-    if (row >= (long long)p.T * p.c.Hkv) return;  // whole groups of 16 lanes leave together
-    const int t = fdiv(p.divH, (int)row), h = (int)row - t * p.c.Hkv;
-    const long long slot = __ldg(p.slots + t);
-    if (slot < 0) return;  // a padding token
-    const long long page = slot >> p.c.page_shift;
-    if (page >= p.c.num_pages) {
-        if (lane == 0) atomicOr(&g_pc_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
-        return;
+    const int rows = p.T * p.c.Hkv;  // below 2^31
+    const int r0 = (int)(blockIdx.x * (THREADS / 16) + (threadIdx.x >> 4)) * R;
+    if (r0 >= rows) return;  // whole groups of 16 lanes leave together
+    uint4 raw[R][2];
+    long long slot[R];
+    int head[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const int row = min(r0 + j, rows - 1);
+        const int t = fdiv(p.divH, row), h = row - t * p.c.Hkv;
+        head[j] = h;
+        slot[j] = r0 + j < rows ? __ldg(p.slots + t) : -1;
+        raw[j][0] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_in) + t * p.kst + h * p.ksh) + lane);
+        raw[j][1] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.v_in) + t * p.vst + h * p.vsh) + lane);
     }
-    const int off = (int)(slot - (page << p.c.page_shift));
-    const long long dst = ((page * p.c.Hkv + h) << p.c.page_shift) + off;
     const unsigned group = 0xffffu << (threadIdx.x & 16);
-    uint4 raw[2];
-    raw[0] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_in) + t * p.kst + h * p.ksh) + lane);
-    raw[1] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.v_in) + t * p.vst + h * p.vsh) + lane);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        void *pages = const_cast<void *>(i ? p.c.v : p.c.k);
-        if constexpr (!E4M3) {
-            static_cast<uint4 *>(pages)[dst * 16 + lane] = raw[i];
-        } else {
-            const T2 *x = reinterpret_cast<const T2 *>(&raw[i]);
-            float2 f[4];
-            float m = 0.0f;
+    for (int j = 0; j < R; ++j) {
+        if (slot[j] < 0) continue;  // a padding token
+        const long long page = slot[j] >> p.c.page_shift;
+        if (page >= p.c.num_pages) {
+            if (lane == 0) atomicOr(&g_pc_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+            continue;
+        }
+        const long long dst = ((page * p.c.Hkv + head[j]) << p.c.page_shift) + (slot[j] - (page << p.c.page_shift));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[j] = Pair<T>::f(x[j]);
-                m = fmaxf(m, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
+        for (int i = 0; i < 2; ++i) {
+            void *pages = const_cast<void *>(i ? p.c.v : p.c.k);
+            if constexpr (!E4M3) {
+                static_cast<uint4 *>(pages)[dst * 16 + lane] = raw[j][i];
+            } else {
+                const T2 *x = reinterpret_cast<const T2 *>(&raw[j][i]);
+                float2 f[4];
+                float m = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    f[q] = Pair<T>::f(x[q]);
+                    m = fmaxf(m, fmaxf(fabsf(f[q].x), fabsf(f[q].y)));
+                }
+#pragma unroll
+                for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, s));
+                const int e = row_exponent(__float_as_uint(m));
+                const float inv = pow2f(-e);
+                uint16_t c[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    c[q] = __nv_cvt_float2_to_fp8x2(make_float2(f[q].x * inv, f[q].y * inv), __NV_SATFINITE, __NV_E4M3);
+                static_cast<uint2 *>(pages)[dst * 16 + lane] =
+                    make_uint2((uint32_t)c[0] | ((uint32_t)c[1] << 16), (uint32_t)c[2] | ((uint32_t)c[3] << 16));
+                if (lane == 0) const_cast<uint8_t *>(i ? p.c.ve : p.c.ke)[dst] = (uint8_t)(e + 127);
             }
-#pragma unroll
-            for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, s));
-            const int e = row_exponent(__float_as_uint(m));
-            const float inv = pow2f(-e);
-            uint2 code;
-            uint16_t c[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                c[j] = __nv_cvt_float2_to_fp8x2(make_float2(f[j].x * inv, f[j].y * inv), __NV_SATFINITE, __NV_E4M3);
-            code.x = (uint32_t)c[0] | ((uint32_t)c[1] << 16);
-            code.y = (uint32_t)c[2] | ((uint32_t)c[3] << 16);
-            static_cast<uint2 *>(pages)[dst * 16 + lane] = code;
-            if (lane == 0) const_cast<uint8_t *>(i ? p.c.ve : p.c.ke)[dst] = (uint8_t)(e + 127);
         }
     }
 }
 
-template <class T, bool E4M3>
-__device__ __forceinline__ uint4 read_row(const void *pages, const uint8_t *exps, long long src, int lane)
-{
-    if constexpr (!E4M3) {
-        return __ldcs(static_cast<const uint4 *>(pages) + src * 16 + lane);
-    } else {
-        const uint2 code = __ldcs(static_cast<const uint2 *>(pages) + src * 16 + lane);
-        const float s = pow2f((int)__ldg(exps + src) - 127);
-        uint4 out;
-        uint32_t *o = reinterpret_cast<uint32_t *>(&out);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t two = ((j < 2 ? code.x : code.y) >> (16 * (j & 1))) & 0xffffu;
-            const uint32_t h2 = e4m3x2_to_f16x2(two);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-            typename Pair<T>::type r = Pair<T>::from(make_float2(f.x * s, f.y * s));
-            o[j] = *reinterpret_cast<uint32_t *>(&r);
-        }
-        return out;
-    }
-}
-
-template <class T, bool E4M3>
+// R rows (tokens of one sequence and head) a group of 16 lanes, all of their
+// loads in flight at once; S_out is padded to a multiple of R in the numbering.
+template <class T, bool E4M3, int R>
 __global__ void __launch_bounds__(THREADS) paged_gather_kernel(const __grid_constant__ PagedGatherParams p)
 {
+    using V = typename std::conditional<E4M3, uint2, uint4>::type;  // what 16 lanes of a row read
     const int lane = threadIdx.x & 15;
-    const long long row = (long long)blockIdx.x * (THREADS / 16) + (threadIdx.x >> 4);  // (b, h, i)
-    if (row >= (long long)p.B * p.c.Hkv * p.S_out) return;
-    const int bh = fdiv(p.divS, (int)row), i = (int)row - bh * p.S_out;
+    const int blocks = (p.S_out + R - 1) / R;
+    const long long at = (long long)blockIdx.x * (THREADS / 16) + (threadIdx.x >> 4);
+    if (at >= (long long)p.B * p.c.Hkv * blocks) return;
+    const int bh = fdiv(p.divS, (int)at), i0 = ((int)at - bh * blocks) * R;
     const int b = fdiv(p.divH, bh), h = bh - b * p.c.Hkv;
-    const long long t = (long long)(p.first ? __ldg(p.first + b) : 0) + i;
-    uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
-    if (t >= 0 && t < __ldg(p.lens + b)) {
-        const long long lp = t >> p.c.page_shift;
-        const int page = lp < p.max_pages ? __ldg(p.table + (long long)b * p.max_pages + lp) : -1;
-        if (page < 0 || page >= p.c.num_pages) {
-            if (lane == 0) atomicOr(&g_pc_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
-        } else {
-            const long long src =
-                (((long long)page * p.c.Hkv + h) << p.c.page_shift) + (t & ((1 << p.c.page_shift) - 1));
-            if (p.k_out) k = read_row<T, E4M3>(p.c.k, p.c.ke, src, lane);
-            if (p.v_out) v = read_row<T, E4M3>(p.c.v, p.c.ve, src, lane);
+    const long long t0 = (long long)(p.first ? __ldg(p.first + b) : 0) + i0;
+    const int len = __ldg(p.lens + b);
+    long long src[R];  // row of the pool, -1: none
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const long long t = t0 + j;
+        src[j] = -1;
+        if (i0 + j < p.S_out && t >= 0 && t < len) {
+            const long long lp = t >> p.c.page_shift;
+            const int page = lp < p.max_pages ? __ldg(p.table + (long long)b * p.max_pages + lp) : -1;
+            if (page >= 0 && page < p.c.num_pages)
+                src[j] = (((long long)page * p.c.Hkv + h) << p.c.page_shift) + (t & ((1 << p.c.page_shift) - 1));
+            else if (lane == 0)
+                atomicOr(&g_pc_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
         }
     }
-    if (p.k_out) __stcs(static_cast<uint4 *>(p.k_out) + row * 16 + lane, k);
-    if (p.v_out) __stcs(static_cast<uint4 *>(p.v_out) + row * 16 + lane, v);
+    V raw[R][2];
+    uint8_t e[R][2];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            raw[j][i] = V();
+            e[j][i] = 127;
+            if (src[j] >= 0 && (i ? p.v_out : p.k_out)) {
+                raw[j][i] = __ldcs(static_cast<const V *>(i ? p.c.v : p.c.k) + src[j] * 16 + lane);
+                if constexpr (E4M3) e[j][i] = __ldg((i ? p.c.ve : p.c.ke) + src[j]);
+            }
+        }
+    }
+    const long long dst = ((long long)bh * p.S_out + i0) * 16 + lane;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        if (i0 + j >= p.S_out) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            void *out = i ? p.v_out : p.k_out;
+            if (!out) continue;
+            uint4 x;
+            if constexpr (E4M3) {
+                const float s = pow2f((int)e[j][i] - 127);
+                uint32_t h2[4];
+                e4m3x4_to_f16x4(raw[j][i].x, h2[0], h2[1]);
+                e4m3x4_to_f16x4(raw[j][i].y, h2[2], h2[3]);
+                uint32_t *o = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2[q]));
+                    const typename Pair<T>::type r = Pair<T>::from(make_float2(f.x * s, f.y * s));
+                    o[q] = *reinterpret_cast<const uint32_t *>(&r);
+                }
+            } else {
+                x = raw[j][i];
+            }
+            __stcs(static_cast<uint4 *>(out) + dst + j * 16, x);
+        }
+    }
+}
+
+}  // namespace
+
+namespace {
+
+template <class T, bool E4M3> cudaError_t append(const PagedAppendParams &p, cudaStream_t stream)
+{
+    // few rows: one for each group, so that they spread over the SMs
+    const long long rows = (long long)p.T * p.c.Hkv;
+    const int R = rows < 32LL * sm_count() ? 1 : 4;
+    const unsigned grid = (unsigned)((rows + R * (THREADS / 16) - 1) / (R * (THREADS / 16)));
+    if (R == 1) paged_append_kernel<T, E4M3, 1><<<grid, THREADS, 0, stream>>>(p);
+    else paged_append_kernel<T, E4M3, 4><<<grid, THREADS, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <class T, bool E4M3> cudaError_t gather(PagedGatherParams &p, cudaStream_t stream)
+{
+    constexpr int R = 4;
+    const int blocks = (p.S_out + R - 1) / R;
+    p.divS = make_fastdiv((uint32_t)blocks);
+    const long long groups = (long long)p.B * p.c.Hkv * blocks;
+    paged_gather_kernel<T, E4M3, R><<<(unsigned)((groups + THREADS / 16 - 1) / (THREADS / 16)), THREADS, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -153,30 +212,16 @@ cudaError_t launch_paged_append(const PagedAppendParams &p0, int in_dtype, int c
 {
     PagedAppendParams p = p0;
     p.divH = make_fastdiv((uint32_t)p.c.Hkv);
-    const long long rows = (long long)p.T * p.c.Hkv;
-    const unsigned grid = (unsigned)((rows + THREADS / 16 - 1) / (THREADS / 16));
-    const bool q = cache_dtype == VQ_E4M3;
-    if (in_dtype == VQ_F16) {
-        if (q) paged_append_kernel<__half, true><<<grid, THREADS, 0, stream>>>(p);
-        else paged_append_kernel<__half, false><<<grid, THREADS, 0, stream>>>(p);
-    } else {
-        if (q) paged_append_kernel<__nv_bfloat16, true><<<grid, THREADS, 0, stream>>>(p);
-        else paged_append_kernel<__nv_bfloat16, false><<<grid, THREADS, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
+    if (cache_dtype != VQ_E4M3) return append<__half, false>(p, stream);  // 16-bit copy
+    return in_dtype == VQ_F16 ? append<__half, true>(p, stream) : append<__nv_bfloat16, true>(p, stream);
 }
 
 cudaError_t launch_paged_gather(const PagedGatherParams &p0, int cache_dtype, int out_dtype, cudaStream_t stream)
 {
     PagedGatherParams p = p0;
     p.divH = make_fastdiv((uint32_t)p.c.Hkv);
-    p.divS = make_fastdiv((uint32_t)p.S_out);
-    const long long rows = (long long)p.B * p.c.Hkv * p.S_out;
-    const unsigned grid = (unsigned)((rows + THREADS / 16 - 1) / (THREADS / 16));
-    if (cache_dtype != VQ_E4M3) paged_gather_kernel<__half, false><<<grid, THREADS, 0, stream>>>(p);  // 16-bit copy
-    else if (out_dtype == VQ_F16) paged_gather_kernel<__half, true><<<grid, THREADS, 0, stream>>>(p);
-    else paged_gather_kernel<__nv_bfloat16, true><<<grid, THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (cache_dtype != VQ_E4M3) return gather<__half, false>(p, stream);  // 16-bit copy
+    return out_dtype == VQ_F16 ? gather<__half, true>(p, stream) : gather<__nv_bfloat16, true>(p, stream);
 }
 
 cudaError_t paged_cache_take_device_error(unsigned *bits, cudaStream_t stream)
