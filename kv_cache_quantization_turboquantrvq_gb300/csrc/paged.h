@@ -126,5 +126,8 @@ cudaError_t paged_attend_take_device_error(unsigned *bits, cudaStream_t stream);
 // Tensor map of pages [rows, 128]: 16-bit boxes of 64 columns, 8-bit boxes of
 // 128 columns (128 bytes a row), `box_rows` rows, 128-byte swizzle.
 bool encode_tmap_pages(CUtensorMap *map, const void *base, uint64_t rows, int elem_bytes, uint32_t box_rows);
+// The same 16-bit rows as [2 halves, rows, 64]: a box holds `box_rows` rows of the
+// first half, then of the second.
+bool encode_tmap_halves(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
 
 }  // namespace vq

@@ -339,8 +339,6 @@ constexpr int KB = 16;         // keys of a warp's block
 constexpr float OFF = 7.0f;    // weights reach up to 2^(OFF + LAG): fp16 stays normal down to 2^-14
 constexpr float LAG = 8.0f;    // the maximum is only followed when it grew by more than this
 
-constexpr int SM_HALF = PG_TILE * 128;  // 128-byte columns of a 16-bit tile
-
 template <bool Q8, int NT> struct SmShape {
     static constexpr int ROW = Q8 ? 128 : 256;            // bytes of a cache row
     static constexpr int KV = PG_TILE * ROW;              // keys, or values, of a tile
@@ -354,7 +352,9 @@ template <bool Q8, int NT> struct SmShape {
     static constexpr int GROUPS = NT == 1 && Q8 ? 2 : 1;
     static_assert(STAGES % GROUPS == 0, "a slot belongs to one group");
     static constexpr int WARPS = 8 * GROUPS;              // that compute
-    static constexpr int THREADS = 32 * (WARPS + 2);
+    static constexpr int PAIRS = GROUPS;                  // of warps that copy: keys and values; they take the tiles in turn
+    static_assert(STAGES % PAIRS == 0, "a slot belongs to one pair");
+    static constexpr int THREADS = 32 * (WARPS + 2 * PAIRS);
     static constexpr int ROWS = 8 * NT;
     static constexpr int MBUF = NT == 1 ? 4 : 2;          // buffers that the warps' outputs are summed in
     static constexpr int MROW = D + 4;                    // row of a buffer (floats)
@@ -549,17 +549,18 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
 
     if (warp >= L::WARPS) {
         // ------------------------------------------------ copies: keys, values
-        const bool val = warp > L::WARPS;
+        const int pair = (warp - L::WARPS) >> 1;
+        const bool val = ((warp - L::WARPS) & 1) != 0;
         const CUtensorMap *map = val ? &p.tmv : &p.tmk;
         const uint8_t *ex = val ? p.c.ve : p.c.ke;
         const int box = min(1 << p.c.page_shift, PG_TILE), nbox = PG_TILE / box;
         const uint64_t pol = l2_policy_evict_first();
-        int tiles = 0;
+        int tiles = 0, last = -1;  // tiles of the CTA before this run; this pair's last one
         bool ok = true;
         do {
             PgView view;
             view.set(r.e, p.window, p.sinks);
-            // a lane per box: its page is looked up one tile ahead
+            // a lane per box: its page is looked up two tiles ahead
             auto row_of = [&](int t) -> int {  // -1: nothing to copy, -2: no such page
                 if (t >= r.tn || lane >= nbox) return -1;
                 const int k = pg_tile_key(r.e, t) + lane * box;
@@ -569,12 +570,28 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                 if (page < 0 || page >= p.c.num_pages) return -2;
                 return ((page * p.c.Hkv + r.h) << p.c.page_shift) + (k & ((1 << p.c.page_shift) - 1));
             };
-            int next = row_of(r.t0);
-            for (int t = r.t0; t < r.tn && ok; ++t) {
-                const int row = next;
-                next = row_of(t + 1);
+            // the exponents of this lane's four keys, one tile ahead (a copy of 16
+            // bytes takes the TMA unit as long as one of 2 KB)
+            auto exps_of = [&](int row) -> uint32_t {
+                if constexpr (!Q8) return 0u;
+                const int k = 4 * lane, rw = __shfl_sync(FULL_MASK, row, k / box);
+                return rw >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(ex + rw + k % box)) : 0x7f7f7f7fu;
+            };
+            int mine = r.t0;  // this pair's first tile of the run
+            if (L::PAIRS > 1 && (tiles & 1) != pair) {
+                ++mine;
+                ring.step();
+            }
+            int row1 = row_of(mine), row2 = row_of(mine + L::PAIRS);
+            uint32_t x1 = exps_of(row1);
+            for (int t = mine; t < r.tn && ok; t += L::PAIRS) {
+                const int row = row1;
+                const uint32_t x = x1;
+                row1 = row2;
+                row2 = row_of(t + 2 * L::PAIRS);
+                x1 = exps_of(row1);
                 if (row < -1) atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
-                if (tiles >= L::STAGES) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&empty[ring.s], ring.par ^ 1u));
+                if (tiles + (t - r.t0) >= L::STAGES) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&empty[ring.s], ring.par ^ 1u));
                 if (!ok) {
                     if (lane == 0) atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_WAIT_TIMEOUT);
                     break;
@@ -583,25 +600,27 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                 // keys' scores are not specified
                 const unsigned held = __ballot_sync(FULL_MASK, row >= 0);
                 unsigned char *dst = stages + ring.s * L::STAGE + (val ? L::KV : 0);
-                unsigned char *dx = exps + ring.s * L::EXP + (val ? PG_TILE : 0);
                 uint64_t *bar = &full[ring.s];
-                if (elect_lane()) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(held) * box * (L::ROW + (Q8 ? 1 : 0))));
-                for (int i = 0; i < nbox; ++i) {
-                    if (!((held >> i) & 1u)) continue;
-                    const int rw = __shfl_sync(FULL_MASK, row, i);
-                    if (elect_lane()) {
-                        tma_load_2d(dst + i * box * 128, map, 0, rw, bar, pol);
-                        if constexpr (Q8) bulk_g2s(dx + i * box, ex + rw, box, bar, pol);
-                        else tma_load_2d(dst + SM_HALF + i * box * 128, map, 64, rw, bar, pol);
-                    }
+                if constexpr (Q8) {
+                    reinterpret_cast<uint32_t *>(exps + ring.s * L::EXP + (val ? PG_TILE : 0))[lane] = x;
+                    __syncwarp();
                 }
+                if (elect_lane()) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(held) * box * L::ROW));
+                __syncwarp();
+                if (row >= 0) {  // a lane per box
+                    if constexpr (Q8) tma_load_2d(dst + lane * box * L::ROW, map, 0, row, bar, pol);
+                    else tma_load_3d(dst + lane * box * L::ROW, map, 0, row, 0, bar, pol);
+                }
+                __syncwarp();
                 ring.step();
-                ++tiles;
+                // (past the other pair's tile, if the run has one more)
+                if (L::PAIRS > 1 && t + 1 < r.tn) ring.step();
+                last = tiles + (t - r.t0);
             }
+            tiles += r.tn - r.t0;
         } while (ok && r.next(p.Hkv, step));
-        // every copy has landed before the CTA may exit
-        for (int k = 0; k < L::STAGES && k < tiles; ++k) {
-            const int j = tiles - 1 - k;
+        // every copy of this pair has landed before the CTA may exit
+        for (int j = last; j >= 0 && j > last - L::STAGES; j -= L::PAIRS) {
             (void)mbar_wait_bounded(&full[j % L::STAGES], (uint32_t)(j / L::STAGES) & 1u);
         }
         if (!alone) pg_wait();
@@ -611,6 +630,10 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
     // ---------------------------------------------------- scores, softmax, values
     const int group = warp >> 3, g8 = lane >> 2, t4 = lane & 3;
     const int kw = KB * (warp & 7);  // this warp's keys of a tile
+    // a box lies in its 128-byte columns one after another: one for codes, two
+    // halves for 16-bit entries
+    const int box = min(1 << p.c.page_shift, PG_TILE), half = box * 128;
+    const int at = (kw / box) * box * L::ROW + (kw % box) * 128;
     int tile = 0;                    // tiles of this CTA so far: group g takes those with tile mod GROUPS == g
     bool ok = true;
     do {
@@ -670,7 +693,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
             }
             const int k0 = pg_tile_key(e, t) + kw;
             if (v.any(k0, k0 + KB)) {
-                const unsigned char *sb = stages + ring.s * L::STAGE + kw * 128;
+                const unsigned char *sb = stages + ring.s * L::STAGE + at;
                 // ---- scores: S^T[key][row]; this lane's keys are g8 and g8 + 8
                 float s[NT][4];
 #pragma unroll
@@ -696,7 +719,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const unsigned char *h = sb + (q >> 1) * SM_HALF;
+                        const unsigned char *h = sb + (q >> 1) * half;
                         const uint4 wa = *reinterpret_cast<const uint4 *>(h + swz128(g8, t4 + 4 * (q & 1)));
                         const uint4 wb = *reinterpret_cast<const uint4 *>(h + swz128(g8 + 8, t4 + 4 * (q & 1)));
 #pragma unroll
@@ -799,7 +822,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
                         uint32_t x[4];
-                        ldsm_x4_t(vbase + (n >> 2) * SM_HALF + swz128(vkey, 2 * (n & 3) + vc), x);
+                        ldsm_x4_t(vbase + (n >> 2) * half + swz128(vkey, 2 * (n & 3) + vc), x);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             mma16<TV>(o[nt][n], x[0] & ka, x[1] & ka, x[2] & kb, x[3] & kb, pf[nt][0], pf[nt][1]);
@@ -916,8 +939,11 @@ cudaError_t launch_paged_small(const PagedAttendParams &p0, int q_dtype, int cac
     const bool q8 = cache_dtype == VQ_E4M3;
     const uint64_t rows = ((uint64_t)p.c.num_pages * p.c.Hkv) << p.c.page_shift;
     const uint32_t box = 1u << p.c.page_shift < (unsigned)PG_TILE ? 1u << p.c.page_shift : (unsigned)PG_TILE;
-    if (!encode_tmap_pages(&p.tmk, p.c.k, rows, q8 ? 1 : 2, box) || !encode_tmap_pages(&p.tmv, p.c.v, rows, q8 ? 1 : 2, box))
-        return cudaErrorInvalidValue;
+    // 16-bit rows as two halves of 64: one copy a box (the TMA unit takes about
+    // 47 ns a copy, whatever its size up to 2 KB)
+    const bool ok = q8 ? encode_tmap_pages(&p.tmk, p.c.k, rows, 1, box) && encode_tmap_pages(&p.tmv, p.c.v, rows, 1, box)
+                       : encode_tmap_halves(&p.tmk, p.c.k, rows, box) && encode_tmap_halves(&p.tmv, p.c.v, rows, box);
+    if (!ok) return cudaErrorInvalidValue;
     if (q_dtype == VQ_F16) return q8 ? dispatch_small<__half, true>(p, stream) : dispatch_small<__half, false>(p, stream);
     return q8 ? dispatch_small<__nv_bfloat16, true>(p, stream) : dispatch_small<__nv_bfloat16, false>(p, stream);
 }

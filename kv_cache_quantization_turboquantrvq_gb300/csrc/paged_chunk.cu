@@ -388,17 +388,16 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                         // a key tile brings the exponents of keys and values
                         const unsigned n = part ? 0u : (unsigned)__popc(__ballot_sync(FULL_MASK, held));
                         if (elect_lane()) mbar_arrive_expect_tx(&raw_full[raw.s], RAW_B + n * 2 * box);
-                        for (int i = 0; i < nbox; ++i) {
-                            const int rw = __shfl_sync(FULL_MASK, at, i);
-                            if (elect_lane()) {
-                                tma_load_2d(sraw + raw.s * RAW_B + i * box * 128, map, 0, rw, &raw_full[raw.s], pol);
-                                if (part == 0 && rw != rows_all) {
-                                    unsigned char *x = sexp + raw.s * 2 * PG_TILE + i * box;
-                                    bulk_g2s(x, p.c.ke + rw, box, &raw_full[raw.s], pol);
-                                    bulk_g2s(x + PG_TILE, p.c.ve + rw, box, &raw_full[raw.s], pol);
-                                }
+                        __syncwarp();
+                        if (lane < nbox) {  // a lane per box
+                            tma_load_2d(sraw + raw.s * RAW_B + lane * box * 128, map, 0, at, &raw_full[raw.s], pol);
+                            if (held && part == 0) {
+                                unsigned char *x = sexp + raw.s * 2 * PG_TILE + lane * box;
+                                bulk_g2s(x, p.c.ke + at, box, &raw_full[raw.s], pol);
+                                bulk_g2s(x + PG_TILE, p.c.ve + at, box, &raw_full[raw.s], pol);
                             }
                         }
+                        __syncwarp();
                         raw.step();
                     } else {
                         if (tiles >= STAGES && !__all_sync(FULL_MASK, wait(&kv_empty[kv.s], kv.par ^ 1u))) {
@@ -406,14 +405,13 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                             break;
                         }
                         if (elect_lane()) mbar_arrive_expect_tx(&kv_full[kv.s], TILE_B);
-                        for (int i = 0; i < nbox; ++i) {
-                            const int rw = __shfl_sync(FULL_MASK, at, i);
-                            if (elect_lane()) {
-                                unsigned char *dst = skv + kv.s * TILE_B + i * box * 128;
-                                tma_load_2d(dst, map, 0, rw, &kv_full[kv.s], pol);
-                                tma_load_2d(dst + HALF_B, map, 64, rw, &kv_full[kv.s], pol);
-                            }
+                        __syncwarp();
+                        if (lane < nbox) {  // a lane per box
+                            unsigned char *dst = skv + kv.s * TILE_B + lane * box * 128;
+                            tma_load_2d(dst, map, 0, at, &kv_full[kv.s], pol);
+                            tma_load_2d(dst + HALF_B, map, 64, at, &kv_full[kv.s], pol);
                         }
+                        __syncwarp();
                         kv.step();
                     }
                     ++tiles;

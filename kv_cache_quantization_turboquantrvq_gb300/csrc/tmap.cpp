@@ -89,4 +89,18 @@ bool encode_tmap_pages(CUtensorMap *map, const void *base, uint64_t rows, int el
     return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_halves(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows)
+{
+    EncodeTiled fn = encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t gd[3] = {64, rows, 2};
+    const cuuint64_t gs[2] = {256, 128};
+    const cuuint32_t bx[3] = {64, box_rows, 2};
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), gd, gs, bx, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 }  // namespace vq
