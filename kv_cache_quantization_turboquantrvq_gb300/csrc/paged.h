@@ -56,6 +56,7 @@ cudaError_t paged_cache_take_device_error(unsigned *bits, cudaStream_t stream);
 // slot for the item a CTA enters in the middle, one for the item it leaves
 // unfinished), merged by the combine kernel in the order of the CTAs.
 constexpr int PG_TILE = 128;
+constexpr int PLAN_CTAS = 512;  // CTAs of a launch at most
 
 struct PgEntry {     // 32 bytes, read as two int4
     int b, tok0, nt; // sequence, first query token (index into q), number of tokens

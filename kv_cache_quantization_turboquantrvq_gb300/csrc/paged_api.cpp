@@ -132,7 +132,7 @@ vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, AttendPlan &pl)
     if (gq > kMaxGroup) return VQ_ERR_UNSUPPORTED;
     if ((long long)T * Hq >= (1LL << 31) || B > (1 << 20)) return VQ_ERR_UNSUPPORTED;
     std::memset(&pl, 0, sizeof(pl));
-    pl.G = sm_count();
+    pl.G = sm_count() < PLAN_CTAS ? sm_count() : PLAN_CTAS;
     if (T == 0 || B == 0 || gq == 0) return VQ_OK;
     // Sequences with at most 16 query rows per kv head go to the small kernel,
     // longer chunks to the tensor-memory kernel.  A call whose bounds leave one

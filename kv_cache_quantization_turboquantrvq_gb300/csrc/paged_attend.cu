@@ -35,6 +35,7 @@ constexpr float NEG_INF = -__builtin_huge_valf();
 // ---------------------------------------------------------------- the plan
 
 constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_NEAR = 3;     // tiles
 constexpr int PLAN_KEPT = 1024;  // entries whose sums stay in shared memory
 
 // Exclusive sum over the block; `total` gets the sum of all.
@@ -107,17 +108,19 @@ struct Shares {
         rem = g ? (int)(total - q * g) : 0;
     }
     __device__ __forceinline__ long long first(int c) const { return q * c + min(c, rem); }
-    // what is merged where CTA c starts, in tile t of nt of an item: the item it
-    // enters in its middle, if no earlier CTA does so
-    __device__ __forceinline__ int parts(int c, int t, int nt) const
-    {
-        const long long u = first(c);
-        if (t == 0 || t > u - first(c - 1)) return 0;
-        int n = 2;
-        while (c + n - 1 < g && first(c + n - 1) < u - t + nt) ++n;
-        return n;
-    }
 };
+
+// What is merged where CTA c of g starts, in tile t of nt of an item: the parts of
+// the item it enters in its middle, if no earlier CTA does so; 0 otherwise.
+template <class F> __device__ __forceinline__ int parts_at(F &&first, int g, int c, int t, int nt)
+{
+    if (t == 0) return 0;
+    const long long u = first(c);
+    if (t > u - first(c - 1)) return 0;
+    int n = 2;
+    while (c + n - 1 < g && first(c + n - 1) < u - t + nt) ++n;
+    return n;
+}
 
 // One CTA: entries of both classes in the order of the sequences, the units
 // before each, and where each CTA of the attention kernels starts.
@@ -128,6 +131,8 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
     // are read back from memory)
     __shared__ long long s_base[2][PLAN_KEPT];
     __shared__ int s_nt[2][PLAN_KEPT];
+    __shared__ long long s_first[PLAN_CTAS + 1];  // first unit of each share
+    __shared__ int4 s_at[PLAN_CTAS + 1];          // its entry, head, tile
     pg_go();
     const int lane = threadIdx.x & 31;
     long long carry = 0;  // entries so far: small in the low half, large in the high one
@@ -188,28 +193,56 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
         __syncthreads();
         Shares sh;
         sh.set(total, pl.G);
-        for (int c = threadIdx.x; c < pl.G; c += PLAN_THREADS) {
-            PgStart st = {};
-            int4 m = make_int4(0, 0, 0, 0);
+        // Where each share starts.  A share of large items moves to the start of an
+        // item that is near: an item cut in two costs its partial results (2 x 133
+        // KB written and read) and a second start, about as much as PLAN_NEAR tiles
+        // (windowed chunks 102.3 us without, 98.4 at 3, 95.5 at 6; a window of 4096
+        // 221.4, 219.5, 231.2; an 8-bit mixed step 186.3, 185.0, 197.3).
+        for (int c = threadIdx.x; c <= sh.g; c += PLAN_THREADS) {
+            long long u = sh.first(c);
+            int4 at = make_int4(0, 0, 0, 0);
             if (c < sh.g) {
-                const long long u = sh.first(c);
                 int a = 0, z = nent - 1;  // the last entry that starts at or before u
                 while (a < z) {
                     const int mid = (a + z + 1) >> 1;
                     if (base(mid) <= u) a = mid;
                     else z = mid - 1;
                 }
-                st.e = pl.ent[a];
-                const int r = (int)(u - base(a)), nt = st.e.ntiles;
-                st.ei = a;
-                st.h = r / nt;
-                st.t = r - st.h * nt;
-                st.left = (int)(sh.first(c + 1) - u);
-                m = make_int4(sh.parts(c, st.t, nt), st.e.tok0, st.e.nt, st.h);
+                const int r = (int)(u - base(a)), nt = tiles(a);
+                at = make_int4(a, r / nt, r % nt, 0);
+                if (k && at.z > 0 && at.z <= PLAN_NEAR) {
+                    u -= at.z;
+                    at.z = 0;
+                } else if (k && at.z > 0 && nt - at.z <= PLAN_NEAR) {
+                    u += nt - at.z;
+                    at.z = 0;
+                    if (++at.y == p.Hkv) {
+                        at.y = 0;
+                        ++at.x;  // (past the last entry: an empty share)
+                    }
+                }
+            }
+            s_first[c] = u;
+            s_at[c] = at;
+        }
+        __syncthreads();
+        auto first = [&](int c) { return s_first[c]; };
+        for (int c = threadIdx.x; c < pl.G; c += PLAN_THREADS) {
+            PgStart st = {};
+            int4 m = make_int4(0, 0, 0, 0);
+            if (c < sh.g && first(c + 1) > first(c)) {
+                const int4 at = s_at[c];
+                st.ei = at.x;
+                st.h = at.y;
+                st.t = at.z;
+                st.left = (int)(first(c + 1) - first(c));
+                st.e = pl.ent[at.x];
+                m = make_int4(parts_at(first, sh.g, c, st.t, st.e.ntiles), st.e.tok0, st.e.nt, st.h);
             }
             pl.start[c] = st;
             pl.cmb[c] = m;
         }
+        __syncthreads();
     }
 }
 
@@ -478,7 +511,8 @@ template <int THREADS> __device__ __forceinline__ void own_plan(const PagedAtten
                     st.left = (int)(sh.first(c + 1) - u);
                     st.e = e;
                     *out = st;
-                    p.small.cmb[c] = make_int4(sh.parts(c, st.t, e.ntiles), e.tok0, e.nt, st.h);
+                    p.small.cmb[c] = make_int4(
+                        parts_at([&](int i) { return sh.first(i); }, sh.g, c, st.t, e.ntiles), e.tok0, e.nt, st.h);
                     break;
                 }
                 base += (long long)e.ntiles * p.Hkv;

@@ -29,10 +29,8 @@ def quantise(x):
     """(codes uint8, exponent + 127 uint8) of rows x [..., 128]."""
     x = x.double().numpy()
     top = np.abs(x).max(-1)
-    e = np.zeros(top.shape, np.int64)
-    for i in np.ndindex(top.shape):
-        if top[i] > 0:
-            e[i] = next((k for k in range(-32, 64) if top[i] <= 448 * 2.0 ** k), 64)
+    e = np.minimum(np.searchsorted(448 * 2.0 ** np.arange(-32, 65), top), 96) - 32  # the least that holds top
+    e[top == 0] = 0
     y = np.clip(x / (2.0 ** e)[..., None], -448, 448)
     pos = E4M3[:127]  # ascending non-negative values
     a = np.abs(y)

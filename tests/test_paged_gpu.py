@@ -400,3 +400,38 @@ def test_fp16_over_long_context_keeps_its_precision(vq):
     """Equal scores over many keys: every weight counts, none may vanish."""
     a = _case(vq, [1], [30000], 1, 1, 128, F16, F16, seed=91, scale=0.0)
     _check(vq, a)
+
+
+# ------------------------------------------------------------- used together
+
+@pytest.mark.parametrize("cache,window,limit", [("float16", 0, 0.01), ("float16", 100, 0.01), ("e4m3", 0, 0.06), ("e4m3", 100, 0.06)])
+def test_the_example_serves_and_compresses(vq, cache, window, limit):
+    """examples/serve_paged.py: prompts in chunks and decodes in one batch, pages
+    given back behind a window, blocks read back for the codecs.  Against plain
+    attention over the uncompressed fp16 keys and values: the fp16 cache adds the
+    weights' and outputs' rounding (2^-11 each; 0.01 leaves room for the plain
+    side's 32-bit sums), e4m3 entries are off by 2^-4 at most and 2^-4 / sqrt(3)
+    in the mean, of keys (which move a weight by their score's error, about
+    2^-4 / sqrt(3) / sqrt(3) of a unit score) and values, averaged over the keys
+    that carry the weight: below the 0.06 of a single entry."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import serve_paged
+    got, want, pages, done = serve_paged.serve(prompts=(300, 177, 512, 130), steps=8, cache=cache, window=window, seed=3)
+    off = float((got - want).norm() / want.norm())
+    assert off < limit, off
+    if window:
+        held = sum(p >= 0 for r in pages.table for p in r)
+        assert held <= 4 * (1 + 100 // 16 + 2)
+    else:
+        kivi, rvq, tokens = serve_paged.compress(pages, done)
+        assert tokens == 128
+        k, v = vq.vq_kivi_unpack_dequant(kivi, 4, 8, 128, 2, 32)
+        c1, _, c2, _ = vq.vq_rvq_codebook(D, 2)
+        kr = vq.vq_rvq_unpack_dequant(*rvq, 2, c1, c2)
+        lens = torch.tensor(done, dtype=torch.int32, device="cuda")
+        k0, v0 = vq.vq_paged_gather(pages.cache, pages.device_table(), lens, 128, dtype=F16)
+        for a, b in ((k, k0), (v, v0), (kr, k0)):
+            assert float((a.float() - b.float()).norm() / b.float().norm()) < 0.6  # 2-bit codes
+    _clean(vq)
