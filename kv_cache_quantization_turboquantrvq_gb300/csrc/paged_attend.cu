@@ -447,17 +447,6 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, fl
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Four e4m3 codes as two pairs of T (exact: both types hold every code).
-template <class T> __device__ __forceinline__ void codes4(uint32_t four, uint32_t &lo, uint32_t &hi);
-template <> __device__ __forceinline__ void codes4<__half>(uint32_t four, uint32_t &lo, uint32_t &hi)
-{
-    e4m3x4_to_f16x4(four, lo, hi);
-}
-template <> __device__ __forceinline__ void codes4<__nv_bfloat16>(uint32_t four, uint32_t &lo, uint32_t &hi)
-{
-    e4m3x4_to_bf16x4(four, 0x7b807b80u, lo, hi);  // 2^120
-}
-
 // The plan of a call whose sequences are all small, made by every CTA for itself
 // (a kernel for it cost a launch, 4 us before the first copy): the start of CTA c
 // into `ws` as a PgStart, what is merged there into the plan's cmb.  Entries are
@@ -529,7 +518,7 @@ template <class T, bool Q8, int NT>
 __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kernel(const __grid_constant__ PagedAttendParams p)
 {
     using L = SmShape<Q8, NT>;
-    using TV = typename std::conditional<Q8, __half, T>::type;  // operand type of the value product
+    using TV = typename std::conditional<Q8, __half, T>::type;  // operand type of both products
     extern __shared__ __align__(128) unsigned char smem_raw[];
     unsigned char *stages = smem_1k(smem_raw);
     float *merge = reinterpret_cast<float *>(stages + L::STAGES * L::STAGE);
@@ -694,6 +683,34 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                 qf[nt][4 * j + 3] = w.w;
             }
         }
+        // Over codes the operands are fp16, which one instruction makes of a pair
+        // of codes (bf16 takes five): bf16 queries become fp16 by a power of two
+        // for each row that brings its largest entry to [2^14, 2^15): exact but
+        // for entries 2^-28 of that and below.
+        float back_q[2 * NT];
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) back_q[i] = 1.0f;
+        if constexpr (Q8 && std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                uint32_t top = 0u;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) top = __vmaxu2(top, qf[nt][j] & 0x7fff7fffu);
+                top = max(top & 0xffffu, top >> 16);
+                top = max(top, __shfl_xor_sync(FULL_MASK, top, 1));
+                top = max(top, __shfl_xor_sync(FULL_MASK, top, 2));
+                const int e = max((int)(top >> 7) - 127, -100);
+                const float f = pow2f(14 - e);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qf[nt][j]));
+                    qf[nt][j] = pack2<__half>(v.x * f, v.y * f);
+                }
+                const float b = pow2f(e - 14);  // of row 8 nt + g8; wanted of rows 8 nt + 2 t4 + {0, 1}
+#pragma unroll
+                for (int i = 0; i < 2; ++i) back_q[2 * nt + i] = __shfl_sync(FULL_MASK, b, 4 * (2 * t4 + i));
+            }
+        }
         // the rows of this lane's results are 8 nt + 2 t4 + {0, 1}; their
         // visible keys: j <= pos, and the window
         int pos[2 * NT], low[2 * NT];
@@ -743,11 +760,11 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             uint32_t a0, a1, a2, a3;
-                            codes4<T>(xa[j], a0, a2);
-                            codes4<T>(xb[j], a1, a3);
+                            e4m3x4_to_f16x4(xa[j], a0, a2);
+                            e4m3x4_to_f16x4(xb[j], a1, a3);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma16<T>(s[nt], a0, a1, a2, a3, qf[nt][8 * q + 2 * j], qf[nt][8 * q + 2 * j + 1]);
+                                mma16<TV>(s[nt], a0, a1, a2, a3, qf[nt][8 * q + 2 * j], qf[nt][8 * q + 2 * j + 1]);
                         }
                     }
                 } else {
@@ -780,7 +797,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[nt][j] = Q8 ? fmaf(s[nt][j], fa[j >> 1], fb[j >> 1]) : s[nt][j] * fa[0];
+                    for (int j = 0; j < 4; ++j) s[nt][j] = Q8 ? fmaf(s[nt][j] * back_q[2 * nt + (j & 1)], fa[j >> 1], fb[j >> 1]) : s[nt][j] * fa[0];
                     if (!whole) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -845,8 +862,8 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                             const uint32_t lo = __byte_perm(x[2 * q] & ka, 0u, 0x3120);
                             const uint32_t hi = __byte_perm(x[2 * q + 1] & kb, 0u, 0x3120);
                             uint32_t a0, a1, a2, a3;
-                            codes4<TV>(lo, a0, a1);
-                            codes4<TV>(hi, a2, a3);
+                            e4m3x4_to_f16x4(lo, a0, a1);
+                            e4m3x4_to_f16x4(hi, a2, a3);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) mma16<TV>(o[nt][n + q], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
                         }
