@@ -813,8 +813,12 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                             *reinterpret_cast<uint4 *>(dst + d1 + 2048 * i) = x1;
                         }
                     };
-                    if (part == 0) convert(T(), false);
-                    else convert(TV(), edge);
+                    if constexpr (std::is_same<T, TV>::value) {
+                        convert(T(), edge && part == 1);  // (one copy of the code)
+                    } else {
+                        if (part == 0) convert(T(), false);
+                        else convert(TV(), edge);
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
