@@ -442,8 +442,8 @@ vq_status vq_paged_gather(const void *k_pages, const void *v_pages, const uint8_
  *   workspace: device memory of at least the size that
  *     vq_paged_attend_workspace reports on the current device, 256-byte
  *     aligned, not shared by calls in flight at the same time.
- * Hq = GQ * Hkv with GQ from 1 to 16.  Results do not depend on the order in
- * which blocks run.
+ * Hq = GQ * Hkv with GQ from 1 to 16; at most 2^30 positions a sequence.  Results
+ * do not depend on the order in which blocks run.
  */
 vq_status vq_paged_attend_workspace(int T, int B, int Hq, int Hkv, int max_q, size_t *bytes);
 vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_stride_h, int q_dtype,

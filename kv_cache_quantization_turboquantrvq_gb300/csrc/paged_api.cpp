@@ -274,7 +274,8 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
     if ((st = attend_plan(T, B, Hq, Hkv, max_q, pl)) != VQ_OK) return st;
     if (!is16(q_dtype) || max_pages < 0 || window < 0 || sinks < 0 || !std::isfinite(scale)) return VQ_ERR_INVALID_ARG;
     if (cache_dtype != VQ_E4M3 && cache_dtype != q_dtype) return VQ_ERR_INVALID_ARG;
-    if ((long long)max_pages * page_size >= (1LL << 31) - 2 * PG_TILE) return VQ_ERR_UNSUPPORTED;
+    // (positions and a window behind them stay within 32 bits)
+    if ((long long)max_pages * page_size > (1LL << 30) || T > (1 << 30)) return VQ_ERR_UNSUPPORTED;
     if (T == 0 || B == 0 || Hq == 0) return VQ_OK;
     if (max_q == 0) return VQ_ERR_INVALID_ARG;
     if ((st = check_view(q, T, Hq, q_stride_t, q_stride_h)) != VQ_OK) return st;
@@ -312,7 +313,7 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
     p.GQ = Hq / Hkv;
     p.max_pages = max_pages;
     p.max_q = max_q;
-    p.window = window;
+    p.window = window <= (long long)max_pages * page_size ? window : 0;  // (longer than any sequence: none)
     p.sinks = sinks;
     p.small_rows = pl.small_rows;
     p.qscale = (float)((double)scale * 1.4426950408889634);

@@ -290,6 +290,15 @@ def test_window_and_first_tokens(vq, dtype, cache, window, sinks):
     _check(vq, _case(vq, news, lens, 1, 4, 16, dtype, cache, window=window, sinks=sinks, seed=window + sinks))
 
 
+def test_window_longer_than_anything(vq):
+    """The largest window and number of first tokens there can be: as without."""
+    a = _case(vq, [1, 40, 3], [200, 90, 1], 1, 4, 16, F16, F16, seed=37)
+    plain = _run(vq, a)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (5, 2 ** 31 - 1), (400, 0)):
+        assert torch.equal(_run(vq, dict(a, window=window, sinks=sinks)), plain)
+    _clean(vq)
+
+
 @pytest.mark.parametrize("dtype,cache", TYPES)
 def test_one_long_sequence_is_split_and_joined(vq, dtype, cache):
     """One sequence over every CTA, single token and chunk, with and without

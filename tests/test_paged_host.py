@@ -96,7 +96,7 @@ def _attend(api, q=A, qst=1024, qsh=128, qt=0, kp=A + M, vp=A + 2 * M, ke=0, ve=
 def test_attend_refusals(api):
     assert _attend(api, D=64) == api.VQ_ERR_UNSUPPORTED
     assert _attend(api, Hq=34) == api.VQ_ERR_UNSUPPORTED             # 17 query heads to a kv head
-    assert _attend(api, mp=1 << 27) == api.VQ_ERR_UNSUPPORTED        # positions past 2^31
+    assert _attend(api, mp=(1 << 26) + 1) == api.VQ_ERR_UNSUPPORTED  # positions past 2^30
     assert _attend(api, Hq=7) == api.VQ_ERR_INVALID_ARG
     assert _attend(api, max_q=0) == api.VQ_ERR_INVALID_ARG
     assert _attend(api, window=-1) == api.VQ_ERR_INVALID_ARG
