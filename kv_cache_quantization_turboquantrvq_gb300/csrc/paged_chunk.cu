@@ -62,13 +62,14 @@ template <bool Q8> struct CkShape {
     static constexpr int STAGES = Q8 ? 3 : 4;   // 16-bit key / value tiles
     static constexpr int RAW = Q8 ? 3 : 0;      // tiles of codes in flight
     static constexpr int META = Q8 ? 2 : 0;     // key tiles whose exponents are unpacked
-    static constexpr int WARPS = Q8 ? 16 : 12;
+    static constexpr int CONV = Q8 ? 8 : 0;     // warps that convert codes
+    static constexpr int WARPS = 12 + CONV;
     static constexpr int THREADS = 32 * WARPS;
-    // registers a thread: at launch, the softmax warps, warps 8-11, warps 12-15;
-    // the shares of all warps add up to the launch's at most
-    static constexpr int REGS = Q8 ? 128 : 168, R_SOFT = Q8 ? 184 : 208, R_CTL = Q8 ? 72 : 88, R_CONV = 72;
-    static_assert(256 * R_SOFT + 128 * R_CTL + (Q8 ? 128 * R_CONV : 0) <= THREADS * REGS, "registers of one CTA");
-    static constexpr int BARS = 2 + 2 * STAGES + 7 + 2 * RAW + 2 * META + 2;
+    // registers a thread: at launch, the softmax warps, warps 8-11, the converting
+    // warps; the shares of all warps add up to the launch's at most
+    static constexpr int REGS = Q8 ? 96 : 168, R_SOFT = Q8 ? 168 : 208, R_CTL = Q8 ? 56 : 88, R_CONV = 40;
+    static_assert(256 * R_SOFT + 128 * R_CTL + 32 * CONV * R_CONV <= THREADS * REGS, "registers of one CTA");
+    static constexpr int BARS = 3 + 2 * STAGES + 7 + 2 * RAW + 2 * META + 2;
     static constexpr int OUTB = Q8 ? 32 : 128;  // bytes a row that a softmax warp lays out at a time for its stores
     static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + 8 * 32 * OUTB + RAW * 2 * PG_TILE +
                                 META * 16 + 8 * BARS + 16;
@@ -216,23 +217,15 @@ template <> __device__ __forceinline__ uint32_t ck_pack<__nv_bfloat16>(float a, 
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// 2^e (e <= 0) twice, as what ck_operand multiplies codes by; 0 where T's range ends.
-template <class T> __device__ __forceinline__ uint32_t ck_factor(int e);
-template <> __device__ __forceinline__ uint32_t ck_factor<__half>(int e)
+// 2^e (e <= 0) twice in fp16; 0 where its range ends.
+__device__ __forceinline__ uint32_t ck_factor(int e)
 {
     e = min(e, 0);
     return 0x00010001u * (e >= -14 ? (uint32_t)(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u);
 }
-template <> __device__ __forceinline__ uint32_t ck_factor<__nv_bfloat16>(int e)
-{
-    // (2^120 of it turns the code's bits, moved to a bf16's place, into its value)
-    return 0x00010001u * ((uint32_t)(120 + 127 + max(min(e, 0), -240)) << 7);
-}
 
-// Four codes times a factor as two pairs of T.
-template <class T> __device__ __forceinline__ void ck_operand(uint32_t four, uint32_t f, uint32_t &lo, uint32_t &hi);
-template <>
-__device__ __forceinline__ void ck_operand<__half>(uint32_t four, uint32_t f, uint32_t &lo, uint32_t &hi)
+// Four codes times a factor as two pairs of fp16.
+__device__ __forceinline__ void ck_operand(uint32_t four, uint32_t f, uint32_t &lo, uint32_t &hi)
 {
     uint32_t a, b;
     e4m3x4_to_f16x4(four, a, b);
@@ -241,10 +234,35 @@ __device__ __forceinline__ void ck_operand<__half>(uint32_t four, uint32_t f, ui
     lo = *reinterpret_cast<const uint32_t *>(&x);
     hi = *reinterpret_cast<const uint32_t *>(&y);
 }
-template <>
-__device__ __forceinline__ void ck_operand<__nv_bfloat16>(uint32_t four, uint32_t f, uint32_t &lo, uint32_t &hi)
+
+// One row of a bf16 query tile becomes fp16, by a power of two that brings its
+// largest entry to [2^14, 2^15): exact but for entries 2^-28 of that and below.
+// Returns the power that undoes it.
+__device__ __forceinline__ float ck_query(unsigned char *tile, int row)
 {
-    e4m3x4_to_bf16x4(four, f, lo, hi);
+    uint32_t top = 0u;
+#pragma unroll 4
+    for (int c = 0; c < 16; ++c) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * HALF_B + swz128(row, c & 7));
+        top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    }
+    const int e = max((int)(max(top & 0xffffu, top >> 16) >> 7) - 127, -100);
+    const float f = pow2f(14 - e);
+#pragma unroll 2
+    for (int c = 0; c < 16; ++c) {
+        uint4 *at = reinterpret_cast<uint4 *>(tile + (c >> 3) * HALF_B + swz128(row, c & 7));
+        uint4 v = *at;
+        auto one = [&](uint32_t &x) {
+            const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x));
+            x = ck_pack<__half>(a.x * f, a.y * f);
+        };
+        one(v.x);
+        one(v.y);
+        one(v.z);
+        one(v.w);
+        *at = v;
+    }
+    return pow2f(e - 14);
 }
 
 // Largest of the bytes that the lanes of a warp hold.
@@ -258,9 +276,10 @@ template <class T, bool Q8>
 __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(const __grid_constant__ PagedAttendParams p)
 {
     using C = CkShape<Q8>;
-    using TV = typename std::conditional<Q8, __half, T>::type;  // weights and values
+    using TV = typename std::conditional<Q8, __half, T>::type;  // of both products' operands
     constexpr int STAGES = C::STAGES;
-    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value, BFV = std::is_same<TV, __nv_bfloat16>::value;
+    constexpr bool BFV = std::is_same<TV, __nv_bfloat16>::value;
+    constexpr bool QC = !std::is_same<T, TV>::value;  // queries are converted
     extern __shared__ __align__(128) unsigned char smem_raw[];
     unsigned char *sq = smem_1k(smem_raw);                  // two query tiles
     unsigned char *skv = sq + 2 * TILE_B;                   // key / value tiles
@@ -273,8 +292,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     uint64_t *s_full = kv_empty + STAGES, *p_full = s_full + 2, *pv_done = p_full + 2, *s_free = pv_done + 2;
     uint64_t *raw_full = s_free + 1, *raw_empty = raw_full + C::RAW;
     uint64_t *meta_full = raw_empty + C::RAW, *meta_empty = meta_full + C::META;
-    uint64_t *drain = meta_empty + C::META;
-    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(drain + 2);
+    uint64_t *drain = meta_empty + C::META, *q_ready = drain + 2;
+    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(q_ready + 1);
     volatile uint32_t *abort_flag = tslot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -283,7 +302,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&kv_full[s], Q8 ? 4 : 1);
+            mbar_init(&kv_full[s], Q8 ? C::CONV : 1);
             mbar_init(&kv_empty[s], 1);
         }
         for (int w = 0; w < 2; ++w) {
@@ -294,14 +313,15 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         mbar_init(s_free, 4);
         for (int s = 0; s < C::RAW; ++s) {
             mbar_init(&raw_full[s], 1);
-            mbar_init(&raw_empty[s], 4);
+            mbar_init(&raw_empty[s], C::CONV);
         }
         for (int s = 0; s < C::META; ++s) {
-            mbar_init(&meta_full[s], 4);
+            mbar_init(&meta_full[s], C::CONV);
             mbar_init(&meta_empty[s], 8);
         }
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
+        mbar_init(q_ready, 8);
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -435,7 +455,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         // ------------------------------------------------ products: warp 9 the
         // scores, warp 10 the values, so that neither's waits hold the other up
         // (one warp for both spent 3600 cycles a tile on waits and issues alone)
-        constexpr uint32_t ID_S = ck_idesc(BF, false), ID_O = ck_idesc(BFV, true);
+        constexpr uint32_t ID_S = ck_idesc(BFV, false), ID_O = ck_idesc(BFV, true);
         const uint64_t dq = qt_desc(smem_u32(sq)), dk = qt_desc(smem_u32(skv)), dv = ck_desc_v(smem_u32(skv));
         const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
         PgRing<STAGES> kv;
@@ -452,7 +472,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 // keys follow keys, or (codes) come in order.
                 if (!Q8 && tiles >= STAGES) await(&kv_empty[kv.s], kv.par ^ 1u);
                 tiles += 2 * (r.tn - r.t0);
-                await(q_full, qpar);
+                await(QC ? q_ready : q_full, qpar);
                 qpar ^= 1u;
                 for (int t = r.t0; t < r.tn && ok; ++t) {
                     await(&kv_full[kv.s], kv.par);
@@ -509,12 +529,22 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         unsigned char *so = sout + warp * 32 * C::OUTB;
         const int tok_in = row / p.GQ;
         const float qabs = fabsf(p.qscale);
-        uint32_t spar = 0, vpar = 0;
+        uint32_t spar = 0, vpar = 0, qpar = 0;
         PgRing<STAGES> vs;  // (16-bit cache) slot of the next tile that the products take
         PgRing<C::META ? C::META : 1> mt;
         bool ok = true;
         do {
             const int nq = r.e.nt > tqt ? 2 : 1;
+            float back_q = 1.0f;
+            if constexpr (QC) {
+                ok = __all_sync(FULL_MASK, wait(q_full, qpar));  // (a warp without rows too: not an item ahead)
+                qpar ^= 1u;
+                if (!ok) break;
+                if (w < nq) back_q = ck_query(sq + w * TILE_B, row);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_ready);
+            }
             if (w >= nq) {  // this half has no rows in the item
                 if constexpr (Q8) {
                     for (int t = r.t0; t < r.tn && ok; ++t) {
@@ -562,7 +592,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 float mul = qabs, add = 0.0f, back = 1.0f;
                 if constexpr (Q8) {
                     const float4 f = smeta[mt.s];
-                    mul = f.x;
+                    mul = QC ? fminf(f.x * back_q, 3.0e38f) : f.x;
                     add = f.y;
                     back = f.z;
                     __syncwarp();
@@ -742,12 +772,14 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         ck_reg_dec<C::R_CONV>();
         // ------------------------------------------------ codes to 16-bit operands
         const int j = threadIdx.x - 12 * 32;
+        constexpr int STEP = 4 * C::CONV, ROWS = PG_TILE / STEP;
+        static_assert(ROWS == 4, "a byte each of a word");
         PgRing<C::RAW ? C::RAW : 1> raw;
         PgRing<STAGES> kv;
         PgRing<C::META ? C::META : 1> mt;
         int tiles = 0, keys = 0;
         uint32_t vtop0 = 0, vtop1 = 0;  // exponents of the values to come: of tile u - 1, of tile u
-        uint64_t vrow0 = 0, vrow1 = 0;
+        uint32_t vrow0 = 0, vrow1 = 0;
         bool ok = true;
         do {
             PgView view;
@@ -761,9 +793,9 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     if (ok && tiles >= STAGES) ok = __all_sync(FULL_MASK, wait(&kv_empty[kv.s], kv.par ^ 1u));
                     if (ok && part == 0 && keys >= C::META) ok = __all_sync(FULL_MASK, wait(&meta_empty[mt.s], mt.par ^ 1u));
                     if (!ok) break;
-                    // rows of this thread: j / 8 + 16 i
+                    // rows of this thread: j / 8 + 4 CONV i
                     uint32_t top;         // the tile's largest exponent
-                    uint64_t rows = 0;    // this thread's rows' exponents, a byte each
+                    uint32_t rows = 0;    // this thread's rows' exponents, a byte each
                     if (part == 0) {
                         const uint32_t *e4 = reinterpret_cast<const uint32_t *>(sexp + raw.s * 2 * PG_TILE) + lane;
                         uint32_t see = 0xffffffffu;  // of this lane's four keys
@@ -776,10 +808,10 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                         vtop1 = max(ck_top(e4[PG_TILE / 4] & see), 87u);
                         const unsigned char *ex = sexp + raw.s * 2 * PG_TILE + (j >> 3);
                         vrow1 = 0;
-#pragma unroll 2
-                        for (int i = 7; i >= 0; --i) {
-                            rows = rows << 8 | ex[16 * i];
-                            vrow1 = vrow1 << 8 | ex[PG_TILE + 16 * i];
+#pragma unroll
+                        for (int i = ROWS - 1; i >= 0; --i) {
+                            rows = rows << 8 | ex[STEP * i];
+                            vrow1 = vrow1 << 8 | ex[PG_TILE + STEP * i];
                         }
                         if (j == 0) {
                             const int A = (int)top - 127, B = (int)vtop1 - 127;
@@ -797,27 +829,19 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     // first, so that the eight fill all banks
                     const bool odd = (j & 4) != 0;
                     const uint32_t d0 = swz128(j >> 3, 2 * (j & 3) + odd), d1 = swz128(j >> 3, 2 * (j & 3) + !odd);
-                    auto convert = [&](auto tag, bool zero_hidden) {
-                        using X = decltype(tag);
+                    const bool hide = edge && part == 1;  // values of keys that no row sees may hold anything
 #pragma unroll 2
-                        for (int i = 0; i < 8; ++i, rows >>= 8) {
-                            uint4 v = *reinterpret_cast<const uint4 *>(src + 2048 * i);
-                            if (zero_hidden && !view.one(k0 + (j >> 3) + 16 * i)) v = make_uint4(0u, 0u, 0u, 0u);
-                            const uint32_t f = ck_factor<X>((int)((uint32_t)rows & 0xffu) - (int)top);
-                            uint4 x0, x1;
-                            ck_operand<X>(odd ? v.z : v.x, f, x0.x, x0.y);
-                            ck_operand<X>(odd ? v.w : v.y, f, x0.z, x0.w);
-                            ck_operand<X>(odd ? v.x : v.z, f, x1.x, x1.y);
-                            ck_operand<X>(odd ? v.y : v.w, f, x1.z, x1.w);
-                            *reinterpret_cast<uint4 *>(dst + d0 + 2048 * i) = x0;
-                            *reinterpret_cast<uint4 *>(dst + d1 + 2048 * i) = x1;
-                        }
-                    };
-                    if constexpr (std::is_same<T, TV>::value) {
-                        convert(T(), edge && part == 1);  // (one copy of the code)
-                    } else {
-                        if (part == 0) convert(T(), false);
-                        else convert(TV(), edge);
+                    for (int i = 0; i < ROWS; ++i, rows >>= 8) {
+                        uint4 v = *reinterpret_cast<const uint4 *>(src + 128 * STEP * i);
+                        if (hide && !view.one(k0 + (j >> 3) + STEP * i)) v = make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t f = ck_factor((int)(rows & 0xffu) - (int)top);
+                        uint4 x0, x1;
+                        ck_operand(odd ? v.z : v.x, f, x0.x, x0.y);
+                        ck_operand(odd ? v.w : v.y, f, x0.z, x0.w);
+                        ck_operand(odd ? v.x : v.z, f, x1.x, x1.y);
+                        ck_operand(odd ? v.y : v.w, f, x1.z, x1.w);
+                        *reinterpret_cast<uint4 *>(dst + d0 + 128 * STEP * i) = x0;
+                        *reinterpret_cast<uint4 *>(dst + d1 + 128 * STEP * i) = x1;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
