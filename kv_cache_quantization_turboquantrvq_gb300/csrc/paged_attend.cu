@@ -35,7 +35,8 @@ constexpr float NEG_INF = -__builtin_huge_valf();
 // ---------------------------------------------------------------- the plan
 
 constexpr int PLAN_THREADS = 1024;
-constexpr int PLAN_NEAR = 3;     // tiles
+constexpr int PLAN_NEAR = 2;     // tiles
+constexpr int PLAN_ITEM = 3, PLAN_ITEM_Q8 = 4;  // tiles
 constexpr int PLAN_KEPT = 1024;  // entries whose sums stay in shared memory
 
 // Exclusive sum over the block; `total` gets the sum of all.
@@ -191,25 +192,38 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
             total += all;
         }
         __syncthreads();
+        // Shares of large items are even in cost: a tile is one, and an item costs as
+        // much as `item` tiles besides (its first products wait for queries, keys
+        // and a softmax, and it writes its output).  Found by fitting the CTAs'
+        // times of the chunk kernel: 1.5 us a tile and 5.0 a run of an item over a
+        // 16-bit cache, 1.8 and 7.3 over codes.
+        const int item = k ? (p.c.ke ? PLAN_ITEM_Q8 : PLAN_ITEM) : 0;
+        auto cost = [&](int i) { return base(i) + (long long)i * item * p.Hkv; };  // before entry i
         Shares sh;
-        sh.set(total, pl.G);
+        sh.set(total + (long long)nent * item * p.Hkv, (int)min((long long)pl.G, total));
         // Where each share starts.  A share of large items moves to the start of an
-        // item that is near: an item cut in two costs its partial results (2 x 133
-        // KB written and read) and a second start, about as much as PLAN_NEAR tiles
-        // (windowed chunks 102.3 us without, 98.4 at 3, 95.5 at 6; a window of 4096
-        // 221.4, 219.5, 231.2; an 8-bit mixed step 186.3, 185.0, 197.3).
+        // item that is at most PLAN_NEAR tiles away: an item cut in two costs its
+        // partial results (2 x 133 KB written and read) and a second start.  With
+        // shares even in tiles (item 0) and none moved: three chunks of 300 to 1000
+        // tokens 162 us, a mixed step over codes 164, one of 12 chunks in 32
+        // sequences 472; with item 3 or 4 and NEAR 2: 155, 152, 419; with NEAR 3:
+        // 156, 151, 419, but a window of 4096 231 us against 224.
         for (int c = threadIdx.x; c <= sh.g; c += PLAN_THREADS) {
-            long long u = sh.first(c);
+            const long long x = sh.first(c);
+            long long u = total;
             int4 at = make_int4(0, 0, 0, 0);
             if (c < sh.g) {
-                int a = 0, z = nent - 1;  // the last entry that starts at or before u
+                int a = 0, z = nent - 1;  // the last entry that starts at or before x
                 while (a < z) {
                     const int mid = (a + z + 1) >> 1;
-                    if (base(mid) <= u) a = mid;
+                    if (cost(mid) <= x) a = mid;
                     else z = mid - 1;
                 }
-                const int r = (int)(u - base(a)), nt = tiles(a);
-                at = make_int4(a, r / nt, r % nt, 0);
+                const int nt = tiles(a);
+                const long long r = x - cost(a), one = (long long)item + nt;
+                const int h = (int)(r / one);
+                at = make_int4(a, h, max(0, (int)(r - h * one) - item), 0);
+                u = base(a) + (long long)h * nt + at.z;
                 if (k && at.z > 0 && at.z <= PLAN_NEAR) {
                     u -= at.z;
                     at.z = 0;
@@ -360,7 +374,7 @@ __global__ void __launch_bounds__(32 * CB_WARPS) paged_combine_kernel(const __gr
 // maximum, sum and output of its own in registers, in groups of 8 that take the
 // tiles in turn.  What bounds a warp is the latency of its chain (wait, scores,
 // maximum, weights, product), so the copies' page lookups and waits are not in
-// it, and two groups hide one another's (8-bit cache: 350 -> ? us).
+// it, and over codes, which take more work a byte, two groups hide one another's.
 //
 // Both products are 16 x 8 x 16 mma.sync with the cache as the 16-row operand:
 // S^T = K Q^T and O^T += V^T W^T, the query rows in the 8-wide dimension, where

@@ -18,12 +18,18 @@
 // Roles (one CTA per SM): two groups of 4 softmax warps, a thread per query
 // row; one warp that streams queries, keys and values by TMA (a box per page);
 // two warps that issue tcgen05.mma, one for scores, one for values.  With an
-// 8-bit cache four more warps turn the codes into 16-bit operands in shared
-// memory.
+// 8-bit cache eight more warps turn the codes into fp16 operands in shared
+// memory (four took 857 us for 4096 fp16 queries over 16384 keys, eight 767; the
+// same chunk over a 16-bit cache 634).
+//
+// What bounds it (that chunk, 16-bit cache: 1.52 PFLOP/s): a pair of tiles takes
+// 1.5 us where the products take 1.07; the score tile waits for its copy to
+// registers between products, and shared memory has 0.75 of that time to feed
+// the operands and take the copies.  A run of an item takes 5 us besides its tiles (7 over codes): the
+// first keys' way through the pipeline and the output's to memory.
 //
 // 8-bit cache.  A factor per key inside the softmax (2 x 128 numbers a tile to
-// every thread) cost more than the softmax itself: 1306 us against 830 for the
-// same chunk over a 16-bit cache.  So the exponents are split in a tile's largest
+// every thread) cost more than the softmax itself.  So the exponents are split in a tile's largest
 // among the keys that are seen, A of keys and B of values, and each key's rest:
 // the operands are code * 2^(a - A) and code * 2^(b - B), and a tile's two
 // exponents act once per score: t = scale 2^A (q . K') + B, w = 2^(t - M) with M
@@ -31,6 +37,10 @@
 // but for the smallest entries of rows more than 2^15 below the tile's largest
 // (fp16; off by 2^-25 2^A, 2^-33 of the largest row: less than the 32-bit sums
 // of that row's own products), so no weight or value leaves its type's range.
+// Operands are fp16 whatever the queries' type, since one instruction makes them
+// of two codes (bf16 takes five: 996 us against 884 for the chunk above, with
+// four warps); bf16 queries become fp16 by a power of two for each row, in place,
+// while the output of the item before is still to be written.
 //
 // The output is rescaled only when a row's maximum grew by more than 2^LAG
 // (the softmax warps do it in tensor memory between two products), so weights
@@ -70,8 +80,7 @@ template <bool Q8> struct CkShape {
     static constexpr int REGS = Q8 ? 96 : 168, R_SOFT = Q8 ? 168 : 208, R_CTL = Q8 ? 56 : 88, R_CONV = 40;
     static_assert(256 * R_SOFT + 128 * R_CTL + 32 * CONV * R_CONV <= THREADS * REGS, "registers of one CTA");
     static constexpr int BARS = 3 + 2 * STAGES + 7 + 2 * RAW + 2 * META + 2;
-    static constexpr int OUTB = Q8 ? 32 : 128;  // bytes a row that a softmax warp lays out at a time for its stores
-    static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + 8 * 32 * OUTB + RAW * 2 * PG_TILE +
+    static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + RAW * 2 * PG_TILE +
                                 META * 16 + 8 * BARS + 16;
 };
 static_assert(CkShape<false>::SMEM <= 232448 && CkShape<true>::SMEM <= 232448, "shared memory of one CTA");
@@ -265,6 +274,14 @@ __device__ __forceinline__ float ck_query(unsigned char *tile, int row)
     return pow2f(e - 14);
 }
 
+// 32 bytes to an address that is a multiple of 32.
+__device__ __forceinline__ void ck_store32(float *at, const uint32_t *v)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Largest of the bytes that the lanes of a warp hold.
 __device__ __forceinline__ uint32_t ck_top(uint32_t four)
 {
@@ -284,8 +301,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     unsigned char *sq = smem_1k(smem_raw);                  // two query tiles
     unsigned char *skv = sq + 2 * TILE_B;                   // key / value tiles
     unsigned char *sraw = skv + STAGES * TILE_B;            // tiles of codes
-    unsigned char *sout = sraw + C::RAW * RAW_B;            // [8 warps][32 rows][OUTB]
-    unsigned char *sexp = sout + 8 * 32 * C::OUTB;          // [RAW][2][128] exponents (of key tiles)
+    unsigned char *sexp = sraw + C::RAW * RAW_B;            // [RAW][2][128] exponents (of key tiles)
     float4 *smeta = reinterpret_cast<float4 *>(sexp + C::RAW * 2 * PG_TILE);  // [META] |scale| 2^A, B, 2^-B
     uint64_t *bars = reinterpret_cast<uint64_t *>(smeta + C::META);
     uint64_t *q_full = bars, *q_empty = bars + 1, *kv_full = bars + 2, *kv_empty = kv_full + STAGES;
@@ -325,15 +341,18 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         *abort_flag = 0u;
         fence_mbar_init();
     }
+    if (warp == 9) tmem_alloc(const_cast<uint32_t *>(tslot), 512);
     pg_wait();  // for the plan
     pg_go();
     PgRun r;
     r.start(p.large.start[blockIdx.x]);
-    if (r.left <= 0) return;  // the whole CTA
-    if (warp == 9) tmem_alloc(const_cast<uint32_t *>(tslot), 512);
     qt_fence_before();
     __syncthreads();
     qt_fence_after();
+    if (r.left <= 0) {  // the whole CTA
+        if (warp == 9) tmem_free(*tslot, 512);
+        return;
+    }
     const uint32_t tmem = *tslot;  // scores at 0, weights at 128 and 192, outputs at 256 and 384
 
     // Bounded wait; gives up (and makes every role give up) after the limit.
@@ -526,35 +545,23 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         const int row = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes, tp = tmem + lanes + 128 + 64 * w, to = tmem + lanes + 256 + 128 * w;
-        unsigned char *so = sout + warp * 32 * C::OUTB;
         const int tok_in = row / p.GQ;
         const float qabs = fabsf(p.qscale);
         uint32_t spar = 0, vpar = 0, qpar = 0;
         PgRing<STAGES> vs;  // (16-bit cache) slot of the next tile that the products take
         PgRing<C::META ? C::META : 1> mt;
         bool ok = true;
+        float back_q = 1.0f;  // undoes the power of two in this row of converted queries
+        bool live = !QC;      // false: before the first item, whose queries are then made ready
         do {
-            const int nq = r.e.nt > tqt ? 2 : 1;
-            float back_q = 1.0f;
-            if constexpr (QC) {
-                ok = __all_sync(FULL_MASK, wait(q_full, qpar));  // (a warp without rows too: not an item ahead)
-                qpar ^= 1u;
-                if (!ok) break;
-                if (w < nq) back_q = ck_query(sq + w * TILE_B, row);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_ready);
-            }
-            if (w >= nq) {  // this half has no rows in the item
-                if constexpr (Q8) {
-                    for (int t = r.t0; t < r.tn && ok; ++t) {
-                        ok = __all_sync(FULL_MASK, wait(&meta_full[mt.s], mt.par));  // (not ahead of its tile)
-                        if (lane == 0) mbar_arrive(&meta_empty[mt.s]);
-                        mt.step();
-                    }
-                    if (!ok) break;
+            const bool rows = live && (w == 0 || r.e.nt > tqt);  // this half has rows in the item
+            if (Q8 && live && !rows) {
+                for (int t = r.t0; t < r.tn && ok; ++t) {
+                    ok = __all_sync(FULL_MASK, wait(&meta_full[mt.s], mt.par));  // (not ahead of its tile)
+                    if (lane == 0) mbar_arrive(&meta_empty[mt.s]);
+                    mt.step();
                 }
-                continue;
+                if (!ok) break;
             }
             PgView view;
             view.set(r.e, p.window, p.sinks);
@@ -564,8 +571,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
             const int low = p.window > 0 ? pos - p.window + 1 : 0;
             const int pos_a = r.e.p0 + w * tqt, pos_z = r.e.p0 + min(r.e.nt, (w + 1) * tqt) - 1;  // this tile's tokens
             float m = NEG_INF, l = 0.0f;
-            vs.step();
-            for (int t = r.t0; t < r.tn; ++t) {
+            if (rows) vs.step();
+            for (int t = rows ? r.t0 : r.tn; t < r.tn; ++t) {
                 const int k0 = pg_tile_key(r.e, t);
                 if (t + 1 < r.tn) vs.step();  // now at the values of tile t
                 const bool whole = k0 + PG_TILE <= pos_a + 1 &&
@@ -592,7 +599,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 float mul = qabs, add = 0.0f, back = 1.0f;
                 if constexpr (Q8) {
                     const float4 f = smeta[mt.s];
-                    mul = QC ? fminf(f.x * back_q, 3.0e38f) : f.x;
+                    mul = QC ? fminf(fmaxf(f.x * back_q, 1e-37f), 3e38f) : f.x;  // (finite, and -inf times it stays)
                     add = f.y;
                     back = f.z;
                     __syncwarp();
@@ -695,10 +702,25 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 if (lane == 0) mbar_arrive(&p_full[w]);
             }
             if (!ok) break;
-            ok = __all_sync(FULL_MASK, wait(&pv_done[w], vpar));
-            vpar ^= 1u;
-            if (!ok) break;
-            qt_fence_after();
+            if (rows) {
+                ok = __all_sync(FULL_MASK, wait(&pv_done[w], vpar));
+                vpar ^= 1u;
+                if (!ok) break;
+                qt_fence_after();
+            }
+            if (QC && (!live || r.left > r.tn - r.t0)) {
+                // the next item's queries, before the output of this one (both
+                // halves, whether they will have rows or not: what a tile without
+                // rows holds is not used)
+                ok = __all_sync(FULL_MASK, wait(q_full, qpar));
+                qpar ^= 1u;
+                if (!ok) break;
+                back_q = ck_query(sq + w * TILE_B, row);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_ready);
+            }
+            if (!rows) continue;
             const bool split = r.t0 > 0 || r.tn < r.e.ntiles;
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             float *part = p.large.part + (size_t)(2 * blockIdx.x + (r.first && r.t0 > 0 ? 0 : 1)) * (PG_LROWS * PG_PART);
@@ -706,68 +728,31 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 part[128 * w + row] = m;
                 part[PG_LROWS + 128 * w + row] = l;
             }
-            // A thread holds a row; stores of one row by many lanes fill whole
-            // sectors, so the warp passes each OUTB bytes of its 32 rows through
-            // shared memory (16-byte pieces exchanged against bank conflicts).
-            constexpr int PIECES = C::OUTB / 16, SWZ = PIECES - 1;
-            const int r4 = lane / PIECES, pc = lane % PIECES;  // row (of 32 / PIECES at a time) and piece of a store
-            auto put = [&](int i, uint4 v) { *reinterpret_cast<uint4 *>(so + lane * C::OUTB + ((i ^ (lane & SWZ)) << 4)) = v; };
-            auto get = [&](int rr) { return *reinterpret_cast<const uint4 *>(so + rr * C::OUTB + ((pc ^ (rr & SWZ)) << 4)); };
-            constexpr int COLS = C::OUTB / 4;  // columns of a block (half as many registers again for 16-bit rows)
+            // A thread holds a row and stores 32 bytes of it at a time, a whole sector.
+            T *dst = static_cast<T *>(p.out) + ((size_t)(r.e.tok0 + tok) * p.Hq + (size_t)r.h * p.GQ + row % p.GQ) * D;
 #pragma unroll 1
-            for (int b = 0; b < D / COLS; ++b) {
-                uint32_t y[COLS < 16 ? 16 : COLS];
-                if constexpr (COLS == 32) qt_ld32(to + COLS * b, y);
-                else ck_ld16(to + (COLS * b & ~15), y);
+            for (int b = 0; b < 4; ++b) {
+                uint32_t y[32];
+                qt_ld32(to + 32 * b, y);
                 qt_wait_ld();
-                if constexpr (COLS == 32) qt_hold(y);
-                else ck_hold16(y);
-                const int o = COLS < 16 && (b & 1) ? COLS : 0;
+                qt_hold(y);
+                if (!mine) continue;
                 if (split) {
 #pragma unroll
-                    for (int i = 0; i < PIECES; ++i) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] = o ? y[(COLS + 4 * i + j) % (COLS < 16 ? 16 : COLS)] : y[4 * i + j];
-                        put(i, make_uint4(v[0], v[1], v[2], v[3]));
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int rr = r4; rr < 32; rr += 32 / PIECES)
-                        *reinterpret_cast<uint4 *>(part + 2 * PG_LROWS + (size_t)(128 * w + 32 * (warp & 3) + rr) * D + COLS * b +
-                                                   4 * pc) = get(rr);
-                    __syncwarp();
+                    for (int i = 0; i < 4; ++i) ck_store32(part + 2 * PG_LROWS + (size_t)(128 * w + row) * D + 32 * b + 8 * i, y + 8 * i);
                 } else {
-                    // half a block of 16-bit output; two blocks make OUTB bytes
-                    const int half = (b & 1) * (PIECES / 2);
 #pragma unroll
-                    for (int i = 0; i < PIECES / 2; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         uint32_t v[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int c = 8 * i + 2 * j;
-                            const uint32_t lo = o ? y[(COLS + c) % (COLS < 16 ? 16 : COLS)] : y[c];
-                            const uint32_t hi = o ? y[(COLS + c + 1) % (COLS < 16 ? 16 : COLS)] : y[c + 1];
-                            v[j] = ck_pack<T>(__uint_as_float(lo) * inv, __uint_as_float(hi) * inv);
-                        }
-                        put(half + i, make_uint4(v[0], v[1], v[2], v[3]));
-                    }
-                    if (b & 1) {
-                        __syncwarp();
-#pragma unroll
-                        for (int rr = r4; rr < 32; rr += 32 / PIECES) {
-                            const int q = 32 * (warp & 3) + rr, qt = q / p.GQ, tk = w * tqt + qt;
-                            if (qt < tqt && tk < r.e.nt)
-                                *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) +
-                                                           ((size_t)(r.e.tok0 + tk) * p.Hq + (size_t)r.h * p.GQ + q % p.GQ) * D +
-                                                           2 * COLS * (b >> 1) + 8 * pc) = get(rr);
-                        }
-                        __syncwarp();
+                        for (int c = 0; c < 4; ++c)
+                            v[c] = ck_pack<T>(__uint_as_float(y[8 * i + 2 * c]) * inv, __uint_as_float(y[8 * i + 2 * c + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(dst + 32 * b + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
             }
             qt_fence_before();  // (ordered before the next run's products by p_full)
-        } while (r.next(p.large, p.Hkv));
+        } while (live ? r.next(p.large, p.Hkv) : (live = true));
     } else if constexpr (Q8) {
         ck_reg_dec<C::R_CONV>();
         // ------------------------------------------------ codes to 16-bit operands
@@ -821,8 +806,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                         top = vtop0;
                         rows = vrow0;
                     }
-                    // (short loops: unrolled in full, the warps' code no longer
-                    // fitted the instruction caches, 1832 us for the chunk of 4096)
+                    // (a short loop: unrolled in full, the warps' code no longer
+                    // fitted the instruction caches and a chunk took twice as long)
                     const unsigned char *src = sraw + raw.s * RAW_B + swz128(j >> 3, j & 7);  // 16 rows on: the same swizzle
                     unsigned char *dst = skv + kv.s * TILE_B + ((j & 7) >> 2) * HALF_B;
                     // eight lanes hold a row; the upper four store their second half

@@ -30,20 +30,6 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t &lo, uin
         : "r"(four));
 }
 
-// Four codes as two bf16 pairs times f / 2^120 (a bf16 twice): sign, exponent
-// and fraction moved to a bf16's places give value * 2^-120, subnormal codes as
-// subnormal bf16, which the product takes.
-__device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t four, uint32_t f, uint32_t &lo, uint32_t &hi)
-{
-    const uint32_t h0 = __byte_perm(four, 0u, 0x1404), h1 = __byte_perm(four, 0u, 0x3424);
-    const uint32_t a = ((h0 >> 4) & 0x07f007f0u) | (h0 & 0x80008000u), b = ((h1 >> 4) & 0x07f007f0u) | (h1 & 0x80008000u);
-    const __nv_bfloat162 g = *reinterpret_cast<const __nv_bfloat162 *>(&f);
-    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), g);
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&b), g);
-    lo = *reinterpret_cast<const uint32_t *>(&x);
-    hi = *reinterpret_cast<const uint32_t *>(&y);
-}
-
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
