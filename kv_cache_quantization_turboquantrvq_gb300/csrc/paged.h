@@ -96,7 +96,10 @@ struct PagedAttendParams {
 };
 constexpr int PG_SROWS = 16;     // rows of a small item
 constexpr int PG_LROWS = 256;    // rows of a large item (two tensor-memory tiles)
-constexpr int PG_PART = 2 + 128; // floats of a row's partial result: max, sum, output
+// Floats of a row's partial result.  A slot holds the rows' maxima, then their
+// sums, then their outputs: of small items row by row, of large ones 32 rows by
+// 32, and of those 8 columns after another, each [32 rows][8].
+constexpr int PG_PART = 2 + 128;
 
 
 // A launch that may start while the kernel before it in the stream still runs

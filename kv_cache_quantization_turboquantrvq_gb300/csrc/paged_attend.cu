@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
 // ------------------------------------------------------- the merge of parts
 
 constexpr int CB_WARPS = 8;
-constexpr int CB_LARGE = 4;  // rows of a warp: large items (few parts, many rows)
+constexpr int CB_LARGE = 2;  // rows of a warp: large items (few parts, many rows; 4 rows and two blocks an SM: 1.5 us more)
 static_assert(PG_LROWS % (CB_WARPS * CB_LARGE) == 0 && PG_SROWS % CB_WARPS == 0, "whole blocks");
 
 template <class T> __device__ __forceinline__ uint2 pack4(float4 v);
@@ -308,7 +308,9 @@ __device__ __forceinline__ void merge_rows(const PagedAttendParams &p, const flo
             for (int j = 0; j < R; ++j) {
                 m[j][i] = s[j];
                 l[j][i] = s[ROWS + j];
-                o[j][i] = *reinterpret_cast<const float4 *>(s - r0 + 2 * ROWS + (size_t)(r0 + j) * D + 4 * lane);
+                const int r = r0 + j, at4 = ROWS == PG_LROWS ? (r & ~31) * D + (lane >> 1) * 256 + (r & 31) * 8 + (lane & 1) * 4
+                                                             : r * D + 4 * lane;
+                o[j][i] = *reinterpret_cast<const float4 *>(s - r0 + 2 * ROWS + at4);
             }
         }
 #pragma unroll
@@ -347,7 +349,7 @@ __device__ __forceinline__ void merge_rows(const PagedAttendParams &p, const flo
 // Blocks x: the CTAs at whose start an item may have to be merged; blocks y: rows
 // of large items, then of small ones.
 template <class T>
-__global__ void __launch_bounds__(32 * CB_WARPS) paged_combine_kernel(const __grid_constant__ PagedAttendParams p)
+__global__ void __launch_bounds__(32 * CB_WARPS, 4) paged_combine_kernel(const __grid_constant__ PagedAttendParams p)
 {
     pg_wait();
     const int first_small = p.large.cap ? PG_LROWS / (CB_WARPS * CB_LARGE) : 0;

@@ -77,10 +77,11 @@ template <bool Q8> struct CkShape {
     static constexpr int THREADS = 32 * WARPS;
     // registers a thread: at launch, the softmax warps, warps 8-11, the converting
     // warps; the shares of all warps add up to the launch's at most
-    static constexpr int REGS = Q8 ? 96 : 168, R_SOFT = Q8 ? 168 : 208, R_CTL = Q8 ? 56 : 88, R_CONV = 40;
+    static constexpr int REGS = Q8 ? 96 : 168, R_SOFT = Q8 ? 176 : 208, R_CTL = Q8 ? 40 : 88, R_CONV = 40;
     static_assert(256 * R_SOFT + 128 * R_CTL + 32 * CONV * R_CONV <= THREADS * REGS, "registers of one CTA");
     static constexpr int BARS = 3 + 2 * STAGES + 7 + 2 * RAW + 2 * META + 2;
-    static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + RAW * 2 * PG_TILE +
+    static constexpr int RUNS = 8 * 64;         // the softmax warps' runs
+    static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + RUNS + RAW * 2 * PG_TILE +
                                 META * 16 + 8 * BARS + 16;
 };
 static_assert(CkShape<false>::SMEM <= 232448 && CkShape<true>::SMEM <= 232448, "shared memory of one CTA");
@@ -250,14 +251,14 @@ __device__ __forceinline__ void ck_operand(uint32_t four, uint32_t f, uint32_t &
 __device__ __forceinline__ float ck_query(unsigned char *tile, int row)
 {
     uint32_t top = 0u;
-#pragma unroll 4
+#pragma unroll 8
     for (int c = 0; c < 16; ++c) {
         const uint4 v = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * HALF_B + swz128(row, c & 7));
         top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
     }
     const int e = max((int)(max(top & 0xffffu, top >> 16) >> 7) - 127, -100);
     const float f = pow2f(14 - e);
-#pragma unroll 2
+#pragma unroll 4
     for (int c = 0; c < 16; ++c) {
         uint4 *at = reinterpret_cast<uint4 *>(tile + (c >> 3) * HALF_B + swz128(row, c & 7));
         uint4 v = *at;
@@ -274,8 +275,42 @@ __device__ __forceinline__ float ck_query(unsigned char *tile, int row)
     return pow2f(e - 14);
 }
 
+// A softmax warp keeps its run in shared memory and reads it where it needs it:
+// what it held in registers beside the scores went to local memory, and after
+// the output's stores came back from L2 1.6 us later.
+__device__ __forceinline__ PgRun ck_run(uint32_t at)
+{
+    int v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[4 * i]), "=r"(v[4 * i + 1]), "=r"(v[4 * i + 2]), "=r"(v[4 * i + 3])
+                     : "r"(at + 16 * i)
+                     : "memory");
+    PgRun r;
+    r.e.b = v[0]; r.e.tok0 = v[1]; r.e.nt = v[2]; r.e.p0 = v[3];
+    r.e.hi = v[4]; r.e.nsink = v[5]; r.e.tl = v[6]; r.e.ntiles = v[7];
+    r.ei = v[8]; r.h = v[9]; r.t0 = v[10]; r.tn = v[11];
+    r.left = v[12]; r.first = v[13] != 0;
+    return r;
+}
+__device__ __forceinline__ void ck_keep(uint32_t at, const PgRun &r, int lane)
+{
+    __syncwarp();
+    if (lane == 0) {
+        const int v[16] = {r.e.b, r.e.tok0, r.e.nt, r.e.p0, r.e.hi, r.e.nsink, r.e.tl, r.e.ntiles,
+                           r.ei, r.h, r.t0, r.tn, r.left, (int)r.first, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 16 * i), "r"(v[4 * i]), "r"(v[4 * i + 1]),
+                         "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
+                         : "memory");
+    }
+    __syncwarp();
+}
+
 // 32 bytes to an address that is a multiple of 32.
-__device__ __forceinline__ void ck_store32(float *at, const uint32_t *v)
+__device__ __forceinline__ void ck_store32(void *at, const uint32_t *v)
 {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -301,7 +336,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     unsigned char *sq = smem_1k(smem_raw);                  // two query tiles
     unsigned char *skv = sq + 2 * TILE_B;                   // key / value tiles
     unsigned char *sraw = skv + STAGES * TILE_B;            // tiles of codes
-    unsigned char *sexp = sraw + C::RAW * RAW_B;            // [RAW][2][128] exponents (of key tiles)
+    unsigned char *srun = sraw + C::RAW * RAW_B;            // [8][64] the softmax warps' runs
+    unsigned char *sexp = srun + C::RUNS;                   // [RAW][2][128] exponents (of key tiles)
     float4 *smeta = reinterpret_cast<float4 *>(sexp + C::RAW * 2 * PG_TILE);  // [META] |scale| 2^A, B, 2^-B
     uint64_t *bars = reinterpret_cast<uint64_t *>(smeta + C::META);
     uint64_t *q_full = bars, *q_empty = bars + 1, *kv_full = bars + 2, *kv_empty = kv_full + STAGES;
@@ -553,7 +589,11 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         bool ok = true;
         float back_q = 1.0f;  // undoes the power of two in this row of converted queries
         bool live = !QC;      // false: before the first item, whose queries are then made ready
+        bool more = true;
+        const uint32_t keep = smem_u32(srun + 64 * warp);
+        ck_keep(keep, r, lane);
         do {
+            const PgRun r = ck_run(keep);
             const bool rows = live && (w == 0 || r.e.nt > tqt);  // this half has rows in the item
             if (Q8 && live && !rows) {
                 for (int t = r.t0; t < r.tn && ok; ++t) {
@@ -708,7 +748,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 if (!ok) break;
                 qt_fence_after();
             }
-            if (QC && (!live || r.left > r.tn - r.t0)) {
+            PgRun z = ck_run(keep);
+            if (QC && (!live || z.left > z.tn - z.t0)) {
                 // the next item's queries, before the output of this one (both
                 // halves, whether they will have rows or not: what a tile without
                 // rows holds is not used)
@@ -720,39 +761,59 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_ready);
             }
-            if (!rows) continue;
-            const bool split = r.t0 > 0 || r.tn < r.e.ntiles;
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            float *part = p.large.part + (size_t)(2 * blockIdx.x + (r.first && r.t0 > 0 ? 0 : 1)) * (PG_LROWS * PG_PART);
-            if (split && mine) {
-                part[128 * w + row] = m;
-                part[PG_LROWS + 128 * w + row] = l;
-            }
-            // A thread holds a row and stores 32 bytes of it at a time, a whole sector.
-            T *dst = static_cast<T *>(p.out) + ((size_t)(r.e.tok0 + tok) * p.Hq + (size_t)r.h * p.GQ + row % p.GQ) * D;
-#pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                uint32_t y[32];
-                qt_ld32(to + 32 * b, y);
-                qt_wait_ld();
-                qt_hold(y);
-                if (!mine) continue;
-                if (split) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) ck_store32(part + 2 * PG_LROWS + (size_t)(128 * w + row) * D + 32 * b + 8 * i, y + 8 * i);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            v[c] = ck_pack<T>(__uint_as_float(y[8 * i + 2 * c]) * inv, __uint_as_float(y[8 * i + 2 * c + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(dst + 32 * b + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
+            if (live && (w == 0 || z.e.nt > tqt)) {
+                const int tok = w * tqt + tok_in;
+                const bool mine = tok_in < tqt && tok < z.e.nt;
+                const bool split = z.t0 > 0 || z.tn < z.e.ntiles;
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                float *part = p.large.part + (size_t)(2 * blockIdx.x + (z.first && z.t0 > 0 ? 0 : 1)) * (PG_LROWS * PG_PART);
+                if (split && mine) {
+                    part[128 * w + row] = m;
+                    part[PG_LROWS + 128 * w + row] = l;
                 }
+                // A thread holds a row and stores 32 bytes of it at a time, a whole
+                // sector.  Partial rows lie 32 by 32, 8 columns after another, so that a
+                // warp's store fills whole lines: a sector of a line each took the L1's
+                // data path a cycle a sector, and the next item's products, which read
+                // shared memory by the same path, 3 us longer.
+                T *dst = static_cast<T *>(p.out) + ((size_t)(z.e.tok0 + tok) * p.Hq + (size_t)z.h * p.GQ + row % p.GQ) * D;
+                float *pd = part + 2 * PG_LROWS + (128 * w + row - lane) * D + 8 * lane;
+                const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t y[32];
+                    qt_ld32(to + 32 * b, y);
+                    qt_wait_ld();
+                    qt_hold(y);
+                    if (mine && split) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) ck_store32(pd + 256 * (4 * b + i), y + 8 * i);
+                    } else if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t v[8];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                v[c] = ck_pack<T>(__uint_as_float(y[16 * i + 2 * c]) * inv, __uint_as_float(y[16 * i + 2 * c + 1]) * inv);
+                            if (wide) {
+                                ck_store32(dst + 32 * b + 16 * i, v);
+                            } else {
+                                uint4 *to16 = reinterpret_cast<uint4 *>(dst + 32 * b + 16 * i);
+                                to16[0] = make_uint4(v[0], v[1], v[2], v[3]);
+                                to16[1] = make_uint4(v[4], v[5], v[6], v[7]);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                qt_fence_before();  // (ordered before the next run's products by p_full)
             }
-            qt_fence_before();  // (ordered before the next run's products by p_full)
-        } while (live ? r.next(p.large, p.Hkv) : (live = true));
+            if (live) {
+                more = z.next(p.large, p.Hkv);
+                ck_keep(keep, z, lane);
+            }
+            live = true;
+        } while (more);
     } else if constexpr (Q8) {
         ck_reg_dec<C::R_CONV>();
         // ------------------------------------------------ codes to 16-bit operands

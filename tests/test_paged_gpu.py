@@ -347,6 +347,44 @@ def test_strided_queries_and_given_buffers(vq, dtype, cache):
     assert torch.equal(got, plain)
 
 
+@pytest.mark.parametrize("dtype,cache", [(F16, F16), (BF16, E4M3)])
+def test_output_at_any_16_bytes(vq, dtype, cache):
+    """An output that starts 16 bytes past a multiple of 32, items whole and cut."""
+    a = _case(vq, [1, 40, 200, 77], [50, 40, 3000, 77], 2, 4, 32, dtype, cache, seed=52)
+    T, Hq, _ = a["q"].shape
+    room = torch.full((T * Hq * D + 16,), float("nan"), dtype=dtype, device="cuda")
+    out = room[8:8 + T * Hq * D].view(T, Hq, D)
+    assert out.data_ptr() % 32 == 16
+    got = _check(vq, a, out=out)
+    assert torch.equal(got, _run(vq, a))
+    assert bool(room[:8].isnan().all()) and bool(room[8 + T * Hq * D:].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_query_rows_of_any_size_over_codes(vq, dtype):
+    """Rows from 2^-60 (fp16: 2^-10) to 1, rows of zeros, and rows with entries far
+    below their largest, for single tokens and chunks of several items."""
+    a = _case(vq, [1, 50, 140, 1], [300, 50, 700, 129], 2, 4, 16, dtype, E4M3, seed=53)
+    gen = torch.Generator().manual_seed(54)
+    T, Hq, _ = a["q"].shape
+    low = -60 if dtype == BF16 else -10
+    size = torch.exp2(torch.randint(low, 1, (T, Hq, 1), generator=gen).float())
+    size[torch.rand(T, Hq, 1, generator=gen) < 0.1] = 0.0
+    inner = torch.exp2(torch.randint(-30, 1, (T, Hq, D), generator=gen).float())
+    inner[: T // 2] = 1.0
+    a["q"] = (a["q"].float() * size * inner).to(dtype)
+    _check(vq, a)
+
+
+def test_more_entries_than_the_plan_keeps_at_hand(vq):
+    """More than a thousand chunks, of one query tile and of two, beside single
+    tokens: the plan reads entries back from memory."""
+    news = [17 + i % 5 if i % 9 else 150 for i in range(1100)]
+    news[3::50] = [1] * len(news[3::50])
+    lens = [n + i % 37 for i, n in enumerate(news)]
+    _check(vq, _case(vq, news, lens, 1, 1, 16, F16, F16, seed=55))
+
+
 def test_repeated_calls_agree_bit_for_bit(vq):
     a = _case(vq, [1, 130, 33], [4000, 700, 2000], 2, 4, 32, BF16, BF16, seed=61)
     first = _run(vq, a)
