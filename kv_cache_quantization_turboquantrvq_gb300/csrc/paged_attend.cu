@@ -194,9 +194,9 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
         __syncthreads();
         // Shares of large items are even in cost: a tile is one, and an item costs as
         // much as `item` tiles besides (its first products wait for queries, keys
-        // and a softmax, and it writes its output).  Found by fitting the CTAs'
-        // times of the chunk kernel: 1.5 us a tile and 5.0 a run of an item over a
-        // 16-bit cache, 1.8 and 7.3 over codes.
+        // and a softmax, and it writes its output): the times of the chunk kernel's
+        // CTAs fit 1.5 us a tile and 5.0 a run of an item over a 16-bit cache, 1.8
+        // and 7.3 over codes.
         const int item = k ? (p.c.ke ? PLAN_ITEM_Q8 : PLAN_ITEM) : 0;
         auto cost = [&](int i) { return base(i) + (long long)i * item * p.Hkv; };  // before entry i
         Shares sh;

@@ -19,18 +19,21 @@
 // row; one warp that streams queries, keys and values by TMA (a box per page);
 // two warps that issue tcgen05.mma, one for scores, one for values.  With an
 // 8-bit cache eight more warps turn the codes into fp16 operands in shared
-// memory (four took 857 us for 4096 fp16 queries over 16384 keys, eight 767; the
-// same chunk over a 16-bit cache 634).
+// memory (4096 bf16 queries over 16384 keys: four took 815 us, eight 763).
 //
-// What bounds it (that chunk, 16-bit cache: 1.52 PFLOP/s): a pair of tiles takes
-// 1.5 us where the products take 1.07; the score tile waits for its copy to
-// registers between products, and shared memory has 0.75 of that time to feed
-// the operands and take the copies.  A run of an item takes 5 us besides its tiles (7 over codes): the
-// first keys' way through the pipeline and the output's to memory.
+// What bounds it (that chunk over a 16-bit cache: 627 us, 1.53 PFLOP/s; over
+// codes 779): a pair of tiles takes 1.5 us where the products take 1.07.  The
+// score tile waits for its copy to registers between products, and by its bytes
+// (192 KB of operands read, 64 KB copied in) shared memory is as busy as the
+// tensor core.  Over codes the softmax warps have 176 registers instead of 208,
+// and 20 warps of four kinds of code share the instruction caches.  A run of an
+// item takes about 4 us besides its tiles (6 over codes): its first keys' way
+// through the pipeline and its output's to memory.
 //
 // 8-bit cache.  A factor per key inside the softmax (2 x 128 numbers a tile to
-// every thread) cost more than the softmax itself.  So the exponents are split in a tile's largest
-// among the keys that are seen, A of keys and B of values, and each key's rest:
+// every thread) cost more than the softmax itself.  So the exponents are split
+// in a tile's largest among the keys that are seen, A of keys and B of values,
+// and each key's rest:
 // the operands are code * 2^(a - A) and code * 2^(b - B), and a tile's two
 // exponents act once per score: t = scale 2^A (q . K') + B, w = 2^(t - M) with M
 // the running maximum of t, out = sum w V' / sum w 2^-B.  The operands are exact
@@ -773,9 +776,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 }
                 // A thread holds a row and stores 32 bytes of it at a time, a whole
                 // sector.  Partial rows lie 32 by 32, 8 columns after another, so that a
-                // warp's store fills whole lines: a sector of a line each took the L1's
-                // data path a cycle a sector, and the next item's products, which read
-                // shared memory by the same path, 3 us longer.
+                // warp's store fills whole lines (row after row, a sector of a line
+                // each, an item's output took 2.1 us, so 1.3).
                 T *dst = static_cast<T *>(p.out) + ((size_t)(z.e.tok0 + tok) * p.Hq + (size_t)z.h * p.GQ + row % p.GQ) * D;
                 float *pd = part + 2 * PG_LROWS + (128 * w + row - lane) * D + 8 * lane;
                 const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
