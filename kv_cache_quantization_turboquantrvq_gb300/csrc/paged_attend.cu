@@ -123,8 +123,8 @@ template <class F> __device__ __forceinline__ int parts_at(F &&first, int g, int
     return n;
 }
 
-// One CTA: entries of both classes in the order of the sequences, the units
-// before each, and where each CTA of the attention kernels starts.
+// One CTA: entries of both classes, sequence by sequence, the units before each,
+// and where each CTA of the attention kernels starts.
 __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __grid_constant__ PagedAttendParams p)
 {
     __shared__ long long ws[32];
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
     const int lane = threadIdx.x & 31;
     long long carry = 0;  // entries so far: small in the low half, large in the high one
     for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
-        const int b = b0 + threadIdx.x;
+        const int b = b0 + (threadIdx.x >> 5) + 32 * lane;  // (few sequences: a warp each)
         int start = 0, n = 0, len = 0;
         if (b < p.B && !sequence(p, b, start, n, len)) atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
         const bool large = n * p.GQ > p.small_rows;
