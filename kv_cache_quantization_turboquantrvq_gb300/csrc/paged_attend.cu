@@ -12,7 +12,10 @@
 // fp16 and bf16) the score is 2^a_j (q . K_j), and the exponent of the value is
 // folded into the weight: w'_j = 2^(s_j + b_j - M) with M the maximum of
 // s_j + b_j, so that w' is at most 1 whatever the exponents, out = sum w'_j V_j
-// / sum w'_j 2^-b_j, and the products take codes that were never scaled.
+// / sum w'_j 2^-b_j, and the products take codes that were never scaled.  A zero
+// value row, which is stored with exponent 0, counts with the least exponent
+// (any serves, as V_j = 0): where the other rows are small, M would else follow
+// it, and their weights would leave fp16's range.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -614,7 +617,13 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
             auto exps_of = [&](int row) -> uint32_t {
                 if constexpr (!Q8) return 0u;
                 const int k = 4 * lane, rw = __shfl_sync(FULL_MASK, row, k / box);
-                return rw >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(ex + rw + k % box)) : 0x7f7f7f7fu;
+                return rw >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(ex + rw + k % box)) : PG_EXP0;
+            };
+            // the same four, zero value rows with the least exponent
+            auto exps_used = [&](int row, uint32_t x) -> uint32_t {
+                if (!val || !__any_sync(FULL_MASK, __vcmpeq4(x, PG_EXP0) != 0u)) return x;
+                const int k = 4 * lane, rw = __shfl_sync(FULL_MASK, row, k / box);
+                return rw >= 0 ? pg_value_exps(x, static_cast<const unsigned char *>(p.c.v) + (long long)(rw + k % box) * D) : x;
             };
             int mine = r.t0;  // this pair's first tile of the run
             if (L::PAIRS > 1 && (tiles & 1) != pair) {
@@ -641,7 +650,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                 unsigned char *dst = stages + ring.s * L::STAGE + (val ? L::KV : 0);
                 uint64_t *bar = &full[ring.s];
                 if constexpr (Q8) {
-                    reinterpret_cast<uint32_t *>(exps + ring.s * L::EXP + (val ? PG_TILE : 0))[lane] = x;
+                    reinterpret_cast<uint32_t *>(exps + ring.s * L::EXP + (val ? PG_TILE : 0))[lane] = exps_used(row, x);
                     __syncwarp();
                 }
                 if (elect_lane()) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(held) * box * L::ROW));

@@ -22,6 +22,30 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t &lo, uin
         : "r"(four));
 }
 
+constexpr uint32_t PG_EXP0 = 0x7f7f7f7fu;  // exponent 0 of four rows, as stored
+
+// Exponents (a byte each) of four consecutive value rows of codes, those of zero
+// rows replaced by the least one.  A zero row is stored with exponent 0, as if
+// it were larger than the rows around it; it adds nothing to an output, so the
+// softmax must not make room for it.  The codes are read only of rows with
+// exponent 0, which are zero or reach beyond 224.
+__device__ __forceinline__ uint32_t pg_value_exps(uint32_t four, const void *rows)
+{
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        if (((four >> (8 * i)) & 0xffu) != (PG_EXP0 & 0xffu)) continue;
+        const uint4 *row = static_cast<const uint4 *>(rows) + 8 * i;
+        uint32_t some = 0u;
+#pragma unroll 1
+        for (int c = 0; c < 8 && some == 0u; c += 2) {
+            const uint4 u = __ldg(row + c), w = __ldg(row + c + 1);
+            some = (u.x | u.y | u.z | u.w | w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;  // (without the signs)
+        }
+        if (some == 0u) four = (four & ~(0xffu << (8 * i))) | (uint32_t)(PG_EMIN + 127) << (8 * i);
+    }
+    return four;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
