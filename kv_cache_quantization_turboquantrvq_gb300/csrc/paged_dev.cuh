@@ -31,19 +31,27 @@ constexpr uint32_t PG_EXP0 = 0x7f7f7f7fu;  // exponent 0 of four rows, as stored
 // exponent 0, which are zero or reach beyond 224.
 __device__ __forceinline__ uint32_t pg_value_exps(uint32_t four, const void *rows)
 {
+    const uint4 *row = static_cast<const uint4 *>(rows);
+    const uint32_t ask = __vcmpeq4(four, PG_EXP0);
+    auto some = [&](int i) {  // of 16 codes, without the signs
+        const uint4 u = __ldg(row + i);
+        return ((u.x | u.y | u.z | u.w) & 0x7f7f7f7fu) != 0u;
+    };
+    // most rows show within their first 16 codes that they are not zero
+    uint32_t zero = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if ((ask >> (8 * i)) & 1u) zero |= some(8 * i) ? 0u : 0xffu << (8 * i);
+    if (zero == 0u) return four;
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) {
-        if (((four >> (8 * i)) & 0xffu) != (PG_EXP0 & 0xffu)) continue;
-        const uint4 *row = static_cast<const uint4 *>(rows) + 8 * i;
-        uint32_t some = 0u;
-#pragma unroll 1
-        for (int c = 0; c < 8 && some == 0u; c += 2) {
-            const uint4 u = __ldg(row + c), w = __ldg(row + c + 1);
-            some = (u.x | u.y | u.z | u.w | w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;  // (without the signs)
-        }
-        if (some == 0u) four = (four & ~(0xffu << (8 * i))) | (uint32_t)(PG_EMIN + 127) << (8 * i);
+        if (((zero >> (8 * i)) & 1u) == 0u) continue;
+        bool any = false;
+#pragma unroll
+        for (int c = 1; c < 8; ++c) any |= some(8 * i + c);
+        if (any) zero &= ~(0xffu << (8 * i));
     }
-    return four;
+    return (four & ~zero) | (zero & (0x01010101u * (uint32_t)(PG_EMIN + 127)));
 }
 
 __device__ __forceinline__ float ex2(float x)
