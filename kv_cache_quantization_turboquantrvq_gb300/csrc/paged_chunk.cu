@@ -22,7 +22,7 @@
 // memory (4096 bf16 queries over 16384 keys: four took 815 us, eight 763).
 //
 // What bounds it (that chunk over a 16-bit cache: 627 us, 1.53 PFLOP/s; over
-// codes 779): a pair of tiles takes 1.5 us where the products take 1.07.  The
+// codes 808): a pair of tiles takes 1.5 us where the products take 1.07.  The
 // score tile waits for its copy to registers between products, and by its bytes
 // (192 KB of operands read, 64 KB copied in) shared memory is as busy as the
 // tensor core.  Over codes the softmax warps have 176 registers instead of 208,
@@ -36,10 +36,16 @@
 // and each key's rest:
 // the operands are code * 2^(a - A) and code * 2^(b - B), and a tile's two
 // exponents act once per score: t = scale 2^A (q . K') + B, w = 2^(t - M) with M
-// the running maximum of t, out = sum w V' / sum w 2^-B.  The operands are exact
-// but for the smallest entries of rows more than 2^15 below the tile's largest
-// (fp16; off by 2^-25 2^A, 2^-33 of the largest row: less than the 32-bit sums
-// of that row's own products), so no weight or value leaves its type's range.
+// the running maximum of t, out = sum w V' / sum w 2^-B.  That holds while the
+// seen keys of a tile have exponents within KEYS_WITHIN and values within
+// VALUES_WITHIN of the largest.  Codes are multiples of 2^-9, so the operands are
+// exact in fp16 down to 2^-15 of the largest row; and M lies at most 2^8 above
+// what some seen value asks for, so that a row's largest w 2^b is at least 2^-1
+// and its weights keep all of fp16's bits down to 2^-13 of that.  A tile whose
+// exponents lie further apart (its one exponent would be that of a row which may
+// have no weight at all) takes the codes as they are, and the exponents act key
+// by key in the softmax, as for single tokens:
+// t_j = scale 2^a_j (q . K_j) + b_j, and sum w_j 2^-b_j below the line.
 // Operands are fp16 whatever the queries' type, since one instruction makes them
 // of two codes (bf16 takes five: 996 us against 884 for the chunk above, with
 // four warps); bf16 queries become fp16 by a power of two for each row, in place,
@@ -67,6 +73,7 @@ VQ_DEFINE_ERROR_WORD(g_pk_err);
 constexpr int D = 128;
 constexpr float NEG_INF = -__builtin_huge_valf();
 constexpr float OFF = 7.0f, LAG = 8.0f;
+constexpr int KEYS_WITHIN = 15, VALUES_WITHIN = 8;  // powers of two that rows of a tile may share an exponent over
 constexpr int TILE_B = PG_TILE * D * 2;  // a 16-bit tile of 128 rows: two halves of 64 columns
 constexpr int HALF_B = TILE_B / 2;
 constexpr int RAW_B = PG_TILE * D;       // a tile of codes
@@ -85,9 +92,49 @@ template <bool Q8> struct CkShape {
     static constexpr int BARS = 3 + 2 * STAGES + 7 + 2 * RAW + 2 * META + 2;
     static constexpr int RUNS = 8 * 64;         // the softmax warps' runs
     static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + RUNS + RAW * 2 * PG_TILE +
-                                META * 16 + 8 * BARS + 16;
+                                META * (16 + 8 * PG_TILE) + 8 * (Q8 ? 2 : 1) * BARS + 16;
 };
 static_assert(CkShape<false>::SMEM <= 232448 && CkShape<true>::SMEM <= 232448, "shared memory of one CTA");
+
+constexpr uint32_t CK_TIMEOUT = 1, CK_BY_KEY = 2;  // why every role stops
+
+template <bool Q8> struct CkBars {
+    using C = CkShape<Q8>;
+    uint64_t *q_full, *q_empty, *kv_full, *kv_empty, *s_full, *p_full, *pv_done, *s_free, *raw_full, *raw_empty, *meta_full,
+        *meta_empty, *drain, *q_ready;
+    __device__ __forceinline__ explicit CkBars(uint64_t *b)
+        : q_full(b), q_empty(b + 1), kv_full(b + 2), kv_empty(kv_full + C::STAGES), s_full(kv_empty + C::STAGES),
+          p_full(s_full + 2), pv_done(p_full + 2), s_free(pv_done + 2), raw_full(s_free + 1), raw_empty(raw_full + C::RAW),
+          meta_full(raw_empty + C::RAW), meta_empty(meta_full + C::META), drain(meta_empty + C::META), q_ready(drain + 2)
+    {
+    }
+    __device__ __forceinline__ void init()
+    {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&kv_full[s], Q8 ? C::CONV : 1);
+            mbar_init(&kv_empty[s], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&s_full[w], 1);
+            mbar_init(&p_full[w], 4);
+            mbar_init(&pv_done[w], 1);
+        }
+        mbar_init(s_free, 4);
+        for (int s = 0; s < C::RAW; ++s) {
+            mbar_init(&raw_full[s], 1);
+            mbar_init(&raw_empty[s], C::CONV);
+        }
+        for (int s = 0; s < C::META; ++s) {
+            mbar_init(&meta_full[s], C::CONV);
+            mbar_init(&meta_empty[s], 8);
+        }
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
+        mbar_init(q_ready, 8);
+    }
+};
 
 // Operand B of the value product: rows are keys (K), 64-column halves side by
 // side (N contiguous): 128-byte swizzle, 8-key groups 1024 bytes apart, the
@@ -230,11 +277,11 @@ template <> __device__ __forceinline__ uint32_t ck_pack<__nv_bfloat16>(float a, 
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// 2^e (e <= 0) twice in fp16; 0 where its range ends.
+// 2^e twice in fp16, -15 <= e <= 0; of a key that nothing sees e may be any number.
 __device__ __forceinline__ uint32_t ck_factor(int e)
 {
-    e = min(e, 0);
-    return 0x00010001u * (e >= -14 ? (uint32_t)(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u);
+    static_assert(KEYS_WITHIN <= 15 && VALUES_WITHIN <= 15, "factors of seen keys");
+    return 0x00010001u * (e >= -14 ? (uint32_t)(min(e, 0) + 15) << 10 : 1u << 9);
 }
 
 // Four codes times a factor as two pairs of fp16.
@@ -321,10 +368,16 @@ __device__ __forceinline__ void ck_store32(void *at, const uint32_t *v)
 }
 
 // Largest of the bytes that the lanes of a warp hold.
-__device__ __forceinline__ uint32_t ck_top(uint32_t four)
+__device__ __forceinline__ int ck_top(uint32_t four)
 {
     four = __vmaxu4(four, four >> 16);
-    return __reduce_max_sync(FULL_MASK, max(four & 0xffu, (four >> 8) & 0xffu));
+    return (int)__reduce_max_sync(FULL_MASK, max(four & 0xffu, (four >> 8) & 0xffu));
+}
+
+// 255 in the bytes that are below `least`.
+__device__ __forceinline__ uint32_t ck_less(uint32_t four, int least)
+{
+    return __vcmpltu4(four, 0x01010101u * (uint32_t)max(least, 0));
 }
 
 template <class T, bool Q8>
@@ -341,54 +394,29 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     unsigned char *sraw = skv + STAGES * TILE_B;            // tiles of codes
     unsigned char *srun = sraw + C::RAW * RAW_B;            // [8][64] the softmax warps' runs
     unsigned char *sexp = srun + C::RUNS;                   // [RAW][2][128] exponents (of key tiles)
-    float4 *smeta = reinterpret_cast<float4 *>(sexp + C::RAW * 2 * PG_TILE);  // [META] |scale| 2^A, B, 2^-B
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smeta + C::META);
-    uint64_t *q_full = bars, *q_empty = bars + 1, *kv_full = bars + 2, *kv_empty = kv_full + STAGES;
-    uint64_t *s_full = kv_empty + STAGES, *p_full = s_full + 2, *pv_done = p_full + 2, *s_free = pv_done + 2;
-    uint64_t *raw_full = s_free + 1, *raw_empty = raw_full + C::RAW;
-    uint64_t *meta_full = raw_empty + C::RAW, *meta_empty = meta_full + C::META;
-    uint64_t *drain = meta_empty + C::META, *q_ready = drain + 2;
-    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(q_ready + 1);
+    float4 *smeta = reinterpret_cast<float4 *>(sexp + C::RAW * 2 * PG_TILE);  // [META] |scale| 2^A, B, 2^-B, 1: key by key
+    float4 *skeys = smeta + C::META;                        // [META][128] |scale| 2^a, b of a tile taken key by key
+    uint64_t *bars = reinterpret_cast<uint64_t *>(skeys + C::META * (PG_TILE / 2));
+    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(bars + (Q8 ? 2 : 1) * C::BARS);
     volatile uint32_t *abort_flag = tslot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tqt = 128 / p.GQ;  // tokens of one query tile
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&kv_full[s], Q8 ? C::CONV : 1);
-            mbar_init(&kv_empty[s], 1);
-        }
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(&s_full[w], 1);
-            mbar_init(&p_full[w], 4);
-            mbar_init(&pv_done[w], 1);
-        }
-        mbar_init(s_free, 4);
-        for (int s = 0; s < C::RAW; ++s) {
-            mbar_init(&raw_full[s], 1);
-            mbar_init(&raw_empty[s], C::CONV);
-        }
-        for (int s = 0; s < C::META; ++s) {
-            mbar_init(&meta_full[s], C::CONV);
-            mbar_init(&meta_empty[s], 8);
-        }
-        mbar_init(&drain[0], 1);
-        mbar_init(&drain[1], 1);
-        mbar_init(q_ready, 8);
+        CkBars<Q8>(bars).init();
+        if constexpr (Q8) CkBars<Q8>(bars + C::BARS).init();
         *abort_flag = 0u;
         fence_mbar_init();
     }
     if (warp == 9) tmem_alloc(const_cast<uint32_t *>(tslot), 512);
     pg_wait();  // for the plan
     pg_go();
-    PgRun r;
-    r.start(p.large.start[blockIdx.x]);
+    PgRun r_all;
+    r_all.start(p.large.start[blockIdx.x]);
     qt_fence_before();
     __syncthreads();
     qt_fence_after();
-    if (r.left <= 0) {  // the whole CTA
+    if (r_all.left <= 0) {  // the whole CTA
         if (warp == 9) tmem_free(*tslot, 512);
         return;
     }
@@ -403,9 +431,33 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
             if (*abort_flag) return false;
             if (globaltimer_ns() - t0 > MBAR_TIMEOUT_NS) {
                 atomicOr(&g_pk_err, (unsigned)VQ_DEVERR_WAIT_TIMEOUT);
-                *abort_flag = 1u;
+                *abort_flag = CK_TIMEOUT;
                 return false;
             }
+        }
+    };
+
+    // A role goes through the CTA's share.  Over codes, the converting warps end
+    // that at the first tile whose exponents lie too far apart, and the CTA starts
+    // again with roles that can take them key by key.  One body for both spent 10
+    // to 18 % more on every tile, since softmax and converting warps have no
+    // register or instruction to spare; so it is 0 to 4 % (4096 queries over 16384
+    // keys: fp16 797 us against 801 without the check, bf16 808 against 779).  With
+    // value rows of 13 sizes 2^-12 to 1 in every tile that call takes 1.5 to 1.7 ms.
+    auto share = [&](auto role) {
+        role(std::false_type(), r_all);
+        if constexpr (Q8) {
+            qt_fence_before();
+            __syncthreads();
+            const bool again = *abort_flag == CK_BY_KEY;
+            if (!again) return;
+            __syncthreads();
+            if (threadIdx.x == 0) *abort_flag = 0u;
+            __syncthreads();
+            qt_fence_after();
+            PgRun r;
+            r.start(p.large.start[blockIdx.x]);
+            role(std::true_type(), r);
         }
     };
 
@@ -413,27 +465,31 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     ck_reg_dec<C::R_CTL>();
     if (warp == 8) {
         // ------------------------------------------------ copies (TMA)
+        share([&](auto pass, PgRun r) {
+        constexpr bool BY_KEY = decltype(pass)::value;
+        const CkBars<Q8> bar(bars + (BY_KEY ? C::BARS : 0));
         const int box = min(1 << p.c.page_shift, PG_TILE), nbox = PG_TILE / box;
         const int rows_all = p.c.num_pages * p.c.Hkv << p.c.page_shift;  // no box holds this row: reads zeros
         const uint64_t pol = ck_policy();
-        PgRing<STAGES> kv;
-        PgRing<C::RAW ? C::RAW : 1> raw;
+        [[maybe_unused]] PgRing<STAGES> kv;
+        [[maybe_unused]] PgRing<C::RAW ? C::RAW : 1> raw;
         uint32_t qpar = 0;
-        int tiles = 0;  // tiles copied
+        int tiles = 0, queries = 0;  // copied
         bool ok = true;
         do {
             if (!r.first) {
-                ok = __all_sync(FULL_MASK, wait(q_empty, qpar));
+                ok = __all_sync(FULL_MASK, wait(bar.q_empty, qpar));
                 qpar ^= 1u;
                 if (!ok) break;
             }
+            ++queries;
             if (elect_lane()) {
                 // tokens past the chunk bring other sequences' rows, past the tensor zeros: never used
                 const int nq = r.e.nt > tqt ? 2 : 1;
-                mbar_arrive_expect_tx(q_full, (uint32_t)(nq * 2 * tqt * p.GQ * 128));
+                mbar_arrive_expect_tx(bar.q_full, (uint32_t)(nq * 2 * tqt * p.GQ * 128));
                 for (int w = 0; w < nq; ++w)
                     for (int hf = 0; hf < 2; ++hf)
-                        tma_load_3d(sq + w * TILE_B + hf * HALF_B, &p.tmq, 64 * hf, r.h * p.GQ, r.e.tok0 + w * tqt, q_full, pol);
+                        tma_load_3d(sq + w * TILE_B + hf * HALF_B, &p.tmq, 64 * hf, r.h * p.GQ, r.e.tok0 + w * tqt, bar.q_full, pol);
             }
             PgView view;
             view.set(r.e, p.window, p.sinks);
@@ -454,40 +510,44 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                         else atomicOr(&g_pk_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
                     }
                 }
+                if (Q8 && !BY_KEY && *abort_flag) {  // (the others then wait in vain, and stop)
+                    ok = false;
+                    break;
+                }
                 for (int part = 0; part < 2; ++part) {  // keys, values
                     if (part == 0 ? t == r.tn : t == r.t0) continue;
                     const CUtensorMap *map = part ? &p.tmv : &p.tmk;
                     const int at = part ? prow : row;
                     if constexpr (Q8) {
-                        if (tiles >= C::RAW && !__all_sync(FULL_MASK, wait(&raw_empty[raw.s], raw.par ^ 1u))) {
+                        if (tiles >= C::RAW && !__all_sync(FULL_MASK, wait(&bar.raw_empty[raw.s], raw.par ^ 1u))) {
                             ok = false;
                             break;
                         }
                         // a key tile brings the exponents of keys and values
                         const unsigned n = part ? 0u : (unsigned)__popc(__ballot_sync(FULL_MASK, held));
-                        if (elect_lane()) mbar_arrive_expect_tx(&raw_full[raw.s], RAW_B + n * 2 * box);
+                        if (elect_lane()) mbar_arrive_expect_tx(&bar.raw_full[raw.s], RAW_B + n * 2 * box);
                         __syncwarp();
                         if (lane < nbox) {  // a lane per box
-                            tma_load_2d(sraw + raw.s * RAW_B + lane * box * 128, map, 0, at, &raw_full[raw.s], pol);
+                            tma_load_2d(sraw + raw.s * RAW_B + lane * box * 128, map, 0, at, &bar.raw_full[raw.s], pol);
                             if (held && part == 0) {
                                 unsigned char *x = sexp + raw.s * 2 * PG_TILE + lane * box;
-                                bulk_g2s(x, p.c.ke + at, box, &raw_full[raw.s], pol);
-                                bulk_g2s(x + PG_TILE, p.c.ve + at, box, &raw_full[raw.s], pol);
+                                bulk_g2s(x, p.c.ke + at, box, &bar.raw_full[raw.s], pol);
+                                bulk_g2s(x + PG_TILE, p.c.ve + at, box, &bar.raw_full[raw.s], pol);
                             }
                         }
                         __syncwarp();
                         raw.step();
                     } else {
-                        if (tiles >= STAGES && !__all_sync(FULL_MASK, wait(&kv_empty[kv.s], kv.par ^ 1u))) {
+                        if (tiles >= STAGES && !__all_sync(FULL_MASK, wait(&bar.kv_empty[kv.s], kv.par ^ 1u))) {
                             ok = false;
                             break;
                         }
-                        if (elect_lane()) mbar_arrive_expect_tx(&kv_full[kv.s], TILE_B);
+                        if (elect_lane()) mbar_arrive_expect_tx(&bar.kv_full[kv.s], TILE_B);
                         __syncwarp();
                         if (lane < nbox) {  // a lane per box
                             unsigned char *dst = skv + kv.s * TILE_B + lane * box * 128;
-                            tma_load_2d(dst, map, 0, at, &kv_full[kv.s], pol);
-                            tma_load_2d(dst + HALF_B, map, 64, at, &kv_full[kv.s], pol);
+                            tma_load_2d(dst, map, 0, at, &bar.kv_full[kv.s], pol);
+                            tma_load_2d(dst + HALF_B, map, 64, at, &bar.kv_full[kv.s], pol);
                         }
                         __syncwarp();
                         kv.step();
@@ -496,19 +556,22 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 }
             }
         } while (ok && r.next(p.large, p.Hkv));
-        // every copy has landed before the CTA may exit
+        // every copy has landed before the CTA may exit, or goes through its share
+        // again (the last queries' too: nobody may have waited for them)
+        if (queries > 0) (void)mbar_wait_bounded(bar.q_full, (uint32_t)(queries - 1) & 1u);
         if constexpr (Q8) {
             for (int k = 0; k < C::RAW && k < tiles; ++k) {
                 const int j = tiles - 1 - k;
-                (void)mbar_wait_bounded(&raw_full[j % C::RAW], (uint32_t)(j / C::RAW) & 1u);
+                (void)mbar_wait_bounded(&bar.raw_full[j % C::RAW], (uint32_t)(j / C::RAW) & 1u);
             }
         } else {
             for (int k = 0; k < STAGES && k < tiles; ++k) {
                 const int j = tiles - 1 - k;
-                (void)mbar_wait_bounded(&kv_full[j % STAGES], (uint32_t)(j / STAGES) & 1u);
+                (void)mbar_wait_bounded(&bar.kv_full[j % STAGES], (uint32_t)(j / STAGES) & 1u);
             }
         }
         __syncwarp();
+        });
     } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------ products: warp 9 the
         // scores, warp 10 the values, so that neither's waits hold the other up
@@ -516,6 +579,9 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         constexpr uint32_t ID_S = ck_idesc(BFV, false), ID_O = ck_idesc(BFV, true);
         const uint64_t dq = qt_desc(smem_u32(sq)), dk = qt_desc(smem_u32(skv)), dv = ck_desc_v(smem_u32(skv));
         const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
+        share([&](auto pass, PgRun r) {
+        constexpr bool BY_KEY = decltype(pass)::value;
+        const CkBars<Q8> bar(bars + (BY_KEY ? C::BARS : 0));
         PgRing<STAGES> kv;
         bool ok = true;
         auto await = [&](uint64_t *bar, uint32_t parity) { ok = ok && __all_sync(FULL_MASK, wait(bar, parity)); };
@@ -528,26 +594,26 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 // have come and gone, or their pass would be taken for this one
                 // (a barrier's parity tells two passes apart, not three).  Later
                 // keys follow keys, or (codes) come in order.
-                if (!Q8 && tiles >= STAGES) await(&kv_empty[kv.s], kv.par ^ 1u);
+                if (!Q8 && tiles >= STAGES) await(&bar.kv_empty[kv.s], kv.par ^ 1u);
                 tiles += 2 * (r.tn - r.t0);
-                await(QC ? q_ready : q_full, qpar);
+                await(QC ? bar.q_ready : bar.q_full, qpar);
                 qpar ^= 1u;
                 for (int t = r.t0; t < r.tn && ok; ++t) {
-                    await(&kv_full[kv.s], kv.par);
+                    await(&bar.kv_full[kv.s], kv.par);
                     for (int w = 0; w < (two ? 2 : 1); ++w) {
-                        await(s_free, fpar);  // the score tile's last use was copied out
+                        await(bar.s_free, fpar);  // the score tile's last use was copied out
                         fpar ^= 1u;
                         if (!ok) break;
                         qt_fence_after();
-                        ck_mma_ss(tm, dq + w * (TILE_B >> 4), dk + kv.s * (TILE_B >> 4), ID_S, smem_u32(&s_full[w]));
+                        ck_mma_ss(tm, dq + w * (TILE_B >> 4), dk + kv.s * (TILE_B >> 4), ID_S, smem_u32(&bar.s_full[w]));
                     }
                     if (!ok) break;
-                    ck_commit(&kv_empty[kv.s]);
+                    ck_commit(&bar.kv_empty[kv.s]);
                     kv.step();
                     if (t > r.t0) kv.step();  // (values of tile t - 1 lie between)
                 }
                 if (!ok) break;
-                ck_commit(q_empty);  // the queries may be replaced
+                ck_commit(bar.q_empty);  // the queries may be replaced
                 kv.step();
             } while (r.next(p.large, p.Hkv));
         } else {
@@ -557,25 +623,28 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 kv.step();
                 for (int t = r.t0; t < r.tn && ok; ++t) {
                     if (t + 1 < r.tn) kv.step();  // (keys of tile t + 1 come first)
-                    await(&kv_full[kv.s], kv.par);
+                    await(&bar.kv_full[kv.s], kv.par);
                     for (int w = 0; w < (two ? 2 : 1); ++w) {
-                        await(&p_full[w], ppar[w]);
+                        await(&bar.p_full[w], ppar[w]);
                         ppar[w] ^= 1u;
                         if (!ok) break;
                         qt_fence_after();
                         ck_mma_ts(tm + 256 + 128 * w, tm + 128 + 64 * w, dv + kv.s * (TILE_B >> 4), ID_O, t > r.t0 ? 1u : 0u,
-                                  smem_u32(&pv_done[w]));
+                                  smem_u32(&bar.pv_done[w]));
                     }
                     if (!ok) break;
-                    ck_commit(&kv_empty[kv.s]);
+                    ck_commit(&bar.kv_empty[kv.s]);
                     kv.step();
                 }
             } while (ok && r.next(p.large, p.Hkv));
         }
         // every product is done before shared and tensor memory are given up
-        ck_commit(&drain[warp - 9]);
-        (void)mbar_wait_bounded(&drain[warp - 9], 0u);
+        ck_commit(&bar.drain[warp - 9]);
+        (void)mbar_wait_bounded(&bar.drain[warp - 9], 0u);
         __syncwarp();
+        });
+    } else {
+        share([](auto, PgRun) {});  // (takes part in the barriers)
     }
     } else if (warp < 8) {
         ck_reg_inc<C::R_SOFT>();
@@ -586,6 +655,10 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         const uint32_t ts = tmem + lanes, tp = tmem + lanes + 128 + 64 * w, to = tmem + lanes + 256 + 128 * w;
         const int tok_in = row / p.GQ;
         const float qabs = fabsf(p.qscale);
+        const uint32_t keep = smem_u32(srun + 64 * warp);
+        share([&](auto pass, PgRun r_) {
+        constexpr bool BY_KEY = decltype(pass)::value;
+        const CkBars<Q8> bar(bars + (BY_KEY ? C::BARS : 0));
         uint32_t spar = 0, vpar = 0, qpar = 0;
         PgRing<STAGES> vs;  // (16-bit cache) slot of the next tile that the products take
         PgRing<C::META ? C::META : 1> mt;
@@ -593,15 +666,14 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         float back_q = 1.0f;  // undoes the power of two in this row of converted queries
         bool live = !QC;      // false: before the first item, whose queries are then made ready
         bool more = true;
-        const uint32_t keep = smem_u32(srun + 64 * warp);
-        ck_keep(keep, r, lane);
+        ck_keep(keep, r_, lane);
         do {
             const PgRun r = ck_run(keep);
             const bool rows = live && (w == 0 || r.e.nt > tqt);  // this half has rows in the item
             if (Q8 && live && !rows) {
                 for (int t = r.t0; t < r.tn && ok; ++t) {
-                    ok = __all_sync(FULL_MASK, wait(&meta_full[mt.s], mt.par));  // (not ahead of its tile)
-                    if (lane == 0) mbar_arrive(&meta_empty[mt.s]);
+                    ok = __all_sync(FULL_MASK, wait(&bar.meta_full[mt.s], mt.par));  // (not ahead of its tile)
+                    if (lane == 0) mbar_arrive(&bar.meta_empty[mt.s]);
                     mt.step();
                 }
                 if (!ok) break;
@@ -620,11 +692,11 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 if (t + 1 < r.tn) vs.step();  // now at the values of tile t
                 const bool whole = k0 + PG_TILE <= pos_a + 1 &&
                                    (p.window == 0 || k0 > pos_z - p.window || k0 + PG_TILE <= view.sink);
-                ok = __all_sync(FULL_MASK, wait(&s_full[w], spar));
+                ok = __all_sync(FULL_MASK, wait(&bar.s_full[w], spar));
                 spar ^= 1u;
                 if (!ok) break;
                 if constexpr (Q8) {
-                    ok = __all_sync(FULL_MASK, wait(&meta_full[mt.s], mt.par));
+                    ok = __all_sync(FULL_MASK, wait(&bar.meta_full[mt.s], mt.par));
                     if (!ok) break;
                 }
                 qt_fence_after();
@@ -637,21 +709,37 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 for (int b = 0; b < 4; ++b) qt_hold(x[b]);
                 qt_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(s_free);
+                if (lane == 0) mbar_arrive(bar.s_free);
                 // t = score * mul + add, in base 2
                 float mul = qabs, add = 0.0f, back = 1.0f;
+                bool own = false;  // the keys' own exponents
                 if constexpr (Q8) {
                     const float4 f = smeta[mt.s];
                     mul = QC ? fminf(fmaxf(f.x * back_q, 1e-37f), 3e38f) : f.x;  // (finite, and -inf times it stays)
                     add = f.y;
                     back = f.z;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&meta_empty[mt.s]);
-                    mt.step();
+                    if constexpr (BY_KEY) own = f.w != 0.0f;
+                    if (!own) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.meta_empty[mt.s]);
+                        mt.step();
+                    }
                 }
                 if (p.qscale < 0.0f) {  // (mul is |scale|)
 #pragma unroll
                     for (int c = 0; c < PG_TILE; ++c) x[c >> 5][c & 31] ^= 0x80000000u;
+                }
+                if (BY_KEY && own) {
+                    const float4 *k2 = skeys + mt.s * (PG_TILE / 2);
+#pragma unroll
+                    for (int c = 0; c < PG_TILE; c += 2) {
+                        const float4 f = k2[c >> 1];
+                        uint32_t &a = x[c >> 5][c & 31], &b = x[c >> 5][(c & 31) + 1];
+                        a = __float_as_uint(fmaf(__uint_as_float(a), QC ? fminf(f.x * back_q, 3e38f) : f.x, f.y));
+                        b = __float_as_uint(fmaf(__uint_as_float(b), QC ? fminf(f.z * back_q, 3e38f) : f.z, f.w));
+                    }
+                    mul = 1.0f;
+                    add = 0.0f;
                 }
                 if (!whole) {
                     // bit c of word b: key k0 + 32 b + c is seen (words, not
@@ -681,7 +769,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     if (grow) m = mx - OFF;
                     l *= f;
                     if (!used) {
-                        ok = __all_sync(FULL_MASK, wait(&pv_done[w], vpar));
+                        ok = __all_sync(FULL_MASK, wait(&bar.pv_done[w], vpar));
                         vpar ^= 1u;
                         if (!ok) break;
                         used = true;
@@ -699,6 +787,21 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     }
                 }
                 const float ms = m > NEG_INF ? m : 0.0f;
+                if (BY_KEY && own) {  // sum w_j 2^-b_j
+                    const float4 *k2 = skeys + mt.s * (PG_TILE / 2);
+                    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < PG_TILE; c += 2) {
+                        const float4 f = k2[c >> 1];
+                        s0 += ex2(__uint_as_float(x[c >> 5][c & 31]) - f.y - ms);
+                        s1 += ex2(__uint_as_float(x[c >> 5][(c & 31) + 1]) - f.w - ms);
+                    }
+                    l += s0 + s1;
+                    back = 0.0f;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.meta_empty[mt.s]);
+                    mt.step();
+                }
                 const float2 neg = make_float2(add - ms, add - ms), mul2 = make_float2(mul, mul);
                 float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -712,7 +815,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                         pk[j >> 1] = ck_pack<TV>(e.x, e.y);
                     }
                     if (b == 0 && !used) {
-                        ok = __all_sync(FULL_MASK, wait(&pv_done[w], vpar));
+                        ok = __all_sync(FULL_MASK, wait(&bar.pv_done[w], vpar));
                         vpar ^= 1u;
                         if (!ok) break;
                         qt_fence_after();
@@ -725,7 +828,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     // values of keys that no row sees may hold anything: zero
                     // them before the product (the second half's comes later)
                     if (w == 0 && (k0 + PG_TILE > view.hi || (k0 < view.lo && k0 + PG_TILE > view.sink))) {
-                        ok = __all_sync(FULL_MASK, wait(&kv_full[vs.s], vs.par));
+                        ok = __all_sync(FULL_MASK, wait(&bar.kv_full[vs.s], vs.par));
                         if (!ok) break;
                         if (!view.one(k0 + row)) {
                             uint4 *z = reinterpret_cast<uint4 *>(skv + vs.s * TILE_B + row * 128);
@@ -742,11 +845,11 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 ck_wait_st();
                 qt_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[w]);
+                if (lane == 0) mbar_arrive(&bar.p_full[w]);
             }
             if (!ok) break;
             if (rows) {
-                ok = __all_sync(FULL_MASK, wait(&pv_done[w], vpar));
+                ok = __all_sync(FULL_MASK, wait(&bar.pv_done[w], vpar));
                 vpar ^= 1u;
                 if (!ok) break;
                 qt_fence_after();
@@ -756,13 +859,13 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 // the next item's queries, before the output of this one (both
                 // halves, whether they will have rows or not: what a tile without
                 // rows holds is not used)
-                ok = __all_sync(FULL_MASK, wait(q_full, qpar));
+                ok = __all_sync(FULL_MASK, wait(bar.q_full, qpar));
                 qpar ^= 1u;
                 if (!ok) break;
                 back_q = ck_query(sq + w * TILE_B, row);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(q_ready);
+                if (lane == 0) mbar_arrive(bar.q_ready);
             }
             if (live && (w == 0 || z.e.nt > tqt)) {
                 const int tok = w * tqt + tok_in;
@@ -808,7 +911,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     }
                     __syncwarp();
                 }
-                qt_fence_before();  // (ordered before the next run's products by p_full)
+                qt_fence_before();  // (ordered before the next run's products by bar.p_full)
             }
             if (live) {
                 more = z.next(p.large, p.Hkv);
@@ -816,17 +919,22 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
             }
             live = true;
         } while (more);
+        });
     } else if constexpr (Q8) {
         ck_reg_dec<C::R_CONV>();
         // ------------------------------------------------ codes to 16-bit operands
         const int j = threadIdx.x - 12 * 32;
         constexpr int STEP = 4 * C::CONV, ROWS = PG_TILE / STEP;
         static_assert(ROWS == 4, "a byte each of a word");
+        share([&](auto pass, PgRun r) {
+        constexpr bool BY_KEY = decltype(pass)::value;
+        const CkBars<Q8> bar(bars + (BY_KEY ? C::BARS : 0));
         PgRing<C::RAW ? C::RAW : 1> raw;
         PgRing<STAGES> kv;
         PgRing<C::META ? C::META : 1> mt;
         int tiles = 0, keys = 0;
-        uint32_t vtop0 = 0, vtop1 = 0;  // exponents of the values to come: of tile u - 1, of tile u
+        uint32_t far = 0u;  // exponents of this lane's keys too far below the tile's largest
+        int vtop0 = 0, vtop1 = 0;  // exponents of the values to come: of tile u - 1, of tile u
         uint32_t vrow0 = 0, vrow1 = 0;
         bool ok = true;
         do {
@@ -837,23 +945,27 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     if (part == 0 ? u == r.tn : u == r.t0) continue;
                     const int k0 = pg_tile_key(r.e, part ? u - 1 : u);
                     const bool edge = k0 + PG_TILE > view.hi || (k0 < view.lo && k0 + PG_TILE > view.sink);
-                    ok = __all_sync(FULL_MASK, wait(&raw_full[raw.s], raw.par));
-                    if (ok && tiles >= STAGES) ok = __all_sync(FULL_MASK, wait(&kv_empty[kv.s], kv.par ^ 1u));
-                    if (ok && part == 0 && keys >= C::META) ok = __all_sync(FULL_MASK, wait(&meta_empty[mt.s], mt.par ^ 1u));
+                    ok = __all_sync(FULL_MASK, wait(&bar.raw_full[raw.s], raw.par));
+                    if (ok && tiles >= STAGES) ok = __all_sync(FULL_MASK, wait(&bar.kv_empty[kv.s], kv.par ^ 1u));
+                    if (ok && part == 0 && keys >= C::META) ok = __all_sync(FULL_MASK, wait(&bar.meta_empty[mt.s], mt.par ^ 1u));
                     if (!ok) break;
                     // rows of this thread: j / 8 + 4 CONV i
-                    uint32_t top;         // the tile's largest exponent
+                    int top;              // the tile's largest exponent; 0: codes are taken as they are
                     uint32_t rows = 0;    // this thread's rows' exponents, a byte each
                     if (part == 0) {
                         const uint32_t *e4 = reinterpret_cast<const uint32_t *>(sexp + raw.s * 2 * PG_TILE) + lane;
+                        const uint32_t ke = e4[0], ve = e4[PG_TILE / 4];
                         uint32_t see = 0xffffffffu;  // of this lane's four keys
                         if (edge) {
                             see = 0u;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) see |= view.one(k0 + 4 * lane + i) ? 0xffu << (8 * i) : 0u;
                         }
-                        top = max(ck_top(e4[0] & see), 87u);  // (at least 2^-40: the factors below stay normal)
-                        vtop1 = max(ck_top(e4[PG_TILE / 4] & see), 87u);
+                        top = ck_top(ke & see);
+                        vtop1 = ck_top(ve & see);
+                        far = ck_less(ke | ~see, top - KEYS_WITHIN) | ck_less(ve | ~see, vtop1 - VALUES_WITHIN);
+                        top = max(top, 87);  // (at least 2^-40: the factors below stay normal)
+                        vtop1 = max(vtop1, 87);
                         const unsigned char *ex = sexp + raw.s * 2 * PG_TILE + (j >> 3);
                         vrow1 = 0;
 #pragma unroll
@@ -861,9 +973,23 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                             rows = rows << 8 | ex[STEP * i];
                             vrow1 = vrow1 << 8 | ex[PG_TILE + STEP * i];
                         }
+                        const bool own = BY_KEY && __any_sync(FULL_MASK, far != 0u);  // the keys' own exponents
                         if (j == 0) {
-                            const int A = (int)top - 127, B = (int)vtop1 - 127;
-                            smeta[mt.s] = make_float4(fabsf(p.qscale) * pow2f(min(A, 127)), (float)B, pow2f(max(-B, -126)), 0.0f);
+                            const int A = top - 127, B = vtop1 - 127;
+                            smeta[mt.s] = make_float4(fabsf(p.qscale) * pow2f(min(A, 127)), (float)B, pow2f(max(-B, -126)),
+                                                      own ? 1.0f : 0.0f);
+                        }
+                        if (own) {  // each warp writes an even share of the keys, four a lane
+                            if (lane / (32 / C::CONV) == (j >> 5)) {
+#pragma unroll 1
+                                for (int i = 0; i < 2; ++i) {
+                                    const int a = (int)(ke >> (16 * i)), b = (int)(ve >> (16 * i));
+                                    auto f = [&](int e) { return fabsf(p.qscale) * pow2f(min(max((e & 0xff) - 127, -126), 127)); };
+                                    skeys[mt.s * (PG_TILE / 2) + 2 * lane + i] =
+                                        make_float4(f(a), (float)((b & 0xff) - 127), f(a >> 8), (float)(((b >> 8) & 0xff) - 127));
+                                }
+                            }
+                            top = vtop1 = 0;
                         }
                     } else {
                         top = vtop0;
@@ -882,7 +1008,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     for (int i = 0; i < ROWS; ++i, rows >>= 8) {
                         uint4 v = *reinterpret_cast<const uint4 *>(src + 128 * STEP * i);
                         if (hide && !view.one(k0 + (j >> 3) + STEP * i)) v = make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t f = ck_factor((int)(rows & 0xffu) - (int)top);
+                        const uint32_t f = ck_factor((int)(rows & 0xffu) - top);
                         uint4 x0, x1;
                         ck_operand(odd ? v.z : v.x, f, x0.x, x0.y);
                         ck_operand(odd ? v.w : v.y, f, x0.z, x0.w);
@@ -894,9 +1020,9 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&raw_empty[raw.s]);
-                        mbar_arrive(&kv_full[kv.s]);
-                        if (part == 0) mbar_arrive(&meta_full[mt.s]);
+                        mbar_arrive(&bar.raw_empty[raw.s]);
+                        mbar_arrive(&bar.kv_full[kv.s]);
+                        if (part == 0) mbar_arrive(&bar.meta_full[mt.s]);
                     }
                     raw.step();
                     kv.step();
@@ -904,12 +1030,18 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     if (part == 0) {
                         mt.step();
                         ++keys;
+                        if (!BY_KEY && __any_sync(FULL_MASK, far != 0u)) {
+                            *abort_flag = CK_BY_KEY;
+                            ok = false;
+                            break;
+                        }
                     }
                 }
                 vtop0 = vtop1;
                 vrow0 = vrow1;
             }
         } while (ok && r.next(p.large, p.Hkv));
+        });
     }
 
     qt_fence_before();

@@ -191,3 +191,28 @@ def test_rows_of_any_size_single_tokens(vq, dtype, lo, hi, keys):
         lo = hi - 24  # (smaller outputs are below fp16's)
     _check(vq, _case(_spread(600, 2, lo, hi, keys), [1, 1], 4, 2, 16, dtype, seed=8), 2.0 ** -32)
     _check(vq, _case(_spread(600, 1, lo, hi, keys), [1], 16, 1, 128, dtype, seed=9), 2.0 ** -32)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lo,hi", [(-3, 3), (-8, 1), (-16, 0), (-20, 6), (-30, 4)])
+@pytest.mark.parametrize("keys", [0, 28])
+def test_rows_of_any_size_chunks(vq, dtype, lo, hi, keys):
+    if dtype == F16 and hi - lo > 24:
+        lo = hi - 24
+    _check(vq, _case(_spread(500, 1, lo, hi, keys), [45, 300], 4, 1, 16, dtype, seed=10), 2.0 ** -24)
+    _check(vq, _case(_spread(700, 2, lo, hi, keys), [130], 2, 2, 128, dtype, window=150, sinks=20, seed=11), 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("news", [[1], [40]])
+def test_a_small_row_carries_the_weight(vq, dtype, news):
+    """One value row, from 2^-20 of its neighbour's size down to 2^-30, has nearly all weight."""
+    for down in (20, 24, 25, 26, 30):
+        def rows(b, gen):
+            k = torch.randn(200, 1, D, generator=gen).double() * 0.1
+            v = torch.randn(200, 1, D, generator=gen).double() * 2.0 ** (10 - down)
+            k[:, :, 0] = -40 / 8 / D ** -0.5
+            k[37, :, 0] = 40 / 8 / D ** -0.5
+            v[38] *= 2.0 ** down
+            return k, v
+        _check(vq, _case(rows, news, 4, 1, 32, dtype, seed=12), 2.0 ** -32 if news == [1] else 2.0 ** -24)
