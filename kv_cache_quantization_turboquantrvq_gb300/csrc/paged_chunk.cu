@@ -22,7 +22,7 @@
 // memory (4096 bf16 queries over 16384 keys: four took 815 us, eight 763).
 //
 // What bounds it (that chunk over a 16-bit cache: 627 us, 1.53 PFLOP/s; over
-// codes 808): a pair of tiles takes 1.5 us where the products take 1.07.  The
+// codes 807): a pair of tiles takes 1.5 us where the products take 1.07.  The
 // score tile waits for its copy to registers between products, and by its bytes
 // (192 KB of operands read, 64 KB copied in) shared memory is as busy as the
 // tensor core.  Over codes the softmax warps have 176 registers instead of 208,
@@ -45,7 +45,9 @@
 // exponents lie further apart (its one exponent would be that of a row which may
 // have no weight at all) takes the codes as they are, and the exponents act key
 // by key in the softmax, as for single tokens:
-// t_j = scale 2^a_j (q . K_j) + b_j, and sum w_j 2^-b_j below the line.
+// t_j = scale 2^a_j (q . K_j) + b_j, and sum w_j 2^-b_j below the line.  So does a
+// tile with zero value rows: those count with the least exponent, which their
+// codes have to be read for.
 // Operands are fp16 whatever the queries' type, since one instruction makes them
 // of two codes (bf16 takes five: 996 us against 884 for the chunk above, with
 // four warps); bf16 queries become fp16 by a power of two for each row, in place,
@@ -87,12 +89,12 @@ template <bool Q8> struct CkShape {
     static constexpr int THREADS = 32 * WARPS;
     // registers a thread: at launch, the softmax warps, warps 8-11, the converting
     // warps; the shares of all warps add up to the launch's at most
-    static constexpr int REGS = Q8 ? 96 : 168, R_SOFT = Q8 ? 176 : 208, R_CTL = Q8 ? 40 : 88, R_CONV = 40;
+    static constexpr int REGS = Q8 ? 96 : 168, R_SOFT = Q8 ? 176 : 208, R_CTL = Q8 ? 48 : 88, R_CONV = 40;
     static_assert(256 * R_SOFT + 128 * R_CTL + 32 * CONV * R_CONV <= THREADS * REGS, "registers of one CTA");
     static constexpr int BARS = 3 + 2 * STAGES + 7 + 2 * RAW + 2 * META + 2;
     static constexpr int RUNS = 8 * 64;         // the softmax warps' runs
     static constexpr int SMEM = 1024 + 2 * TILE_B + STAGES * TILE_B + RAW * RAW_B + RUNS + RAW * 2 * PG_TILE +
-                                META * (16 + 8 * PG_TILE) + 8 * (Q8 ? 2 : 1) * BARS + 16;
+                                RAW * 32 + META * (16 + 8 * PG_TILE) + 8 * (Q8 ? 2 : 1) * BARS + 16;
 };
 static_assert(CkShape<false>::SMEM <= 232448 && CkShape<true>::SMEM <= 232448, "shared memory of one CTA");
 
@@ -344,6 +346,16 @@ __device__ __forceinline__ PgRun ck_run(uint32_t at)
     r.left = v[12]; r.first = v[13] != 0;
     return r;
 }
+// The run of the softmax warp that is furthest behind.
+__device__ __forceinline__ PgRun ck_run_behind(const unsigned char *srun)
+{
+    auto left = [&](int w) { return reinterpret_cast<const volatile int *>(srun + 64 * w)[12]; };
+    int b = 0;
+#pragma unroll 1
+    for (int w = 1; w < 8; ++w)
+        if (left(w) > left(b)) b = w;
+    return ck_run(smem_u32(srun + 64 * b));
+}
 __device__ __forceinline__ void ck_keep(uint32_t at, const PgRun &r, int lane)
 {
     __syncwarp();
@@ -396,7 +408,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     unsigned char *sexp = srun + C::RUNS;                   // [RAW][2][128] exponents (of key tiles)
     float4 *smeta = reinterpret_cast<float4 *>(sexp + C::RAW * 2 * PG_TILE);  // [META] |scale| 2^A, B, 2^-B, 1: key by key
     float4 *skeys = smeta + C::META;                        // [META][128] |scale| 2^a, b of a tile taken key by key
-    uint64_t *bars = reinterpret_cast<uint64_t *>(skeys + C::META * (PG_TILE / 2));
+    int *srow = reinterpret_cast<int *>(skeys + C::META * (PG_TILE / 2));     // [RAW][8] rows of a key tile's boxes
+    uint64_t *bars = reinterpret_cast<uint64_t *>(srow + C::RAW * 8);
     volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(bars + (Q8 ? 2 : 1) * C::BARS);
     volatile uint32_t *abort_flag = tslot + 1;
 
@@ -438,25 +451,26 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     };
 
     // A role goes through the CTA's share.  Over codes, the converting warps end
-    // that at the first tile whose exponents lie too far apart, and the CTA starts
-    // again with roles that can take them key by key.  One body for both spent 10
-    // to 18 % more on every tile, since softmax and converting warps have no
-    // register or instruction to spare; so it is 0 to 4 % (4096 queries over 16384
-    // keys: fp16 797 us against 801 without the check, bf16 808 against 779).  With
-    // value rows of 13 sizes 2^-12 to 1 in every tile that call takes 1.5 to 1.7 ms.
+    // that at the first tile whose exponents lie too far apart or that may have
+    // zero value rows, and the CTA goes on from that item's run with roles that can
+    // take the exponents key by key.  One body for both took 10 to 18 % longer on
+    // every tile, since softmax and converting warps have no register or instruction
+    // to spare; the check in a warp of its own 14 %, in the copying warp 6 to 14 %.
+    // So it is 1 to 4 % (4096 queries over 16384 keys: fp16 805 us against 801
+    // without the check, bf16 807 against 779), and that call takes 1.2 ms where
+    // token 0 has a zero value row, 1.1 where values reach beyond 224 (exponent 0)
+    // and 1.5 to 1.7 where every tile has value rows of 13 sizes from 2^-12 to 1.
     auto share = [&](auto role) {
         role(std::false_type(), r_all);
         if constexpr (Q8) {
             qt_fence_before();
             __syncthreads();
-            const bool again = *abort_flag == CK_BY_KEY;
-            if (!again) return;
+            if (*abort_flag != CK_BY_KEY) return;
+            const PgRun r = ck_run_behind(srun);
             __syncthreads();
             if (threadIdx.x == 0) *abort_flag = 0u;
             __syncthreads();
             qt_fence_after();
-            PgRun r;
-            r.start(p.large.start[blockIdx.x]);
             role(std::true_type(), r);
         }
     };
@@ -477,7 +491,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         int tiles = 0, queries = 0;  // copied
         bool ok = true;
         do {
-            if (!r.first) {
+            if (queries > 0) {
                 ok = __all_sync(FULL_MASK, wait(bar.q_empty, qpar));
                 qpar ^= 1u;
                 if (!ok) break;
@@ -525,6 +539,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                         }
                         // a key tile brings the exponents of keys and values
                         const unsigned n = part ? 0u : (unsigned)__popc(__ballot_sync(FULL_MASK, held));
+                        if (BY_KEY && part == 0 && lane < nbox) srow[raw.s * 8 + lane] = held ? row : -1;
+                        __syncwarp();
                         if (elect_lane()) mbar_arrive_expect_tx(&bar.raw_full[raw.s], RAW_B + n * 2 * box);
                         __syncwarp();
                         if (lane < nbox) {  // a lane per box
@@ -933,6 +949,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         PgRing<STAGES> kv;
         PgRing<C::META ? C::META : 1> mt;
         int tiles = 0, keys = 0;
+        const int box = min(1 << p.c.page_shift, PG_TILE);
         uint32_t far = 0u;  // exponents of this lane's keys too far below the tile's largest
         int vtop0 = 0, vtop1 = 0;  // exponents of the values to come: of tile u - 1, of tile u
         uint32_t vrow0 = 0, vrow1 = 0;
@@ -954,7 +971,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     uint32_t rows = 0;    // this thread's rows' exponents, a byte each
                     if (part == 0) {
                         const uint32_t *e4 = reinterpret_cast<const uint32_t *>(sexp + raw.s * 2 * PG_TILE) + lane;
-                        const uint32_t ke = e4[0], ve = e4[PG_TILE / 4];
+                        const uint32_t ke = e4[0];
+                        uint32_t ve = e4[PG_TILE / 4];
                         uint32_t see = 0xffffffffu;  // of this lane's four keys
                         if (edge) {
                             see = 0u;
@@ -963,6 +981,15 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                         }
                         top = ck_top(ke & see);
                         vtop1 = ck_top(ve & see);
+                        if constexpr (BY_KEY) {
+                            if (vtop1 >= 127) {
+                                const uint32_t exp0 = __vcmpeq4(ve | ~see, PG_EXP0);
+                                const int rw = exp0 != 0u ? srow[raw.s * 8 + 4 * lane / box] : -1;
+                                if (rw >= 0)
+                                    ve = pg_value_exps(ve | ~see, static_cast<const unsigned char *>(p.c.v) + (long long)(rw + 4 * lane % box) * D);
+                                vtop1 = ck_top(ve & see);
+                            }
+                        }
                         far = ck_less(ke | ~see, top - KEYS_WITHIN) | ck_less(ve | ~see, vtop1 - VALUES_WITHIN);
                         top = max(top, 87);  // (at least 2^-40: the factors below stay normal)
                         vtop1 = max(vtop1, 87);
@@ -1030,7 +1057,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     if (part == 0) {
                         mt.step();
                         ++keys;
-                        if (!BY_KEY && __any_sync(FULL_MASK, far != 0u)) {
+                        // (exponent 0, or more: there may be zero rows)
+                        if (!BY_KEY && (__any_sync(FULL_MASK, far != 0u) || vtop1 >= 127)) {
                             *abort_flag = CK_BY_KEY;
                             ok = false;
                             break;

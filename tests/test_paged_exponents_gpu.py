@@ -147,6 +147,15 @@ def test_a_zero_value_row_that_takes_attention_single_tokens(vq, dtype, size, sc
     _check(vq, _case(_first_zero(900, 1, size, score), [1], GQ, 1, 64, dtype, window=300, sinks=1, seed=2), 2.0 ** -32)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("size,score", [(1.0, 8.0), (1e-2, 11.0), (1e-3, 9.0), (1e-4, 9.0)])
+@pytest.mark.parametrize("PS", [16, 128, 256])
+def test_a_zero_value_row_that_takes_attention_chunks(vq, dtype, size, score, PS):
+    _check(vq, _case(_first_zero(700, 1, size, score), [40], 4, 1, PS, dtype, seed=3), 2.0 ** -24)
+    _check(vq, _case(_first_zero(900, 1, size, score), [70, 33], 2, 1, PS, dtype, window=200, sinks=1, seed=4),
+           2.0 ** -24)
+
+
 def _many_zero(n, Hkv, size):
     """A third of the value rows, and whole stretches of them, are zero."""
     def rows(b, gen):
@@ -164,6 +173,22 @@ def _many_zero(n, Hkv, size):
 def test_zero_value_rows_everywhere_single_tokens(vq, dtype, size):
     _check(vq, _case(_many_zero(700, 2, size), [1, 1], 4, 2, 32, dtype, seed=5), 2.0 ** -32)
     _check(vq, _case(_many_zero(300, 1, size), [1], 4, 1, 16, dtype, seed=7), 2.0 ** -32)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("size", [0.3, 1e-4, 0.0])
+def test_zero_value_rows_everywhere_chunks(vq, dtype, size):
+    _check(vq, _case(_many_zero(600, 2, size), [50, 130], 3, 2, 32, dtype, seed=6), 2.0 ** -24)
+    _check(vq, _case(_many_zero(300, 1, size), [60], 4, 1, 16, dtype, seed=7), 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("size,score", [(1e-2, 11.0), (1e-4, 9.0)])
+def test_a_zero_value_row_in_the_middle_of_a_share(vq, dtype, size, score):
+    """Several items and many tiles for every block, so that blocks meet the zero
+    row at an item's start, after others that they finished: items of two query
+    tiles and of one, whole ones and cut ones."""
+    _check(vq, _case(_first_zero(2100, 8, size, score), [150, 20, 70, 40], 4, 8, 64, dtype, seed=14), 2.0 ** -24)
 
 
 def _spread(n, Hkv, lo, hi, keys=0):
