@@ -1003,8 +1003,9 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                         const bool own = BY_KEY && __any_sync(FULL_MASK, far != 0u);  // the keys' own exponents
                         if (j == 0) {
                             const int A = top - 127, B = vtop1 - 127;
-                            smeta[mt.s] = make_float4(fabsf(p.qscale) * pow2f(min(A, 127)), (float)B, pow2f(max(-B, -126)),
-                                                      own ? 1.0f : 0.0f);
+                            // (the factor stays a number that -inf times it stays -inf, however small the scale)
+                            smeta[mt.s] = make_float4(fmaxf(fabsf(p.qscale) * pow2f(min(A, 127)), 1e-37f), (float)B,
+                                                      pow2f(max(-B, -126)), own ? 1.0f : 0.0f);
                         }
                         if (own) {  // each warp writes an even share of the keys, four a lane
                             if (lane / (32 / C::CONV) == (j >> 5)) {

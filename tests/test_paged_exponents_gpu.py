@@ -241,3 +241,14 @@ def test_a_small_row_carries_the_weight(vq, dtype, news):
             v[38] *= 2.0 ** down
             return k, v
         _check(vq, _case(rows, news, 4, 1, 32, dtype, seed=12), 2.0 ** -32 if news == [1] else 2.0 ** -24)
+
+
+@pytest.mark.parametrize("news", [[1, 1], [33, 1]])
+def test_small_scales_over_codes(vq, news):
+    """Scales so small that their product with a key's exponent has no 32-bit
+    number: plain means, as scale 0."""
+    def rows(b, gen):
+        return torch.randn(150, 1, D, generator=gen).double() * 1e-9, torch.randn(150, 1, D, generator=gen).double()
+    a = _case(rows, news, 4, 1, 16, F16, seed=13)
+    for scale in (0.0, 1e-30, 1e-36, 1e-45):
+        _check(vq, dict(a, scale=scale), 2.0 ** -24)
