@@ -467,13 +467,23 @@ def _raw_stream(stream, t):
     return raw(t.device.index) if raw is not None else torch.cuda.current_stream().cuda_stream
 
 
-def _use(stream, *tensors):
-    """Tensors allocated here for a call on another stream than the current one stay
-    reserved until that stream is done with them."""
-    if stream is not None and hasattr(stream, "cuda_stream"):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _empty(shape, dtype, device, stream, returned=True):
+    """An empty tensor that a call on `stream` (None: the current one) writes.  It is
+    made on that stream: a block of the current stream's could still be in use by
+    kernels queued there, and would go back to it while the call still runs.  What
+    is returned is reserved for the current stream's use too."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and current.cuda_stream != stream.cuda_stream:
+        t.record_stream(current)
+    return t
 
 
 def paged_cache(num_pages: int, Hkv: int, page_size: int, dtype, device="cuda", D: int = 128) -> dict:
@@ -527,7 +537,8 @@ def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtyp
                     want_k=True, want_v=True, stream=None):
     """Read tokens first[b] + [0, S_out) of every sequence back: (k, v)
     [B, Hkv, S_out, 128] of dtype (the cache's; float16 by default from an 8-bit
-    cache), zeros past lens[b].  block_table [B, max_pages], lens and first [B] int32."""
+    cache), zeros past lens[b].  block_table [B, max_pages], lens and first [B] int32.
+    stream: a torch stream or a handle; outputs made here are its memory."""
     import torch
     args = _cache_args(cache)
     i32 = torch.int32
@@ -537,22 +548,19 @@ def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtyp
         dtype = torch.float16 if args[4] == VQ_E4M3 else cache["k_pages"].dtype
     shape = (B, args[6], S_out, args[8])
     dev = block_table.device
-    made = []
     ptrs = [None, None]
     outs = [k_out if want_k else None, v_out if want_v else None]
     for i, want in enumerate((want_k, want_v)):
         if not want:
             continue
         if outs[i] is None:
-            outs[i] = torch.empty(shape, dtype=dtype, device=dev)
-            made.append(outs[i])
+            outs[i] = _empty(shape, dtype, dev, stream)
             ptrs[i] = outs[i].data_ptr()
         else:
             ptrs[i] = _typed(outs[i], dtype, shape, "k_out, v_out")
     _check(lib().vq_paged_gather(*args, table, max_pages, _typed(lens, i32, (B,), "lens"),
                                  None if first is None else _typed(first, i32, (B,), "first"), B, S_out,
                                  _dtype_code(dtype), *ptrs, _raw_stream(stream, block_table)), "vq_paged_gather")
-    _use(stream, *made)
     return outs[0], outs[1]
 
 
@@ -573,7 +581,8 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
     last of them at position lens[b] - 1; each sees the keys up to its own
     position, with a window those of the last `window` positions and the first
     `sinks`.  cu_q [B + 1], lens [B], block_table [B, max_pages] int32.  Returns
-    [T, Hq, 128] of q's dtype; the workspace (uint8) is allocated when not given."""
+    [T, Hq, 128] of q's dtype; the workspace (uint8) is allocated when not given.
+    stream: a torch stream or a handle; what is made here is its memory."""
     import torch
     args = _cache_args(cache)
     i32 = torch.int32
@@ -583,10 +592,8 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
     view = _rows_view(q, Hq, D, "q")
     table = _typed(block_table, i32, (B, max_pages), "block_table")
     cu, ln = _typed(cu_q, i32, (B + 1,), "cu_q"), _typed(lens, i32, (B,), "lens")
-    made = []
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
-        made.append(out)
+        out = _empty((T, Hq, D), dtype, dev, stream)
         po = out.data_ptr()
     else:
         po = _typed(out, dtype, (T, Hq, D), "out")
@@ -597,12 +604,9 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
             if len(_workspace_bytes) > 4096:
                 _workspace_bytes.clear()
             wb = _workspace_bytes[key] = vq_paged_attend_workspace(T, B, Hq, args[6], max_q)
-        workspace = torch.empty(max(wb, 16), dtype=torch.uint8, device=dev)
-        made.append(workspace)
+        workspace = _empty(max(wb, 16), torch.uint8, dev, stream, returned=False)
     else:
         wb = workspace.numel() * workspace.element_size()
     _check(lib().vq_paged_attend(*view, _dtype_code(dtype), *args, table, max_pages, cu, ln, T, B, Hq, max_q, window, sinks,
                                  scale, po, workspace.data_ptr(), wb, _raw_stream(stream, q)), "vq_paged_attend")
-    if stream is not None:
-        _use(stream, *made)
     return out
