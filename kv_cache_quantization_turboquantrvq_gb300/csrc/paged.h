@@ -93,6 +93,8 @@ struct PagedAttendParams {
     int small_rows;              // sequences with at most this many query rows per kv head are small
     float qscale;                // softmax scale * log2(e)
     PgPlan small, large;         // cap 0: the class is not used
+    unsigned long long *planned; // (both classes) `call` from when the plan is made until the merge
+    unsigned long long call;     // a number of this call's own, not 0
 };
 constexpr int PG_SROWS = 16;     // rows of a small item
 constexpr int PG_LROWS = 256;    // rows of a large item (two tensor-memory tiles)

@@ -1,5 +1,6 @@
 // paged_api.cpp - the extern "C" entry points of the paged-cache operators:
 // argument validation, the workspace's layout, launches.  Host code only.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -14,6 +15,7 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kMaxGroup = 16;  // query heads per kv head
+constexpr size_t kPlanned = 256;  // at the workspace's end: the word that says the plan is made
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -149,7 +151,7 @@ vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, AttendPlan &pl)
     if (large) pl.large_cap = (T + pl.large_tq - 1) / pl.large_tq + B;
     pl.s = layout(0, pl.small_cap, pl.G, PG_SROWS);
     pl.l = layout(pl.s.end, pl.large_cap, pl.G, PG_LROWS);
-    pl.bytes = pl.l.end;
+    pl.bytes = pl.l.end + (small && large ? kPlanned : 0);
     return VQ_OK;
 }
 
@@ -323,6 +325,11 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     place(p.small, ws, pl.s, pl.small_cap, pl.G, pl.small_tq);
     place(p.large, ws, pl.l, pl.large_cap, pl.G, pl.large_tq);
+    if (pl.small_cap && pl.large_cap) {
+        static std::atomic<unsigned long long> calls{0};
+        p.planned = reinterpret_cast<unsigned long long *>(ws + pl.l.end);
+        p.call = ++calls;
+    }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // (a call of small sequences alone: its kernel makes the plan)
     cudaError_t e = pl.large_cap ? launch_paged_plan(p, s) : cudaSuccess;

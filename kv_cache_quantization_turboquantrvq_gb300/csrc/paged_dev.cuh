@@ -76,6 +76,18 @@ __device__ __forceinline__ bool elect_lane()
 __device__ __forceinline__ void pg_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pg_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A word written after, and read before, other memory by kernels that overlap.
+__device__ __forceinline__ void pg_release(unsigned long long *at, unsigned long long v)
+{
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(at), "l"(v) : "memory");
+}
+__device__ __forceinline__ unsigned long long pg_acquire(const unsigned long long *at)
+{
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(at) : "memory");
+    return v;
+}
+
 // Barrier of the first THREADS threads of the CTA.
 template <int THREADS> __device__ __forceinline__ void bar_compute()
 {

@@ -99,3 +99,41 @@ def test_handles_and_streams_give_the_same(vq, cache, news):
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(k, kw) and torch.equal(v, vw)
     assert vq.vq_device_error() == 0
+
+
+@pytest.mark.parametrize("cache", [torch.float16, torch.float8_e4m3fn])
+def test_a_captured_mixed_call_follows_its_inputs(vq, cache):
+    """Plan, chunks, single tokens and merge overlap on the GPU; replayed with other
+    lengths, other numbers of new tokens and other queries, back to back, each
+    replay gives what a call of its own gives."""
+    a = _call(vq, [300, 1, 1, 40], [2700, 900, 1500, 1300], cache=cache, seed=2)
+    T = a["q"].shape[0]
+    out = torch.empty_like(a["q"])
+    ws = torch.full((vq.vq_paged_attend_workspace(T, 4, 8, 2, 300),), 255, dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        vq.vq_paged_attend(out=out, workspace=ws, **a)
+    gen = torch.Generator().manual_seed(3)
+    seen, want = [], []
+    for i in range(12):
+        cut = sorted(torch.randint(0, 301, (3,), generator=gen).tolist())
+        cu = [0, cut[0], cut[1], cut[2], min(T, cut[2] + 300)] if i % 2 else [0, 300, 301, 302, 342]
+        lens = [int(torch.randint(m // 4, m + 1, (1,), generator=gen)) for m in (2700, 900, 1500, 1300)]
+        q = torch.randn(a["q"].shape, generator=gen).to(a["q"].dtype).cuda()
+        cu, lens = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (cu, lens))
+        w = torch.zeros_like(out)
+        vq.vq_paged_attend(**dict(a, q=q, cu_q=cu, lens=lens, out=w))
+        seen.append((q, cu, lens))
+        want.append(w)
+    torch.cuda.synchronize()
+    got = [torch.zeros_like(out) for _ in want]
+    for (q, cu, lens), o in zip(seen, got):  # (no wait between the replays)
+        a["q"].copy_(q)
+        a["cu_q"].copy_(cu)
+        a["lens"].copy_(lens)
+        out.zero_()
+        g.replay()
+        o.copy_(out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert vq.vq_device_error() == 0
