@@ -426,7 +426,8 @@ vq_status vq_paged_gather(const void *k_pages, const void *v_pages, const uint8_
  *     type), strided: the new tokens of all sequences one after another.
  *   cu_q [B + 1] int32, device: sequence b has tokens [cu_q[b], cu_q[b + 1]) of
  *     q, n_b of them, at most max_q (more set VQ_DEVERR_BAD_OFFSET, and the
- *     tokens past max_q are left out).
+ *     tokens past max_q are left out).  Numbers outside [0, T] and numbers that
+ *     decrease set it too; outputs are then unspecified.
  *   lens [B] int32, device: tokens of sequence b in the cache, the new ones
  *     (already written) included.
  * Token i of sequence b is at position p = lens[b] - n_b + i and sees the keys

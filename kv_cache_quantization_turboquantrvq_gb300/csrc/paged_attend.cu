@@ -89,16 +89,20 @@ __device__ __forceinline__ PgEntry make_entry(const PagedAttendParams &p, int b,
 }
 
 // The first query token, the number of new tokens and the length of sequence b,
-// within the buffers whatever the numbers given; false: more tokens than max_q.
-__device__ __forceinline__ bool sequence(const PagedAttendParams &p, int b, int &start, int &n, int &len)
+// within the buffers whatever the numbers given, and whether they make sense:
+// SEQ_BACK, the next sequence starts before this one; SEQ_BAD, tokens outside the
+// queries, or more than max_q.
+enum { SEQ_OK = 0, SEQ_BAD = 1, SEQ_BACK = 2 };
+__device__ __forceinline__ int sequence(const PagedAttendParams &p, int b, int &start, int &n, int &len)
 {
     const int cap = (int)min((long long)p.max_pages << p.c.page_shift, 0x7fffffffLL);
-    start = min(max(__ldg(p.cu + b), 0), p.T);
-    n = min(max(__ldg(p.cu + b + 1), start), p.T) - start;
+    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
+    start = min(max(c0, 0), p.T);
+    n = min(max(c1, start), p.T) - start;
     len = min(max(__ldg(p.lens + b), 0), cap);
-    const bool ok = n <= p.max_q;
+    const bool bad = n > p.max_q || c0 < 0 || c1 > p.T;
     n = min(n, p.max_q);
-    return ok;
+    return c1 < c0 ? SEQ_BACK : bad ? SEQ_BAD : SEQ_OK;
 }
 
 // Even shares of the units: the first `rem` of `g` CTAs take one more than q.
@@ -143,7 +147,11 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
     for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
         const int b = b0 + (threadIdx.x >> 5) + 32 * lane;  // (few sequences: a warp each)
         int start = 0, n = 0, len = 0;
-        if (b < p.B && !sequence(p, b, start, n, len)) atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+        const int sense = b < p.B ? sequence(p, b, start, n, len) : SEQ_OK;
+        if (sense != SEQ_OK) atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+        // Sequences that do not go back share no token, so their entries fit.  Others
+        // could have any number of entries: none of them is planned.
+        if (__syncthreads_or(sense == SEQ_BACK)) break;
         const bool large = n * p.GQ > p.small_rows;
         const int tq = large ? p.large.tq : p.small.tq;
         const int cnt = (n + tq - 1) / tq;
@@ -154,11 +162,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
         // sequences of one entry write it themselves, a warp writes those of more
         auto put = [&](int b_, int start_, int n_, int len_, bool large_, int first_, int i) {
             const PgPlan &pl = large_ ? p.large : p.small;
-            const int at = first_ + i;
-            if (at >= pl.cap) {
-                atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
-                return;
-            }
+            const int at = first_ + i;  // below pl.cap
             const PgEntry e = make_entry(p, b_, start_, n_, len_, pl.tq, i);
             pl.ent[at] = e;
             if (at < PLAN_KEPT) s_nt[large_][at] = e.ntiles;
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
     for (int k = 0; k < 2; ++k) {
         const PgPlan &pl = k ? p.large : p.small;
         if (pl.cap == 0) continue;
-        const int nent = min(pl.cap, (int)(k ? carry >> 32 : carry & 0xffffffffLL));
+        const int nent = (int)(k ? carry >> 32 : carry & 0xffffffffLL);
         auto tiles = [&](int i) { return i < PLAN_KEPT ? s_nt[k][i] : pl.ent[i].ntiles; };
         auto base = [&](int i) { return i < PLAN_KEPT ? s_base[k][i] : pl.base[i]; };
         long long total = 0;
@@ -482,7 +486,7 @@ template <int THREADS> __device__ __forceinline__ void own_plan(const PagedAtten
     bool fits = true;
     for (int b = b0; b < b1; ++b) {
         int start, n, len;
-        fits = sequence(p, b, start, n, len) && fits;
+        fits = sequence(p, b, start, n, len) == SEQ_OK && fits;
         if (n > 0) mine += (long long)make_entry(p, b, start, n, len, p.small.tq, 0).ntiles * p.Hkv;
     }
     if (!fits && c == 0) atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
