@@ -429,7 +429,9 @@ vq_status vq_paged_gather(const void *k_pages, const void *v_pages, const uint8_
  *     tokens past max_q are left out).  Numbers outside [0, T] and numbers that
  *     decrease set it too; outputs are then unspecified.
  *   lens [B] int32, device: tokens of sequence b in the cache, the new ones
- *     (already written) included.
+ *     (already written) included.  A length that is negative or past the block
+ *     table's max_pages * page_size sets VQ_DEVERR_BAD_OFFSET where the sequence
+ *     has new tokens, whose outputs are then unspecified.
  * Token i of sequence b is at position p = lens[b] - n_b + i and sees the keys
  * j <= p that satisfy: window == 0, or j > p - window, or j < sinks.
  *   out[t][hq] = sum_j softmax_j(scale * q[t][hq] . k_j) v_j over them, kv head

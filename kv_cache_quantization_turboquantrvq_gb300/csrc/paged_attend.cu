@@ -91,7 +91,7 @@ __device__ __forceinline__ PgEntry make_entry(const PagedAttendParams &p, int b,
 // The first query token, the number of new tokens and the length of sequence b,
 // within the buffers whatever the numbers given, and whether they make sense:
 // SEQ_BACK, the next sequence starts before this one; SEQ_BAD, tokens outside the
-// queries, or more than max_q.
+// queries, more than max_q, or of a sequence longer than its pages.
 enum { SEQ_OK = 0, SEQ_BAD = 1, SEQ_BACK = 2 };
 __device__ __forceinline__ int sequence(const PagedAttendParams &p, int b, int &start, int &n, int &len)
 {
@@ -99,8 +99,9 @@ __device__ __forceinline__ int sequence(const PagedAttendParams &p, int b, int &
     const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
     start = min(max(c0, 0), p.T);
     n = min(max(c1, start), p.T) - start;
-    len = min(max(__ldg(p.lens + b), 0), cap);
-    const bool bad = n > p.max_q || c0 < 0 || c1 > p.T;
+    const int given = __ldg(p.lens + b);
+    len = min(max(given, 0), cap);
+    const bool bad = n > p.max_q || c0 < 0 || c1 > p.T || (n > 0 && len != given);
     n = min(n, p.max_q);
     return c1 < c0 ? SEQ_BACK : bad ? SEQ_BAD : SEQ_OK;
 }

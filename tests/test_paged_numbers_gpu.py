@@ -34,6 +34,21 @@ def _run(vq, T, cu, lens, max_q, pages=8, PS=16, GQ=4):
     return out, code
 
 
+@pytest.mark.parametrize("T,cu,max_q", [(3, [0, 1, 2, 3], 1), (82, [0, 1, 41, 82], 41)])
+def test_a_length_past_the_table_is_reported(vq, T, cu, max_q):
+    want, code = _run(vq, T, cu, [100, 128, 60], max_q)
+    assert code == 0
+    for bad in (129, 10 ** 6, 2 ** 31 - 1, -1):
+        got, code = _run(vq, T, cu, [100, bad, 60], max_q)
+        assert code == vq.VQ_DEVERR_BAD_OFFSET
+        assert torch.equal(got[:cu[1]], want[:cu[1]]) and torch.equal(got[cu[2]:], want[cu[2]:])
+
+
+def test_a_length_past_the_table_of_a_sequence_without_new_tokens_is_not(vq):
+    for T, cu, max_q in ((2, [0, 1, 1, 2], 1), (80, [0, 40, 40, 80], 41)):
+        assert _run(vq, T, cu, [100, 10 ** 6, 60], max_q)[1] == 0
+
+
 @pytest.mark.parametrize("cu", [[0, 3, 1, 4], [0, 4, 0, 4], [-2, 1, 2, 4], [0, 1, 2, 5], [2, 1, 0, -1]])
 def test_offsets_of_single_tokens_that_make_no_sense(vq, cu):
     assert _run(vq, 4, cu, [100, 90, 60], 4)[1] == vq.VQ_DEVERR_BAD_OFFSET
