@@ -606,6 +606,8 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
             wb = _workspace_bytes[key] = vq_paged_attend_workspace(T, B, Hq, args[6], max_q)
         workspace = _empty(max(wb, 16), torch.uint8, dev, stream, returned=False)
     else:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous CUDA tensor")
         wb = workspace.numel() * workspace.element_size()
     _check(lib().vq_paged_attend(*view, _dtype_code(dtype), *args, table, max_pages, cu, ln, T, B, Hq, max_q, window, sinks,
                                  scale, po, workspace.data_ptr(), wb, _raw_stream(stream, q)), "vq_paged_attend")
