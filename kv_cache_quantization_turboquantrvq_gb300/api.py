@@ -440,18 +440,29 @@ def _dtype_code(dtype) -> int:
     return code
 
 
-def _typed(t, dtype, shape, what):
-    """Raise ValueError unless t is a contiguous CUDA tensor of this dtype and shape."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+def _gpu(t, what) -> int:
+    """The index of the GPU that t lies on (ValueError: on none)."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s: a CUDA tensor" % what)
+    return dev
+
+
+def _typed(t, dtype, shape, what, dev=None):
+    """The address of t; ValueError unless it is a contiguous CUDA tensor of this dtype
+    and shape (on GPU dev)."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s: a contiguous CUDA tensor %s of %s" % (what, tuple(shape), dtype))
+    if (t.get_device() != dev) if dev is not None else not t.is_cuda:
+        raise ValueError("%s: on the GPU of the other tensors" % what)
     return t.data_ptr()
 
 
-def _rows_view(t, heads, D, what):
-    """(address, token stride, head stride) of a [T, heads, D] view whose rows are contiguous."""
+def _rows_view(t, heads, D, what, dev):
+    """(address, token stride, head stride) of a [T, heads, D] view on GPU dev whose rows are contiguous."""
     shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != D or not t.is_cuda:
-        raise ValueError("%s: a CUDA tensor [tokens, %d, %d]" % (what, heads, D))
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D or t.get_device() != dev:
+        raise ValueError("%s: a CUDA tensor [tokens, %d, %d] on the GPU of the other tensors" % (what, heads, D))
     st = t.stride()
     if st[2] != 1:
         raise ValueError("%s: the entries of a head have to be contiguous" % what)
@@ -500,21 +511,30 @@ def paged_cache(num_pages: int, Hkv: int, page_size: int, dtype, device="cuda", 
     return c
 
 
-def _cache_args(cache):
-    """(k, v, k_exp, v_exp, dtype, num_pages, Hkv, page_size, D) of a cache dict."""
+def _on_gpu(dev, function, *args):
+    """The status of a library call made with GPU dev current, as its sizes and launches want."""
+    import torch
+    if torch.cuda.current_device() == dev:
+        return function(*args)
+    with torch.cuda.device(dev):
+        return function(*args)
+
+
+def _cache_args(cache, dev):
+    """(k, v, k_exp, v_exp, dtype, num_pages, Hkv, page_size, D) of a cache dict on GPU dev."""
     k, v = cache["k_pages"], cache["v_pages"]
     dtype, shape = k.dtype, k.shape
     code = _dtype_code(dtype)
     if len(shape) != 4:
         raise ValueError("k_pages: [num_pages, Hkv, page_size, D]")
-    kp, vp = _typed(k, dtype, shape, "k_pages"), _typed(v, dtype, shape, "v_pages")
+    kp, vp = _typed(k, dtype, shape, "k_pages", dev), _typed(v, dtype, shape, "v_pages", dev)
     ke = ve = None
     if code == VQ_E4M3:
         import torch
         ke, ve = cache.get("k_exp"), cache.get("v_exp")
         if ke is None or ve is None:
             raise ValueError("a float8_e4m3fn cache has k_exp and v_exp")
-        ke, ve = _typed(ke, torch.uint8, shape[:3], "k_exp"), _typed(ve, torch.uint8, shape[:3], "v_exp")
+        ke, ve = _typed(ke, torch.uint8, shape[:3], "k_exp", dev), _typed(ve, torch.uint8, shape[:3], "v_exp", dev)
     return (kp, vp, ke, ve, code, *shape)
 
 
@@ -523,13 +543,14 @@ def vq_paged_append(k, v, cache: dict, slots, stream=None) -> dict:
     strided) of new tokens into the paged cache at slots [T] int64 (page *
     page_size + place; negative: not written).  Returns the cache."""
     import torch
-    args = _cache_args(cache)
+    dev = _gpu(k, "k")
+    args = _cache_args(cache, dev)
     T = k.shape[0]
     if k.dtype != v.dtype or v.shape[0] != T:
         raise ValueError("k and v: the same tokens and dtype")
-    views = _rows_view(k, args[6], args[8], "k") + _rows_view(v, args[6], args[8], "v")
-    _check(lib().vq_paged_append(*views, _dtype_code(k.dtype), T, _typed(slots, torch.int64, (T,), "slots"), *args,
-                                 _raw_stream(stream, k)), "vq_paged_append")
+    views = _rows_view(k, args[6], args[8], "k", dev) + _rows_view(v, args[6], args[8], "v", dev)
+    _check(_on_gpu(dev, lib().vq_paged_append, *views, _dtype_code(k.dtype), T,
+                   _typed(slots, torch.int64, (T,), "slots", dev), *args, _raw_stream(stream, k)), "vq_paged_append")
     return cache
 
 
@@ -540,10 +561,11 @@ def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtyp
     cache), zeros past lens[b].  block_table [B, max_pages], lens and first [B] int32.
     stream: a torch stream or a handle; outputs made here are its memory."""
     import torch
-    args = _cache_args(cache)
+    gpu = _gpu(block_table, "block_table")
+    args = _cache_args(cache, gpu)
     i32 = torch.int32
     B, max_pages = block_table.shape
-    table = _typed(block_table, i32, (B, max_pages), "block_table")
+    table = _typed(block_table, i32, (B, max_pages), "block_table", gpu)
     if dtype is None:
         dtype = torch.float16 if args[4] == VQ_E4M3 else cache["k_pages"].dtype
     shape = (B, args[6], S_out, args[8])
@@ -557,10 +579,10 @@ def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtyp
             outs[i] = _empty(shape, dtype, dev, stream)
             ptrs[i] = outs[i].data_ptr()
         else:
-            ptrs[i] = _typed(outs[i], dtype, shape, "k_out, v_out")
-    _check(lib().vq_paged_gather(*args, table, max_pages, _typed(lens, i32, (B,), "lens"),
-                                 None if first is None else _typed(first, i32, (B,), "first"), B, S_out,
-                                 _dtype_code(dtype), *ptrs, _raw_stream(stream, block_table)), "vq_paged_gather")
+            ptrs[i] = _typed(outs[i], dtype, shape, "k_out, v_out", gpu)
+    _check(_on_gpu(gpu, lib().vq_paged_gather, *args, table, max_pages, _typed(lens, i32, (B,), "lens", gpu),
+                   None if first is None else _typed(first, i32, (B,), "first", gpu), B, S_out,
+                   _dtype_code(dtype), *ptrs, _raw_stream(stream, block_table)), "vq_paged_gather")
     return outs[0], outs[1]
 
 
@@ -584,31 +606,32 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
     [T, Hq, 128] of q's dtype; the workspace (uint8) is allocated when not given.
     stream: a torch stream or a handle; what is made here is its memory."""
     import torch
-    args = _cache_args(cache)
+    gpu = _gpu(q, "q")
+    args = _cache_args(cache, gpu)
     i32 = torch.int32
     B, max_pages = block_table.shape
     T, Hq, _ = q.shape
     D, dtype, dev = args[8], q.dtype, q.device
-    view = _rows_view(q, Hq, D, "q")
-    table = _typed(block_table, i32, (B, max_pages), "block_table")
-    cu, ln = _typed(cu_q, i32, (B + 1,), "cu_q"), _typed(lens, i32, (B,), "lens")
+    view = _rows_view(q, Hq, D, "q", gpu)
+    table = _typed(block_table, i32, (B, max_pages), "block_table", gpu)
+    cu, ln = _typed(cu_q, i32, (B + 1,), "cu_q", gpu), _typed(lens, i32, (B,), "lens", gpu)
     if out is None:
         out = _empty((T, Hq, D), dtype, dev, stream)
         po = out.data_ptr()
     else:
-        po = _typed(out, dtype, (T, Hq, D), "out")
+        po = _typed(out, dtype, (T, Hq, D), "out", gpu)
     if workspace is None:
-        key = (T, B, Hq, args[6], max_q, dev.index)
+        key = (T, B, Hq, args[6], max_q, gpu)
         wb = _workspace_bytes.get(key)
         if wb is None:
             if len(_workspace_bytes) > 4096:
                 _workspace_bytes.clear()
-            wb = _workspace_bytes[key] = vq_paged_attend_workspace(T, B, Hq, args[6], max_q)
+            wb = _workspace_bytes[key] = _on_gpu(gpu, vq_paged_attend_workspace, T, B, Hq, args[6], max_q)
         workspace = _empty(max(wb, 16), torch.uint8, dev, stream, returned=False)
     else:
-        if not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace: a contiguous CUDA tensor")
+        if workspace.get_device() != gpu or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous CUDA tensor on the GPU of the other tensors")
         wb = workspace.numel() * workspace.element_size()
-    _check(lib().vq_paged_attend(*view, _dtype_code(dtype), *args, table, max_pages, cu, ln, T, B, Hq, max_q, window, sinks,
-                                 scale, po, workspace.data_ptr(), wb, _raw_stream(stream, q)), "vq_paged_attend")
+    _check(_on_gpu(gpu, lib().vq_paged_attend, *view, _dtype_code(dtype), *args, table, max_pages, cu, ln, T, B, Hq, max_q,
+                   window, sinks, scale, po, workspace.data_ptr(), wb, _raw_stream(stream, q)), "vq_paged_attend")
     return out

@@ -120,3 +120,29 @@ def test_a_workspace_has_to_be_whole_memory_of_the_gpu(api, workspace):
     with pytest.raises(ValueError):
         _attend(api, workspace=workspace)
     assert not api.log
+
+
+@pytest.mark.parametrize("call,name,bad", [
+    (_append, "k", Fake((5, 2, D), F16, 1)), (_append, "v", Fake((5, 2, D), F16, 1)),
+    (_append, "slots", Fake((5,), torch.int64, 1)), (_append, "cache", _cache(0, v_pages=Fake((4, 2, 16, D), F16, 1))),
+    (_gather, "block_table", Fake((2, 3), I32, 1)), (_gather, "lens", Fake((2,), I32, 1)),
+    (_gather, "first", Fake((2,), I32, 1)), (_gather, "k_out", Fake((2, 2, 7, D), F16, 1)), (_gather, "cache", _cache(1)),
+    (_attend, "q", Fake((5, 8, D), F16, 1)), (_attend, "cache", _cache(1)), (_attend, "block_table", Fake((2, 3), I32, 1)),
+    (_attend, "cu_q", Fake((3,), I32, 1)), (_attend, "lens", Fake((2,), I32, 1)), (_attend, "out", Fake((5, 8, D), F16, 1)),
+    (_attend, "workspace", Fake((1 << 20,), U8, 1))])
+def test_tensors_of_two_gpus_are_refused(api, call, name, bad):
+    with pytest.raises(ValueError):
+        call(api, **{name: bad})
+    assert not api.log
+
+
+@pytest.mark.parametrize("call", [_append, _gather, _attend])
+def test_the_tensors_gpu_is_made_current(api, call):
+    call(api, device=1)
+    assert [d for _, d, _ in api.log] == [1]
+
+
+def test_the_workspace_is_sized_for_the_tensors_gpu(api, monkeypatch):
+    monkeypatch.setattr(api, "_empty", lambda shape, dtype, device, stream, returned=True: Fake((shape,), dtype, 1))
+    _attend(api, device=1, workspace=None)
+    assert [(n, d) for n, d, _ in api.log] == [("vq_paged_attend_workspace", 1), ("vq_paged_attend", 1)]
