@@ -511,6 +511,13 @@ def paged_cache(num_pages: int, Hkv: int, page_size: int, dtype, device="cuda", 
     return c
 
 
+def _int32(*values):
+    """ValueError for numbers that a C int would cut to other ones."""
+    for v in values:
+        if v >= 1 << 31:
+            raise ValueError("%d: less than 2^31" % v)
+
+
 def _on_gpu(dev, function, *args):
     """The status of a library call made with GPU dev current, as its sizes and launches want."""
     import torch
@@ -561,6 +568,7 @@ def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtyp
     cache), zeros past lens[b].  block_table [B, max_pages], lens and first [B] int32.
     stream: a torch stream or a handle; outputs made here are its memory."""
     import torch
+    _int32(S_out)
     gpu = _gpu(block_table, "block_table")
     args = _cache_args(cache, gpu)
     i32 = torch.int32
@@ -606,6 +614,7 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
     [T, Hq, 128] of q's dtype; the workspace (uint8) is allocated when not given.
     stream: a torch stream or a handle; what is made here is its memory."""
     import torch
+    _int32(max_q, window, sinks)
     gpu = _gpu(q, "q")
     args = _cache_args(cache, gpu)
     i32 = torch.int32

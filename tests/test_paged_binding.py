@@ -146,3 +146,14 @@ def test_the_workspace_is_sized_for_the_tensors_gpu(api, monkeypatch):
     monkeypatch.setattr(api, "_empty", lambda shape, dtype, device, stream, returned=True: Fake((shape,), dtype, 1))
     _attend(api, device=1, workspace=None)
     assert [(n, d) for n, d, _ in api.log] == [("vq_paged_attend_workspace", 1), ("vq_paged_attend", 1)]
+
+
+@pytest.mark.parametrize("call,name", [(_attend, "max_q"), (_attend, "window"), (_attend, "sinks"), (_gather, "S_out")])
+@pytest.mark.parametrize("value", [1 << 31, (1 << 32) + 4, 1 << 40])
+def test_numbers_past_32_bits_are_refused(api, call, name, value):
+    kw = {name: value}
+    if name == "S_out":
+        kw.update(k_out=Fake((2, 2, value, D), F16), v_out=Fake((2, 2, value, D), F16))
+    with pytest.raises(ValueError):
+        call(api, **kw)
+    assert not api.log
