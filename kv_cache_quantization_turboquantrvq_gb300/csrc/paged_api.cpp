@@ -274,7 +274,8 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
     if (st != VQ_OK) return st;
     AttendPlan pl;
     if ((st = attend_plan(T, B, Hq, Hkv, max_q, pl)) != VQ_OK) return st;
-    if (!is16(q_dtype) || max_pages < 0 || window < 0 || sinks < 0 || !std::isfinite(scale)) return VQ_ERR_INVALID_ARG;
+    const float qscale = (float)((double)scale * 1.4426950408889634);  // the kernels' exponents are of base 2
+    if (!is16(q_dtype) || max_pages < 0 || window < 0 || sinks < 0 || !std::isfinite(qscale)) return VQ_ERR_INVALID_ARG;
     if (cache_dtype != VQ_E4M3 && cache_dtype != q_dtype) return VQ_ERR_INVALID_ARG;
     // (positions and a window behind them stay within 32 bits)
     if ((long long)max_pages * page_size > (1LL << 30) || T > (1 << 30)) return VQ_ERR_UNSUPPORTED;
@@ -318,7 +319,7 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
     p.window = window <= (long long)max_pages * page_size ? window : 0;  // (longer than any sequence: none)
     p.sinks = sinks;
     p.small_rows = pl.small_rows;
-    p.qscale = (float)((double)scale * 1.4426950408889634);
+    p.qscale = qscale;
     // (scale 0: any factor that makes every finite score vanish, so that the
     // mask's -inf times it stays -inf)
     if (p.qscale == 0.0f) p.qscale = 1e-30f;
