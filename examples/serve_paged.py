@@ -11,7 +11,7 @@ every sequence that decodes, all in one batch.
      out of the pages and are compressed                     vq_kivi_quant_pack,
                                                              vq_rvq_encode_pack
 
-Run: python examples/serve_paged.py [--cache e4m3|float16] [--window N]
+Run: python examples/serve_paged.py [--cache e4m3|float16|bfloat16] [--window N]
 """
 import argparse
 import math
@@ -58,7 +58,7 @@ def serve(prompts=(300, 77, 512, 1), steps=20, chunk=128, heads=8, group=4, cach
     """Runs the loop; returns (outputs of the last step, the same from plain
     attention over all keys and values, number of free pages)."""
     gen = torch.Generator("cuda").manual_seed(seed)
-    dt = torch.float16
+    dt = torch.bfloat16 if cache == "bfloat16" else torch.float16
     width = heads * group * D
     hidden = 256
     w = torch.randn(hidden, (heads * group + 2 * heads) * D, generator=gen, device="cuda", dtype=dt) / math.sqrt(hidden)
@@ -126,7 +126,7 @@ def compress(pages, done, block=128):
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
-    ap.add_argument("--cache", default="e4m3", choices=["e4m3", "float16"])
+    ap.add_argument("--cache", default="e4m3", choices=["e4m3", "float16", "bfloat16"])
     ap.add_argument("--window", type=int, default=0)
     a = ap.parse_args()
     build.build()

@@ -408,10 +408,10 @@ vq_status vq_paged_append(const void *k_in, long long k_stride_t, long long k_st
  * vq_paged_gather - reads S_out tokens of every sequence back: k_out, v_out
  * [B, Hkv, S_out, D] (either may be NULL) get tokens first[b] + i (first NULL:
  * i) of sequence b, zeros where that is negative or not below lens[b].
- *   out_dtype VQ_F16 or VQ_BF16; a 16-bit cache has the same type.  From an
- *     8-bit cache: code * 2^(exp - 127) rounded once.
+ *   out_dtype VQ_F16 or VQ_BF16, of an fp16 cache VQ_F16.  Of another type than the
+ *     cache's: the value (code * 2^(exp - 127) of an 8-bit cache) rounded once.
  *   lens, first [B] int32, device.
- * The layout is the one vq_rvq_encode_pack, vq_kivi_quant_pack and
+ * With VQ_F16 the outputs are what vq_rvq_encode_pack, vq_kivi_quant_pack and
  * vq_flush_decode take.
  */
 vq_status vq_paged_gather(const void *k_pages, const void *v_pages, const uint8_t *k_exp, const uint8_t *v_exp,

@@ -564,8 +564,8 @@ def vq_paged_append(k, v, cache: dict, slots, stream=None) -> dict:
 def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtype=None, k_out=None, v_out=None,
                     want_k=True, want_v=True, stream=None):
     """Read tokens first[b] + [0, S_out) of every sequence back: (k, v)
-    [B, Hkv, S_out, 128] of dtype (the cache's; float16 by default from an 8-bit
-    cache), zeros past lens[b].  block_table [B, max_pages], lens and first [B] int32.
+    [B, Hkv, S_out, 128] of dtype (the cache's, float16 from an 8-bit one; float16,
+    which the codecs take, from any), zeros past lens[b].  block_table [B, max_pages], lens and first [B] int32.
     stream: a torch stream or a handle; outputs made here are its memory."""
     import torch
     _int32(S_out)

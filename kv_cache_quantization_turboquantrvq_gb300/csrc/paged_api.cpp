@@ -221,7 +221,7 @@ vq_status vq_paged_gather(const void *k_pages, const void *v_pages, const uint8_
     vq_status st = check_cache_shape(a, D);
     if (st != VQ_OK) return st;
     if (B < 0 || S_out < 0 || max_pages < 0 || !is16(out_dtype)) return VQ_ERR_INVALID_ARG;
-    if (cache_dtype != VQ_E4M3 && cache_dtype != out_dtype) return VQ_ERR_INVALID_ARG;
+    if (cache_dtype == VQ_F16 && out_dtype != VQ_F16) return VQ_ERR_INVALID_ARG;
     if (!k_out && !v_out) return VQ_ERR_INVALID_ARG;
     if ((long long)B * Hkv * S_out >= (1LL << 31)) return VQ_ERR_UNSUPPORTED;
     if ((long long)B * S_out == 0) return VQ_OK;

@@ -114,11 +114,25 @@ __global__ void __launch_bounds__(THREADS) paged_append_kernel(const __grid_cons
     }
 }
 
+// Eight entries of one 16-bit type as another: bf16 as fp16 (what the codecs take),
+// rounded once to nearest, past 65504 to infinity.
+__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v)
+{
+    auto two = [](uint32_t x) {
+        const __half2 h = __float22half2_rn(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x)));
+        return *reinterpret_cast<const uint32_t *>(&h);
+    };
+    return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+}
+
 // R rows (tokens of one sequence and head) a group of 16 lanes, all of their
 // loads in flight at once; S_out is padded to a multiple of R in the numbering.
-template <class T, bool E4M3>
+// T: output type; KIND: what the pages hold.
+enum { GATHER_SAME, GATHER_BF16, GATHER_E4M3 };
+template <class T, int KIND>
 __global__ void __launch_bounds__(THREADS) paged_gather_kernel(const __grid_constant__ PagedGatherParams p)
 {
+    constexpr bool E4M3 = KIND == GATHER_E4M3;
     using V = typename std::conditional<E4M3, uint2, uint4>::type;  // what 16 lanes of a row read
     const int lane = threadIdx.x & 15;
     const int blocks = (p.S_out + R - 1) / R;
@@ -177,6 +191,8 @@ __global__ void __launch_bounds__(THREADS) paged_gather_kernel(const __grid_cons
                     const typename Pair<T>::type r = Pair<T>::from(make_float2(f.x * s, f.y * s));
                     o[q] = *reinterpret_cast<const uint32_t *>(&r);
                 }
+            } else if constexpr (KIND == GATHER_BF16) {
+                x = bf16x8_to_f16x8(raw[j][i]);
             } else {
                 x = raw[j][i];
             }
@@ -197,12 +213,12 @@ template <class T, bool E4M3> cudaError_t append(const PagedAppendParams &p, cud
     return cudaGetLastError();
 }
 
-template <class T, bool E4M3> cudaError_t gather(PagedGatherParams &p, cudaStream_t stream)
+template <class T, int KIND> cudaError_t gather(PagedGatherParams &p, cudaStream_t stream)
 {
     const int blocks = (p.S_out + R - 1) / R;
     p.divS = make_fastdiv((uint32_t)blocks);
     const long long groups = (long long)p.B * p.c.Hkv * blocks;
-    paged_gather_kernel<T, E4M3><<<(unsigned)((groups + THREADS / 16 - 1) / (THREADS / 16)), THREADS, 0, stream>>>(p);
+    paged_gather_kernel<T, KIND><<<(unsigned)((groups + THREADS / 16 - 1) / (THREADS / 16)), THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -220,8 +236,9 @@ cudaError_t launch_paged_gather(const PagedGatherParams &p0, int cache_dtype, in
 {
     PagedGatherParams p = p0;
     p.divH = make_fastdiv((uint32_t)p.c.Hkv);
-    if (cache_dtype != VQ_E4M3) return gather<__half, false>(p, stream);  // 16-bit copy
-    return out_dtype == VQ_F16 ? gather<__half, true>(p, stream) : gather<__nv_bfloat16, true>(p, stream);
+    if (cache_dtype == out_dtype) return gather<__half, GATHER_SAME>(p, stream);  // 16-bit copy
+    if (cache_dtype == VQ_BF16) return gather<__half, GATHER_BF16>(p, stream);
+    return out_dtype == VQ_F16 ? gather<__half, GATHER_E4M3>(p, stream) : gather<__nv_bfloat16, GATHER_E4M3>(p, stream);
 }
 
 cudaError_t paged_cache_take_device_error(unsigned *bits, cudaStream_t stream)
