@@ -513,18 +513,26 @@ def paged_cache(num_pages: int, Hkv: int, page_size: int, dtype, device="cuda", 
 
 def _int32(*values):
     """ValueError for numbers that a C int would cut to other ones."""
-    for v in values:
-        if v >= 1 << 31:
-            raise ValueError("%d: less than 2^31" % v)
+    if max(values) >= 1 << 31:
+        raise ValueError("%d: less than 2^31" % max(values))
 
 
-def _on_gpu(dev, function, *args):
-    """The status of a library call made with GPU dev current, as its sizes and launches want."""
+_gpus = 0  # how many this process sees; 0: not asked yet
+
+
+def _on_gpu(dev, function):
+    """`function` as it is called with GPU dev current, which a call's sizes and launches are for."""
     import torch
-    if torch.cuda.current_device() == dev:
-        return function(*args)
-    with torch.cuda.device(dev):
-        return function(*args)
+    global _gpus
+    if _gpus == 0:
+        _gpus = torch.cuda.device_count()
+    if _gpus == 1 or torch.cuda.current_device() == dev:
+        return function
+
+    def there(*args):
+        with torch.cuda.device(dev):
+            return function(*args)
+    return there
 
 
 def _cache_args(cache, dev):
@@ -556,8 +564,9 @@ def vq_paged_append(k, v, cache: dict, slots, stream=None) -> dict:
     if k.dtype != v.dtype or v.shape[0] != T:
         raise ValueError("k and v: the same tokens and dtype")
     views = _rows_view(k, args[6], args[8], "k", dev) + _rows_view(v, args[6], args[8], "v", dev)
-    _check(_on_gpu(dev, lib().vq_paged_append, *views, _dtype_code(k.dtype), T,
-                   _typed(slots, torch.int64, (T,), "slots", dev), *args, _raw_stream(stream, k)), "vq_paged_append")
+    _check(_on_gpu(dev, lib().vq_paged_append)(*views, _dtype_code(k.dtype), T,
+                                               _typed(slots, torch.int64, (T,), "slots", dev), *args,
+                                               _raw_stream(stream, k)), "vq_paged_append")
     return cache
 
 
@@ -568,7 +577,7 @@ def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtyp
     which the codecs take, from any), zeros past lens[b].  block_table [B, max_pages], lens and first [B] int32.
     stream: a torch stream or a handle; outputs made here are its memory."""
     import torch
-    _int32(S_out)
+    _int32(0, S_out)
     gpu = _gpu(block_table, "block_table")
     args = _cache_args(cache, gpu)
     i32 = torch.int32
@@ -588,9 +597,10 @@ def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtyp
             ptrs[i] = outs[i].data_ptr()
         else:
             ptrs[i] = _typed(outs[i], dtype, shape, "k_out, v_out", gpu)
-    _check(_on_gpu(gpu, lib().vq_paged_gather, *args, table, max_pages, _typed(lens, i32, (B,), "lens", gpu),
-                   None if first is None else _typed(first, i32, (B,), "first", gpu), B, S_out,
-                   _dtype_code(dtype), *ptrs, _raw_stream(stream, block_table)), "vq_paged_gather")
+    _check(_on_gpu(gpu, lib().vq_paged_gather)(*args, table, max_pages, _typed(lens, i32, (B,), "lens", gpu),
+                                               None if first is None else _typed(first, i32, (B,), "first", gpu), B,
+                                               S_out, _dtype_code(dtype), *ptrs, _raw_stream(stream, block_table)),
+           "vq_paged_gather")
     return outs[0], outs[1]
 
 
@@ -635,12 +645,13 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
         if wb is None:
             if len(_workspace_bytes) > 4096:
                 _workspace_bytes.clear()
-            wb = _workspace_bytes[key] = _on_gpu(gpu, vq_paged_attend_workspace, T, B, Hq, args[6], max_q)
+            wb = _workspace_bytes[key] = _on_gpu(gpu, vq_paged_attend_workspace)(T, B, Hq, args[6], max_q)
         workspace = _empty(max(wb, 16), torch.uint8, dev, stream, returned=False)
     else:
         if workspace.get_device() != gpu or not workspace.is_contiguous():
             raise ValueError("workspace: a contiguous CUDA tensor on the GPU of the other tensors")
         wb = workspace.numel() * workspace.element_size()
-    _check(_on_gpu(gpu, lib().vq_paged_attend, *view, _dtype_code(dtype), *args, table, max_pages, cu, ln, T, B, Hq, max_q,
-                   window, sinks, scale, po, workspace.data_ptr(), wb, _raw_stream(stream, q)), "vq_paged_attend")
+    _check(_on_gpu(gpu, lib().vq_paged_attend)(*view, _dtype_code(dtype), *args, table, max_pages, cu, ln, T, B, Hq, max_q,
+                                               window, sinks, scale, po, workspace.data_ptr(), wb,
+                                               _raw_stream(stream, q)), "vq_paged_attend")
     return out

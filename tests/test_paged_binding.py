@@ -72,6 +72,7 @@ def api(monkeypatch):
 
     monkeypatch.setattr(torch.cuda, "device", On)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(api, "_gpus", 2)
     api._workspace_bytes.clear()
     api.log = log
     yield api
