@@ -110,6 +110,15 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _fp16(*tensors):
+    """ValueError for keys or values of another floating type than the codecs read
+    (a bf16 cache's blocks are read back as fp16 by vq_paged_gather)."""
+    import torch
+    for t in tensors:
+        if t is not None and t.is_floating_point() and t.dtype != torch.float16:
+            raise ValueError("keys and values of dtype %s: float16" % t.dtype)
+
+
 def vq_status_str(status: int) -> str:
     return lib().vq_status_str(status).decode()
 
@@ -147,6 +156,7 @@ def vq_rvq_encode_pack(k, bits: int, c1, b1, c2, b2, packed1=None, packed2=None,
     """Encode fp16 keys k [B, H, S, D] into (packed1, packed2, norms); with
     `signs` (4 uint32 words) the randomised-sign rotation H diag(s)."""
     import torch
+    _fp16(k)
     B, H, S, D = k.shape
     S_dst = S if S_dst is None else S_dst
     W = rvq_words(D, bits)
@@ -290,6 +300,7 @@ def vq_kivi_quant_pack(k, v, bits: int, group: int, residual_length: int, outs=N
     Returns a dict with k_packed, k_scale, k_zero, v_packed, v_scale, v_zero
     (allocated when `outs` does not provide them)."""
     import torch
+    _fp16(k, v)
     ref = k if k is not None else v
     B, H, S, D = ref.shape
     S_q = max(S - residual_length, 0)
@@ -377,6 +388,7 @@ def vq_flush_decode(k, v, residual_length: int, dst_off=None, S_dst=None, rvq=No
       window = dict([k_win, v_win, win_off, R_cap])
     Returns a dict with every output tensor."""
     import torch
+    _fp16(k, v)
     ref = k if k is not None else v
     B, H, T, D = ref.shape
     R = int(residual_length)
