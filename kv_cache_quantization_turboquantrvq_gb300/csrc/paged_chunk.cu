@@ -59,6 +59,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "device_common.cuh"
@@ -1086,11 +1087,18 @@ cudaError_t launch_chunk(const PagedAttendParams &p, cudaStream_t stream)
     constexpr int smem = CkShape<Q8>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    // the warps trade registers inside the launch's share: never start with fewer
-    cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, kern);
-    if (e != cudaSuccess) return e;
-    if (at.numRegs != CkShape<Q8>::REGS) return cudaErrorLaunchOutOfResources;
+    // The warps trade registers inside the launch's share, and a warp that asks for
+    // more than is there waits forever: never start with fewer than the shares add up
+    // to.  (The compiler gives such a kernel what its launch bounds allow, which is
+    // REGS.)
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes at;
+        e = cudaFuncGetAttributes(&at, kern);
+        if (e != cudaSuccess) return e;
+        regs.store(at.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < CkShape<Q8>::REGS) return cudaErrorLaunchOutOfResources;
     return launch_early(kern, dim3(p.large.G), CkShape<Q8>::THREADS, smem, stream, p);
 }
 
