@@ -491,13 +491,11 @@ def _raw_stream(stream, t):
 
 
 def _empty(shape, dtype, device, stream, returned=True):
-    """An empty tensor that a call on `stream` (None: the current one) writes.  It is
-    made on that stream: a block of the current stream's could still be in use by
-    kernels queued there, and would go back to it while the call still runs.  What
-    is returned is reserved for the current stream's use too."""
+    """An empty tensor that a call on `stream`, not None, writes.  It is made on that
+    stream: a block of the current stream's could still be in use by kernels queued
+    there, and would go back to it while the call still runs.  What is returned is
+    reserved for the current stream's use too."""
     import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
@@ -523,12 +521,7 @@ def paged_cache(num_pages: int, Hkv: int, page_size: int, dtype, device="cuda", 
     return c
 
 
-def _int32(*values):
-    """ValueError for numbers that a C int would cut to other ones."""
-    if max(values) >= 1 << 31:
-        raise ValueError("%d: less than 2^31" % max(values))
-
-
+_INT_MAX = (1 << 31) - 1  # (ctypes cuts larger numbers to other ones)
 _gpus = 0  # how many this process sees; 0: not asked yet
 
 
@@ -589,7 +582,8 @@ def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtyp
     which the codecs take, from any), zeros past lens[b].  block_table [B, max_pages], lens and first [B] int32.
     stream: a torch stream or a handle; outputs made here are its memory."""
     import torch
-    _int32(0, S_out)
+    if S_out > _INT_MAX:
+        raise ValueError("S_out: less than 2^31")
     gpu = _gpu(block_table, "block_table")
     args = _cache_args(cache, gpu)
     i32 = torch.int32
@@ -605,7 +599,7 @@ def vq_paged_gather(cache: dict, block_table, lens, S_out: int, first=None, dtyp
         if not want:
             continue
         if outs[i] is None:
-            outs[i] = _empty(shape, dtype, dev, stream)
+            outs[i] = torch.empty(shape, dtype=dtype, device=dev) if stream is None else _empty(shape, dtype, dev, stream)
             ptrs[i] = outs[i].data_ptr()
         else:
             ptrs[i] = _typed(outs[i], dtype, shape, "k_out, v_out", gpu)
@@ -636,7 +630,8 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
     [T, Hq, 128] of q's dtype; the workspace (uint8) is allocated when not given.
     stream: a torch stream or a handle; what is made here is its memory."""
     import torch
-    _int32(max_q, window, sinks)
+    if max_q > _INT_MAX or window > _INT_MAX or sinks > _INT_MAX:
+        raise ValueError("max_q, window and sinks: less than 2^31")
     gpu = _gpu(q, "q")
     args = _cache_args(cache, gpu)
     i32 = torch.int32
@@ -647,7 +642,8 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
     table = _typed(block_table, i32, (B, max_pages), "block_table", gpu)
     cu, ln = _typed(cu_q, i32, (B + 1,), "cu_q", gpu), _typed(lens, i32, (B,), "lens", gpu)
     if out is None:
-        out = _empty((T, Hq, D), dtype, dev, stream)
+        shape = (T, Hq, D)
+        out = torch.empty(shape, dtype=dtype, device=dev) if stream is None else _empty(shape, dtype, dev, stream)
         po = out.data_ptr()
     else:
         po = _typed(out, dtype, (T, Hq, D), "out", gpu)
@@ -658,7 +654,9 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
             if len(_workspace_bytes) > 4096:
                 _workspace_bytes.clear()
             wb = _workspace_bytes[key] = _on_gpu(gpu, vq_paged_attend_workspace)(T, B, Hq, args[6], max_q)
-        workspace = _empty(max(wb, 16), torch.uint8, dev, stream, returned=False)
+        wb = max(wb, 16)
+        workspace = (torch.empty(wb, dtype=torch.uint8, device=dev) if stream is None
+                     else _empty(wb, torch.uint8, dev, stream, returned=False))
     else:
         if workspace.get_device() != gpu or not workspace.is_contiguous():
             raise ValueError("workspace: a contiguous CUDA tensor on the GPU of the other tensors")
