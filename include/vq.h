@@ -422,6 +422,7 @@ vq_status vq_paged_gather(const void *k_pages, const void *v_pages, const uint8_
 /*
  * vq_paged_attend - attention of the new tokens of B sequences over their
  * pages, one token each (decode), a chunk of a prompt each, or any mix.
+ *   scale: finite, and finite times log2(e).
  *   q [T, Hq, D] of q_dtype (VQ_F16 or VQ_BF16; a 16-bit cache has the same
  *     type), strided: the new tokens of all sequences one after another.
  *   cu_q [B + 1] int32, device: sequence b has tokens [cu_q[b], cu_q[b + 1]) of
@@ -439,8 +440,11 @@ vq_status vq_paged_gather(const void *k_pages, const void *v_pages, const uint8_
  *   contiguous; tokens of no sequence are not written.
  * Scores, softmax and sums are held in 32 bits; the softmax weights enter the
  * value product as 16-bit numbers (fp16 over an 8-bit cache, else the cache's
- * type), half a step of rounding each.  Keys that no new token of a sequence
- * sees may hold anything, infinities and NaN among it.  A visible entry must be
+ * type), half a step of rounding each.  fp16's steps end at 2^-24: a weight below
+ * 2^-21 of its row's largest is off by up to 2^-32 of that largest.  Over an 8-bit
+ * cache that goes for weights times the 2^(exp - 127) of their values, with 2^-13
+ * and 2^-24 in chunks; zero value rows count in the softmax's sum alone.  Keys that
+ * no new token of a sequence sees may hold anything, infinities and NaN among it.  A visible entry must be
  * finite: one that is not may reach the outputs of tokens that do not see it.
  *   workspace: device memory of at least the size that
  *     vq_paged_attend_workspace reports on the current device, 256-byte

@@ -21,8 +21,9 @@
 // 8-bit cache eight more warps turn the codes into fp16 operands in shared
 // memory (4096 bf16 queries over 16384 keys: four took 815 us, eight 763).
 //
-// What bounds it (that chunk over a 16-bit cache: 627 us, 1.53 PFLOP/s; over
-// codes 807): a pair of tiles takes 1.5 us where the products take 1.07.  The
+// What bounds it (that chunk over a 16-bit cache: 675 us, 1.42 PFLOP/s, where the
+// inputs change from call to call, 627 on one set of tensors; over codes, on one
+// set, 807): a pair of tiles takes 1.5 us where the products take 1.07.  The
 // score tile waits for its copy to registers between products, and by its bytes
 // (192 KB of operands read, 64 KB copied in) shared memory is as busy as the
 // tensor core.  Over codes the softmax warps have 176 registers instead of 208,
