@@ -461,6 +461,46 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
                           vq_stream_t stream);
 
 /*
+ * Keeping a part of a sequence: the softmax weight that tokens got so far says
+ * which of them can go.
+ *   weights [num_pages, Hkv, page_size] fp32, device: a number for every place of
+ *     the cache.  Tokens of a sequence whose pages another sequence shares must
+ *     not be moved.
+ *
+ * vq_paged_select - the tokens that sequence b keeps for each kv head: all of its
+ * lens[b] tokens where they are no more than `budget`; else the first `sinks`, the
+ * last `recent`, and of those in between the ones of largest weight (of equal
+ * weights the earlier ones; 0 and -0 are equal, NaN is largest), `budget` in all.
+ *   keep [B, Hkv, budget] int32: their indices in ascending order, -1 behind them.
+ *   counts [B] int32: min(lens[b], budget).
+ *   sinks + recent <= budget.  A length that is negative or past the block table
+ *   (taken as 0, as max_pages * page_size) and a page of the tokens in between that
+ *   is not in the pool (its weights count as lowest) set VQ_DEVERR_BAD_OFFSET.
+ *
+ * vq_paged_compact - moves tokens together, in place: of sequence b and kv head h
+ * token keep[b][h][i], i < counts[b], goes to place first[b] + i (first NULL: i) of
+ * the same sequence - its key, its value, their exponents, and its weight where
+ * `weights` is given.  Other places keep what they hold; the sequence then has
+ * first[b] + counts[b] tokens.
+ *   keep [B, Hkv, K] int32, device, with strides of sequence and head in elements
+ *     (a head stride of 0: one list for all heads); ascending, and no token may come
+ *     before the place it goes to.  A token that breaks this, or whose page or place
+ *     is not in the pool, is left out and sets VQ_DEVERR_BAD_OFFSET; so do counts
+ *     outside [0, K] (cut to it) and a `first` outside the block table (nothing
+ *     moves).  Where the list does not ascend, what the moved places hold is
+ *     unspecified.
+ * Both: B * Hkv at most 2^24, at most 2^30 positions a sequence; one kernel launch;
+ * nothing is allocated.
+ */
+vq_status vq_paged_select(const float *weights, int num_pages, int Hkv, int page_size, const int32_t *block_table,
+                          int max_pages, const int32_t *lens, int B, int budget, int recent, int sinks, int32_t *keep,
+                          int32_t *counts, vq_stream_t stream);
+vq_status vq_paged_compact(void *k_pages, void *v_pages, uint8_t *k_exp, uint8_t *v_exp, int cache_dtype, int num_pages,
+                           int Hkv, int page_size, int D, const int32_t *block_table, int max_pages, const int32_t *keep,
+                           long long keep_stride_b, long long keep_stride_h, int K, const int32_t *counts,
+                           const int32_t *first, int B, float *weights, vq_stream_t stream);
+
+/*
  * vq_device_error - waits for `stream`, then reads and clears the library's
  * device error word (VQ_DEVERR_* bits) into *code_out (host pointer).
  * Returns VQ_ERR_DEVICE if the word was non-zero, VQ_OK otherwise.

@@ -32,7 +32,8 @@ EXPORTED = ("vq_status_str", "vq_version", "vq_rvq_codebook", "vq_rvq_encode_pac
             "vq_device_error", "vq_rvq_attend_workspace", "vq_rvq_attend", "vq_rvq_attend_noalloc",
             "vq_rvq_encode_pack_rs", "vq_rvq_unpack_dequant_rs", "vq_rvq_attend_rs",
             "vq_kivi_attend_workspace", "vq_kivi_attend", "vq_qjl_encode", "vq_flush_decode",
-            "vq_paged_append", "vq_paged_gather", "vq_paged_attend_workspace", "vq_paged_attend")
+            "vq_paged_append", "vq_paged_gather", "vq_paged_attend_workspace", "vq_paged_attend",
+            "vq_paged_select", "vq_paged_compact")
 VQ_F16, VQ_BF16, VQ_E4M3 = 0, 1, 2
 VQ_ATTEND_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -81,6 +82,8 @@ def lib():
     L.vq_paged_attend_workspace.argtypes = [I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
     L.vq_paged_attend.argtypes = [P, Q, Q, I, P, P, P, P, I, I, I, I, I, P, I, P, P, I, I, I, I, I, I,
                                   ctypes.c_float, P, P, ctypes.c_size_t, P]
+    L.vq_paged_select.argtypes = [P, I, I, I, P, I, P, I, I, I, I, P, P, P]
+    L.vq_paged_compact.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, Q, Q, I, P, P, I, P, P]
     for name in EXPORTED[2:]:
         getattr(L, name).restype = I
     _lib = L
@@ -665,3 +668,62 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
                                                window, sinks, scale, po, workspace.data_ptr(), wb,
                                                _raw_stream(stream, q)), "vq_paged_attend")
     return out
+
+
+def vq_paged_select(weights, block_table, lens, budget: int, recent: int = 0, sinks: int = 0, keep=None, counts=None,
+                    stream=None):
+    """The tokens that each sequence and kv head keeps by their accumulated weights
+    [num_pages, Hkv, page_size] (float32): all, or the first `sinks`, the last
+    `recent` and the heaviest in between, `budget` in all.  block_table
+    [B, max_pages], lens [B] int32.  Returns (keep [B, Hkv, budget], ascending, -1
+    behind the kept ones; counts [B]), int32.
+    stream: a torch stream or a handle; outputs made here are its memory."""
+    import torch
+    if budget > _INT_MAX or recent > _INT_MAX or sinks > _INT_MAX:
+        raise ValueError("budget, recent and sinks: less than 2^31")
+    gpu = _gpu(block_table, "block_table")
+    i32 = torch.int32
+    NP, H, PS = weights.shape
+    B, max_pages = block_table.shape
+    w = _typed(weights, torch.float32, (NP, H, PS), "weights", gpu)
+    table = _typed(block_table, i32, (B, max_pages), "block_table", gpu)
+    ptrs, outs = [], [keep, counts]
+    for i, (shape, name) in enumerate((((B, H, max(budget, 0)), "keep"), ((B,), "counts"))):
+        if outs[i] is None:
+            dev = block_table.device
+            outs[i] = torch.empty(shape, dtype=i32, device=dev) if stream is None else _empty(shape, i32, dev, stream)
+            ptrs.append(outs[i].data_ptr())
+        else:
+            ptrs.append(_typed(outs[i], i32, shape, name, gpu))
+    _check(_on_gpu(gpu, lib().vq_paged_select)(w, NP, H, PS, table, max_pages, _typed(lens, i32, (B,), "lens", gpu), B,
+                                               budget, recent, sinks, *ptrs, _raw_stream(stream, block_table)),
+           "vq_paged_select")
+    return outs[0], outs[1]
+
+
+def vq_paged_compact(cache: dict, block_table, keep, counts, first=None, weights=None, stream=None) -> dict:
+    """Move tokens of each sequence together, in place: token keep[b, h, i],
+    i < counts[b], of kv head h goes to place first[b] + i (first None: i), with its
+    exponents, and its weight in weights [num_pages, Hkv, page_size] (float32) where
+    that is given.  keep [B, Hkv or 1, K] int32 (1: one list for all heads), rows
+    ascending and contiguous, no token before its place; counts, first [B] and
+    block_table [B, max_pages] int32.  Returns the cache."""
+    import torch
+    gpu = _gpu(block_table, "block_table")
+    args = _cache_args(cache, gpu)
+    i32 = torch.int32
+    B, max_pages = block_table.shape
+    table = _typed(block_table, i32, (B, max_pages), "block_table", gpu)
+    shape = keep.shape
+    if len(shape) != 3 or shape[0] != B or shape[1] not in (1, args[6]) or keep.dtype != i32 or keep.get_device() != gpu:
+        raise ValueError("keep: an int32 CUDA tensor [%d, %d or 1, tokens] on the GPU of the other tensors" % (B, args[6]))
+    st = keep.stride()
+    if st[2] != 1 and shape[2] > 1:
+        raise ValueError("keep: the entries of a list have to be contiguous")
+    w = None if weights is None else _typed(weights, torch.float32, cache["k_pages"].shape[:3], "weights", gpu)
+    _check(_on_gpu(gpu, lib().vq_paged_compact)(*args, table, max_pages, keep.data_ptr(), st[0],
+                                                0 if shape[1] == 1 else st[1], shape[2],
+                                                _typed(counts, i32, (B,), "counts", gpu),
+                                                None if first is None else _typed(first, i32, (B,), "first", gpu), B, w,
+                                                _raw_stream(stream, block_table)), "vq_paged_compact")
+    return cache

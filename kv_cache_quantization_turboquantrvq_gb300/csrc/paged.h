@@ -45,6 +45,28 @@ struct PagedGatherParams {
 cudaError_t launch_paged_gather(const PagedGatherParams &p, int cache_dtype, int out_dtype, cudaStream_t stream);
 cudaError_t paged_cache_take_device_error(unsigned *bits, cudaStream_t stream);
 
+// ------------------------------------------------ keeping a part of the cache
+
+struct PagedSelectParams {
+    const float *weights;             // [num_pages, Hkv, page_size]
+    const int32_t *table, *lens;
+    int32_t *keep, *counts;           // [B, Hkv, budget], [B]
+    int num_pages, Hkv, page_shift;
+    int B, max_pages, budget, recent, sinks;
+    int held;                         // weights of a CTA that stay in shared memory (set by the launcher)
+};
+cudaError_t launch_paged_select(const PagedSelectParams &p, cudaStream_t stream);
+
+struct PagedCompactParams {
+    PagedCache c;
+    const int32_t *table, *keep, *counts, *first;  // first may be null (0)
+    float *weights;                                // [num_pages, Hkv, page_size], may be null
+    long long keep_b, keep_h;                      // strides of keep: sequence, head (0: one list for all heads)
+    int B, max_pages, K;
+};
+cudaError_t launch_paged_compact(const PagedCompactParams &p, int cache_dtype, cudaStream_t stream);
+cudaError_t paged_keep_take_device_error(unsigned *bits, cudaStream_t stream);
+
 // ------------------------------------------------------------ the attention
 //
 // The new tokens of the sequences are cut into entries (tq consecutive tokens
