@@ -461,6 +461,31 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
                           vq_stream_t stream);
 
 /*
+ * vq_paged_attend_tree - attention of a tree of drafted tokens of each sequence,
+ * as speculative decoding verifies them in one call.
+ *   parents [T] int32, device: of token i of sequence b (q row cu_q[b] + i) the
+ *     token among the sequence's new ones that it follows, below i, or -1: it
+ *     follows the last token before them.  Any other number sets
+ *     VQ_DEVERR_BAD_OFFSET and counts as -1.
+ * The drafted tokens are in the cache in the order given, the last n_b of lens[b]
+ * (n_b > lens[b] sets VQ_DEVERR_BAD_OFFSET, outputs of that sequence are then
+ * unspecified).  Token i is at position p = lens[b] - n_b + its number of ancestors
+ * among the new tokens.  It sees the keys before the tree by the rule of
+ * vq_paged_attend, and of the tree itself and its ancestors, by that rule on their
+ * positions (window == 0, or position > p - window, or position < sinks).
+ * At most 256 drafted tokens a sequence (max_q; VQ_ERR_UNSUPPORTED above); a sequence
+ * with one new token of parent -1 is a decode as in vq_paged_attend.  Everything else
+ * as vq_paged_attend.
+ */
+vq_status vq_paged_attend_tree_workspace(int T, int B, int Hq, int Hkv, int max_q, size_t *bytes);
+vq_status vq_paged_attend_tree(const void *q, long long q_stride_t, long long q_stride_h, int q_dtype,
+                               const void *k_pages, const void *v_pages, const uint8_t *k_exp, const uint8_t *v_exp,
+                               int cache_dtype, int num_pages, int Hkv, int page_size, int D, const int32_t *block_table,
+                               int max_pages, const int32_t *cu_q, const int32_t *lens, const int32_t *parents, int T, int B,
+                               int Hq, int max_q, int window, int sinks, float scale, void *out, void *workspace,
+                               size_t workspace_bytes, vq_stream_t stream);
+
+/*
  * Keeping a part of a sequence: the softmax weight that tokens got so far says
  * which of them can go.
  *   weights [num_pages, Hkv, page_size] fp32, device: a number for every place of

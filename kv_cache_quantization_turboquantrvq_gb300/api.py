@@ -33,7 +33,7 @@ EXPORTED = ("vq_status_str", "vq_version", "vq_rvq_codebook", "vq_rvq_encode_pac
             "vq_rvq_encode_pack_rs", "vq_rvq_unpack_dequant_rs", "vq_rvq_attend_rs",
             "vq_kivi_attend_workspace", "vq_kivi_attend", "vq_qjl_encode", "vq_flush_decode",
             "vq_paged_append", "vq_paged_gather", "vq_paged_attend_workspace", "vq_paged_attend",
-            "vq_paged_select", "vq_paged_compact")
+            "vq_paged_attend_tree_workspace", "vq_paged_attend_tree", "vq_paged_select", "vq_paged_compact")
 VQ_F16, VQ_BF16, VQ_E4M3 = 0, 1, 2
 VQ_ATTEND_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -82,6 +82,9 @@ def lib():
     L.vq_paged_attend_workspace.argtypes = [I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
     L.vq_paged_attend.argtypes = [P, Q, Q, I, P, P, P, P, I, I, I, I, I, P, I, P, P, I, I, I, I, I, I,
                                   ctypes.c_float, P, P, ctypes.c_size_t, P]
+    L.vq_paged_attend_tree_workspace.argtypes = L.vq_paged_attend_workspace.argtypes
+    L.vq_paged_attend_tree.argtypes = [P, Q, Q, I, P, P, P, P, I, I, I, I, I, P, I, P, P, P, I, I, I, I, I, I,
+                                       ctypes.c_float, P, P, ctypes.c_size_t, P]
     L.vq_paged_select.argtypes = [P, I, I, I, P, I, P, I, I, I, I, P, P, P]
     L.vq_paged_compact.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, Q, Q, I, P, P, I, P, P]
     for name in EXPORTED[2:]:
@@ -623,15 +626,10 @@ def vq_paged_attend_workspace(T: int, B: int, Hq: int, Hkv: int, max_q: int) -> 
 _workspace_bytes: dict = {}  # sizes by shape and device: the call's own arithmetic, repeated every step
 
 
-def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q: int, window: int = 0, sinks: int = 0,
-                    out=None, workspace=None, stream=None):
-    """Attention of new tokens q [T, Hq, 128] (rows may be strided) over a paged
-    cache.  Sequence b has tokens cu_q[b] .. cu_q[b + 1] - 1 (at most max_q), the
-    last of them at position lens[b] - 1; each sees the keys up to its own
-    position, with a window those of the last `window` positions and the first
-    `sinks`.  cu_q [B + 1], lens [B], block_table [B, max_pages] int32.  Returns
-    [T, Hq, 128] of q's dtype; the workspace (uint8) is allocated when not given.
-    stream: a torch stream or a handle; what is made here is its memory."""
+def _attend_args(sized, q, cache, block_table, cu_q, lens, max_q, window, sinks, out, workspace, stream, *more):
+    """What the attention calls share: (out, gpu, arguments up to lens, (T, B, Hq, max_q,
+    window, sinks), (out, workspace, bytes, stream)).  sized: the call's workspace
+    function, which takes T, B, Hq, Hkv, max_q and `more`."""
     import torch
     if max_q > _INT_MAX or window > _INT_MAX or sinks > _INT_MAX:
         raise ValueError("max_q, window and sinks: less than 2^31")
@@ -651,12 +649,12 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
     else:
         po = _typed(out, dtype, (T, Hq, D), "out", gpu)
     if workspace is None:
-        key = (T, B, Hq, args[6], max_q, gpu)
+        key = (sized, T, B, Hq, args[6], max_q, gpu, more)
         wb = _workspace_bytes.get(key)
         if wb is None:
             if len(_workspace_bytes) > 4096:
                 _workspace_bytes.clear()
-            wb = _workspace_bytes[key] = _on_gpu(gpu, vq_paged_attend_workspace)(T, B, Hq, args[6], max_q)
+            wb = _workspace_bytes[key] = _on_gpu(gpu, sized)(T, B, Hq, args[6], max_q, *more)
         wb = max(wb, 16)
         workspace = (torch.empty(wb, dtype=torch.uint8, device=dev) if stream is None
                      else _empty(wb, torch.uint8, dev, stream, returned=False))
@@ -664,9 +662,46 @@ def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q
         if workspace.get_device() != gpu or not workspace.is_contiguous():
             raise ValueError("workspace: a contiguous CUDA tensor on the GPU of the other tensors")
         wb = workspace.numel() * workspace.element_size()
-    _check(_on_gpu(gpu, lib().vq_paged_attend)(*view, _dtype_code(dtype), *args, table, max_pages, cu, ln, T, B, Hq, max_q,
-                                               window, sinks, scale, po, workspace.data_ptr(), wb,
-                                               _raw_stream(stream, q)), "vq_paged_attend")
+    return (out, gpu, (*view, _dtype_code(dtype), *args, table, max_pages, cu, ln), (T, B, Hq, max_q, window, sinks),
+            (po, workspace.data_ptr(), wb, _raw_stream(stream, q)), workspace)
+
+
+def vq_paged_attend(q, cache: dict, block_table, cu_q, lens, scale: float, max_q: int, window: int = 0, sinks: int = 0,
+                    out=None, workspace=None, stream=None):
+    """Attention of new tokens q [T, Hq, 128] (rows may be strided) over a paged
+    cache.  Sequence b has tokens cu_q[b] .. cu_q[b + 1] - 1 (at most max_q), the
+    last of them at position lens[b] - 1; each sees the keys up to its own
+    position, with a window those of the last `window` positions and the first
+    `sinks`.  cu_q [B + 1], lens [B], block_table [B, max_pages] int32.  Returns
+    [T, Hq, 128] of q's dtype; the workspace (uint8) is allocated when not given.
+    stream: a torch stream or a handle; what is made here is its memory."""
+    out, gpu, args, sizes, last, _held = _attend_args(vq_paged_attend_workspace, q, cache, block_table, cu_q, lens, max_q,
+                                                      window, sinks, out, workspace, stream)
+    _check(_on_gpu(gpu, lib().vq_paged_attend)(*args, *sizes, scale, *last), "vq_paged_attend")
+    return out
+
+
+def vq_paged_attend_tree_workspace(T: int, B: int, Hq: int, Hkv: int, max_q: int) -> int:
+    """Workspace bytes vq_paged_attend_tree needs for these shapes on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(lib().vq_paged_attend_tree_workspace(T, B, Hq, Hkv, max_q, ctypes.byref(n)), "vq_paged_attend_tree_workspace")
+    return int(n.value)
+
+
+def vq_paged_attend_tree(q, cache: dict, block_table, cu_q, lens, parents, scale: float, max_q: int, window: int = 0,
+                         sinks: int = 0, out=None, workspace=None, stream=None):
+    """Attention of a tree of drafted tokens of each sequence over a paged cache: as
+    vq_paged_attend, but of the new tokens each sees itself and its ancestors.
+    parents [T] int32: the new token of its sequence that a token follows (below
+    its own index), or -1: the last token before the tree; a token's position is
+    lens[b] - n_b plus its number of ancestors.  max_q: at most 256.  The drafted
+    tokens are in the cache, in the order given; vq_paged_compact then moves an
+    accepted path together."""
+    import torch
+    out, gpu, args, sizes, last, _held = _attend_args(vq_paged_attend_tree_workspace, q, cache, block_table, cu_q, lens,
+                                                      max_q, window, sinks, out, workspace, stream)
+    up = _typed(parents, torch.int32, (sizes[0],), "parents", gpu)
+    _check(_on_gpu(gpu, lib().vq_paged_attend_tree)(*args, up, *sizes, scale, *last), "vq_paged_attend_tree")
     return out
 
 

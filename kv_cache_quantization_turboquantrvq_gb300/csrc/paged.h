@@ -82,7 +82,8 @@ constexpr int PLAN_CTAS = 512;  // CTAs of a launch at most
 
 struct PgEntry {     // 32 bytes, read as two int4
     int b, tok0, nt; // sequence, first query token (index into q), number of tokens
-    int p0;          // position of the first token in its sequence (may be negative)
+    int p0;          // position of the first token in its sequence (may be negative);
+                     // of a tree, of the sequence's first drafted token
     int hi;          // keys [0, hi) are visible to some row
     int nsink;       // leading tiles that hold the first tokens kept by the window
     int tl;          // first tile after those
@@ -103,6 +104,11 @@ struct PgPlan {
     int cap, G, tq;    // entries that fit, CTAs, tokens per entry
 };
 
+// What the new tokens of a call are: each sequence's next ones in order, or a tree
+// of drafts, in which a token sees its ancestors only.
+enum PgMode { PG_CHAIN, PG_TREE };
+constexpr int PG_TREE_MAX = 256, PG_TREE_WORDS = PG_TREE_MAX / 32;  // tokens of a tree
+
 struct PagedAttendParams {
     CUtensorMap tmk, tmv, tmq;
     PagedCache c;
@@ -117,6 +123,9 @@ struct PagedAttendParams {
     PgPlan small, large;         // cap 0: the class is not used
     unsigned long long *planned; // (both classes) `call` from when the plan is made until the merge
     unsigned long long call;     // a number of this call's own, not 0
+    const int32_t *parents;      // [T] trees; null: no tree
+    uint32_t *masks;             // [T][PG_TREE_WORDS] trees in the large class: the new tokens that a token sees
+    int32_t *depth;              // [T] and its number of ancestors
 };
 constexpr int PG_SROWS = 16;     // rows of a small item
 constexpr int PG_LROWS = 256;    // rows of a large item (two tensor-memory tiles)

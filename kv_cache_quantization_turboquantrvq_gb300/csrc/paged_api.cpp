@@ -40,9 +40,10 @@ struct AttendPlan {
     int small_rows, small_cap, small_tq, large_cap, large_tq, G;
     size_t bytes;
     Layout s, l;
+    size_t planned, masks, depth;
 };
 
-vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, AttendPlan &pl)
+vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, PgMode mode, AttendPlan &pl)
 {
     if (T < 0 || B < 0 || Hq < 0 || Hkv <= 0 || max_q < 0 || Hq % Hkv != 0) return VQ_ERR_INVALID_ARG;
     const int gq = Hq / Hkv;
@@ -66,7 +67,10 @@ vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, AttendPlan &pl)
     if (large) pl.large_cap = (T + pl.large_tq - 1) / pl.large_tq + B;
     pl.s = layout(0, pl.small_cap, pl.G, PG_SROWS);
     pl.l = layout(pl.s.end, pl.large_cap, pl.G, PG_LROWS);
-    pl.bytes = pl.l.end + (small && large ? kPlanned : 0);
+    pl.planned = pl.l.end;
+    pl.masks = pl.planned + (small && large ? kPlanned : 0);
+    pl.depth = pl.masks + (mode == PG_TREE && large ? up((size_t)T * PG_TREE_WORDS * 4) : 0);
+    pl.bytes = pl.depth + (mode == PG_TREE && large ? up((size_t)T * 4) : 0);
     return VQ_OK;
 }
 
@@ -80,6 +84,97 @@ void place(PgPlan &d, unsigned char *ws, const Layout &l, int cap, int G, int tq
     d.cap = cap;
     d.G = G;
     d.tq = tq;
+}
+
+// What a call's new tokens are besides the next ones in order.
+struct AttendExtra {
+    PgMode mode;
+    const int32_t *parents;
+};
+
+vq_status attend(const AttendExtra &x, const CacheArgs &a, int D, const void *q, long long q_stride_t, long long q_stride_h,
+                 int q_dtype, const int32_t *block_table, int max_pages, const int32_t *cu_q, const int32_t *lens, int T,
+                 int B, int Hq, int max_q, int window, int sinks, float scale, void *out, void *workspace,
+                 size_t workspace_bytes, vq_stream_t stream)
+{
+    const int Hkv = a.Hkv, num_pages = a.num_pages, page_size = a.page_size, cache_dtype = a.dtype;
+    vq_status st = check_cache_shape(a, D);
+    if (st != VQ_OK) return st;
+    AttendPlan pl;
+    if ((st = attend_plan(T, B, Hq, Hkv, max_q, x.mode, pl)) != VQ_OK) return st;
+    const float qscale = (float)((double)scale * 1.4426950408889634);  // the kernels' exponents are of base 2
+    if (!is16(q_dtype) || max_pages < 0 || window < 0 || sinks < 0 || !std::isfinite(qscale)) return VQ_ERR_INVALID_ARG;
+    if (cache_dtype != VQ_E4M3 && cache_dtype != q_dtype) return VQ_ERR_INVALID_ARG;
+    // (positions and a window behind them stay within 32 bits)
+    if ((long long)max_pages * page_size > (1LL << 30) || T > (1 << 30)) return VQ_ERR_UNSUPPORTED;
+    if (x.mode == PG_TREE && max_q > PG_TREE_MAX) return VQ_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0 || Hq == 0) return VQ_OK;
+    if (max_q == 0) return VQ_ERR_INVALID_ARG;
+    if ((st = check_view(q, T, Hq, q_stride_t, q_stride_h)) != VQ_OK) return st;
+    // an empty pool or table: no key is visible, but the maps need an address
+    if (num_pages == 0 || max_pages == 0) return VQ_ERR_INVALID_ARG;
+    if ((st = check_cache_ptrs(a, true, true)) != VQ_OK) return st;
+    if (!block_table || !cu_q || !lens || !out || !workspace) return VQ_ERR_INVALID_ARG;
+    if (x.mode == PG_TREE && !x.parents) return VQ_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(lens, 4) || !aligned(out, 16) || !aligned(workspace, 256) ||
+        !aligned(x.parents, 4))
+        return VQ_ERR_MISALIGNED;
+    if (workspace_bytes < pl.bytes) return VQ_ERR_INVALID_ARG;
+    const Span outs[2] = {{out, (size_t)T * Hq * kD * 2}, {workspace, pl.bytes}};
+    const Span ins[9] = {{q, view_bytes(T, Hq, q_stride_t, q_stride_h)}, {a.k, a.entry_bytes()},
+                         {a.v, a.entry_bytes()}, {a.exp_bytes() ? a.ke : nullptr, a.exp_bytes()},
+                         {a.exp_bytes() ? a.ve : nullptr, a.exp_bytes()},
+                         {block_table, (size_t)B * max_pages * 4}, {cu_q, (size_t)(B + 1) * 4}, {lens, (size_t)B * 4},
+                         {x.parents, (size_t)T * 4}};
+    for (const Span &o : outs)
+        for (const Span &i : ins)
+            if (overlap(o, i)) return VQ_ERR_ALIASING;
+    if (overlap(outs[0], outs[1])) return VQ_ERR_ALIASING;
+
+    PagedAttendParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.c = device_cache(a);
+    p.q = q;
+    p.qst = q_stride_t;
+    p.qsh = q_stride_h;
+    p.table = block_table;
+    p.cu = cu_q;
+    p.lens = lens;
+    p.out = out;
+    p.T = T;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.GQ = Hq / Hkv;
+    p.max_pages = max_pages;
+    p.max_q = max_q;
+    p.window = window <= (long long)max_pages * page_size ? window : 0;  // (longer than any sequence: none)
+    p.sinks = sinks;
+    p.small_rows = pl.small_rows;
+    p.qscale = qscale;
+    // (scale 0: any factor that makes every finite score vanish, so that the
+    // mask's -inf times it stays -inf)
+    if (p.qscale == 0.0f) p.qscale = 1e-30f;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    place(p.small, ws, pl.s, pl.small_cap, pl.G, pl.small_tq);
+    place(p.large, ws, pl.l, pl.large_cap, pl.G, pl.large_tq);
+    if (pl.small_cap && pl.large_cap) {
+        static std::atomic<unsigned long long> calls{0};
+        p.planned = reinterpret_cast<unsigned long long *>(ws + pl.planned);
+        p.call = ++calls;
+    }
+    if (x.mode == PG_TREE) {
+        p.parents = x.parents;
+        p.masks = reinterpret_cast<uint32_t *>(ws + pl.masks);
+        p.depth = reinterpret_cast<int32_t *>(ws + pl.depth);
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // (a call of small sequences alone: its kernel makes the plan)
+    cudaError_t e = pl.large_cap ? launch_paged_plan(p, s) : cudaSuccess;
+    if (e == cudaSuccess && pl.large_cap) e = launch_paged_large(p, q_dtype, cache_dtype, s);
+    if (e == cudaSuccess && pl.small_cap) e = launch_paged_small(p, q_dtype, cache_dtype, s);
+    if (e == cudaSuccess) e = launch_paged_combine(p, q_dtype, s);
+    return status_of(e);
 }
 
 }  // namespace
@@ -171,7 +266,7 @@ vq_status vq_paged_attend_workspace(int T, int B, int Hq, int Hkv, int max_q, si
 {
     if (!bytes) return VQ_ERR_INVALID_ARG;
     AttendPlan pl;
-    const vq_status st = attend_plan(T, B, Hq, Hkv, max_q, pl);
+    const vq_status st = attend_plan(T, B, Hq, Hkv, max_q, PG_CHAIN, pl);
     if (st != VQ_OK) return st;
     *bytes = pl.bytes;
     return VQ_OK;
@@ -185,74 +280,31 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
                           vq_stream_t stream)
 {
     const CacheArgs a = {k_pages, v_pages, k_exp, v_exp, cache_dtype, num_pages, Hkv, page_size};
-    vq_status st = check_cache_shape(a, D);
-    if (st != VQ_OK) return st;
-    AttendPlan pl;
-    if ((st = attend_plan(T, B, Hq, Hkv, max_q, pl)) != VQ_OK) return st;
-    const float qscale = (float)((double)scale * 1.4426950408889634);  // the kernels' exponents are of base 2
-    if (!is16(q_dtype) || max_pages < 0 || window < 0 || sinks < 0 || !std::isfinite(qscale)) return VQ_ERR_INVALID_ARG;
-    if (cache_dtype != VQ_E4M3 && cache_dtype != q_dtype) return VQ_ERR_INVALID_ARG;
-    // (positions and a window behind them stay within 32 bits)
-    if ((long long)max_pages * page_size > (1LL << 30) || T > (1 << 30)) return VQ_ERR_UNSUPPORTED;
-    if (T == 0 || B == 0 || Hq == 0) return VQ_OK;
-    if (max_q == 0) return VQ_ERR_INVALID_ARG;
-    if ((st = check_view(q, T, Hq, q_stride_t, q_stride_h)) != VQ_OK) return st;
-    // an empty pool or table: no key is visible, but the maps need an address
-    if (num_pages == 0 || max_pages == 0) return VQ_ERR_INVALID_ARG;
-    if ((st = check_cache_ptrs(a, true, true)) != VQ_OK) return st;
-    if (!block_table || !cu_q || !lens || !out || !workspace) return VQ_ERR_INVALID_ARG;
-    if (!aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(lens, 4) || !aligned(out, 16) || !aligned(workspace, 256))
-        return VQ_ERR_MISALIGNED;
-    if (workspace_bytes < pl.bytes) return VQ_ERR_INVALID_ARG;
-    const Span outs[2] = {{out, (size_t)T * Hq * kD * 2}, {workspace, pl.bytes}};
-    const Span ins[8] = {{q, view_bytes(T, Hq, q_stride_t, q_stride_h)}, {k_pages, a.entry_bytes()},
-                         {v_pages, a.entry_bytes()}, {a.exp_bytes() ? k_exp : nullptr, a.exp_bytes()},
-                         {a.exp_bytes() ? v_exp : nullptr, a.exp_bytes()},
-                         {block_table, (size_t)B * max_pages * 4}, {cu_q, (size_t)(B + 1) * 4}, {lens, (size_t)B * 4}};
-    for (const Span &o : outs)
-        for (const Span &i : ins)
-            if (overlap(o, i)) return VQ_ERR_ALIASING;
-    if (overlap(outs[0], outs[1])) return VQ_ERR_ALIASING;
+    return attend({PG_CHAIN, nullptr}, a, D, q, q_stride_t, q_stride_h, q_dtype, block_table, max_pages, cu_q, lens, T, B, Hq,
+                  max_q, window, sinks, scale, out, workspace, workspace_bytes, stream);
+}
 
-    PagedAttendParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.c = device_cache(a);
-    p.q = q;
-    p.qst = q_stride_t;
-    p.qsh = q_stride_h;
-    p.table = block_table;
-    p.cu = cu_q;
-    p.lens = lens;
-    p.out = out;
-    p.T = T;
-    p.B = B;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.GQ = Hq / Hkv;
-    p.max_pages = max_pages;
-    p.max_q = max_q;
-    p.window = window <= (long long)max_pages * page_size ? window : 0;  // (longer than any sequence: none)
-    p.sinks = sinks;
-    p.small_rows = pl.small_rows;
-    p.qscale = qscale;
-    // (scale 0: any factor that makes every finite score vanish, so that the
-    // mask's -inf times it stays -inf)
-    if (p.qscale == 0.0f) p.qscale = 1e-30f;
-    unsigned char *ws = static_cast<unsigned char *>(workspace);
-    place(p.small, ws, pl.s, pl.small_cap, pl.G, pl.small_tq);
-    place(p.large, ws, pl.l, pl.large_cap, pl.G, pl.large_tq);
-    if (pl.small_cap && pl.large_cap) {
-        static std::atomic<unsigned long long> calls{0};
-        p.planned = reinterpret_cast<unsigned long long *>(ws + pl.l.end);
-        p.call = ++calls;
-    }
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // (a call of small sequences alone: its kernel makes the plan)
-    cudaError_t e = pl.large_cap ? launch_paged_plan(p, s) : cudaSuccess;
-    if (e == cudaSuccess && pl.large_cap) e = launch_paged_large(p, q_dtype, cache_dtype, s);
-    if (e == cudaSuccess && pl.small_cap) e = launch_paged_small(p, q_dtype, cache_dtype, s);
-    if (e == cudaSuccess) e = launch_paged_combine(p, q_dtype, s);
-    return status_of(e);
+vq_status vq_paged_attend_tree_workspace(int T, int B, int Hq, int Hkv, int max_q, size_t *bytes)
+{
+    if (!bytes) return VQ_ERR_INVALID_ARG;
+    AttendPlan pl;
+    const vq_status st = attend_plan(T, B, Hq, Hkv, max_q, PG_TREE, pl);
+    if (st != VQ_OK) return st;
+    if (max_q > PG_TREE_MAX) return VQ_ERR_UNSUPPORTED;
+    *bytes = pl.bytes;
+    return VQ_OK;
+}
+
+vq_status vq_paged_attend_tree(const void *q, long long q_stride_t, long long q_stride_h, int q_dtype,
+                               const void *k_pages, const void *v_pages, const uint8_t *k_exp, const uint8_t *v_exp,
+                               int cache_dtype, int num_pages, int Hkv, int page_size, int D, const int32_t *block_table,
+                               int max_pages, const int32_t *cu_q, const int32_t *lens, const int32_t *parents, int T, int B,
+                               int Hq, int max_q, int window, int sinks, float scale, void *out, void *workspace,
+                               size_t workspace_bytes, vq_stream_t stream)
+{
+    const CacheArgs a = {k_pages, v_pages, k_exp, v_exp, cache_dtype, num_pages, Hkv, page_size};
+    return attend({PG_TREE, parents}, a, D, q, q_stride_t, q_stride_h, q_dtype, block_table, max_pages, cu_q, lens, T, B, Hq,
+                  max_q, window, sinks, scale, out, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

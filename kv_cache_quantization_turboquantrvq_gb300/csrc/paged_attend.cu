@@ -8,6 +8,14 @@
 // over the keys j <= p with (no window, or j > p - window, or j < sinks).  Rows
 // that see no key give zeros.
 //
+// Trees of drafts.  The new token i of depth d_i (its number of ancestors among the
+// new ones) is at position p = lens[b] - n_b + d_i and sees the earlier tokens of
+// the sequence as above, and of the new ones itself and its ancestors, by the same
+// rule on their positions.  The new tokens lie in the cache in the order given, so
+// these are bits over the last n_b keys: at most 16 of a small item, which its warps
+// find by themselves, and PG_TREE_WORDS words a token for the large ones, which the
+// plan's launch writes.
+//
 // 8-bit cache.  With k_j = 2^a_j K_j and v_j = 2^b_j V_j (codes K, V exact in
 // fp16 and bf16) the score is 2^a_j (q . K_j), and the exponent of the value is
 // folded into the weight: w'_j = 2^(s_j + b_j - M) with M the maximum of
@@ -76,8 +84,8 @@ __device__ __forceinline__ PgEntry make_entry(const PagedAttendParams &p, int b,
     e.b = b;
     e.tok0 = start + i * tq;
     e.nt = min(tq, n - i * tq);
-    e.p0 = len - n + i * tq;
-    e.hi = max(0, e.p0 + e.nt);
+    e.p0 = len - n + (p.parents ? 0 : i * tq);
+    e.hi = max(0, len - n + i * tq + e.nt);
     const int lo = p.window > 0 ? max(0, e.p0 - p.window + 1) : 0;
     const int sink = p.window > 0 ? min(p.sinks, e.hi) : 0;
     const int th = (e.hi + PG_TILE - 1) / PG_TILE, st = (sink + PG_TILE - 1) / PG_TILE, tl = lo / PG_TILE;
@@ -91,7 +99,8 @@ __device__ __forceinline__ PgEntry make_entry(const PagedAttendParams &p, int b,
 // The first query token, the number of new tokens and the length of sequence b,
 // within the buffers whatever the numbers given, and whether they make sense:
 // SEQ_BACK, the next sequence starts before this one; SEQ_BAD, tokens outside the
-// queries, more than max_q, or of a sequence longer than its pages.
+// queries, more than max_q, or of a sequence longer than its pages, a tree that is
+// longer than its sequence.
 enum { SEQ_OK = 0, SEQ_BAD = 1, SEQ_BACK = 2 };
 __device__ __forceinline__ int sequence(const PagedAttendParams &p, int b, int &start, int &n, int &len)
 {
@@ -101,7 +110,7 @@ __device__ __forceinline__ int sequence(const PagedAttendParams &p, int b, int &
     n = min(max(c1, start), p.T) - start;
     const int given = __ldg(p.lens + b);
     len = min(max(given, 0), cap);
-    const bool bad = n > p.max_q || c0 < 0 || c1 > p.T || (n > 0 && len != given);
+    const bool bad = n > p.max_q || c0 < 0 || c1 > p.T || (n > 0 && len != given) || (p.parents && n > len);
     n = min(n, p.max_q);
     return c1 < c0 ? SEQ_BACK : bad ? SEQ_BAD : SEQ_OK;
 }
@@ -131,8 +140,40 @@ template <class F> __device__ __forceinline__ int parts_at(F &&first, int g, int
     return n;
 }
 
+// The masks and depths of the tokens of sequence b, a thread each: up its ancestors
+// twice, for its depth and for the bits.  A parent that does not come before its
+// token is reported and taken for the last cached token.
+__device__ __forceinline__ void tree_masks(const PagedAttendParams &p, int b, int *parent, uint32_t *rows)
+{
+    int start = 0, n = 0, len = 0;
+    (void)sequence(p, b, start, n, len);  // (the plan reports)
+    const int i = threadIdx.x, base = len - n;
+    n = min(n, PG_TREE_MAX);
+    if (i < n) {
+        int a = __ldg(p.parents + start + i);
+        if (a < -1 || a >= i) {
+            atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+            a = -1;
+        }
+        parent[i] = a;
+    }
+    __syncthreads();
+    if (i >= n) return;
+    uint32_t *row = rows + i * PG_TREE_WORDS;
+    for (int w = 0; w < PG_TREE_WORDS; ++w) row[w] = 0u;
+    int depth = 0;
+    for (int a = parent[i]; a >= 0; a = parent[a]) ++depth;
+    int up = 0;
+    for (int a = i; a >= 0; a = parent[a], ++up)
+        if (p.window == 0 || up < p.window || base + depth - up < p.sinks) row[a >> 5] |= 1u << (a & 31);
+    p.depth[start + i] = depth;
+    uint4 *dst = reinterpret_cast<uint4 *>(p.masks + (size_t)(start + i) * PG_TREE_WORDS);
+    for (int w = 0; w < PG_TREE_WORDS / 4; ++w) dst[w] = make_uint4(row[4 * w], row[4 * w + 1], row[4 * w + 2], row[4 * w + 3]);
+}
+
 // One CTA: entries of both classes, sequence by sequence, the units before each,
-// and where each CTA of the attention kernels starts.
+// and where each CTA of the attention kernels starts.  (Trees: a CTA a sequence
+// more, for its tokens' masks.)
 __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __grid_constant__ PagedAttendParams p)
 {
     __shared__ long long ws[32];
@@ -143,6 +184,11 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
     __shared__ long long s_first[PLAN_CTAS + 1];  // first unit of each share
     __shared__ int4 s_at[PLAN_CTAS + 1];          // its entry, head, tile
     pg_go();
+    if (blockIdx.x > 0) {
+        static_assert(PG_TREE_MAX * PG_TREE_WORDS <= 4 * PLAN_KEPT && PG_TREE_MAX <= 2 * PLAN_KEPT, "room for a tree");
+        tree_masks(p, (int)blockIdx.x - 1, s_nt[0], reinterpret_cast<uint32_t *>(s_base));
+        return;
+    }
     const int lane = threadIdx.x & 31;
     long long carry = 0;  // entries so far: small in the low half, large in the high one
     for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
@@ -557,7 +603,7 @@ __device__ __forceinline__ bool planned(const PagedAttendParams &p)
 }
 
 // T: query and output type; Q8: e4m3 cache (values are then taken as fp16)
-template <class T, bool Q8, int NT>
+template <class T, bool Q8, int NT, int MODE>
 __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kernel(const __grid_constant__ PagedAttendParams p)
 {
     using L = SmShape<Q8, NT>;
@@ -765,11 +811,41 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
         // the rows of this lane's results are 8 nt + 2 t4 + {0, 1}; their
         // visible keys: j <= pos, and the window
         int pos[2 * NT], low[2 * NT];
+        [[maybe_unused]] uint32_t draft[2 * NT];  // (trees) the new tokens that the row sees; pos: the keys before them
+        if constexpr (MODE == PG_TREE) {
+            int parent = lane < e.nt ? __ldg(p.parents + e.tok0 + lane) : -1;
+            if (parent < -1 || parent >= lane) {
+                atomicOr(&g_pa_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+                parent = -1;
+            }
+            int depth = 0, up = 0;
+            uint32_t mask = 0u;
+            for (int a = parent; __any_sync(FULL_MASK, a >= 0);) {
+                const int next = __shfl_sync(FULL_MASK, parent, max(a, 0));
+                depth += a >= 0 ? 1 : 0;
+                a = a >= 0 ? next : -1;
+            }
+            for (int a = lane; __any_sync(FULL_MASK, a >= 0); ++up) {
+                const int next = __shfl_sync(FULL_MASK, parent, max(a, 0));
+                if (a >= 0 && (p.window == 0 || up < p.window || e.p0 + depth - up < p.sinks)) mask |= 1u << a;
+                a = a >= 0 ? next : -1;
+            }
 #pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) {
-            const int row = 8 * (i >> 1) + 2 * t4 + (i & 1);
-            pos[i] = row < rows ? e.p0 + row / p.GQ : -1;
-            low[i] = p.window > 0 ? pos[i] - p.window + 1 : 0;
+            for (int i = 0; i < 2 * NT; ++i) {
+                const int row = 8 * (i >> 1) + 2 * t4 + (i & 1), tok = row / p.GQ;
+                const int d = __shfl_sync(FULL_MASK, depth, tok);
+                const uint32_t mk = __shfl_sync(FULL_MASK, mask, tok);
+                pos[i] = row < rows ? e.p0 - 1 : -1;
+                low[i] = p.window > 0 ? e.p0 + d - p.window + 1 : 0;
+                draft[i] = row < rows ? mk : 0u;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * NT; ++i) {
+                const int row = 8 * (i >> 1) + 2 * t4 + (i & 1);
+                pos[i] = row < rows ? e.p0 + row / p.GQ : -1;
+                low[i] = p.window > 0 ? pos[i] - p.window + 1 : 0;
+            }
         }
         const int lo_all = p.window > 0 ? e.p0 + e.nt - p.window : 0;  // the last row's first key in the window
         float m[2 * NT], l[2 * NT], o[NT][8][4];
@@ -832,7 +908,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                     }
                 }
                 // ---- scale, mask
-                const bool whole = k0 + KB <= e.p0 + 1 && (p.window == 0 || k0 >= lo_all || k0 + KB <= v.sink);
+                const bool whole = k0 + KB <= e.p0 + (MODE == PG_TREE ? 0 : 1) && (p.window == 0 || k0 >= lo_all || k0 + KB <= v.sink);
                 float fa[2] = {p.qscale, p.qscale}, fb[2] = {0.0f, 0.0f}, back[2] = {1.0f, 1.0f};
                 if constexpr (Q8) {
 #pragma unroll
@@ -853,7 +929,8 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int k = k0 + g8 + 8 * (j >> 1), i = 2 * nt + (j & 1);
-                            const bool in = k <= pos[i] && (k >= low[i] || k < v.sink);
+                            bool in = k <= pos[i] && (k >= low[i] || k < v.sink);
+                            if constexpr (MODE == PG_TREE) in = in || ((unsigned)(k - e.p0) < 32u && (draft[i] >> (k - e.p0)) & 1u);
                             s[nt][j] = in ? s[nt][j] : NEG_INF;
                         }
                     }
@@ -1009,10 +1086,10 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
     if (!alone) pg_wait();
 }
 
-template <class T, bool Q8, int NT>
+template <class T, bool Q8, int NT, int MODE>
 cudaError_t launch_small(const PagedAttendParams &p, cudaStream_t stream)
 {
-    auto kern = paged_small_kernel<T, Q8, NT>;
+    auto kern = paged_small_kernel<T, Q8, NT, MODE>;
     constexpr int smem = SmShape<Q8, NT>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -1021,17 +1098,23 @@ cudaError_t launch_small(const PagedAttendParams &p, cudaStream_t stream)
     return cudaGetLastError();
 }
 
+template <class T, bool Q8, int MODE>
+cudaError_t dispatch_small(const PagedAttendParams &p, cudaStream_t stream)
+{
+    return p.small_rows <= 8 ? launch_small<T, Q8, 1, MODE>(p, stream) : launch_small<T, Q8, 2, MODE>(p, stream);
+}
+
 template <class T, bool Q8>
 cudaError_t dispatch_small(const PagedAttendParams &p, cudaStream_t stream)
 {
-    return p.small_rows <= 8 ? launch_small<T, Q8, 1>(p, stream) : launch_small<T, Q8, 2>(p, stream);
+    return p.parents ? dispatch_small<T, Q8, PG_TREE>(p, stream) : dispatch_small<T, Q8, PG_CHAIN>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedAttendParams &p, cudaStream_t stream)
 {
-    paged_plan_kernel<<<1, PLAN_THREADS, 0, stream>>>(p);
+    paged_plan_kernel<<<p.parents ? 1 + p.B : 1, PLAN_THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

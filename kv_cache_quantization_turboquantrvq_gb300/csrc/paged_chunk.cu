@@ -394,7 +394,16 @@ __device__ __forceinline__ uint32_t ck_less(uint32_t four, int least)
     return __vcmpltu4(four, 0x01010101u * (uint32_t)max(least, 0));
 }
 
-template <class T, bool Q8>
+// 32 of the bits of a tree's token from bit `at` on (at may be negative), out of its words.
+__device__ __forceinline__ uint32_t ck_tree(const uint32_t *words, bool any, int at)
+{
+    const int w = at >> 5;
+    const uint32_t lo = any && w >= 0 && w < PG_TREE_WORDS ? words[w] : 0u;
+    const uint32_t hi = any && w >= -1 && w < PG_TREE_WORDS - 1 ? words[w + 1] : 0u;
+    return __funnelshift_r(lo, hi, at & 31);
+}
+
+template <class T, bool Q8, int MODE>
 __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(const __grid_constant__ PagedAttendParams p)
 {
     using C = CkShape<Q8>;
@@ -700,9 +709,12 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
             view.set(r.e, p.window, p.sinks);
             const int tok = w * tqt + tok_in;
             const bool mine = tok_in < tqt && tok < r.e.nt;
-            const int pos = mine ? r.e.p0 + tok : -1;
+            constexpr bool TREE = MODE == PG_TREE;
+            const int ahead = TREE ? r.e.hi - r.e.p0 - r.e.nt : 0;  // tokens of the tree before this item's
+            const int pos = mine ? r.e.p0 + (TREE ? p.depth[r.e.tok0 + tok] : tok) : -1;
             const int low = p.window > 0 ? pos - p.window + 1 : 0;
-            const int pos_a = r.e.p0 + w * tqt, pos_z = r.e.p0 + min(r.e.nt, (w + 1) * tqt) - 1;  // this tile's tokens
+            // this tile's tokens: the last key that all of them see is at pos_a, none is later than pos_z
+            const int pos_a = TREE ? r.e.p0 - 1 : r.e.p0 + w * tqt, pos_z = r.e.p0 + ahead + min(r.e.nt, (w + 1) * tqt) - 1;
             float m = NEG_INF, l = 0.0f;
             if (rows) vs.step();
             for (int t = rows ? r.t0 : r.tn; t < r.tn; ++t) {
@@ -762,10 +774,12 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 if (!whole) {
                     // bit c of word b: key k0 + 32 b + c is seen (words, not
                     // comparisons key by key: those became branches)
-                    const int hi = pos - k0 + 1, lo = low - k0, sink = view.sink - k0;
+                    const int hi = (TREE ? mine ? r.e.p0 : k0 : pos + 1) - k0, lo = low - k0, sink = view.sink - k0;
+                    const uint32_t *draft = TREE ? p.masks + (size_t)(r.e.tok0 + (mine ? tok : 0)) * PG_TREE_WORDS : nullptr;
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
-                        const uint32_t see = ck_below(hi - 32 * b) & (~ck_below(lo - 32 * b) | ck_below(sink - 32 * b));
+                        uint32_t see = ck_below(hi - 32 * b) & (~ck_below(lo - 32 * b) | ck_below(sink - 32 * b));
+                        if constexpr (TREE) see |= ck_tree(draft, mine, k0 + 32 * b - r.e.p0);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) x[b][j] = (see >> j) & 1u ? x[b][j] : 0xff800000u;
                     }
@@ -1081,10 +1095,10 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
     if (warp == 9) tmem_free(tmem, 512);
 }
 
-template <class T, bool Q8>
+template <class T, bool Q8, int MODE>
 cudaError_t launch_chunk(const PagedAttendParams &p, cudaStream_t stream)
 {
-    auto kern = paged_chunk_kernel<T, Q8>;
+    auto kern = paged_chunk_kernel<T, Q8, MODE>;
     constexpr int smem = CkShape<Q8>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -1103,6 +1117,11 @@ cudaError_t launch_chunk(const PagedAttendParams &p, cudaStream_t stream)
     return launch_early(kern, dim3(p.large.G), CkShape<Q8>::THREADS, smem, stream, p);
 }
 
+template <class T, bool Q8> cudaError_t dispatch_chunk(const PagedAttendParams &p, cudaStream_t stream)
+{
+    return p.parents ? launch_chunk<T, Q8, PG_TREE>(p, stream) : launch_chunk<T, Q8, PG_CHAIN>(p, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_large(const PagedAttendParams &p0, int q_dtype, int cache_dtype, cudaStream_t stream)
@@ -1118,8 +1137,8 @@ cudaError_t launch_paged_large(const PagedAttendParams &p0, int q_dtype, int cac
     const uint64_t strides[2] = {(uint64_t)(p.Hq > 1 ? p.qsh : D) * 2, (uint64_t)(p.T > 1 ? p.qst : (long long)p.Hq * D) * 2};
     const uint32_t qbox[3] = {64u, (uint32_t)p.GQ, (uint32_t)(128 / p.GQ)};
     if (!encode_tmap_f16(&p.tmq, p.q, 3, dims, strides, qbox, true, true)) return cudaErrorInvalidValue;
-    if (q_dtype == VQ_F16) return q8 ? launch_chunk<__half, true>(p, stream) : launch_chunk<__half, false>(p, stream);
-    return q8 ? launch_chunk<__nv_bfloat16, true>(p, stream) : launch_chunk<__nv_bfloat16, false>(p, stream);
+    if (q_dtype == VQ_F16) return q8 ? dispatch_chunk<__half, true>(p, stream) : dispatch_chunk<__half, false>(p, stream);
+    return q8 ? dispatch_chunk<__nv_bfloat16, true>(p, stream) : dispatch_chunk<__nv_bfloat16, false>(p, stream);
 }
 
 cudaError_t paged_chunk_take_device_error(unsigned *bits, cudaStream_t stream)
