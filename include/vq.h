@@ -489,8 +489,24 @@ vq_status vq_paged_attend_tree(const void *q, long long q_stride_t, long long q_
  * Keeping a part of a sequence: the softmax weight that tokens got so far says
  * which of them can go.
  *   weights [num_pages, Hkv, page_size] fp32, device: a number for every place of
- *     the cache.  Tokens of a sequence whose pages another sequence shares must
- *     not be moved.
+ *     the cache.  Two sequences that share a page cannot have weights of their own
+ *     in it, and must not be moved.
+ *
+ * vq_paged_attend_weigh - vq_paged_attend, which also adds up the weights: for every
+ * token j that some new token of its sequence sees, and every kv head,
+ *   weight[j] = (j is a new token ? 0 : decay * weight[j]) + the sum, over the last
+ *   `observe` new tokens of the sequence (0: all) and the head's query heads, of the
+ *   softmax weight that j has in their output.
+ * The new tokens' weights are set, whatever was there, and with decay 0 all are;
+ * weights of tokens that no new token sees stay as they are.  0 <= decay <= 1.
+ * The sums are held in 32 bits, in an order that is the same on every call.  Where
+ * sequences of one call share a page, its weights are unspecified.
+ *   weights: 16-byte aligned.
+ *   workspace: of vq_paged_attend_weigh_workspace, which also depends on the block
+ *     table's width: besides the attention's own, 4 bytes for every query row, and
+ *     for every place of the block table and kv head 4 bytes for each query row of
+ *     single tokens (at most 16, and 8 at least where max_q is longer).
+ * Everything else as vq_paged_attend.
  *
  * vq_paged_select - the tokens that sequence b keeps for each kv head: all of its
  * lens[b] tokens where they are no more than `budget`; else the first `sinks`, the
@@ -514,9 +530,16 @@ vq_status vq_paged_attend_tree(const void *q, long long q_stride_t, long long q_
  *     outside [0, K] (cut to it) and a `first` outside the block table (nothing
  *     moves).  Where the list does not ascend, what the moved places hold is
  *     unspecified.
- * Both: B * Hkv at most 2^24, at most 2^30 positions a sequence; one kernel launch;
- * nothing is allocated.
+ * vq_paged_select and vq_paged_compact: B * Hkv at most 2^24, at most 2^30 positions
+ * a sequence; one kernel launch; nothing is allocated.
  */
+vq_status vq_paged_attend_weigh_workspace(int T, int B, int Hq, int Hkv, int max_q, int max_pages, int page_size, size_t *bytes);
+vq_status vq_paged_attend_weigh(const void *q, long long q_stride_t, long long q_stride_h, int q_dtype,
+                                const void *k_pages, const void *v_pages, const uint8_t *k_exp, const uint8_t *v_exp,
+                                int cache_dtype, int num_pages, int Hkv, int page_size, int D, const int32_t *block_table,
+                                int max_pages, const int32_t *cu_q, const int32_t *lens, int T, int B, int Hq, int max_q,
+                                int window, int sinks, float scale, float *weights, int observe, float decay, void *out,
+                                void *workspace, size_t workspace_bytes, vq_stream_t stream);
 vq_status vq_paged_select(const float *weights, int num_pages, int Hkv, int page_size, const int32_t *block_table,
                           int max_pages, const int32_t *lens, int B, int budget, int recent, int sinks, int32_t *keep,
                           int32_t *counts, vq_stream_t stream);

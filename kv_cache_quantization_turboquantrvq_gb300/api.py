@@ -33,7 +33,8 @@ EXPORTED = ("vq_status_str", "vq_version", "vq_rvq_codebook", "vq_rvq_encode_pac
             "vq_rvq_encode_pack_rs", "vq_rvq_unpack_dequant_rs", "vq_rvq_attend_rs",
             "vq_kivi_attend_workspace", "vq_kivi_attend", "vq_qjl_encode", "vq_flush_decode",
             "vq_paged_append", "vq_paged_gather", "vq_paged_attend_workspace", "vq_paged_attend",
-            "vq_paged_attend_tree_workspace", "vq_paged_attend_tree", "vq_paged_select", "vq_paged_compact")
+            "vq_paged_attend_tree_workspace", "vq_paged_attend_tree",
+            "vq_paged_attend_weigh_workspace", "vq_paged_attend_weigh", "vq_paged_select", "vq_paged_compact")
 VQ_F16, VQ_BF16, VQ_E4M3 = 0, 1, 2
 VQ_ATTEND_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -85,6 +86,9 @@ def lib():
     L.vq_paged_attend_tree_workspace.argtypes = L.vq_paged_attend_workspace.argtypes
     L.vq_paged_attend_tree.argtypes = [P, Q, Q, I, P, P, P, P, I, I, I, I, I, P, I, P, P, P, I, I, I, I, I, I,
                                        ctypes.c_float, P, P, ctypes.c_size_t, P]
+    L.vq_paged_attend_weigh_workspace.argtypes = [I, I, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
+    L.vq_paged_attend_weigh.argtypes = [P, Q, Q, I, P, P, P, P, I, I, I, I, I, P, I, P, P, I, I, I, I, I, I, ctypes.c_float,
+                                        P, I, ctypes.c_float, P, P, ctypes.c_size_t, P]
     L.vq_paged_select.argtypes = [P, I, I, I, P, I, P, I, I, I, I, P, P, P]
     L.vq_paged_compact.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, Q, Q, I, P, P, I, P, P]
     for name in EXPORTED[2:]:
@@ -702,6 +706,35 @@ def vq_paged_attend_tree(q, cache: dict, block_table, cu_q, lens, parents, scale
                                                       max_q, window, sinks, out, workspace, stream)
     up = _typed(parents, torch.int32, (sizes[0],), "parents", gpu)
     _check(_on_gpu(gpu, lib().vq_paged_attend_tree)(*args, up, *sizes, scale, *last), "vq_paged_attend_tree")
+    return out
+
+
+def vq_paged_attend_weigh_workspace(T: int, B: int, Hq: int, Hkv: int, max_q: int, max_pages: int, page_size: int) -> int:
+    """Workspace bytes vq_paged_attend_weigh needs for these shapes on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(lib().vq_paged_attend_weigh_workspace(T, B, Hq, Hkv, max_q, max_pages, page_size, ctypes.byref(n)),
+           "vq_paged_attend_weigh_workspace")
+    return int(n.value)
+
+
+def vq_paged_attend_weigh(q, cache: dict, weights, block_table, cu_q, lens, scale: float, max_q: int, window: int = 0,
+                          sinks: int = 0, observe: int = 0, decay: float = 1.0, out=None, workspace=None, stream=None):
+    """vq_paged_attend, which also adds up the softmax weight that each cached token
+    gets: weights [num_pages, Hkv, page_size] (float32, updated in place) of every
+    token that some new token sees become decay times what they were (of the new
+    tokens: 0) plus the sum over the last `observe` new tokens of the sequence (0:
+    all) and the query heads of the kv head.  Sequences must not share pages.  The
+    workspace grows with the block table's width
+    (vq_paged_attend_weigh_workspace)."""
+    import torch
+    if observe > _INT_MAX:
+        raise ValueError("observe: less than 2^31")
+    shape = cache["k_pages"].shape
+    w = _typed(weights, torch.float32, shape[:3], "weights", _gpu(q, "q"))
+    out, gpu, args, sizes, last, _held = _attend_args(vq_paged_attend_weigh_workspace, q, cache, block_table, cu_q, lens,
+                                                      max_q, window, sinks, out, workspace, stream, block_table.shape[1],
+                                                      shape[2])
+    _check(_on_gpu(gpu, lib().vq_paged_attend_weigh)(*args, *sizes, scale, w, observe, decay, *last), "vq_paged_attend_weigh")
     return out
 
 

@@ -18,8 +18,8 @@ LIB = os.path.join(HERE, "libvqflush.so")
 BUILD = os.path.join(HERE, "_build")
 
 SOURCES = ["rvq.cu", "rvq_generic.cu", "kivi.cu", "flush.cu", "attend.cu", "kattend.cu", "qjl.cu", "paged_cache.cu",
-           "paged_attend.cu", "paged_chunk.cu", "paged_keep.cu", "api.cpp", "paged_api.cpp", "paged_keep_api.cpp",
-           "codebook.cpp", "grid.cpp", "tmap.cpp"]
+           "paged_attend.cu", "paged_chunk.cu", "paged_weigh.cu", "paged_keep.cu", "api.cpp", "paged_api.cpp",
+           "paged_keep_api.cpp", "codebook.cpp", "grid.cpp", "tmap.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-std=c++17", "-O3", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -921,7 +921,9 @@ vq_status vq_device_error(vq_stream_t stream, int *code_out)
     if (paged_chunk_take_device_error(&j, s) != cudaSuccess) return VQ_ERR_CUDA;
     unsigned k = 0;
     if (paged_keep_take_device_error(&k, s) != cudaSuccess) return VQ_ERR_CUDA;
-    *code_out = (int)(a | b | c | d | e | f | g | h | i | j | k);
+    unsigned l = 0;
+    if (paged_weigh_take_device_error(&l, s) != cudaSuccess) return VQ_ERR_CUDA;
+    *code_out = (int)(a | b | c | d | e | f | g | h | i | j | k | l);
     return *code_out ? VQ_ERR_DEVICE : VQ_OK;
 }
 

@@ -105,8 +105,9 @@ struct PgPlan {
 };
 
 // What the new tokens of a call are: each sequence's next ones in order, or a tree
-// of drafts, in which a token sees its ancestors only.
-enum PgMode { PG_CHAIN, PG_TREE };
+// of drafts, in which a token sees its ancestors only; or (WEIGH) the next ones,
+// whose softmax weights are added up too.
+enum PgMode { PG_CHAIN, PG_TREE, PG_WEIGH };
 constexpr int PG_TREE_MAX = 256, PG_TREE_WORDS = PG_TREE_MAX / 32;  // tokens of a tree
 
 struct PagedAttendParams {
@@ -126,7 +127,16 @@ struct PagedAttendParams {
     const int32_t *parents;      // [T] trees; null: no tree
     uint32_t *masks;             // [T][PG_TREE_WORDS] trees in the large class: the new tokens that a token sees
     int32_t *depth;              // [T] and its number of ancestors
+    // (WEIGH)
+    float *lse;                  // [T, Hq] log2 of each query row's sum of 2^score; null: no weights
+    float *scores;               // [B, Hkv, srows, keys] scores of single tokens, or sums over parts of a chunk
+    int srows, keys;
+    long long *wbase;            // [B + 1] units of weighing before each sequence of the large class
+    float *weights;              // [num_pages, Hkv, page_size]
+    float decay;
+    int observe;                 // new tokens of a sequence that count, the last ones; 0: all
 };
+constexpr int PG_PARTS = 4;      // parts that a chunk's query rows are weighed in, at most
 constexpr int PG_SROWS = 16;     // rows of a small item
 constexpr int PG_LROWS = 256;    // rows of a large item (two tensor-memory tiles)
 // Floats of a row's partial result.  A slot holds the rows' maxima, then their
@@ -157,6 +167,9 @@ cudaError_t launch_paged_plan(const PagedAttendParams &p, cudaStream_t stream);
 cudaError_t launch_paged_small(const PagedAttendParams &p, int q_dtype, int cache_dtype, cudaStream_t stream);
 cudaError_t launch_paged_large(const PagedAttendParams &p, int q_dtype, int cache_dtype, cudaStream_t stream);
 cudaError_t paged_chunk_take_device_error(unsigned *bits, cudaStream_t stream);
+cudaError_t launch_paged_weigh(const PagedAttendParams &p, int q_dtype, int cache_dtype, cudaStream_t stream);
+cudaError_t launch_paged_weigh_update(const PagedAttendParams &p, cudaStream_t stream);
+cudaError_t paged_weigh_take_device_error(unsigned *bits, cudaStream_t stream);
 cudaError_t launch_paged_combine(const PagedAttendParams &p, int q_dtype, cudaStream_t stream);
 cudaError_t paged_attend_take_device_error(unsigned *bits, cudaStream_t stream);
 
@@ -166,5 +179,8 @@ bool encode_tmap_pages(CUtensorMap *map, const void *base, uint64_t rows, int el
 // The same 16-bit rows as [2 halves, rows, 64]: a box holds `box_rows` rows of the
 // first half, then of the second.
 bool encode_tmap_halves(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
+// A call's queries: boxes of 64 columns, the heads of a kv head, the tokens of a tile
+// of 128 rows.
+bool encode_tmap_queries(CUtensorMap *map, const PagedAttendParams &p);
 
 }  // namespace vq

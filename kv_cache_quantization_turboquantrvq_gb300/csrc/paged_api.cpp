@@ -40,10 +40,13 @@ struct AttendPlan {
     int small_rows, small_cap, small_tq, large_cap, large_tq, G;
     size_t bytes;
     Layout s, l;
-    size_t planned, masks, depth;
+    size_t planned, masks, depth;    // (trees)
+    size_t wbase, lse, scores;       // (weights)
+    int srows;
 };
 
-vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, PgMode mode, AttendPlan &pl)
+// keys (PG_WEIGH): tokens that the block table has room for.
+vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, PgMode mode, long long keys, AttendPlan &pl)
 {
     if (T < 0 || B < 0 || Hq < 0 || Hkv <= 0 || max_q < 0 || Hq % Hkv != 0) return VQ_ERR_INVALID_ARG;
     const int gq = Hq / Hkv;
@@ -71,6 +74,16 @@ vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, PgMode mode, Att
     pl.masks = pl.planned + (small && large ? kPlanned : 0);
     pl.depth = pl.masks + (mode == PG_TREE && large ? up((size_t)T * PG_TREE_WORDS * 4) : 0);
     pl.bytes = pl.depth + (mode == PG_TREE && large ? up((size_t)T * 4) : 0);
+    if (mode == PG_WEIGH) {
+        // scores of the small kernel's rows, or the parts of a chunk's sums
+        pl.srows = small ? (pl.small_rows < max_q * gq ? pl.small_rows : max_q * gq) : 0;
+        if (large && pl.srows < 2 * PG_PARTS) pl.srows = 2 * PG_PARTS;
+        if ((double)B * Hkv * pl.srows * (double)keys >= 1e15) return VQ_ERR_UNSUPPORTED;
+        pl.wbase = pl.bytes;
+        pl.lse = pl.wbase + (large ? up((size_t)(B + 1) * 8) : 0);
+        pl.scores = pl.lse + up((size_t)T * Hq * 4);
+        pl.bytes = pl.scores + up((size_t)B * Hkv * pl.srows * (size_t)keys * 4);
+    }
     return VQ_OK;
 }
 
@@ -89,7 +102,10 @@ void place(PgPlan &d, unsigned char *ws, const Layout &l, int cap, int G, int tq
 // What a call's new tokens are besides the next ones in order.
 struct AttendExtra {
     PgMode mode;
-    const int32_t *parents;
+    const int32_t *parents;  // PG_TREE
+    float *weights;          // PG_WEIGH
+    int observe;
+    float decay;
 };
 
 vq_status attend(const AttendExtra &x, const CacheArgs &a, int D, const void *q, long long q_stride_t, long long q_stride_h,
@@ -101,13 +117,14 @@ vq_status attend(const AttendExtra &x, const CacheArgs &a, int D, const void *q,
     vq_status st = check_cache_shape(a, D);
     if (st != VQ_OK) return st;
     AttendPlan pl;
-    if ((st = attend_plan(T, B, Hq, Hkv, max_q, x.mode, pl)) != VQ_OK) return st;
+    if ((st = attend_plan(T, B, Hq, Hkv, max_q, x.mode, (long long)(max_pages > 0 ? max_pages : 0) * page_size, pl)) != VQ_OK) return st;
     const float qscale = (float)((double)scale * 1.4426950408889634);  // the kernels' exponents are of base 2
     if (!is16(q_dtype) || max_pages < 0 || window < 0 || sinks < 0 || !std::isfinite(qscale)) return VQ_ERR_INVALID_ARG;
     if (cache_dtype != VQ_E4M3 && cache_dtype != q_dtype) return VQ_ERR_INVALID_ARG;
     // (positions and a window behind them stay within 32 bits)
     if ((long long)max_pages * page_size > (1LL << 30) || T > (1 << 30)) return VQ_ERR_UNSUPPORTED;
     if (x.mode == PG_TREE && max_q > PG_TREE_MAX) return VQ_ERR_UNSUPPORTED;
+    if (x.mode == PG_WEIGH && (x.observe < 0 || !(x.decay >= 0.0f && x.decay <= 1.0f))) return VQ_ERR_INVALID_ARG;
     if (T == 0 || B == 0 || Hq == 0) return VQ_OK;
     if (max_q == 0) return VQ_ERR_INVALID_ARG;
     if ((st = check_view(q, T, Hq, q_stride_t, q_stride_h)) != VQ_OK) return st;
@@ -115,12 +132,12 @@ vq_status attend(const AttendExtra &x, const CacheArgs &a, int D, const void *q,
     if (num_pages == 0 || max_pages == 0) return VQ_ERR_INVALID_ARG;
     if ((st = check_cache_ptrs(a, true, true)) != VQ_OK) return st;
     if (!block_table || !cu_q || !lens || !out || !workspace) return VQ_ERR_INVALID_ARG;
-    if (x.mode == PG_TREE && !x.parents) return VQ_ERR_INVALID_ARG;
+    if ((x.mode == PG_TREE && !x.parents) || (x.mode == PG_WEIGH && !x.weights)) return VQ_ERR_INVALID_ARG;
     if (!aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(lens, 4) || !aligned(out, 16) || !aligned(workspace, 256) ||
-        !aligned(x.parents, 4))
+        !aligned(x.parents, 4) || !aligned(x.weights, 16))
         return VQ_ERR_MISALIGNED;
     if (workspace_bytes < pl.bytes) return VQ_ERR_INVALID_ARG;
-    const Span outs[2] = {{out, (size_t)T * Hq * kD * 2}, {workspace, pl.bytes}};
+    const Span outs[3] = {{out, (size_t)T * Hq * kD * 2}, {workspace, pl.bytes}, {x.weights, (size_t)a.rows() * 4}};
     const Span ins[9] = {{q, view_bytes(T, Hq, q_stride_t, q_stride_h)}, {a.k, a.entry_bytes()},
                          {a.v, a.entry_bytes()}, {a.exp_bytes() ? a.ke : nullptr, a.exp_bytes()},
                          {a.exp_bytes() ? a.ve : nullptr, a.exp_bytes()},
@@ -129,7 +146,7 @@ vq_status attend(const AttendExtra &x, const CacheArgs &a, int D, const void *q,
     for (const Span &o : outs)
         for (const Span &i : ins)
             if (overlap(o, i)) return VQ_ERR_ALIASING;
-    if (overlap(outs[0], outs[1])) return VQ_ERR_ALIASING;
+    if (overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || overlap(outs[1], outs[2])) return VQ_ERR_ALIASING;
 
     PagedAttendParams p;
     std::memset(&p, 0, sizeof(p));
@@ -168,12 +185,24 @@ vq_status attend(const AttendExtra &x, const CacheArgs &a, int D, const void *q,
         p.masks = reinterpret_cast<uint32_t *>(ws + pl.masks);
         p.depth = reinterpret_cast<int32_t *>(ws + pl.depth);
     }
+    if (x.mode == PG_WEIGH) {
+        p.wbase = pl.large_cap ? reinterpret_cast<long long *>(ws + pl.wbase) : nullptr;
+        p.lse = reinterpret_cast<float *>(ws + pl.lse);
+        p.scores = reinterpret_cast<float *>(ws + pl.scores);
+        p.srows = pl.srows;
+        p.keys = max_pages * page_size;
+        p.weights = x.weights;
+        p.decay = x.decay;
+        p.observe = x.observe;
+    }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // (a call of small sequences alone: its kernel makes the plan)
     cudaError_t e = pl.large_cap ? launch_paged_plan(p, s) : cudaSuccess;
     if (e == cudaSuccess && pl.large_cap) e = launch_paged_large(p, q_dtype, cache_dtype, s);
     if (e == cudaSuccess && pl.small_cap) e = launch_paged_small(p, q_dtype, cache_dtype, s);
     if (e == cudaSuccess) e = launch_paged_combine(p, q_dtype, s);
+    if (e == cudaSuccess && x.mode == PG_WEIGH && pl.large_cap) e = launch_paged_weigh(p, q_dtype, cache_dtype, s);
+    if (e == cudaSuccess && x.mode == PG_WEIGH) e = launch_paged_weigh_update(p, s);
     return status_of(e);
 }
 
@@ -266,7 +295,7 @@ vq_status vq_paged_attend_workspace(int T, int B, int Hq, int Hkv, int max_q, si
 {
     if (!bytes) return VQ_ERR_INVALID_ARG;
     AttendPlan pl;
-    const vq_status st = attend_plan(T, B, Hq, Hkv, max_q, PG_CHAIN, pl);
+    const vq_status st = attend_plan(T, B, Hq, Hkv, max_q, PG_CHAIN, 0, pl);
     if (st != VQ_OK) return st;
     *bytes = pl.bytes;
     return VQ_OK;
@@ -280,7 +309,7 @@ vq_status vq_paged_attend(const void *q, long long q_stride_t, long long q_strid
                           vq_stream_t stream)
 {
     const CacheArgs a = {k_pages, v_pages, k_exp, v_exp, cache_dtype, num_pages, Hkv, page_size};
-    return attend({PG_CHAIN, nullptr}, a, D, q, q_stride_t, q_stride_h, q_dtype, block_table, max_pages, cu_q, lens, T, B, Hq,
+    return attend({PG_CHAIN, nullptr, nullptr, 0, 0.0f}, a, D, q, q_stride_t, q_stride_h, q_dtype, block_table, max_pages, cu_q, lens, T, B, Hq,
                   max_q, window, sinks, scale, out, workspace, workspace_bytes, stream);
 }
 
@@ -288,7 +317,7 @@ vq_status vq_paged_attend_tree_workspace(int T, int B, int Hq, int Hkv, int max_
 {
     if (!bytes) return VQ_ERR_INVALID_ARG;
     AttendPlan pl;
-    const vq_status st = attend_plan(T, B, Hq, Hkv, max_q, PG_TREE, pl);
+    const vq_status st = attend_plan(T, B, Hq, Hkv, max_q, PG_TREE, 0, pl);
     if (st != VQ_OK) return st;
     if (max_q > PG_TREE_MAX) return VQ_ERR_UNSUPPORTED;
     *bytes = pl.bytes;
@@ -303,8 +332,31 @@ vq_status vq_paged_attend_tree(const void *q, long long q_stride_t, long long q_
                                size_t workspace_bytes, vq_stream_t stream)
 {
     const CacheArgs a = {k_pages, v_pages, k_exp, v_exp, cache_dtype, num_pages, Hkv, page_size};
-    return attend({PG_TREE, parents}, a, D, q, q_stride_t, q_stride_h, q_dtype, block_table, max_pages, cu_q, lens, T, B, Hq,
+    return attend({PG_TREE, parents, nullptr, 0, 0.0f}, a, D, q, q_stride_t, q_stride_h, q_dtype, block_table, max_pages, cu_q, lens, T, B, Hq,
                   max_q, window, sinks, scale, out, workspace, workspace_bytes, stream);
+}
+
+vq_status vq_paged_attend_weigh_workspace(int T, int B, int Hq, int Hkv, int max_q, int max_pages, int page_size, size_t *bytes)
+{
+    if (!bytes || max_pages < 0) return VQ_ERR_INVALID_ARG;
+    if (shift_of(page_size) < 0 || (long long)max_pages * page_size > (1LL << 30)) return VQ_ERR_UNSUPPORTED;
+    AttendPlan pl;
+    const vq_status st = attend_plan(T, B, Hq, Hkv, max_q, PG_WEIGH, (long long)max_pages * page_size, pl);
+    if (st != VQ_OK) return st;
+    *bytes = pl.bytes;
+    return VQ_OK;
+}
+
+vq_status vq_paged_attend_weigh(const void *q, long long q_stride_t, long long q_stride_h, int q_dtype,
+                                const void *k_pages, const void *v_pages, const uint8_t *k_exp, const uint8_t *v_exp,
+                                int cache_dtype, int num_pages, int Hkv, int page_size, int D, const int32_t *block_table,
+                                int max_pages, const int32_t *cu_q, const int32_t *lens, int T, int B, int Hq, int max_q,
+                                int window, int sinks, float scale, float *weights, int observe, float decay, void *out,
+                                void *workspace, size_t workspace_bytes, vq_stream_t stream)
+{
+    const CacheArgs a = {k_pages, v_pages, k_exp, v_exp, cache_dtype, num_pages, Hkv, page_size};
+    return attend({PG_WEIGH, nullptr, weights, observe, decay}, a, D, q, q_stride_t, q_stride_h, q_dtype, block_table, max_pages,
+                  cu_q, lens, T, B, Hq, max_q, window, sinks, scale, out, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

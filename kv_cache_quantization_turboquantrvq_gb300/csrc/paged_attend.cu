@@ -78,56 +78,6 @@ __device__ __forceinline__ long long block_scan(long long v, long long *ws, long
     return before + x - v;
 }
 
-__device__ __forceinline__ PgEntry make_entry(const PagedAttendParams &p, int b, int start, int n, int len, int tq, int i)
-{
-    PgEntry e;
-    e.b = b;
-    e.tok0 = start + i * tq;
-    e.nt = min(tq, n - i * tq);
-    e.p0 = len - n + (p.parents ? 0 : i * tq);
-    e.hi = max(0, len - n + i * tq + e.nt);
-    const int lo = p.window > 0 ? max(0, e.p0 - p.window + 1) : 0;
-    const int sink = p.window > 0 ? min(p.sinks, e.hi) : 0;
-    const int th = (e.hi + PG_TILE - 1) / PG_TILE, st = (sink + PG_TILE - 1) / PG_TILE, tl = lo / PG_TILE;
-    // leading tiles that reach the window make one run with it
-    e.nsink = st >= tl ? 0 : st;
-    e.tl = st >= tl ? 0 : tl;
-    e.ntiles = max(1, e.nsink + th - e.tl);
-    return e;
-}
-
-// The first query token, the number of new tokens and the length of sequence b,
-// within the buffers whatever the numbers given, and whether they make sense:
-// SEQ_BACK, the next sequence starts before this one; SEQ_BAD, tokens outside the
-// queries, more than max_q, or of a sequence longer than its pages, a tree that is
-// longer than its sequence.
-enum { SEQ_OK = 0, SEQ_BAD = 1, SEQ_BACK = 2 };
-__device__ __forceinline__ int sequence(const PagedAttendParams &p, int b, int &start, int &n, int &len)
-{
-    const int cap = (int)min((long long)p.max_pages << p.c.page_shift, 0x7fffffffLL);
-    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
-    start = min(max(c0, 0), p.T);
-    n = min(max(c1, start), p.T) - start;
-    const int given = __ldg(p.lens + b);
-    len = min(max(given, 0), cap);
-    const bool bad = n > p.max_q || c0 < 0 || c1 > p.T || (n > 0 && len != given) || (p.parents && n > len);
-    n = min(n, p.max_q);
-    return c1 < c0 ? SEQ_BACK : bad ? SEQ_BAD : SEQ_OK;
-}
-
-// Even shares of the units: the first `rem` of `g` CTAs take one more than q.
-struct Shares {
-    long long q;
-    int g, rem;
-    __device__ __forceinline__ void set(long long total, int G)
-    {
-        g = (int)min((long long)G, total);
-        q = g ? total / g : 0;
-        rem = g ? (int)(total - q * g) : 0;
-    }
-    __device__ __forceinline__ long long first(int c) const { return q * c + min(c, rem); }
-};
-
 // What is merged where CTA c of g starts, in tile t of nt of an item: the parts of
 // the item it enters in its middle, if no earlier CTA does so; 0 otherwise.
 template <class F> __device__ __forceinline__ int parts_at(F &&first, int g, int c, int t, int nt)
@@ -227,6 +177,22 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
         }
     }
     __syncthreads();
+    if (p.wbase) {  // the units of weighing: a key tile, a head, a part of the query rows
+        long long units = 0;
+        bool back = false;
+        for (int b0 = 0; b0 < p.B && !back; b0 += PLAN_THREADS) {
+            const int b = b0 + threadIdx.x;
+            int start = 0, n = 0, len = 0;
+            const int sense = b < p.B ? sequence(p, b, start, n, len) : SEQ_OK;
+            back = __syncthreads_or(sense == SEQ_BACK);
+            long long u = 0, all;
+            if (n * p.GQ > p.small_rows) u = (long long)make_entry(p, b, start, n, len, n, 0).ntiles * p.Hkv * pg_parts(p, n);
+            const long long before = block_scan(u, ws, all);
+            if (b < p.B) p.wbase[b] = units + before;
+            units += all;
+        }
+        if (threadIdx.x == 0) p.wbase[p.B] = back ? 0 : units;
+    }
     for (int k = 0; k < 2; ++k) {
         const PgPlan &pl = k ? p.large : p.small;
         if (pl.cap == 0) continue;
@@ -395,7 +361,9 @@ __device__ __forceinline__ void merge_rows(const PagedAttendParams &p, const flo
         const int tok = half * tqt + rr / p.GQ, g = rr % p.GQ;
         if (rr >= tqt * p.GQ || tok >= at.z) continue;  // a row of no token
         const float inv = L[j] > 0.0f ? 1.0f / L[j] : 0.0f;
-        T *dst = static_cast<T *>(p.out) + ((size_t)(at.y + tok) * p.Hq + (size_t)at.w * p.GQ + g) * D + 4 * lane;
+        const size_t qrow = (size_t)(at.y + tok) * p.Hq + (size_t)at.w * p.GQ + g;
+        if (p.lse && lane == 0) p.lse[qrow] = pg_lse(M[j], L[j]);
+        T *dst = static_cast<T *>(p.out) + qrow * D + 4 * lane;
         *reinterpret_cast<uint2 *>(dst) =
             pack4<T>(make_float4(O[j].x * inv, O[j].y * inv, O[j].z * inv, O[j].w * inv));
     }
@@ -908,6 +876,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                     }
                 }
                 // ---- scale, mask
+                [[maybe_unused]] float raw[NT][4];  // (WEIGH) scores without the values' exponents
                 const bool whole = k0 + KB <= e.p0 + (MODE == PG_TREE ? 0 : 1) && (p.window == 0 || k0 >= lo_all || k0 + KB <= v.sink);
                 float fa[2] = {p.qscale, p.qscale}, fb[2] = {0.0f, 0.0f}, back[2] = {1.0f, 1.0f};
                 if constexpr (Q8) {
@@ -924,7 +893,11 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[nt][j] = Q8 ? fmaf(s[nt][j] * back_q[2 * nt + (j & 1)], fa[j >> 1], fb[j >> 1]) : s[nt][j] * fa[0];
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = s[nt][j] * back_q[2 * nt + (j & 1)];
+                        if constexpr (MODE == PG_WEIGH) raw[nt][j] = x * fa[Q8 ? j >> 1 : 0];
+                        s[nt][j] = Q8 ? fmaf(x, fa[j >> 1], fb[j >> 1]) : s[nt][j] * fa[0];
+                    }
                     if (!whole) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -932,6 +905,19 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                             bool in = k <= pos[i] && (k >= low[i] || k < v.sink);
                             if constexpr (MODE == PG_TREE) in = in || ((unsigned)(k - e.p0) < 32u && (draft[i] >> (k - e.p0)) & 1u);
                             s[nt][j] = in ? s[nt][j] : NEG_INF;
+                            if constexpr (MODE == PG_WEIGH) raw[nt][j] = in ? raw[nt][j] : NEG_INF;
+                        }
+                    }
+                    if constexpr (MODE == PG_WEIGH) {
+                        // [row][key]: a store of the warp fills whole sectors (keys lie in
+                        // order along g8, four rows along t4)
+                        float *at = p.scores + (((size_t)e.b * p.Hkv + r.h) * p.srows + 8 * nt + 2 * t4) * p.keys + k0 + g8;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (8 * nt + 2 * t4 + i < rows) {
+                                at[(size_t)i * p.keys] = raw[nt][i];
+                                at[(size_t)i * p.keys + 8] = raw[nt][i + 2];
+                            }
                         }
                     }
                     // ---- softmax: a row's 16 scores lie in the 8 lanes of one t4
@@ -1077,8 +1063,9 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
             } else {
                 const float inv = Ls > 0.0f ? 1.0f / Ls : 0.0f;
                 x.x *= inv; x.y *= inv; x.z *= inv; x.w *= inv;
-                T *dst = static_cast<T *>(p.out) +
-                         ((size_t)(e.tok0 + row / p.GQ) * p.Hq + (size_t)r.h * p.GQ + row % p.GQ) * D + 4 * lane;
+                const size_t qrow = (size_t)(e.tok0 + row / p.GQ) * p.Hq + (size_t)r.h * p.GQ + row % p.GQ;
+                if (MODE == PG_WEIGH && lane == 0) p.lse[qrow] = pg_lse(M, Ls);
+                T *dst = static_cast<T *>(p.out) + qrow * D + 4 * lane;
                 *reinterpret_cast<uint2 *>(dst) = pack4<T>(x);
             }
         }
@@ -1107,7 +1094,9 @@ cudaError_t dispatch_small(const PagedAttendParams &p, cudaStream_t stream)
 template <class T, bool Q8>
 cudaError_t dispatch_small(const PagedAttendParams &p, cudaStream_t stream)
 {
-    return p.parents ? dispatch_small<T, Q8, PG_TREE>(p, stream) : dispatch_small<T, Q8, PG_CHAIN>(p, stream);
+    return p.parents ? dispatch_small<T, Q8, PG_TREE>(p, stream)
+           : p.lse   ? dispatch_small<T, Q8, PG_WEIGH>(p, stream)
+                     : dispatch_small<T, Q8, PG_CHAIN>(p, stream);
 }
 
 }  // namespace

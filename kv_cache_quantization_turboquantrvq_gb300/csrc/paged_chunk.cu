@@ -66,6 +66,7 @@
 #include "device_common.cuh"
 #include "paged.h"
 #include "paged_dev.cuh"
+#include "paged_tc.cuh"
 #include "tcgen05.cuh"
 
 namespace vq {
@@ -78,9 +79,6 @@ constexpr int D = 128;
 constexpr float NEG_INF = -__builtin_huge_valf();
 constexpr float OFF = 7.0f, LAG = 8.0f;
 constexpr int KEYS_WITHIN = 15, VALUES_WITHIN = 8;  // powers of two that rows of a tile may share an exponent over
-constexpr int TILE_B = PG_TILE * D * 2;  // a 16-bit tile of 128 rows: two halves of 64 columns
-constexpr int HALF_B = TILE_B / 2;
-constexpr int RAW_B = PG_TILE * D;       // a tile of codes
 
 template <bool Q8> struct CkShape {
     static constexpr int STAGES = Q8 ? 3 : 4;   // 16-bit key / value tiles
@@ -149,45 +147,6 @@ __device__ __forceinline__ uint64_t ck_desc_v(uint32_t saddr)
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// Instruction descriptor: fp32 accumulator, M = N = 128, both operands fp16 or
-// both bf16; `b_mn`: B has its N dimension contiguous.
-__host__ __device__ constexpr uint32_t ck_idesc(bool bf16, bool b_mn)
-{
-    return qt_idesc(128) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u);
-}
-
-// The products of one 128 x 128 x 128 tile, eight K = 16 steps, by one elected
-// thread of the (whole, converged) warp.  One block of PTX each, so that the
-// operands' addresses stay in uniform registers: issued one by one from a
-// branch on the lane number, an instruction took 107 cycles to issue where the
-// tensor core needs 64.  `bar` (shared) gets an arrival when they are done.
-
-// D = A B, both from shared memory, rows of 64 entries: steps 32 bytes apart,
-// the second half of K HALF_B further.
-__device__ __forceinline__ void ck_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t bar)
-{
-    static_assert(HALF_B == 16384, "the descriptors' steps below");
-    asm volatile(
-        "{\n\t.reg .pred q, f, t;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "setp.ne.b32 t, 1, 0;\n\tsetp.ne.b32 f, 0, 0;\n\t"
-        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\tadd.s64 a4, %1, 1024;\n\t"
-        "add.s64 a5, %1, 1026;\n\tadd.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
-        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\tadd.s64 b4, %2, 1024;\n\t"
-        "add.s64 b5, %2, 1026;\n\tadd.s64 b6, %2, 1028;\n\tadd.s64 b7, %2, 1030;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, t;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(bar)
-        : "memory");
-}
-
 // D (+)= A B with A (16-bit pairs) in tensor memory, 8 columns a step, and B's
 // rows (keys) 2048 bytes a step; acc 0: D is overwritten.
 __device__ __forceinline__ void ck_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t bar)
@@ -214,16 +173,6 @@ __device__ __forceinline__ void ck_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         : "memory");
 }
 
-// An arrival on `bar` when every product that this warp's elected thread issued
-// is done.
-__device__ __forceinline__ void ck_commit(uint64_t *bar)
-{
-    asm volatile(
-        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-        : "memory");
-}
-
 __device__ __forceinline__ void ck_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
@@ -235,14 +184,6 @@ __device__ __forceinline__ void ck_st16(uint32_t taddr, const uint32_t (&r)[16])
 }
 
 __device__ __forceinline__ void ck_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// L2 policy of the cache's tiles: other CTAs read them too.
-__device__ __forceinline__ uint64_t ck_policy()
-{
-    uint64_t pol;
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-    return pol;
-}
 
 // 16 consecutive fp32 columns of this thread's tensor-memory lane.
 __device__ __forceinline__ void ck_ld16(uint32_t taddr, uint32_t (&r)[16])
@@ -261,25 +202,8 @@ __device__ __forceinline__ void ck_hold16(uint32_t (&r)[16])
     for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[j])::"memory");
 }
 
-__device__ __forceinline__ float2 ck_f2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
-
-// A word with its n lowest bits set (none for n <= 0, all from 32 on).
-__device__ __forceinline__ uint32_t ck_below(int n) { return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u; }
-
 template <int N> __device__ __forceinline__ void ck_reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void ck_reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-template <class T> __device__ __forceinline__ uint32_t ck_pack(float a, float b);
-template <> __device__ __forceinline__ uint32_t ck_pack<__half>(float a, float b)
-{
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-template <> __device__ __forceinline__ uint32_t ck_pack<__nv_bfloat16>(float a, float b)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 
 // 2^e twice in fp16, -15 <= e <= 0; of a key that nothing sees e may be any number.
 __device__ __forceinline__ uint32_t ck_factor(int e)
@@ -775,7 +699,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     // bit c of word b: key k0 + 32 b + c is seen (words, not
                     // comparisons key by key: those became branches)
                     const int hi = (TREE ? mine ? r.e.p0 : k0 : pos + 1) - k0, lo = low - k0, sink = view.sink - k0;
-                    const uint32_t *draft = TREE ? p.masks + (size_t)(r.e.tok0 + (mine ? tok : 0)) * PG_TREE_WORDS : nullptr;
+                    [[maybe_unused]] const uint32_t *draft = TREE ? p.masks + (size_t)(r.e.tok0 + (mine ? tok : 0)) * PG_TREE_WORDS : nullptr;
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         uint32_t see = ck_below(hi - 32 * b) & (~ck_below(lo - 32 * b) | ck_below(sink - 32 * b));
@@ -905,6 +829,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 const bool split = z.t0 > 0 || z.tn < z.e.ntiles;
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 float *part = p.large.part + (size_t)(2 * blockIdx.x + (z.first && z.t0 > 0 ? 0 : 1)) * (PG_LROWS * PG_PART);
+                if (MODE == PG_WEIGH && mine && !split)
+                    p.lse[(size_t)(z.e.tok0 + tok) * p.Hq + (size_t)z.h * p.GQ + row % p.GQ] = pg_lse(m, l);
                 if (split && mine) {
                     part[128 * w + row] = m;
                     part[PG_LROWS + 128 * w + row] = l;
@@ -1119,7 +1045,9 @@ cudaError_t launch_chunk(const PagedAttendParams &p, cudaStream_t stream)
 
 template <class T, bool Q8> cudaError_t dispatch_chunk(const PagedAttendParams &p, cudaStream_t stream)
 {
-    return p.parents ? launch_chunk<T, Q8, PG_TREE>(p, stream) : launch_chunk<T, Q8, PG_CHAIN>(p, stream);
+    return p.parents ? launch_chunk<T, Q8, PG_TREE>(p, stream)
+           : p.lse   ? launch_chunk<T, Q8, PG_WEIGH>(p, stream)
+                     : launch_chunk<T, Q8, PG_CHAIN>(p, stream);
 }
 
 }  // namespace
@@ -1132,11 +1060,7 @@ cudaError_t launch_paged_large(const PagedAttendParams &p0, int q_dtype, int cac
     const uint32_t box = 1u << p.c.page_shift < (unsigned)PG_TILE ? 1u << p.c.page_shift : (unsigned)PG_TILE;
     if (!encode_tmap_pages(&p.tmk, p.c.k, rows, q8 ? 1 : 2, box) || !encode_tmap_pages(&p.tmv, p.c.v, rows, q8 ? 1 : 2, box))
         return cudaErrorInvalidValue;
-    // queries: boxes of 64 columns, the heads of a kv head, the tokens of a tile
-    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.Hq, (uint64_t)p.T};
-    const uint64_t strides[2] = {(uint64_t)(p.Hq > 1 ? p.qsh : D) * 2, (uint64_t)(p.T > 1 ? p.qst : (long long)p.Hq * D) * 2};
-    const uint32_t qbox[3] = {64u, (uint32_t)p.GQ, (uint32_t)(128 / p.GQ)};
-    if (!encode_tmap_f16(&p.tmq, p.q, 3, dims, strides, qbox, true, true)) return cudaErrorInvalidValue;
+    if (!encode_tmap_queries(&p.tmq, p)) return cudaErrorInvalidValue;
     if (q_dtype == VQ_F16) return q8 ? dispatch_chunk<__half, true>(p, stream) : dispatch_chunk<__half, false>(p, stream);
     return q8 ? dispatch_chunk<__nv_bfloat16, true>(p, stream) : dispatch_chunk<__nv_bfloat16, false>(p, stream);
 }

@@ -61,6 +61,10 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// log2 of a row's sum of 2^score out of the maximum and the sum below it; +inf where
+// the row sees nothing, so that no weight comes of it.
+__device__ __forceinline__ float pg_lse(float m, float l) { return l > 0.0f ? m + log2f(l) : __builtin_huge_valf(); }
+
 // One lane of the (whole, converged) warp, the same each time.  Copies and
 // products issued under it keep their operands in uniform registers.
 __device__ __forceinline__ bool elect_lane()
@@ -117,10 +121,70 @@ __device__ __forceinline__ PgEntry pg_entry(const PgEntry *e)
     return r;
 }
 
+// Tokens [i tq, (i + 1) tq) of sequence b's n new ones as an entry.
+__device__ __forceinline__ PgEntry make_entry(const PagedAttendParams &p, int b, int start, int n, int len, int tq, int i)
+{
+    PgEntry e;
+    e.b = b;
+    e.tok0 = start + i * tq;
+    e.nt = min(tq, n - i * tq);
+    e.p0 = len - n + (p.parents ? 0 : i * tq);
+    e.hi = max(0, len - n + i * tq + e.nt);
+    const int lo = p.window > 0 ? max(0, e.p0 - p.window + 1) : 0;
+    const int sink = p.window > 0 ? min(p.sinks, e.hi) : 0;
+    const int th = (e.hi + PG_TILE - 1) / PG_TILE, st = (sink + PG_TILE - 1) / PG_TILE, tl = lo / PG_TILE;
+    // leading tiles that reach the window make one run with it
+    e.nsink = st >= tl ? 0 : st;
+    e.tl = st >= tl ? 0 : tl;
+    e.ntiles = max(1, e.nsink + th - e.tl);
+    return e;
+}
+
+// The first query token, the number of new tokens and the length of sequence b,
+// within the buffers whatever the numbers given, and whether they make sense:
+// SEQ_BACK, the next sequence starts before this one; SEQ_BAD, tokens outside the
+// queries, more than max_q, or of a sequence longer than its pages, a tree that is
+// longer than its sequence.
+enum { SEQ_OK = 0, SEQ_BAD = 1, SEQ_BACK = 2 };
+__device__ __forceinline__ int sequence(const PagedAttendParams &p, int b, int &start, int &n, int &len)
+{
+    const int cap = (int)min((long long)p.max_pages << p.c.page_shift, 0x7fffffffLL);
+    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
+    start = min(max(c0, 0), p.T);
+    n = min(max(c1, start), p.T) - start;
+    const int given = __ldg(p.lens + b);
+    len = min(max(given, 0), cap);
+    const bool bad = n > p.max_q || c0 < 0 || c1 > p.T || (n > 0 && len != given) || (p.parents && n > len);
+    n = min(n, p.max_q);
+    return c1 < c0 ? SEQ_BACK : bad ? SEQ_BAD : SEQ_OK;
+}
+
+// Even shares of the units: the first `rem` of `g` CTAs take one more than q.
+struct Shares {
+    long long q;
+    int g, rem;
+    __device__ __forceinline__ void set(long long total, int G)
+    {
+        g = (int)min((long long)G, total);
+        q = g ? total / g : 0;
+        rem = g ? (int)(total - q * g) : 0;
+    }
+    __device__ __forceinline__ long long first(int c) const { return q * c + min(c, rem); }
+};
+
 // first key of tile t of an entry
 __device__ __forceinline__ int pg_tile_key(const PgEntry &e, int t)
 {
     return (t < e.nsink ? t : e.tl + (t - e.nsink)) * PG_TILE;
+}
+
+// (WEIGH) the first of n new tokens that counts, and the parts that a chunk's query
+// tiles are shared out in: of 8 tiles or more.
+__device__ __forceinline__ int pg_counted(const PagedAttendParams &p, int n) { return p.observe > 0 ? max(0, n - p.observe) : 0; }
+__device__ __forceinline__ int pg_parts(const PagedAttendParams &p, int n)
+{
+    const int tqt = 128 / p.GQ, tiles = (n - pg_counted(p, n) + tqt - 1) / tqt;
+    return min(max(tiles / 8, 1), PG_PARTS);
 }
 
 // One CTA's share as runs of tiles of one item each.

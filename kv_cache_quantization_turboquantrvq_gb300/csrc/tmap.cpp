@@ -103,4 +103,12 @@ bool encode_tmap_halves(CUtensorMap *map, const void *base, uint64_t rows, uint3
     return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_queries(CUtensorMap *map, const PagedAttendParams &p)
+{
+    const uint64_t dims[3] = {128, (uint64_t)p.Hq, (uint64_t)p.T};
+    const uint64_t strides[2] = {(uint64_t)(p.Hq > 1 ? p.qsh : 128) * 2, (uint64_t)(p.T > 1 ? p.qst : (long long)p.Hq * 128) * 2};
+    const uint32_t box[3] = {64u, (uint32_t)p.GQ, (uint32_t)(128 / p.GQ)};
+    return encode_tmap_f16(map, p.q, 3, dims, strides, box, true, true);
+}
+
 }  // namespace vq

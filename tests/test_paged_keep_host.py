@@ -1,5 +1,7 @@
-"""Refusals of the calls that keep a part of a paged cache (host arithmetic, no
+"""Refusals of tree attention and of the calls that keep a part of a paged cache (host arithmetic, no
 GPU: fake addresses that never reach a device)."""
+import ctypes
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -123,4 +125,101 @@ def test_bound_refusals(binding, call, name, bad):  # noqa: F811
 def test_numbers_past_32_bits_are_refused(binding, name, value):  # noqa: F811
     with pytest.raises(ValueError):
         _bind_select(binding, **{name: value})
+    assert not binding.log
+
+
+# ------------------------------------------------- trees and weights: refusals
+
+def _tree(api, parents=A + 8 * M, max_q=4, wb=1 << 30, q=A, qst=1024, T=8, Hq=8, out=A + 6 * M, ws=A + 7 * M, window=0, scale=0.1):
+    return api.lib().vq_paged_attend_tree(P(q), qst, 128, 0, P(A + M), P(A + 2 * M), P(0), P(0), 0, 4, 2, 16, 128, P(A + 3 * M), 3,
+                                          P(A + 4 * M), P(A + 5 * M), P(parents), T, 2, Hq, max_q, window, 0,
+                                          ctypes.c_float(scale), P(out), P(ws), wb, None)
+
+
+def test_tree_refusals(api):  # noqa: F811
+    assert _tree(api, max_q=257) == api.VQ_ERR_UNSUPPORTED
+    assert _tree(api, Hq=34) == api.VQ_ERR_UNSUPPORTED
+    assert _tree(api, max_q=0) == api.VQ_ERR_INVALID_ARG
+    assert _tree(api, parents=0) == api.VQ_ERR_INVALID_ARG
+    assert _tree(api, window=-1) == api.VQ_ERR_INVALID_ARG
+    assert _tree(api, scale=float("inf")) == api.VQ_ERR_INVALID_ARG
+    assert _tree(api, wb=1000) == api.VQ_ERR_INVALID_ARG
+    assert _tree(api, parents=A + 8 * M + 2) == api.VQ_ERR_MISALIGNED
+    assert _tree(api, qst=1028) == api.VQ_ERR_MISALIGNED
+    assert _tree(api, parents=A + 6 * M) == api.VQ_ERR_ALIASING        # over the output
+    assert _tree(api, parents=A + 7 * M + 64) == api.VQ_ERR_ALIASING   # in the workspace
+    assert _tree(api, T=0, parents=0) == api.VQ_OK
+    n = ctypes.c_size_t(0)
+    f = api.lib().vq_paged_attend_tree_workspace
+    assert f(8, 2, 8, 2, 4, None) == api.VQ_ERR_INVALID_ARG
+    assert f(8, 2, 8, 2, 257, ctypes.byref(n)) == api.VQ_ERR_UNSUPPORTED
+    assert f(8, 2, 7, 2, 4, ctypes.byref(n)) == api.VQ_ERR_INVALID_ARG
+    assert f(800, 2, 8, 2, 256, ctypes.byref(n)) == api.VQ_OK and n.value >= 800 * 36
+
+
+def _weigh(api, w=A + 8 * M, observe=0, decay=1.0, max_q=4, wb=1 << 29, q=A, T=8, Hq=8, out=A + 6 * M, ws=A + 7 * M, mp=3, PS=16):
+    return api.lib().vq_paged_attend_weigh(P(q), 1024, 128, 0, P(A + M), P(A + 2 * M), P(0), P(0), 0, 4, 2, PS, 128, P(A + 3 * M), mp,
+                                           P(A + 4 * M), P(A + 5 * M), T, 2, Hq, max_q, 0, 0, ctypes.c_float(0.1), P(w), observe,
+                                           ctypes.c_float(decay), P(out), P(ws), wb, None)
+
+
+def test_weigh_refusals(api):  # noqa: F811
+    assert _weigh(api, observe=-1) == api.VQ_ERR_INVALID_ARG
+    for decay in (-0.1, 1.1, float("nan"), float("inf")):
+        assert _weigh(api, decay=decay) == api.VQ_ERR_INVALID_ARG
+    assert _weigh(api, w=0) == api.VQ_ERR_INVALID_ARG
+    assert _weigh(api, wb=1000) == api.VQ_ERR_INVALID_ARG
+    assert _weigh(api, w=A + 8 * M + 8) == api.VQ_ERR_MISALIGNED
+    assert _weigh(api, w=A + 6 * M) == api.VQ_ERR_ALIASING             # over the output
+    assert _weigh(api, w=A + 7 * M + 64) == api.VQ_ERR_ALIASING        # in the workspace
+    assert _weigh(api, w=A + M) == api.VQ_ERR_ALIASING                 # over the keys
+    assert _weigh(api, w=A + 5 * M) == api.VQ_ERR_ALIASING             # over the lengths
+    assert _weigh(api, T=0, w=0) == api.VQ_OK
+    n = ctypes.c_size_t(0)
+    f = api.lib().vq_paged_attend_weigh_workspace
+    assert f(8, 2, 8, 2, 4, 3, 16, None) == api.VQ_ERR_INVALID_ARG
+    assert f(8, 2, 8, 2, 4, -1, 16, ctypes.byref(n)) == api.VQ_ERR_INVALID_ARG
+    assert f(8, 2, 8, 2, 4, 3, 24, ctypes.byref(n)) == api.VQ_ERR_UNSUPPORTED
+    assert f(8, 2, 8, 2, 4, (1 << 26) + 1, 16, ctypes.byref(n)) == api.VQ_ERR_UNSUPPORTED
+    assert f(1 << 20, 1 << 20, 64, 64, 1, 1 << 22, 256, ctypes.byref(n)) == api.VQ_ERR_UNSUPPORTED  # a petabyte
+    assert f(64, 64, 32, 8, 1, 1024, 16, ctypes.byref(n)) == api.VQ_OK and n.value >= 64 * 8 * 4 * 16384 * 4
+
+
+def _bind_tree(b, device=0, **kw):
+    a = dict(q=Fake((5, 8, 128), torch.float16, device), cache=_cache(device), block_table=Fake((2, 3), I32, device),
+             cu_q=Fake((3,), I32, device), lens=Fake((2,), I32, device), parents=Fake((5,), I32, device), scale=0.1, max_q=4,
+             out=Fake((5, 8, 128), torch.float16, device), workspace=Fake((1 << 20,), torch.uint8, device), stream=64)
+    a.update(kw)
+    return b.vq_paged_attend_tree(**a)
+
+
+def _bind_weigh(b, device=0, **kw):
+    a = dict(q=Fake((5, 8, 128), torch.float16, device), cache=_cache(device), block_table=Fake((2, 3), I32, device),
+             cu_q=Fake((3,), I32, device), lens=Fake((2,), I32, device), weights=Fake((4, 2, 16), F32, device), scale=0.1, max_q=4,
+             out=Fake((5, 8, 128), torch.float16, device), workspace=Fake((1 << 20,), torch.uint8, device), stream=64)
+    a.update(kw)
+    return b.vq_paged_attend_weigh(**a)
+
+
+def test_bound_attention_reaches_the_library_on_its_gpu(binding, monkeypatch):  # noqa: F811
+    _bind_tree(binding, device=1)
+    _bind_weigh(binding, device=1)
+    monkeypatch.setattr(binding, "_empty", lambda shape, dtype, device, stream, returned=True: Fake((shape,), dtype, 1))
+    _bind_tree(binding, device=1, workspace=None)
+    _bind_weigh(binding, device=1, workspace=None)
+    _bind_weigh(binding, device=1, workspace=None, block_table=Fake((2, 5), I32, 1))
+    assert [(n, d) for n, d, _ in binding.log] == [(x, 1) for x in (
+        "vq_paged_attend_tree", "vq_paged_attend_weigh", "vq_paged_attend_tree_workspace", "vq_paged_attend_tree",
+        "vq_paged_attend_weigh_workspace", "vq_paged_attend_weigh", "vq_paged_attend_weigh_workspace", "vq_paged_attend_weigh")]
+
+
+@pytest.mark.parametrize("call,name,bad", [
+    (_bind_tree, "parents", Fake((4,), I32)), (_bind_tree, "parents", Fake((5,), torch.int64)), (_bind_tree, "parents", Fake((5,), I32, 1)),
+    (_bind_tree, "parents", Fake((5,), I32, contiguous=False)), (_bind_tree, "lens", Fake((2,), I32, 1)),
+    (_bind_weigh, "weights", Fake((4, 2, 16), F32, 1)), (_bind_weigh, "weights", Fake((4, 2, 32), F32)),
+    (_bind_weigh, "weights", Fake((4, 2, 16), torch.float16)), (_bind_weigh, "weights", Fake((4, 2, 16), F32, contiguous=False)),
+    (_bind_weigh, "cache", _cache(1)), (_bind_weigh, "observe", 1 << 31), (_bind_weigh, "max_q", 1 << 32), (_bind_tree, "window", 1 << 40)])
+def test_bound_attention_refusals(binding, call, name, bad):  # noqa: F811
+    with pytest.raises(ValueError):
+        call(binding, **{name: bad})
     assert not binding.log
