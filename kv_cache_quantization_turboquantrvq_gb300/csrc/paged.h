@@ -128,7 +128,7 @@ struct PagedAttendParams {
     uint32_t *masks;             // [T][PG_TREE_WORDS] trees in the large class: the new tokens that a token sees
     int32_t *depth;              // [T] and its number of ancestors
     // (WEIGH)
-    float *lse;                  // [T, Hq] log2 of each query row's sum of 2^score; null: no weights
+    float *lse;                  // [Hkv, T, GQ] log2 of each query row's sum of 2^score; null: no weights
     float *scores;               // [B, Hkv, srows, keys] scores of single tokens, or sums over parts of a chunk
     int srows, keys;
     long long *wbase;            // [B + 1] units of weighing before each sequence of the large class
@@ -136,7 +136,7 @@ struct PagedAttendParams {
     float decay;
     int observe;                 // new tokens of a sequence that count, the last ones; 0: all
 };
-constexpr int PG_PARTS = 4;      // parts that a chunk's query rows are weighed in, at most
+constexpr int PG_PARTS = 8;      // parts that a chunk's query rows are weighed in, at most
 constexpr int PG_SROWS = 16;     // rows of a small item
 constexpr int PG_LROWS = 256;    // rows of a large item (two tensor-memory tiles)
 // Floats of a row's partial result.  A slot holds the rows' maxima, then their

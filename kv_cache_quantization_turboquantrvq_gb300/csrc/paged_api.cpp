@@ -77,7 +77,7 @@ vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, PgMode mode, lon
     if (mode == PG_WEIGH) {
         // scores of the small kernel's rows, or the parts of a chunk's sums
         pl.srows = small ? (pl.small_rows < max_q * gq ? pl.small_rows : max_q * gq) : 0;
-        if (large && pl.srows < 2 * PG_PARTS) pl.srows = 2 * PG_PARTS;
+        if (large && pl.srows < PG_PARTS) pl.srows = PG_PARTS;
         if ((double)B * Hkv * pl.srows * (double)keys >= 1e15) return VQ_ERR_UNSUPPORTED;
         pl.wbase = pl.bytes;
         pl.lse = pl.wbase + (large ? up((size_t)(B + 1) * 8) : 0);

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
         }
     }
     __syncthreads();
-    if (p.wbase) {  // the units of weighing: a key tile, a head, a part of the query rows
+    if (p.wbase) {  // the units of weighing: two key tiles, a head, a part of the query rows
         long long units = 0;
         bool back = false;
         for (int b0 = 0; b0 < p.B && !back; b0 += PLAN_THREADS) {
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) paged_plan_kernel(const __gri
             const int sense = b < p.B ? sequence(p, b, start, n, len) : SEQ_OK;
             back = __syncthreads_or(sense == SEQ_BACK);
             long long u = 0, all;
-            if (n * p.GQ > p.small_rows) u = (long long)make_entry(p, b, start, n, len, n, 0).ntiles * p.Hkv * pg_parts(p, n);
+            if (n * p.GQ > p.small_rows) u = (long long)((make_entry(p, b, start, n, len, n, 0).ntiles + 1) / 2) * p.Hkv * pg_parts(p, n);
             const long long before = block_scan(u, ws, all);
             if (b < p.B) p.wbase[b] = units + before;
             units += all;
@@ -362,7 +362,7 @@ __device__ __forceinline__ void merge_rows(const PagedAttendParams &p, const flo
         if (rr >= tqt * p.GQ || tok >= at.z) continue;  // a row of no token
         const float inv = L[j] > 0.0f ? 1.0f / L[j] : 0.0f;
         const size_t qrow = (size_t)(at.y + tok) * p.Hq + (size_t)at.w * p.GQ + g;
-        if (p.lse && lane == 0) p.lse[qrow] = pg_lse(M[j], L[j]);
+        if (p.lse && lane == 0) p.lse[pg_lse_at(p, at.y + tok, at.w, g)] = pg_lse(M[j], L[j]);
         T *dst = static_cast<T *>(p.out) + qrow * D + 4 * lane;
         *reinterpret_cast<uint2 *>(dst) =
             pack4<T>(make_float4(O[j].x * inv, O[j].y * inv, O[j].z * inv, O[j].w * inv));
@@ -374,6 +374,7 @@ __device__ __forceinline__ void merge_rows(const PagedAttendParams &p, const flo
 template <class T>
 __global__ void __launch_bounds__(32 * CB_WARPS, 4) paged_combine_kernel(const __grid_constant__ PagedAttendParams p)
 {
+    pg_go();
     pg_wait();
     if (p.planned && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.planned = 0;  // (a graph repeats the call's number)
     const int first_small = p.large.cap ? PG_LROWS / (CB_WARPS * CB_LARGE) : 0;
@@ -1064,7 +1065,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                 const float inv = Ls > 0.0f ? 1.0f / Ls : 0.0f;
                 x.x *= inv; x.y *= inv; x.z *= inv; x.w *= inv;
                 const size_t qrow = (size_t)(e.tok0 + row / p.GQ) * p.Hq + (size_t)r.h * p.GQ + row % p.GQ;
-                if (MODE == PG_WEIGH && lane == 0) p.lse[qrow] = pg_lse(M, Ls);
+                if (MODE == PG_WEIGH && lane == 0) p.lse[pg_lse_at(p, e.tok0 + row / p.GQ, r.h, row % p.GQ)] = pg_lse(M, Ls);
                 T *dst = static_cast<T *>(p.out) + qrow * D + 4 * lane;
                 *reinterpret_cast<uint2 *>(dst) = pack4<T>(x);
             }

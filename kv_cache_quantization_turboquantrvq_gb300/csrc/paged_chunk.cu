@@ -830,7 +830,7 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 float *part = p.large.part + (size_t)(2 * blockIdx.x + (z.first && z.t0 > 0 ? 0 : 1)) * (PG_LROWS * PG_PART);
                 if (MODE == PG_WEIGH && mine && !split)
-                    p.lse[(size_t)(z.e.tok0 + tok) * p.Hq + (size_t)z.h * p.GQ + row % p.GQ] = pg_lse(m, l);
+                    p.lse[pg_lse_at(p, z.e.tok0 + tok, z.h, row % p.GQ)] = pg_lse(m, l);
                 if (split && mine) {
                     part[128 * w + row] = m;
                     part[PG_LROWS + 128 * w + row] = l;

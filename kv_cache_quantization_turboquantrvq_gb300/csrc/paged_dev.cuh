@@ -65,6 +65,13 @@ __device__ __forceinline__ float ex2(float x)
 // the row sees nothing, so that no weight comes of it.
 __device__ __forceinline__ float pg_lse(float m, float l) { return l > 0.0f ? m + log2f(l) : __builtin_huge_valf(); }
 
+// Where the row of query head g of kv head h's has it: a chunk's rows of one kv head
+// lie one after another.
+__device__ __forceinline__ size_t pg_lse_at(const PagedAttendParams &p, int tok, int h, int g)
+{
+    return ((size_t)h * p.T + tok) * p.GQ + g;
+}
+
 // One lane of the (whole, converged) warp, the same each time.  Copies and
 // products issued under it keep their operands in uniform registers.
 __device__ __forceinline__ bool elect_lane()

@@ -32,21 +32,23 @@ constexpr float NEG_INF = -__builtin_huge_valf();
 // The keys are the 128 rows of the product and stay, the query rows are its columns
 // and stream through: a thread of the softmax warps holds a key and adds up its row
 // of 2^(score - lse) over the columns, without a word to any other thread, and the
-// sums need no atomics: a unit is one key tile of one head against one of at most
+// sums need no atomics: a unit is two key tiles of one head against one of at most
 // PG_PARTS parts of the query tiles, and writes its own numbers, which the update
-// below adds in their order.
+// below adds in their order.  (One key tile a unit, its query tiles taken by the two
+// groups in turn, asked L2 for 32 KB a product, which takes 512 cycles: as much as
+// the SM's path to L2 carries.)
 //
 // Roles (one CTA per SM): a warp that finds the CTA's units and copies keys and
-// queries by TMA, one that issues the products into a ring of four score tiles in
-// tensor memory, one that brings the rows' -lse, two groups of 4 softmax warps that
-// take the tiles of a unit in turn; with an 8-bit cache four more warps turn a
-// unit's codes into operands of the queries' type (exact in both).  The keys'
-// exponents act on the scores, a factor a thread.
+// queries by TMA, one that issues the products, two that bring the rows' -lse, two
+// groups of 4 softmax warps, one for each key tile, with two score tiles each in
+// tensor memory; with an 8-bit cache four more warps turn a unit's codes into
+// operands of the queries' type (exact in both).  The keys' exponents act on the
+// scores, a factor a thread.
 template <bool Q8> struct WgShape {
-    static constexpr int KST = 2;              // key tiles
-    static constexpr int QST = Q8 ? 3 : 4;     // query tiles
+    static constexpr int KST = Q8 ? 3 : 4;     // key tiles
+    static constexpr int QST = 3;              // query tiles
     static constexpr int RAW = Q8 ? 2 : 0;     // tiles of codes
-    static constexpr int LST = 4;              // rows' -lse
+    static constexpr int LST = 2;              // rows' -lse
     static constexpr int IST = 4;              // units known ahead
     static constexpr int CONV = Q8 ? 4 : 0;
     static constexpr int WARPS = 12 + CONV;
@@ -79,11 +81,11 @@ template <bool Q8> struct WgBars {
         }
         for (int s = 0; s < C::LST; ++s) {
             mbar_init(&l_full[s], 1);
-            mbar_init(&l_empty[s], 4);
+            mbar_init(&l_empty[s], 8);
         }
         for (int s = 0; s < C::IST; ++s) {
             mbar_init(&i_full[s], 1);
-            mbar_init(&i_empty[s], 2 + 8 + C::CONV);
+            mbar_init(&i_empty[s], 3 + 8 + C::CONV);
         }
         for (int s = 0; s < 4; ++s) {
             mbar_init(&s_full[s], 1);
@@ -100,7 +102,7 @@ template <bool Q8> struct WgBars {
 // One unit, as the roles read it from shared memory.
 struct WgItem {
     int b, h, part;      // b < 0: no more units
-    int k0, hi;          // its first key, and the end of the sequence's
+    int k0, k1, hi;      // its tiles' first keys (the second -1: there is none), and the end of the sequence's
     int start, n, base;  // the sequence's first query token, new tokens, keys before them
     int i0, qa, qz;      // the first token that counts; query tiles [qa, qz) of those
 };
@@ -123,16 +125,18 @@ __device__ __forceinline__ WgItem wg_find(const PagedAttendParams &p, long long 
     w.part = (int)(r % parts);
     r /= parts;
     w.h = (int)(r % p.Hkv);
-    w.k0 = pg_tile_key(e, (int)(r / p.Hkv));
+    const int t = 2 * (int)(r / p.Hkv);
+    w.k0 = pg_tile_key(e, t);
+    w.k1 = t + 1 < e.ntiles ? pg_tile_key(e, t + 1) : -1;
     w.hi = e.hi;
     w.base = e.p0;
     w.i0 = pg_counted(p, w.n);
-    // the tokens that may see a key of the tile: at or behind its first one, and with
-    // a window not too far behind its last
-    const int sink = p.window > 0 ? min(p.sinks, e.hi) : 0;
+    // the tokens that may see a key of the tiles: at or behind the first one, and with
+    // a window not too far behind the last
+    const int sink = p.window > 0 ? min(p.sinks, e.hi) : 0, z1 = max(w.k0, w.k1);
     const long long ia = max(w.i0, w.k0 - w.base);
     long long iz = w.n;
-    if (p.window > 0 && w.k0 >= sink) iz = min(iz, (long long)w.k0 - w.base + PG_TILE - 1 + p.window);
+    if (p.window > 0 && w.k0 >= sink) iz = min(iz, (long long)z1 - w.base + PG_TILE - 1 + p.window);
     int qa = 0, cnt = 0;
     if (ia < iz) {
         qa = (int)((ia - w.i0) / tqt);
@@ -246,39 +250,42 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
             items.step();
             if (!more) break;
             if (w.qa >= w.qz) continue;
-            int row = rows_all;
-            if (lane < nbox) {
-                const int k = w.k0 + lane * box;
-                const int lp = k >> p.c.page_shift;
-                const int page = k < w.hi && lp < p.max_pages ? __ldg(p.table + (long long)w.b * p.max_pages + lp) : -1;
-                // (a page that is not there was reported by the attention; its keys are not weighed)
-                if (page >= 0 && page < p.c.num_pages)
-                    row = ((page * p.c.Hkv + w.h) << p.c.page_shift) + (k & ((1 << p.c.page_shift) - 1));
-            }
-            uint64_t *full;
-            if constexpr (Q8) {
-                await(&bar.raw_empty[raw.s], raw.par ^ 1u);
-                if (!ok) break;
-                full = &bar.raw_full[raw.s];
-                if (elect_lane()) mbar_arrive_expect_tx(full, RAW_B);
-                __syncwarp();
-                if (lane < nbox) tma_load_2d(sraw + raw.s * RAW_B + lane * box * 128, &p.tmk, 0, row, full, pol);
-                raw.step();
-            } else {
-                await(&bar.k_empty[ks.s], ks.par ^ 1u);
-                if (!ok) break;
-                full = &bar.k_full[ks.s];
-                if (elect_lane()) mbar_arrive_expect_tx(full, TILE_B);
-                __syncwarp();
+            for (int i = 0; i < (w.k1 < 0 ? 1 : 2); ++i) {
+                int row = rows_all;
                 if (lane < nbox) {
-                    unsigned char *dst = sk + ks.s * TILE_B + lane * box * 128;
-                    tma_load_2d(dst, &p.tmk, 0, row, full, pol);
-                    tma_load_2d(dst + HALF_B, &p.tmk, 64, row, full, pol);
+                    const int k = (i ? w.k1 : w.k0) + lane * box;
+                    const int lp = k >> p.c.page_shift;
+                    const int page = k < w.hi && lp < p.max_pages ? __ldg(p.table + (long long)w.b * p.max_pages + lp) : -1;
+                    // (a page that is not there was reported by the attention; its keys are not weighed)
+                    if (page >= 0 && page < p.c.num_pages)
+                        row = ((page * p.c.Hkv + w.h) << p.c.page_shift) + (k & ((1 << p.c.page_shift) - 1));
                 }
-                ks.step();
+                uint64_t *full;
+                if constexpr (Q8) {
+                    await(&bar.raw_empty[raw.s], raw.par ^ 1u);
+                    if (!ok) break;
+                    full = &bar.raw_full[raw.s];
+                    if (elect_lane()) mbar_arrive_expect_tx(full, RAW_B);
+                    __syncwarp();
+                    if (lane < nbox) tma_load_2d(sraw + raw.s * RAW_B + lane * box * 128, &p.tmk, 0, row, full, pol);
+                    raw.step();
+                } else {
+                    await(&bar.k_empty[ks.s], ks.par ^ 1u);
+                    if (!ok) break;
+                    full = &bar.k_full[ks.s];
+                    if (elect_lane()) mbar_arrive_expect_tx(full, TILE_B);
+                    __syncwarp();
+                    if (lane < nbox) {
+                        unsigned char *dst = sk + ks.s * TILE_B + lane * box * 128;
+                        tma_load_2d(dst, &p.tmk, 0, row, full, pol);
+                        tma_load_2d(dst + HALF_B, &p.tmk, 64, row, full, pol);
+                    }
+                    ks.step();
+                }
+                ++keys;
+                __syncwarp();
             }
-            ++keys;
-            __syncwarp();
+            if (!ok) break;
             for (int q = w.qa; q < w.qz; ++q) {
                 await(&bar.q_empty[qs.s], qs.par ^ 1u);
                 if (!ok) break;
@@ -317,47 +324,66 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
         WgItem w;
         while (next(w)) {
             if (w.qa >= w.qz) continue;
+            const int two = w.k1 < 0 ? 1 : 2;
+            PgRing<C::KST> k2 = ks;
+            if (two == 2) k2.step();
             await(&bar.k_full[ks.s], ks.par);
-            for (int j = 0; j < w.qz - w.qa && ok; ++j) {
-                const int g = j & 1, slot = 2 * g + (int)(done[g] & 1u);
+            await(&bar.k_full[k2.s], k2.par);
+            for (int j = w.qa; j < w.qz && ok; ++j) {
                 await(&bar.q_full[qs.s], qs.par);
-                await(&bar.s_empty[slot], ((done[g] >> 1) & 1u) ^ 1u);
+                for (int g = 0; g < two; ++g) {
+                    const int slot = 2 * g + (int)(done[g] & 1u);
+                    await(&bar.s_empty[slot], ((done[g] >> 1) & 1u) ^ 1u);
+                    if (!ok) break;
+                    qt_fence_after();
+                    ck_mma_ss(tm + 128 * slot, dk + (g ? k2.s : ks.s) * (TILE_B >> 4), dq + qs.s * (TILE_B >> 4), ID,
+                              smem_u32(&bar.s_full[slot]));
+                    ++done[g];
+                }
                 if (!ok) break;
-                qt_fence_after();
-                ck_mma_ss(tm + 128 * slot, dk + ks.s * (TILE_B >> 4), dq + qs.s * (TILE_B >> 4), ID, smem_u32(&bar.s_full[slot]));
                 ck_commit(&bar.q_empty[qs.s]);
                 qs.step();
-                ++done[g];
             }
             if (!ok) break;
             ck_commit(&bar.k_empty[ks.s]);
+            if (two == 2) ck_commit(&bar.k_empty[k2.s]);
+            ks = k2;
             ks.step();
         }
         // every product is done before shared and tensor memory are given up
         ck_commit(bar.drain);
         (void)mbar_wait_bounded(bar.drain, 0u);
         __syncwarp();
-    } else if (warp == 2) {
-        // ------------------------------------------------ the rows' -lse
-        PgRing<C::LST> ls;
+    } else if (warp < 4) {
+        // ------------------------------------------------ the rows' -lse: two warps in turn
+        uint32_t run = 0u;  // tiles of all units so far
         WgItem w;
         while (next(w)) {
-            for (int q = w.qa; q < w.qz; ++q) {
-                float x[4];
+            const int cnt = max(w.qz - w.qa, 0), j0 = (int)((run ^ (uint32_t)warp) & 1u);  // its first tile of the unit
+            const float *rows = p.lse + ((size_t)w.h * p.T + w.start + w.i0) * p.GQ;
+            auto load = [&](int j, float (&x)[4]) {  // (the next tile's while this one waits for its place)
+                const int c0 = (w.qa + j) * cols, end = j < cnt ? min(cols, (w.n - w.i0) * p.GQ - c0) : 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = 32 * i + lane, tok = w.i0 + q * tqt + c / p.GQ;
-                    x[i] = c < cols && tok < w.n ? -p.lse[(size_t)(w.start + tok) * p.Hq + (size_t)w.h * p.GQ + c % p.GQ] : NEG_INF;
-                }
-                await(&bar.l_empty[ls.s], ls.par ^ 1u);
+                for (int i = 0; i < 4; ++i) x[i] = 32 * i + lane < end ? -rows[c0 + 32 * i + lane] : NEG_INF;
+            };
+            float x[4], y[4];
+            load(j0, x);
+            for (int j = j0; j < cnt; j += 2) {
+                load(j + 2, y);
+                const uint32_t at = run + (uint32_t)j;
+                const int ls = (int)(at % C::LST);
+                await(&bar.l_empty[ls], ((at / C::LST) & 1u) ^ 1u);
                 if (!ok) break;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) slse[ls.s * 128 + 32 * i + lane] = x[i];
+                for (int i = 0; i < 4; ++i) {
+                    slse[ls * 128 + 32 * i + lane] = x[i];
+                    x[i] = y[i];
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.l_full[ls.s]);
-                ls.step();
+                if (lane == 0) mbar_arrive(&bar.l_full[ls]);
             }
             if (!ok) break;
+            run += (uint32_t)cnt;
         }
     } else if (warp >= 4 && warp < 12) {
         // ------------------------------------------------ a thread per key
@@ -366,11 +392,12 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
         uint32_t run = 0u, done = 0u;  // tiles of all units so far, of this group
         WgItem w;
         while (next(w)) {
-            const int k = w.k0 + row, cnt = w.qz - w.qa;
+            const bool any = g == 0 || w.k1 >= 0;  // this group has a key tile
+            const int kt = g ? w.k1 : w.k0, k = kt + row, cnt = w.qz - w.qa;
             float mul = p.qscale;
             if constexpr (Q8) {
                 const int lp = k >> p.c.page_shift;
-                const int page = k < w.hi && lp < p.max_pages ? __ldg(p.table + (long long)w.b * p.max_pages + lp) : -1;
+                const int page = any && k < w.hi && lp < p.max_pages ? __ldg(p.table + (long long)w.b * p.max_pages + lp) : -1;
                 if (page >= 0 && page < p.c.num_pages) {
                     const int at = ((page * p.c.Hkv + w.h) << p.c.page_shift) + (k & ((1 << p.c.page_shift) - 1));
                     mul *= pow2f(min(max((int)__ldg(p.c.ke + at) - 127, -126), 127));
@@ -381,14 +408,17 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
             const int ia = k - w.base;
             const int iz = p.window > 0 && k >= sink ? (int)min((long long)w.n, (long long)ia + p.window) : w.n;
             // whole tiles: all of their tokens see all keys
-            const int first = w.k0 + PG_TILE - 1 - w.base;
-            const long long last = p.window > 0 && w.k0 + PG_TILE > sink ? (long long)w.k0 - w.base + p.window : w.n;
-            float2 sum = make_float2(0.0f, 0.0f);
-            for (int j = g; j < cnt; j += 2) {
+            const int first = kt + PG_TILE - 1 - w.base;
+            const long long last = p.window > 0 && kt + PG_TILE > sink ? (long long)kt - w.base + p.window : w.n;
+            float2 sum[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.0f, 0.0f);
+            for (int j = 0; j < cnt; ++j) {
                 const uint32_t at = run + (uint32_t)j;
                 const int slot = 2 * g + (int)(done & 1u), ls = (int)(at % C::LST);
                 const int it0 = w.i0 + (w.qa + j) * tqt;
                 const bool whole = it0 >= first && it0 + tqt <= w.n && it0 + tqt <= last;
+                const bool none = it0 + tqt <= kt - w.base;  // (all before the tile)
                 uint32_t see[4];
                 if (!whole) {
                     const int lo = min(max(ia - it0, 0), 128) * p.GQ, hi = min(max(min(iz, w.n) - it0, 0), 128) * p.GQ;
@@ -396,51 +426,58 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
                     for (int b = 0; b < 4; ++b) see[b] = ck_below(hi - 32 * b) & ~ck_below(lo - 32 * b);
                 }
                 await(&bar.l_full[ls], (at / C::LST) & 1u);
-                await(&bar.s_full[slot], (done >> 1) & 1u);
+                if (any) await(&bar.s_full[slot], (done >> 1) & 1u);
                 if (!ok) break;
-                ++done;
-                qt_fence_after();
-                const float2 mul2 = make_float2(mul, mul);
+                if (any) ++done;
+                if (any && !none) {
+                    qt_fence_after();
+                    const float2 mul2 = make_float2(mul, mul);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t x[2][32];
-                    qt_ld32(lanes + 128 * slot + 64 * half, x[0]);
-                    qt_ld32(lanes + 128 * slot + 64 * half + 32, x[1]);
-                    qt_wait_ld();
-                    qt_hold(x[0]);
-                    qt_hold(x[1]);
-                    if (half == 1) {
-                        qt_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.s_empty[slot]);
-                    }
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t x[2][32];
+                        qt_ld32(lanes + 128 * slot + 64 * half, x[0]);
+                        qt_ld32(lanes + 128 * slot + 64 * half + 32, x[1]);
+                        qt_wait_ld();
+                        qt_hold(x[0]);
+                        qt_hold(x[1]);
+                        if (half == 1) {
+                            qt_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar.s_empty[slot]);
+                        }
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const float4 *nl = reinterpret_cast<const float4 *>(slse + ls * 128 + 64 * half + 32 * b);
+                        for (int b = 0; b < 2; ++b) {
+                            const float4 *nl = reinterpret_cast<const float4 *>(slse + ls * 128 + 64 * half + 32 * b);
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            const float4 n4 = nl[c >> 2];
-                            float2 t0 = __ffma2_rn(ck_f2(x[b][c], x[b][c + 1]), mul2, make_float2(n4.x, n4.y));
-                            float2 t1 = __ffma2_rn(ck_f2(x[b][c + 2], x[b][c + 3]), mul2, make_float2(n4.z, n4.w));
-                            if (!whole) {
-                                const uint32_t s = see[2 * half + b] >> c;
-                                t0.x = s & 1u ? t0.x : NEG_INF;
-                                t0.y = s & 2u ? t0.y : NEG_INF;
-                                t1.x = s & 4u ? t1.x : NEG_INF;
-                                t1.y = s & 8u ? t1.y : NEG_INF;
+                            for (int c = 0; c < 32; c += 4) {
+                                const float4 n4 = nl[c >> 2];
+                                float2 t0 = __ffma2_rn(ck_f2(x[b][c], x[b][c + 1]), mul2, make_float2(n4.x, n4.y));
+                                float2 t1 = __ffma2_rn(ck_f2(x[b][c + 2], x[b][c + 3]), mul2, make_float2(n4.z, n4.w));
+                                if (!whole) {
+                                    const uint32_t s = see[2 * half + b] >> c;
+                                    t0.x = s & 1u ? t0.x : NEG_INF;
+                                    t0.y = s & 2u ? t0.y : NEG_INF;
+                                    t1.x = s & 4u ? t1.x : NEG_INF;
+                                    t1.y = s & 8u ? t1.y : NEG_INF;
+                                }
+                                float2 &s0 = sum[(c >> 1) & 2], &s1 = sum[((c >> 1) & 2) + 1];
+                                s0 = __fadd2_rn(s0, make_float2(ex2(t0.x), ex2(t0.y)));
+                                s1 = __fadd2_rn(s1, make_float2(ex2(t1.x), ex2(t1.y)));
                             }
-                            sum = __fadd2_rn(sum, make_float2(ex2(t0.x), ex2(t0.y)));
-                            sum = __fadd2_rn(sum, make_float2(ex2(t1.x), ex2(t1.y)));
                         }
                     }
+                } else if (any) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.s_empty[slot]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.l_empty[ls]);
             }
             if (!ok) break;
             run += (uint32_t)max(cnt, 0);
-            if (k < p.keys)
-                p.scores[(((size_t)w.b * p.Hkv + w.h) * p.srows + 2 * w.part + g) * p.keys + k] = sum.x + sum.y;
+            if (any && k < p.keys)
+                p.scores[(((size_t)w.b * p.Hkv + w.h) * p.srows + w.part) * p.keys + k] =
+                    ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
         }
     } else if constexpr (Q8) {
         if (warp >= 12) {
@@ -451,35 +488,38 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
             WgItem w;
             while (next(w)) {
                 if (w.qa >= w.qz) continue;
-                await(&bar.raw_full[raw.s], raw.par);
-                await(&bar.k_empty[ks.s], ks.par ^ 1u);
-                if (!ok) break;
-                // eight lanes a row; the upper four store their second half first, so
-                // that the eight fill all banks
-                const unsigned char *src = sraw + raw.s * RAW_B + swz128(j >> 3, j & 7);
-                unsigned char *dst = sk + ks.s * TILE_B + ((j & 7) >> 2) * HALF_B;
-                const bool odd = (j & 4) != 0;
-                const uint32_t d0 = swz128(j >> 3, 2 * (j & 3) + odd), d1 = swz128(j >> 3, 2 * (j & 3) + !odd);
+                for (int t = 0; t < (w.k1 < 0 ? 1 : 2); ++t) {
+                    await(&bar.raw_full[raw.s], raw.par);
+                    await(&bar.k_empty[ks.s], ks.par ^ 1u);
+                    if (!ok) break;
+                    // eight lanes a row; the upper four store their second half first, so
+                    // that the eight fill all banks
+                    const unsigned char *src = sraw + raw.s * RAW_B + swz128(j >> 3, j & 7);
+                    unsigned char *dst = sk + ks.s * TILE_B + ((j & 7) >> 2) * HALF_B;
+                    const bool odd = (j & 4) != 0;
+                    const uint32_t d0 = swz128(j >> 3, 2 * (j & 3) + odd), d1 = swz128(j >> 3, 2 * (j & 3) + !odd);
 #pragma unroll 2
-                for (int i = 0; i < PG_TILE / (4 * C::CONV); ++i) {
-                    const int step = 128 * 4 * C::CONV * i;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(src + step);
-                    uint4 x0, x1;
-                    wg_operand<T>(odd ? v.z : v.x, x0.x, x0.y);
-                    wg_operand<T>(odd ? v.w : v.y, x0.z, x0.w);
-                    wg_operand<T>(odd ? v.x : v.z, x1.x, x1.y);
-                    wg_operand<T>(odd ? v.y : v.w, x1.z, x1.w);
-                    *reinterpret_cast<uint4 *>(dst + d0 + step) = x0;
-                    *reinterpret_cast<uint4 *>(dst + d1 + step) = x1;
+                    for (int i = 0; i < PG_TILE / (4 * C::CONV); ++i) {
+                        const int step = 128 * 4 * C::CONV * i;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(src + step);
+                        uint4 x0, x1;
+                        wg_operand<T>(odd ? v.z : v.x, x0.x, x0.y);
+                        wg_operand<T>(odd ? v.w : v.y, x0.z, x0.w);
+                        wg_operand<T>(odd ? v.x : v.z, x1.x, x1.y);
+                        wg_operand<T>(odd ? v.y : v.w, x1.z, x1.w);
+                        *reinterpret_cast<uint4 *>(dst + d0 + step) = x0;
+                        *reinterpret_cast<uint4 *>(dst + d1 + step) = x1;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bar.raw_empty[raw.s]);
+                        mbar_arrive(&bar.k_full[ks.s]);
+                    }
+                    raw.step();
+                    ks.step();
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bar.raw_empty[raw.s]);
-                    mbar_arrive(&bar.k_full[ks.s]);
-                }
-                raw.step();
-                ks.step();
+                if (!ok) break;
             }
         }
     }
@@ -511,7 +551,6 @@ __global__ void __launch_bounds__(UPD_THREADS) paged_weigh_update_kernel(const _
 {
     __shared__ long long sums[UPD_THREADS / 32];
     __shared__ int at[3];
-    pg_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto groups = [&](int b, PgEntry &e, int &start, int &n) -> int {
         int len = 0;
@@ -541,7 +580,10 @@ __global__ void __launch_bounds__(UPD_THREADS) paged_weigh_update_kernel(const _
     }
     Shares sh;
     sh.set(total, gridDim.x);
-    if ((int)blockIdx.x >= sh.g) return;
+    if ((int)blockIdx.x >= sh.g) {
+        pg_wait();
+        return;
+    }
     const long long u0 = sh.first(blockIdx.x);
     if (u0 >= before && u0 < before + mine) {  // one thread: the share starts in its sequences
         for (int b = b0; b < b1; ++b) {
@@ -557,6 +599,7 @@ __global__ void __launch_bounds__(UPD_THREADS) paged_weigh_update_kernel(const _
         }
     }
     __syncthreads();
+    pg_wait();  // (for the scores and sums; the shares come of the call's inputs)
     int b = at[0], h = at[1], g = at[2];
     int left = (int)(sh.first(blockIdx.x + 1) - u0), gs = groups(b, e, start, n);
     for (; left > 0; --left) {
@@ -570,7 +613,7 @@ __global__ void __launch_bounds__(UPD_THREADS) paged_weigh_update_kernel(const _
                 float *wp = p.weights + (((size_t)page * p.c.Hkv + h) << p.c.page_shift) + (k & ((1 << p.c.page_shift) - 1));
                 const float4 old = *reinterpret_cast<const float4 *>(wp);
                 const bool large = n * p.GQ > p.small_rows;
-                const int r0 = large ? 0 : pg_counted(p, n) * p.GQ, r1 = large ? 2 * pg_parts(p, n) : n * p.GQ;
+                const int r0 = large ? 0 : pg_counted(p, n) * p.GQ, r1 = large ? pg_parts(p, n) : n * p.GQ;
                 const float *src = p.scores + ((size_t)b * p.Hkv + h) * p.srows * p.keys + k;
                 float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 for (int r = r0; r < r1; r += 4) {
@@ -580,7 +623,7 @@ __global__ void __launch_bounds__(UPD_THREADS) paged_weigh_update_kernel(const _
                     for (int i = 0; i < 4; ++i) {
                         const int q = min(r + i, r1 - 1);
                         s[i] = __ldcs(reinterpret_cast<const float4 *>(src + (size_t)q * p.keys));
-                        l[i] = large ? 0.0f : p.lse[(size_t)(start + q / p.GQ) * p.Hq + (size_t)h * p.GQ + q % p.GQ];
+                        l[i] = large ? 0.0f : p.lse[((size_t)h * p.T + start) * p.GQ + q];
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
