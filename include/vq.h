@@ -488,8 +488,8 @@ vq_status vq_paged_attend_tree(const void *q, long long q_stride_t, long long q_
 /*
  * Keeping a part of a sequence: the softmax weight that tokens got so far says
  * which of them can go.
- *   weights [num_pages, Hkv, page_size] fp32, device: a number for every place of
- *     the cache.  Two sequences that share a page cannot have weights of their own
+ *   weights [num_pages, Hkv, page_size] fp32, device, 16-byte aligned: a number for
+ *     every place of the cache.  Two sequences that share a page cannot have weights of their own
  *     in it, and must not be moved.
  *
  * vq_paged_attend_weigh - vq_paged_attend, which also adds up the weights: for every
@@ -501,7 +501,6 @@ vq_status vq_paged_attend_tree(const void *q, long long q_stride_t, long long q_
  * weights of tokens that no new token sees stay as they are.  0 <= decay <= 1.
  * The sums are held in 32 bits, in an order that is the same on every call.  Where
  * sequences of one call share a page, its weights are unspecified.
- *   weights: 16-byte aligned.
  *   workspace: of vq_paged_attend_weigh_workspace, which also depends on the block
  *     table's width: besides the attention's own, 4 bytes for every query row, and
  *     for every place of the block table and kv head 4 bytes for each query row of

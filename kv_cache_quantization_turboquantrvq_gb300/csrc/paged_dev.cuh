@@ -186,12 +186,12 @@ __device__ __forceinline__ int pg_tile_key(const PgEntry &e, int t)
 }
 
 // (WEIGH) the first of n new tokens that counts, and the parts that a chunk's query
-// tiles are shared out in: of 8 tiles or more.
+// tiles are shared out in: of 16 tiles or more.
 __device__ __forceinline__ int pg_counted(const PagedAttendParams &p, int n) { return p.observe > 0 ? max(0, n - p.observe) : 0; }
 __device__ __forceinline__ int pg_parts(const PagedAttendParams &p, int n)
 {
     const int tqt = 128 / p.GQ, tiles = (n - pg_counted(p, n) + tqt - 1) / tqt;
-    return min(max(tiles / 8, 1), PG_PARTS);
+    return min(max(tiles / 16, 1), PG_PARTS);
 }
 
 // One CTA's share as runs of tiles of one item each.

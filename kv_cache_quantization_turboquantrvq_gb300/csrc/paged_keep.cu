@@ -30,10 +30,12 @@ namespace cg = cooperative_groups;
 // the other passes, so each is read once.
 //
 // A cluster of CTAs takes one row (sequence, head), each CTA a contiguous part of
-// it; they read one another's histograms and counts.
+// it; they read one another's histograms and counts.  Weights are handled four
+// tokens at a time (a page holds whole fours), those of tokens outside the middle
+// as 0, which no weight is.
 constexpr int SEL_THREADS = 512, SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_BINS = 2048;
-constexpr int SEL_MAX = 40960;  // weights of a CTA that stay in shared memory
+constexpr int SEL_MAX = 10240;  // fours of a CTA that stay in shared memory
 static_assert(SEL_BINS == 4 * SEL_THREADS, "four bins a thread");
 
 struct SelShared {
@@ -43,7 +45,7 @@ struct SelShared {
     unsigned bin, above, inside;     // the digit's bin, what lies above it, what lies in it
 };
 
-// The order of weights as integers: 0 and -0 alike, NaN largest.
+// The order of weights as integers, none of them 0: 0 and -0 alike, NaN largest.
 __device__ __forceinline__ unsigned sel_key(float x)
 {
     if (x != x) return 0xffffffffu;
@@ -55,7 +57,8 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
 {
     extern __shared__ __align__(16) unsigned char sel_raw[];
     SelShared &s = *reinterpret_cast<SelShared *>(sel_raw);
-    unsigned *keys = reinterpret_cast<unsigned *>(sel_raw + sizeof(SelShared));  // [p.held]
+    static_assert(sizeof(SelShared) % 4 == 0, "fours behind it");
+    uint4 *keys = reinterpret_cast<uint4 *>(sel_raw + (sizeof(SelShared) + 15) / 16 * 16);  // [p.held]
     const cg::cluster_group cluster = cg::this_cluster();
     const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int row = (int)blockIdx.x / cs, b = row / p.Hkv, h = row - b * p.Hkv;
@@ -74,38 +77,65 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
     }
     for (int i = me; i < p.sinks; i += all) keep[i] = i;
     for (int i = me; i < p.recent; i += all) keep[p.budget - p.recent + i] = L - p.recent + i;
-    const int mid = L - p.sinks - p.recent;
+    const int m0 = p.sinks, m1 = L - p.recent;  // the middle
     int need = p.budget - p.sinks - p.recent;
     if (need == 0) return;
+    auto together = [&] {  // a barrier of the cluster
+        if (cs == 1) __syncthreads();
+        else cluster.sync();
+    };
 
-    const int seg = (mid + cs - 1) / cs, s0 = min(rank * seg, mid), n = min(seg, mid - s0);  // this CTA's part
-    const int t0 = p.sinks + s0;                                                             // its first token
+    const int fours = (m1 + 3) / 4 - m0 / 4, seg = (fours + cs - 1) / cs, s0 = min(rank * seg, fours);
+    const int n = min(seg, fours - s0), t0 = 4 * (m0 / 4 + s0);  // this CTA's fours, and its first token
     const int32_t *table = p.table + (size_t)b * p.max_pages;
-    auto fetch = [&](int i) -> unsigned {  // of token t0 + i
-        const int t = t0 + i, page = __ldg(table + (t >> p.page_shift));
+    const int in_page = (1 << p.page_shift) - 1;
+    auto keys_of = [&](int t, float4 x) {
+        uint4 k = make_uint4(sel_key(x.x), sel_key(x.y), sel_key(x.z), sel_key(x.w));
+        if (t < m0 || t + 4 > m1) {
+            k.x = t >= m0 && t < m1 ? k.x : 0u;
+            k.y = t + 1 >= m0 && t + 1 < m1 ? k.y : 0u;
+            k.z = t + 2 >= m0 && t + 2 < m1 ? k.z : 0u;
+            k.w = t + 3 >= m0 && t + 3 < m1 ? k.w : 0u;
+        }
+        return k;
+    };
+    // where the weights of tokens t .. t + 3 lie; null, reported: in no page
+    auto where = [&](int t) -> const float4 * {
+        const int page = __ldg(table + (t >> p.page_shift));
         if (page < 0 || page >= p.num_pages) {
             atomicOr(&g_pe_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
-            return 0u;
+            return nullptr;
         }
-        return sel_key(__ldg(p.weights + (((size_t)page * p.Hkv + h) << p.page_shift) + (t & ((1 << p.page_shift) - 1))));
+        return reinterpret_cast<const float4 *>(p.weights + ((((size_t)page * p.Hkv + h) << p.page_shift) + (t & in_page)));
     };
-    auto key = [&](int i) { return i < p.held ? keys[i] : fetch(i); };
+    const float lowest = -__builtin_huge_valf();
+    auto four = [&](int i) -> uint4 {
+        if (i < p.held) return keys[i];
+        const float4 *at = where(t0 + 4 * i);
+        return keys_of(t0 + 4 * i, at ? __ldg(at) : make_float4(lowest, lowest, lowest, lowest));
+    };
 
     for (int i = tid; i < SEL_BINS; i += SEL_THREADS) s.hist[0][i] = 0u;
     __syncthreads();
-    for (int i0 = 0; i0 < n; i0 += 8 * SEL_THREADS) {
-        unsigned k[8];
+    constexpr int U = 4;
+    for (int i0 = tid; i0 < n; i0 += U * SEL_THREADS) {
+        float4 x[U];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int i = i0 + u * SEL_THREADS + tid;
-            k[u] = i < n ? fetch(i) : 0u;
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * SEL_THREADS;
+            const float4 *at = i < n ? where(t0 + 4 * i) : nullptr;
+            x[u] = at ? __ldg(at) : make_float4(lowest, lowest, lowest, lowest);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int i = i0 + u * SEL_THREADS + tid;
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * SEL_THREADS;
             if (i >= n) break;
-            if (i < p.held) keys[i] = k[u];
-            atomicAdd(&s.hist[0][k[u] >> 21], 1u);
+            const uint4 k = keys_of(t0 + 4 * i, x[u]);
+            if (i < p.held) keys[i] = k;
+            if (k.x) atomicAdd(&s.hist[0][k.x >> 21], 1u);
+            if (k.y) atomicAdd(&s.hist[0][k.y >> 21], 1u);
+            if (k.z) atomicAdd(&s.hist[0][k.z >> 21], 1u);
+            if (k.w) atomicAdd(&s.hist[0][k.w >> 21], 1u);
         }
     }
     unsigned lo = 0u, hi = 0xffffffffu;  // weights above hi are taken, of [lo, hi] the first `need`
@@ -114,24 +144,32 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const int buf = pass & 1;
         if (pass > 0) {
+            auto count = [&](unsigned k) {
+                if (k >= lo && k <= hi && k != 0u) atomicAdd(&s.hist[buf][(k - lo) >> shift], 1u);
+            };
             for (int i = tid; i < n; i += SEL_THREADS) {
-                const unsigned k = key(i);
-                if (k >= lo && k <= hi) atomicAdd(&s.hist[buf][(k - lo) >> shift], 1u);
+                const uint4 k = four(i);
+                count(k.x);
+                count(k.y);
+                count(k.z);
+                count(k.w);
             }
         }
-        cluster.sync();
+        together();
         // four bins a thread, from the top: bins 2044 - 4 tid ...
         const int b0 = SEL_BINS - 4 - 4 * tid;
-        uint4 c = make_uint4(0u, 0u, 0u, 0u);
-        for (int r = 0; r < cs; ++r) {
-            const unsigned *other = cluster.map_shared_rank(s.hist[buf], r);
-            const uint4 x = *reinterpret_cast<const uint4 *>(other + b0);
-            c.x += x.x; c.y += x.y; c.z += x.z; c.w += x.w;
+        uint4 c = *reinterpret_cast<const uint4 *>(s.hist[buf] + b0);
+        if (cs > 1) {
+            c = make_uint4(0u, 0u, 0u, 0u);
+            for (int r = 0; r < cs; ++r) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(s.hist[buf], r) + b0);
+                c.x += x.x; c.y += x.y; c.z += x.z; c.w += x.w;
+            }
         }
         // (the other buffer's readers have passed the barrier above)
         for (int i = tid; i < SEL_BINS; i += SEL_THREADS) s.hist[buf ^ 1][i] = 0u;
-        const unsigned four = c.x + c.y + c.z + c.w;
-        unsigned x = four;
+        const unsigned sum = c.x + c.y + c.z + c.w;
+        unsigned x = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const unsigned y = __shfl_up_sync(FULL_MASK, x, d);
@@ -139,15 +177,20 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
         }
         if (lane == 31) s.warp_sum[warp] = x;
         __syncthreads();
-        unsigned above = x - four;
-        for (int w = 0; w < warp; ++w) above += s.warp_sum[w];
-        if (above < (unsigned)need && above + four >= (unsigned)need) {  // one thread
+        unsigned above = x - sum;
+#pragma unroll
+        for (int w = 0; w < SEL_WARPS; ++w) above += w < warp ? s.warp_sum[w] : 0u;
+        if (above < (unsigned)need && above + sum >= (unsigned)need) {  // one thread
             const unsigned cc[4] = {c.w, c.z, c.y, c.x};
-            int i = 0;
-            while (above + cc[i] < (unsigned)need) above += cc[i++];
-            s.bin = (unsigned)(b0 + 3 - i);
+            int at = 3;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                if (at == 3 && above + cc[i] >= (unsigned)need) at = i;
+                if (at == 3) above += cc[i];
+            }
+            s.bin = (unsigned)(b0 + 3 - at);
             s.above = above;
-            s.inside = cc[i];
+            s.inside = at == 0 ? cc[0] : at == 1 ? cc[1] : at == 2 ? cc[2] : cc[3];
         }
         __syncthreads();
         need -= (int)s.above;
@@ -157,54 +200,76 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
         __syncthreads();
         if (done) break;
     }
+    lo = max(lo, 1u);
 
     // taken tokens of this CTA's part, warp by warp, then of all parts before
     const int per = ((n + SEL_WARPS - 1) / SEL_WARPS + 31) & ~31;
     const int w0 = min(warp * per, n), w1 = min(w0 + per, n);
+    auto over = [&](unsigned k) { return k > hi ? 1u : 0u; };
+    auto even = [&](unsigned k) { return k >= lo && k <= hi ? 1u : 0u; };
     unsigned gt = 0u, tie = 0u;
-    for (int i = w0; i < w1; i += 32) {
-        const unsigned k = i + lane < w1 ? key(i + lane) : 0u;
-        const bool in = i + lane < w1;
-        gt += __popc(__ballot_sync(FULL_MASK, in && k > hi));
-        tie += __popc(__ballot_sync(FULL_MASK, in && k >= lo && k <= hi));
+    for (int i = w0 + lane; i < w1; i += 32) {
+        const uint4 k = four(i);
+        gt += over(k.x) + over(k.y) + over(k.z) + over(k.w);
+        tie += even(k.x) + even(k.y) + even(k.z) + even(k.w);
     }
+    gt = __reduce_add_sync(FULL_MASK, gt);
+    tie = __reduce_add_sync(FULL_MASK, tie);
     if (lane == 0) {
         s.warp_gt[warp] = gt;
         s.warp_tie[warp] = tie;
     }
     __syncthreads();
-    if (tid == 0) {
-        unsigned g = 0u, t = 0u;
-        for (int w = 0; w < SEL_WARPS; ++w) {
-            g += s.warp_gt[w];
-            t += s.warp_tie[w];
-        }
-        s.gt = g;
-        s.tie = t;
-    }
-    cluster.sync();
     unsigned bg = 0u, bt = 0u;
-    for (int r = 0; r < rank; ++r) {
-        bg += *cluster.map_shared_rank(&s.gt, r);
-        bt += *cluster.map_shared_rank(&s.tie, r);
+    if (cs > 1) {
+        if (tid == 0) {
+            unsigned g = 0u, t = 0u;
+            for (int w = 0; w < SEL_WARPS; ++w) {
+                g += s.warp_gt[w];
+                t += s.warp_tie[w];
+            }
+            s.gt = g;
+            s.tie = t;
+        }
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {
+            bg += *cluster.map_shared_rank(&s.gt, r);
+            bt += *cluster.map_shared_rank(&s.tie, r);
+        }
     }
     for (int w = 0; w < warp; ++w) {
         bg += s.warp_gt[w];
         bt += s.warp_tie[w];
     }
-    const unsigned below = (1u << lane) - 1u;
+    int32_t *dst = keep + p.sinks;
     for (int i = w0; i < w1; i += 32) {
-        const bool in = i + lane < w1;
-        const unsigned k = in ? key(i + lane) : 0u;
-        const bool over = in && k > hi, eq = in && k >= lo && k <= hi;
-        const unsigned mg = __ballot_sync(FULL_MASK, over), mt = __ballot_sync(FULL_MASK, eq);
-        const unsigned ties = bt + __popc(mt & below);
-        if (over || (eq && ties < (unsigned)need))
-            keep[p.sinks + bg + __popc(mg & below) + min(ties, (unsigned)need)] = t0 + i + lane;
-        bg += __popc(mg);
-        bt += __popc(mt);
+        const uint4 k = i + lane < w1 ? four(i + lane) : make_uint4(0u, 0u, 0u, 0u);
+        // counts of both kinds in one number: at most 128 of each
+        const unsigned mine = (over(k.x) + over(k.y) + over(k.z) + over(k.w)) << 16 | (even(k.x) + even(k.y) + even(k.z) + even(k.w));
+        unsigned x = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned y = __shfl_up_sync(FULL_MASK, x, d);
+            if (lane >= d) x += y;
+        }
+        unsigned g = bg + ((x - mine) >> 16), t = bt + ((x - mine) & 0xffffu);
+        auto put = [&](unsigned kk, int j) {
+            const bool eq = even(kk) != 0u;
+            if (over(kk) || (eq && t < (unsigned)need)) dst[g + min(t, (unsigned)need)] = t0 + 4 * (i + lane) + j;
+            g += over(kk);
+            t += eq ? 1u : 0u;
+        };
+        if (mine) {
+            put(k.x, 0);
+            put(k.y, 1);
+            put(k.z, 2);
+            put(k.w, 3);
+        }
+        const unsigned total = __shfl_sync(FULL_MASK, x, 31);
+        bg += total >> 16;
+        bt += total & 0xffffu;
     }
-    cluster.sync();  // (the counts are read by others)
+    if (cs > 1) cluster.sync();  // (the counts are read by others)
 }
 
 // ------------------------------------------------------------- moving rows
@@ -213,13 +278,28 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
 // behind it, in place.  A cluster takes one row (sequence, head) in rounds of
 // MOVE_ROWS tokens a CTA: all tokens of a round are read before any is written,
 // and the places that a round writes lie before every token that a later round
-// reads.
-constexpr int MOVE_THREADS = 512, MOVE_R = 4, MOVE_ROWS = MOVE_THREADS / 16 * MOVE_R;
+// reads - so the next rounds' tokens are already on their way (asynchronous copies
+// to shared memory, where the lane that asked for them takes them) while this
+// round waits for the cluster and writes.  A row's list entry, its pages and its
+// data come one after another, each a round ahead of its use (all in the round of
+// the copy: evict_16x16k_bf16 177 us; without copies ahead 138).  Bound by HBM: a
+// row read and written.
+constexpr int MOVE_THREADS = 256, MOVE_R = 4, MOVE_ROWS = MOVE_THREADS / 16 * MOVE_R, MOVE_STAGES = 3;
+constexpr int MOVE_AHEAD = MOVE_STAGES - 1;  // rounds that are copied ahead
+constexpr int MOVE_SLOTS = 8;                // rounds whose rows are known
+
+template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+}
 
 template <class V>  // what each of 16 lanes moves of a row: uint4 of 16-bit entries, uint2 of codes
 __global__ void __launch_bounds__(MOVE_THREADS) paged_compact_kernel(const __grid_constant__ PagedCompactParams p)
 {
     constexpr bool Q8 = sizeof(V) == 8;
+    extern __shared__ __align__(16) unsigned char move_raw[];
+    __shared__ int2 s_rows[MOVE_SLOTS][MOVE_ROWS];  // of the pool: from, to; to -1: the row stays, or is left out
+    V *buf = reinterpret_cast<V *>(move_raw) + threadIdx.x;  // [stage][row of the lane][key, value], THREADS apart
     const cg::cluster_group cluster = cg::this_cluster();
     const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int row = (int)blockIdx.x / cs, b = row / p.c.Hkv, h = row - b * p.c.Hkv;
@@ -231,58 +311,107 @@ __global__ void __launch_bounds__(MOVE_THREADS) paged_compact_kernel(const __gri
     const bool inside = at >= 0 && at <= cap;
     if (!inside) n = 0;
     if ((given != n || !inside) && threadIdx.x == 0) atomicOr(&g_pe_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
-    auto place = [&](int t) -> long long {  // row of the pool, -1: no such page
-        const int page = __ldg(table + (t >> p.c.page_shift));
-        if (page < 0 || page >= p.c.num_pages) return -1;
-        return (((long long)page * p.c.Hkv + h) << p.c.page_shift) + (t & ((1 << p.c.page_shift) - 1));
+    const int step = cs * MOVE_ROWS, rounds = (n + step - 1) / step;
+    // The first threads find a row each, in three steps: its list entry (and the one
+    // before), the pages of both ends, its rows of the pool.
+    struct Entry { int t, before; };
+    struct Ends { int t, from, to; };  // t < 0: nothing to move
+    const int i0 = rank * MOVE_ROWS + (int)threadIdx.x;  // (of the first round)
+    auto entry = [&](int round) {
+        const int i = round * step + i0;
+        Entry e = {-1, -1};
+        if (round < rounds && i < n) {
+            e.t = __ldg(keep + i);
+            e.before = i > 0 ? __ldg(keep + i - 1) : -1;
+        }
+        return e;
     };
-    for (int r0 = 0; r0 < n; r0 += cs * MOVE_ROWS) {
-        V k[MOVE_R], v[MOVE_R];
-        float w[MOVE_R];
-        uint8_t ke[MOVE_R], ve[MOVE_R];
-        long long src[MOVE_R], dst[MOVE_R];
-#pragma unroll
-        for (int j = 0; j < MOVE_R; ++j) {
-            const int i = r0 + rank * MOVE_ROWS + j * (MOVE_THREADS / 16) + group;
-            src[j] = -1;
-            if (i >= n) continue;
-            const int t = __ldg(keep + i), before = i > 0 ? __ldg(keep + i - 1) : -1;
-            if (t == at + i && t < cap) continue;  // stays where it is
-            if (t > before && t > at + i && t < cap) {
-                src[j] = place(t);
-                dst[j] = place(at + i);
-                if (dst[j] < 0) src[j] = -1;
-            }
-            if (src[j] < 0 && lane == 0) atomicOr(&g_pe_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+    auto ends = [&](int round, Entry e) {
+        const int i = round * step + i0;
+        Ends x = {-1, -1, -1};
+        if (round >= rounds || i >= n || (e.t == at + i && e.t < cap)) return x;  // (stays where it is)
+        if (e.t > e.before && e.t > at + i && e.t < cap) {
+            x.t = e.t;
+            x.from = __ldg(table + (e.t >> p.c.page_shift));
+            x.to = __ldg(table + ((at + i) >> p.c.page_shift));
+        } else {
+            atomicOr(&g_pe_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
         }
-#pragma unroll
-        for (int j = 0; j < MOVE_R; ++j) {
-            if (src[j] < 0) continue;
-            k[j] = __ldcs(static_cast<const V *>(p.c.k) + src[j] * 16 + lane);
-            v[j] = __ldcs(static_cast<const V *>(p.c.v) + src[j] * 16 + lane);
-            if (lane == 0) {
-                if constexpr (Q8) {
-                    ke[j] = p.c.ke[src[j]];
-                    ve[j] = p.c.ve[src[j]];
-                }
-                if (p.weights) w[j] = p.weights[src[j]];
-            }
+        return x;
+    };
+    auto rows = [&](int round, Ends x) {
+        int2 r = make_int2(-1, -1);
+        if (x.t >= 0) {
+            const int in = (1 << p.c.page_shift) - 1;
+            if (x.from >= 0 && x.from < p.c.num_pages && x.to >= 0 && x.to < p.c.num_pages)
+                r = make_int2(((x.from * p.c.Hkv + h) << p.c.page_shift) + (x.t & in),
+                              ((x.to * p.c.Hkv + h) << p.c.page_shift) + ((at + round * step + i0) & in));
+            else
+                atomicOr(&g_pe_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
         }
-        cluster.sync();
+        s_rows[round % MOVE_SLOTS][threadIdx.x] = r;
+    };
+    const bool finds = threadIdx.x < MOVE_ROWS;
+    Entry e = {-1, -1};
+    Ends x = {-1, -1, -1};
+    if (finds) {
+        Entry e3[MOVE_STAGES];
+        Ends x3[MOVE_STAGES];
+#pragma unroll
+        for (int s = 0; s < MOVE_STAGES; ++s) e3[s] = entry(s);
+        const Entry e4 = entry(MOVE_STAGES);
+        e = entry(MOVE_STAGES + 1);
+#pragma unroll
+        for (int s = 0; s < MOVE_STAGES; ++s) x3[s] = ends(s, e3[s]);
+        x = ends(MOVE_STAGES, e4);
+#pragma unroll
+        for (int s = 0; s < MOVE_STAGES; ++s) rows(s, x3[s]);
+    }
+    __syncthreads();
+    uint32_t part[MOVE_STAGES][MOVE_R];  // a row's exponents and weight, a lane each
+    auto fetch = [&](int round, uint32_t (&small)[MOVE_R], int stage) {
 #pragma unroll
         for (int j = 0; j < MOVE_R; ++j) {
-            if (src[j] < 0) continue;
-            static_cast<V *>(const_cast<void *>(p.c.k))[dst[j] * 16 + lane] = k[j];
-            static_cast<V *>(const_cast<void *>(p.c.v))[dst[j] * 16 + lane] = v[j];
-            if (lane == 0) {
-                if constexpr (Q8) {
-                    const_cast<uint8_t *>(p.c.ke)[dst[j]] = ke[j];
-                    const_cast<uint8_t *>(p.c.ve)[dst[j]] = ve[j];
-                }
-                if (p.weights) p.weights[dst[j]] = w[j];
+            const int2 r = s_rows[round % MOVE_SLOTS][j * (MOVE_THREADS / 16) + group];
+            if (r.y < 0) continue;
+            V *d = buf + (stage * MOVE_R + j) * 2 * MOVE_THREADS;
+            copy_async<sizeof(V)>(d, static_cast<const V *>(p.c.k) + (size_t)r.x * 16 + lane);
+            copy_async<sizeof(V)>(d + MOVE_THREADS, static_cast<const V *>(p.c.v) + (size_t)r.x * 16 + lane);
+            if (Q8 && lane < 2) small[j] = (lane ? p.c.ve : p.c.ke)[r.x];
+            if (p.weights && lane == 2) small[j] = __float_as_uint(p.weights[r.x]);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < MOVE_AHEAD; ++s) fetch(s, part[s], s);
+    for (int r0 = 0; r0 < rounds; r0 += MOVE_STAGES) {
+#pragma unroll
+        for (int s = 0; s < MOVE_STAGES; ++s) {
+            const int r = r0 + s;
+            if (r >= rounds) break;
+            fetch(r + MOVE_AHEAD, part[(s + MOVE_AHEAD) % MOVE_STAGES], (s + MOVE_AHEAD) % MOVE_STAGES);
+            // (rows of the round after that one, which the barrier below shows to all)
+            if (finds) {
+                rows(r + MOVE_STAGES, x);
+                x = ends(r + MOVE_STAGES + 1, e);
+                e = entry(r + MOVE_STAGES + 2);
+            }
+            asm volatile("cp.async.wait_group %0;" ::"n"(MOVE_AHEAD) : "memory");  // this round's rows are here
+            if (cs == 1) __syncthreads();
+            else cluster.sync();
+#pragma unroll
+            for (int j = 0; j < MOVE_R; ++j) {
+                const int to = s_rows[r % MOVE_SLOTS][j * (MOVE_THREADS / 16) + group].y;
+                if (to < 0) continue;
+                const V *d = buf + (s * MOVE_R + j) * 2 * MOVE_THREADS;
+                static_cast<V *>(const_cast<void *>(p.c.k))[(size_t)to * 16 + lane] = d[0];
+                static_cast<V *>(const_cast<void *>(p.c.v))[(size_t)to * 16 + lane] = d[MOVE_THREADS];
+                if (Q8 && lane < 2) const_cast<uint8_t *>(lane ? p.c.ve : p.c.ke)[to] = (uint8_t)part[s][j];
+                if (p.weights && lane == 2) p.weights[to] = __uint_as_float(part[s][j]);
             }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <class... A, class... B>
@@ -309,12 +438,15 @@ cudaError_t launch_paged_select(const PagedSelectParams &p0, cudaStream_t stream
     PagedSelectParams p = p0;
     const unsigned rows = (unsigned)p.B * (unsigned)p.Hkv;
     const long long cap = (long long)p.max_pages << p.page_shift;
+    // CTAs a row: as many as keep its weights at hand, and more where there are few rows
     int cs = 1;
-    while (cs < 8 && cap / cs > SEL_BINS && ((long long)rows * cs < sm_count() || cap / cs > SEL_MAX)) cs *= 2;
-    p.held = (int)(cap / cs + 1 < SEL_MAX ? cap / cs + 1 : SEL_MAX);
-    const size_t smem = sizeof(SelShared) + sizeof(unsigned) * (size_t)p.held;
+    while (cs < 8 && cap / cs > SEL_BINS && ((long long)rows * cs < sm_count() || cap / 4 / cs > SEL_MAX)) cs *= 2;
+    const long long held = (cap / 4 + 1 + cs) / cs;
+    p.held = (int)(held < SEL_MAX ? held : SEL_MAX);
+    constexpr size_t fixed = (sizeof(SelShared) + 15) / 16 * 16;
+    const size_t smem = fixed + sizeof(uint4) * (size_t)p.held;
     cudaError_t e = cudaFuncSetAttribute(paged_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(sizeof(SelShared) + sizeof(unsigned) * SEL_MAX));
+                                         (int)(fixed + sizeof(uint4) * SEL_MAX));
     if (e != cudaSuccess) return e;
     return launch_clusters(paged_select_kernel, rows, cs, SEL_THREADS, smem, stream, p);
 }
@@ -325,8 +457,12 @@ cudaError_t launch_paged_compact(const PagedCompactParams &p, int cache_dtype, c
     const int chunks = (p.K + MOVE_ROWS - 1) / MOVE_ROWS;
     int cs = 1;
     while (cs < 8 && cs < chunks) cs *= 2;
-    return launch_clusters(cache_dtype == VQ_E4M3 ? paged_compact_kernel<uint2> : paged_compact_kernel<uint4>, rows, cs,
-                           MOVE_THREADS, 0, stream, p);
+    const bool q8 = cache_dtype == VQ_E4M3;
+    const int smem = MOVE_STAGES * MOVE_R * 2 * MOVE_THREADS * (q8 ? (int)sizeof(uint2) : (int)sizeof(uint4));
+    auto kern = q8 ? paged_compact_kernel<uint2> : paged_compact_kernel<uint4>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(kern, rows, cs, MOVE_THREADS, smem, stream, p);
 }
 
 cudaError_t paged_keep_take_device_error(unsigned *bits, cudaStream_t stream)

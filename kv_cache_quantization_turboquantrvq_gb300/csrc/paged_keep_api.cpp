@@ -25,7 +25,7 @@ vq_status vq_paged_select(const float *weights, int num_pages, int Hkv, int page
     if ((long long)B * Hkv > (1LL << 24)) return VQ_ERR_UNSUPPORTED;
     if (B == 0) return VQ_OK;
     if (!lens || !counts || (budget > 0 && !keep) || (max_pages > 0 && (!weights || !block_table))) return VQ_ERR_INVALID_ARG;
-    if (!aligned(weights, 4) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(keep, 4) || !aligned(counts, 4))
+    if (!aligned(weights, 16) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(keep, 4) || !aligned(counts, 4))
         return VQ_ERR_MISALIGNED;
     const Span outs[2] = {{keep, (size_t)B * Hkv * budget * 4}, {counts, (size_t)B * 4}};
     const Span ins[3] = {{weights, (size_t)a.rows() * 4}, {block_table, (size_t)B * max_pages * 4}, {lens, (size_t)B * 4}};

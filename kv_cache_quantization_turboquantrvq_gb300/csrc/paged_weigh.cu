@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
                 const int it0 = w.i0 + (w.qa + j) * tqt;
                 const bool whole = it0 >= first && it0 + tqt <= w.n && it0 + tqt <= last;
                 const bool none = it0 + tqt <= kt - w.base;  // (all before the tile)
-                uint32_t see[4];
+                uint32_t see[4] = {0u, 0u, 0u, 0u};
                 if (!whole) {
                     const int lo = min(max(ia - it0, 0), 128) * p.GQ, hi = min(max(min(iz, w.n) - it0, 0), 128) * p.GQ;
 #pragma unroll
@@ -432,29 +432,26 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
                 if (any && !none) {
                     qt_fence_after();
                     const float2 mul2 = make_float2(mul, mul);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                    const uint32_t ts = lanes + 128 * slot;
+                    // 32 columns at a time, the next ones on their way from tensor memory
+                    auto tile = [&](auto masked) {
+                        constexpr bool MASKED = decltype(masked)::value;
                         uint32_t x[2][32];
-                        qt_ld32(lanes + 128 * slot + 64 * half, x[0]);
-                        qt_ld32(lanes + 128 * slot + 64 * half + 32, x[1]);
+                        qt_ld32(ts, x[0]);
                         qt_wait_ld();
                         qt_hold(x[0]);
-                        qt_hold(x[1]);
-                        if (half == 1) {
-                            qt_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&bar.s_empty[slot]);
-                        }
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const float4 *nl = reinterpret_cast<const float4 *>(slse + ls * 128 + 64 * half + 32 * b);
+                        for (int b = 0; b < 4; ++b) {
+                            if (b < 3) qt_ld32(ts + 32 * (b + 1), x[(b + 1) & 1]);
+                            const float4 *nl = reinterpret_cast<const float4 *>(slse + ls * 128 + 32 * b);
 #pragma unroll
                             for (int c = 0; c < 32; c += 4) {
+                                const uint32_t *y = x[b & 1] + c;
                                 const float4 n4 = nl[c >> 2];
-                                float2 t0 = __ffma2_rn(ck_f2(x[b][c], x[b][c + 1]), mul2, make_float2(n4.x, n4.y));
-                                float2 t1 = __ffma2_rn(ck_f2(x[b][c + 2], x[b][c + 3]), mul2, make_float2(n4.z, n4.w));
-                                if (!whole) {
-                                    const uint32_t s = see[2 * half + b] >> c;
+                                float2 t0 = __ffma2_rn(ck_f2(y[0], y[1]), mul2, make_float2(n4.x, n4.y));
+                                float2 t1 = __ffma2_rn(ck_f2(y[2], y[3]), mul2, make_float2(n4.z, n4.w));
+                                if constexpr (MASKED) {
+                                    const uint32_t s = see[b] >> c;
                                     t0.x = s & 1u ? t0.x : NEG_INF;
                                     t0.y = s & 2u ? t0.y : NEG_INF;
                                     t1.x = s & 4u ? t1.x : NEG_INF;
@@ -464,8 +461,19 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
                                 s0 = __fadd2_rn(s0, make_float2(ex2(t0.x), ex2(t0.y)));
                                 s1 = __fadd2_rn(s1, make_float2(ex2(t1.x), ex2(t1.y)));
                             }
+                            if (b < 3) {
+                                qt_wait_ld();
+                                qt_hold(x[(b + 1) & 1]);
+                            }
+                            if (b == 2) {  // the last columns have come: the score tile's place is free
+                                qt_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&bar.s_empty[slot]);
+                            }
                         }
-                    }
+                    };
+                    if (whole) tile(std::false_type());
+                    else tile(std::true_type());
                 } else if (any) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.s_empty[slot]);
