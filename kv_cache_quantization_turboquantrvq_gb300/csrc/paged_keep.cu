@@ -36,7 +36,8 @@ namespace cg = cooperative_groups;
 constexpr int SEL_THREADS = 512, SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_BINS = 2048;
 constexpr int SEL_MAX = 10240;  // fours of a CTA that stay in shared memory
-static_assert(SEL_BINS == 4 * SEL_THREADS, "four bins a thread");
+constexpr int SEL_OWN = SEL_BINS / SEL_THREADS;  // bins of a thread
+static_assert(SEL_OWN * SEL_THREADS == SEL_BINS && SEL_OWN % 4 == 0, "whole fours of bins a thread");
 
 struct SelShared {
     unsigned hist[2][SEL_BINS];
@@ -99,39 +100,35 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
         }
         return k;
     };
-    // where the weights of tokens t .. t + 3 lie; null, reported: in no page
-    auto where = [&](int t) -> const float4 * {
-        const int page = __ldg(table + (t >> p.page_shift));
-        if (page < 0 || page >= p.num_pages) {
-            atomicOr(&g_pe_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
-            return nullptr;
-        }
-        return reinterpret_cast<const float4 *>(p.weights + ((((size_t)page * p.Hkv + h) << p.page_shift) + (t & in_page)));
+    // the weights of tokens t .. t + 3, which lie in this page; the lowest: it is not in the pool
+    auto weights_of = [&](int t, int page) {
+        const float low = -__builtin_huge_valf();
+        if ((unsigned)page >= (unsigned)p.num_pages) return make_float4(low, low, low, low);
+        return __ldg(reinterpret_cast<const float4 *>(p.weights + ((((size_t)page * p.Hkv + h) << p.page_shift) + (t & in_page))));
     };
-    const float lowest = -__builtin_huge_valf();
     auto four = [&](int i) -> uint4 {
         if (i < p.held) return keys[i];
-        const float4 *at = where(t0 + 4 * i);
-        return keys_of(t0 + 4 * i, at ? __ldg(at) : make_float4(lowest, lowest, lowest, lowest));
+        const int t = t0 + 4 * i;
+        return keys_of(t, weights_of(t, __ldg(table + (t >> p.page_shift))));
     };
 
     for (int i = tid; i < SEL_BINS; i += SEL_THREADS) s.hist[0][i] = 0u;
     __syncthreads();
     constexpr int U = 4;
     for (int i0 = tid; i0 < n; i0 += U * SEL_THREADS) {
+        int page[U];
         float4 x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * SEL_THREADS;
-            const float4 *at = i < n ? where(t0 + 4 * i) : nullptr;
-            x[u] = at ? __ldg(at) : make_float4(lowest, lowest, lowest, lowest);
-        }
+        for (int u = 0; u < U; ++u) page[u] = __ldg(table + ((t0 + 4 * min(i0 + u * SEL_THREADS, n - 1)) >> p.page_shift));
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = weights_of(t0 + 4 * min(i0 + u * SEL_THREADS, n - 1), page[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = i0 + u * SEL_THREADS;
             if (i >= n) break;
             const uint4 k = keys_of(t0 + 4 * i, x[u]);
             if (i < p.held) keys[i] = k;
+            if ((unsigned)page[u] >= (unsigned)p.num_pages) atomicOr(&g_pe_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
             if (k.x) atomicAdd(&s.hist[0][k.x >> 21], 1u);
             if (k.y) atomicAdd(&s.hist[0][k.y >> 21], 1u);
             if (k.z) atomicAdd(&s.hist[0][k.z >> 21], 1u);
@@ -145,7 +142,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
         const int buf = pass & 1;
         if (pass > 0) {
             auto count = [&](unsigned k) {
-                if (k >= lo && k <= hi && k != 0u) atomicAdd(&s.hist[buf][(k - lo) >> shift], 1u);
+                if (k - lo <= hi - lo) atomicAdd(&s.hist[buf][(k - lo) >> shift], 1u);
             };
             for (int i = tid; i < n; i += SEL_THREADS) {
                 const uint4 k = four(i);
@@ -156,19 +153,24 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
             }
         }
         together();
-        // four bins a thread, from the top: bins 2044 - 4 tid ...
-        const int b0 = SEL_BINS - 4 - 4 * tid;
-        uint4 c = *reinterpret_cast<const uint4 *>(s.hist[buf] + b0);
-        if (cs > 1) {
-            c = make_uint4(0u, 0u, 0u, 0u);
-            for (int r = 0; r < cs; ++r) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(s.hist[buf], r) + b0);
-                c.x += x.x; c.y += x.y; c.z += x.z; c.w += x.w;
+        // a thread's bins, from the top
+        const int b0 = SEL_BINS - SEL_OWN * (tid + 1);
+        unsigned c[SEL_OWN];
+#pragma unroll
+        for (int i = 0; i < SEL_OWN; ++i) c[i] = 0u;
+        for (int r = 0; r < cs; ++r) {
+            const unsigned *other = cs == 1 ? s.hist[buf] : cluster.map_shared_rank(s.hist[buf], r);
+#pragma unroll
+            for (int i = 0; i < SEL_OWN; i += 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(other + b0 + i);
+                c[i] += x.x; c[i + 1] += x.y; c[i + 2] += x.z; c[i + 3] += x.w;
             }
         }
         // (the other buffer's readers have passed the barrier above)
-        for (int i = tid; i < SEL_BINS; i += SEL_THREADS) s.hist[buf ^ 1][i] = 0u;
-        const unsigned sum = c.x + c.y + c.z + c.w;
+        for (int i = tid; i < SEL_BINS / 4; i += SEL_THREADS) reinterpret_cast<uint4 *>(s.hist[buf ^ 1])[i] = make_uint4(0u, 0u, 0u, 0u);
+        unsigned sum = 0u;
+#pragma unroll
+        for (int i = 0; i < SEL_OWN; ++i) sum += c[i];
         unsigned x = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -177,36 +179,35 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
         }
         if (lane == 31) s.warp_sum[warp] = x;
         __syncthreads();
-        unsigned above = x - sum;
-#pragma unroll
-        for (int w = 0; w < SEL_WARPS; ++w) above += w < warp ? s.warp_sum[w] : 0u;
+        unsigned above = x - sum + __reduce_add_sync(FULL_MASK, lane < warp ? s.warp_sum[lane] : 0u);
         if (above < (unsigned)need && above + sum >= (unsigned)need) {  // one thread
-            const unsigned cc[4] = {c.w, c.z, c.y, c.x};
-            int at = 3;
+            bool found = false;
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                if (at == 3 && above + cc[i] >= (unsigned)need) at = i;
-                if (at == 3) above += cc[i];
+            for (int i = SEL_OWN - 1; i >= 0; --i) {
+                if (!found && above + c[i] >= (unsigned)need) {
+                    found = true;
+                    s.bin = (unsigned)(b0 + i);
+                    s.above = above;
+                    s.inside = c[i];
+                }
+                above += c[i];
             }
-            s.bin = (unsigned)(b0 + 3 - at);
-            s.above = above;
-            s.inside = at == 0 ? cc[0] : at == 1 ? cc[1] : at == 2 ? cc[2] : cc[3];
         }
         __syncthreads();
         need -= (int)s.above;
-        lo += s.bin << shift;
-        hi = lo + ((1u << shift) - 1u);
+        const unsigned from = lo + (s.bin << shift);
+        hi = min(hi, from + ((1u << shift) - 1u));
+        lo = max(from, 1u);  // (not the tokens outside the middle)
         const bool done = s.inside == (unsigned)need;
         __syncthreads();
         if (done) break;
     }
-    lo = max(lo, 1u);
 
     // taken tokens of this CTA's part, warp by warp, then of all parts before
     const int per = ((n + SEL_WARPS - 1) / SEL_WARPS + 31) & ~31;
     const int w0 = min(warp * per, n), w1 = min(w0 + per, n);
     auto over = [&](unsigned k) { return k > hi ? 1u : 0u; };
-    auto even = [&](unsigned k) { return k >= lo && k <= hi ? 1u : 0u; };
+    auto even = [&](unsigned k) { return k - lo <= hi - lo ? 1u : 0u; };
     unsigned gt = 0u, tie = 0u;
     for (int i = w0 + lane; i < w1; i += 32) {
         const uint4 k = four(i);
@@ -237,10 +238,8 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
             bt += *cluster.map_shared_rank(&s.tie, r);
         }
     }
-    for (int w = 0; w < warp; ++w) {
-        bg += s.warp_gt[w];
-        bt += s.warp_tie[w];
-    }
+    bg += __reduce_add_sync(FULL_MASK, lane < warp ? s.warp_gt[lane] : 0u);
+    bt += __reduce_add_sync(FULL_MASK, lane < warp ? s.warp_tie[lane] : 0u);
     int32_t *dst = keep + p.sinks;
     for (int i = w0; i < w1; i += 32) {
         const uint4 k = i + lane < w1 ? four(i + lane) : make_uint4(0u, 0u, 0u, 0u);
@@ -368,7 +367,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) paged_compact_kernel(const __gri
         for (int s = 0; s < MOVE_STAGES; ++s) rows(s, x3[s]);
     }
     __syncthreads();
-    uint32_t part[MOVE_STAGES][MOVE_R];  // a row's exponents and weight, a lane each
+    uint32_t part[MOVE_STAGES][MOVE_R] = {};  // a row's exponents and weight, a lane each
     auto fetch = [&](int round, uint32_t (&small)[MOVE_R], int stage) {
 #pragma unroll
         for (int j = 0; j < MOVE_R; ++j) {
@@ -397,8 +396,17 @@ __global__ void __launch_bounds__(MOVE_THREADS) paged_compact_kernel(const __gri
                 e = entry(r + MOVE_STAGES + 2);
             }
             asm volatile("cp.async.wait_group %0;" ::"n"(MOVE_AHEAD) : "memory");  // this round's rows are here
-            if (cs == 1) __syncthreads();
-            else cluster.sync();
+            // and the small parts of them: a number made of them is there when they are
+            bool odd = false;
+#pragma unroll
+            for (int j = 0; j < MOVE_R; ++j) odd ^= (part[s][j] & 1u) != 0u;
+            __syncthreads_or(odd);
+            // All that the cluster's barrier has to order are these reads, which are done;
+            // with a fence it would wait for the writes of the round before.
+            if (cs > 1) {
+                asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+                asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+            }
 #pragma unroll
             for (int j = 0; j < MOVE_R; ++j) {
                 const int to = s_rows[r % MOVE_SLOTS][j * (MOVE_THREADS / 16) + group].y;
@@ -456,7 +464,7 @@ cudaError_t launch_paged_compact(const PagedCompactParams &p, int cache_dtype, c
     const unsigned rows = (unsigned)p.B * (unsigned)p.c.Hkv;
     const int chunks = (p.K + MOVE_ROWS - 1) / MOVE_ROWS;
     int cs = 1;
-    while (cs < 8 && cs < chunks) cs *= 2;
+    while (cs < 8 && cs < chunks && (long long)rows * cs < 2 * sm_count()) cs *= 2;
     const bool q8 = cache_dtype == VQ_E4M3;
     const int smem = MOVE_STAGES * MOVE_R * 2 * MOVE_THREADS * (q8 ? (int)sizeof(uint2) : (int)sizeof(uint4));
     auto kern = q8 ? paged_compact_kernel<uint2> : paged_compact_kernel<uint4>;
