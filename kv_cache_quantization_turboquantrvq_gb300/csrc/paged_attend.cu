@@ -817,6 +817,8 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
             }
         }
         const int lo_all = p.window > 0 ? e.p0 + e.nt - p.window : 0;  // the last row's first key in the window
+        [[maybe_unused]] float *scores = nullptr;  // (WEIGH) of this lane's first row and key
+        if constexpr (MODE == PG_WEIGH) scores = p.scores + (((size_t)e.b * p.Hkv + r.h) * p.srows + 2 * t4) * p.keys + g8;
         float m[2 * NT], l[2 * NT], o[NT][8][4];
 #pragma unroll
         for (int i = 0; i < 2 * NT; ++i) {
@@ -912,7 +914,7 @@ __global__ void __launch_bounds__(SmShape<Q8, NT>::THREADS, 1) paged_small_kerne
                     if constexpr (MODE == PG_WEIGH) {
                         // [row][key]: a store of the warp fills whole sectors (keys lie in
                         // order along g8, four rows along t4)
-                        float *at = p.scores + (((size_t)e.b * p.Hkv + r.h) * p.srows + 8 * nt + 2 * t4) * p.keys + k0 + g8;
+                        float *at = scores + (size_t)(8 * nt) * p.keys + k0;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             if (8 * nt + 2 * t4 + i < rows) {

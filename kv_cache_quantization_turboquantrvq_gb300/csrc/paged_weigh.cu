@@ -554,8 +554,9 @@ template <class T, bool Q8> cudaError_t launch_weigh(const PagedAttendParams &p,
 // with all loads in flight.  Bound by HBM: 4 bytes a row and key and 8 for the
 // weight.
 constexpr int UPD_THREADS = 256, UPD_TILES = UPD_THREADS / 32;
+constexpr int UPD_ROWS = 4;  // rows' scores in flight
 
-__global__ void __launch_bounds__(UPD_THREADS) paged_weigh_update_kernel(const __grid_constant__ PagedAttendParams p)
+__global__ void __launch_bounds__(UPD_THREADS, 4) paged_weigh_update_kernel(const __grid_constant__ PagedAttendParams p)
 {
     __shared__ long long sums[UPD_THREADS / 32];
     __shared__ int at[3];
@@ -607,63 +608,97 @@ __global__ void __launch_bounds__(UPD_THREADS) paged_weigh_update_kernel(const _
         }
     }
     __syncthreads();
-    pg_wait();  // (for the scores and sums; the shares come of the call's inputs)
     int b = at[0], h = at[1], g = at[2];
     int left = (int)(sh.first(blockIdx.x + 1) - u0), gs = groups(b, e, start, n);
-    for (; left > 0; --left) {
+    // Where this thread's four keys of a unit are: their weights (null: nothing to do),
+    // scores or sums, and the rows of those.
+    struct Four {
+        float *w;
+        const float *s;
+        const float *l;  // the rows' lse (null: sums of a chunk's parts)
+        int rows;
+        uint32_t see;    // bits of the keys that are seen, and (from bit 4 on) that are new
+    };
+    auto find = [&]() {
+        Four f;
+        f.w = nullptr;
         PgView view;
         view.set(e, p.window, p.sinks);
         const int t = UPD_TILES * g + warp, k = pg_tile_key(e, t) + 4 * lane;
-        if (t < e.ntiles && view.any(k, k + 4)) {
-            const int lp = k >> p.c.page_shift;
-            const int page = lp < p.max_pages ? __ldg(p.table + (long long)b * p.max_pages + lp) : -1;
-            if (page >= 0 && page < p.c.num_pages) {
-                float *wp = p.weights + (((size_t)page * p.c.Hkv + h) << p.c.page_shift) + (k & ((1 << p.c.page_shift) - 1));
-                const float4 old = *reinterpret_cast<const float4 *>(wp);
-                const bool large = n * p.GQ > p.small_rows;
-                const int r0 = large ? 0 : pg_counted(p, n) * p.GQ, r1 = large ? pg_parts(p, n) : n * p.GQ;
-                const float *src = p.scores + ((size_t)b * p.Hkv + h) * p.srows * p.keys + k;
-                float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                for (int r = r0; r < r1; r += 4) {
-                    float4 s[4];
-                    float l[4];
+        if (t >= e.ntiles || !view.any(k, k + 4)) return f;
+        const int lp = k >> p.c.page_shift;
+        const int page = lp < p.max_pages ? __ldg(p.table + (long long)b * p.max_pages + lp) : -1;
+        if (page < 0 || page >= p.c.num_pages) return f;
+        f.w = p.weights + (((size_t)page * p.c.Hkv + h) << p.c.page_shift) + (k & ((1 << p.c.page_shift) - 1));
+        const bool large = n * p.GQ > p.small_rows;
+        const int r0 = large ? 0 : pg_counted(p, n) * p.GQ;
+        f.rows = large ? pg_parts(p, n) : n * p.GQ - r0;
+        f.s = p.scores + (((size_t)b * p.Hkv + h) * p.srows + r0) * p.keys + k;
+        f.l = large ? nullptr : p.lse + ((size_t)h * p.T + start) * p.GQ + r0;
+        f.see = 0u;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int q = min(r + i, r1 - 1);
-                        s[i] = __ldcs(reinterpret_cast<const float4 *>(src + (size_t)q * p.keys));
-                        l[i] = large ? 0.0f : p.lse[((size_t)h * p.T + start) * p.GQ + q];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (r + i >= r1) break;
-                        a[0] += large ? s[i].x : ex2(s[i].x - l[i]);
-                        a[1] += large ? s[i].y : ex2(s[i].y - l[i]);
-                        a[2] += large ? s[i].z : ex2(s[i].z - l[i]);
-                        a[3] += large ? s[i].w : ex2(s[i].w - l[i]);
-                    }
-                }
-                // (decay 0 does not ask what was there)
-                auto now = [&](int i, float o) {
-                    return k + i >= e.p0 || p.decay == 0.0f ? a[i] : fmaf(p.decay, o, a[i]);
-                };
-                const float4 y = make_float4(now(0, old.x), now(1, old.y), now(2, old.z), now(3, old.w));
-                if (view.one(k) && view.one(k + 1) && view.one(k + 2) && view.one(k + 3)) {
-                    *reinterpret_cast<float4 *>(wp) = y;
-                } else {
-                    if (view.one(k)) wp[0] = y.x;
-                    if (view.one(k + 1)) wp[1] = y.y;
-                    if (view.one(k + 2)) wp[2] = y.z;
-                    if (view.one(k + 3)) wp[3] = y.w;
-                }
-            }
-        }
-        if (++g == gs && left > 1) {
+        for (int i = 0; i < 4; ++i) f.see |= (view.one(k + i) ? 1u << i : 0u) | (k + i >= e.p0 ? 16u << i : 0u);
+        return f;
+    };
+    auto step = [&]() -> bool {  // to the share's next unit
+        if (--left <= 0) return false;
+        if (++g == gs) {
             g = 0;
             if (++h == p.Hkv) {
                 h = 0;
                 do gs = ++b < p.B ? groups(b, e, start, n) : 1;
                 while (gs == 0);
             }
+        }
+        return true;
+    };
+    Four f = find();
+    pg_wait();  // (for the scores and sums; the shares come of the call's inputs)
+    for (bool more = true; more;) {
+        const Four now = f;
+        float4 old = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s[UPD_ROWS];
+        float l[UPD_ROWS];
+        auto fetch = [&](int r) {
+#pragma unroll
+            for (int i = 0; i < UPD_ROWS; ++i) {
+                if (r + i >= now.rows) break;
+                s[i] = __ldcs(reinterpret_cast<const float4 *>(now.s + (size_t)(r + i) * p.keys));
+                l[i] = now.l ? now.l[r + i] : 0.0f;
+            }
+        };
+        if (now.w) {
+            old = *reinterpret_cast<const float4 *>(now.w);
+            fetch(0);
+        }
+        more = step();
+        if (more) f = find();  // (the next unit's page, while this one's numbers come)
+        if (!now.w) continue;
+        float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r = 0;;) {
+#pragma unroll
+            for (int i = 0; i < UPD_ROWS; ++i) {
+                if (r + i >= now.rows) break;
+                a[0] += now.l ? ex2(s[i].x - l[i]) : s[i].x;
+                a[1] += now.l ? ex2(s[i].y - l[i]) : s[i].y;
+                a[2] += now.l ? ex2(s[i].z - l[i]) : s[i].z;
+                a[3] += now.l ? ex2(s[i].w - l[i]) : s[i].w;
+            }
+            r += UPD_ROWS;
+            if (r >= now.rows) break;
+            fetch(r);
+        }
+        // (decay 0 does not ask what was there)
+        auto sum = [&](int i, float o) {
+            return ((now.see >> (4 + i)) & 1u) || p.decay == 0.0f ? a[i] : fmaf(p.decay, o, a[i]);
+        };
+        const float4 y = make_float4(sum(0, old.x), sum(1, old.y), sum(2, old.z), sum(3, old.w));
+        if ((now.see & 15u) == 15u) {
+            *reinterpret_cast<float4 *>(now.w) = y;
+        } else {
+            if (now.see & 1u) now.w[0] = y.x;
+            if (now.see & 2u) now.w[1] = y.y;
+            if (now.see & 4u) now.w[2] = y.z;
+            if (now.see & 8u) now.w[3] = y.w;
         }
     }
 }
@@ -684,7 +719,7 @@ cudaError_t launch_paged_weigh(const PagedAttendParams &p0, int q_dtype, int cac
 cudaError_t launch_paged_weigh_update(const PagedAttendParams &p, cudaStream_t stream)
 {
     const int G = p.small.cap ? p.small.G : p.large.G;
-    return launch_early(paged_weigh_update_kernel, dim3(8 * G), UPD_THREADS, 0, stream, p);
+    return launch_early(paged_weigh_update_kernel, dim3(4 * G), UPD_THREADS, 0, stream, p);
 }
 
 cudaError_t paged_weigh_take_device_error(unsigned *bits, cudaStream_t stream)

@@ -8,6 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 import paged_ref as ref  # noqa: E402
 import paged_tree_ref as tref  # noqa: E402
+import test_paged_exponents_gpu as exponents  # noqa: E402
 from test_paged_gpu import TYPES, _clean, _cuda, _poisoned, vq  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
@@ -122,7 +123,7 @@ def test_window_and_first_tokens(vq, dtype, cache, window, sinks, kind):  # noqa
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
-@pytest.mark.parametrize("news", [[1, 1, 1], [3, 1, 4], [100, 1, 256]])
+@pytest.mark.parametrize("news", [[1, 1, 1], [3, 1, 4], [64, 1, 256]])
 def test_chains_are_plain_attention(vq, dtype, cache, news):  # noqa: F811
     """A tree without branches gives what the same tokens give in order, bit for bit."""
     a = _case(vq, news, [2500, 700, 1300], 2, 4, 32, dtype, cache, seed=31, kind="chain")
@@ -138,6 +139,43 @@ def test_many_tiles_for_every_block(vq, dtype, cache):  # noqa: F811
     news, lens = [16, 70, 1, 200, 64, 33], [2100, 3300, 900, 2500, 130, 1900]
     _check(vq, _case(vq, news, lens, 8, 4, 128, dtype, cache, seed=36))
     _check(vq, _case(vq, [2] * 40, [1500 + 61 * i for i in range(40)], 8, 4, 64, dtype, cache, seed=37))
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("GQ,n", [(4, 5), (4, 32), (4, 33), (16, 8), (1, 128), (7, 18)])
+def test_one_query_tile(vq, dtype, cache, GQ, n):  # noqa: F811
+    """Rows that fill one query tile, or just not; runs of one key tile, of an even and
+    of an odd number, cut ones among them."""
+    news = [n, n, max(1, n - 1), n, n, n]
+    lens = [n, 128, 129 + n, 300 + n, 2000 + n, 6000 + n]
+    _check(vq, _case(vq, news, lens, 2, GQ, 32, dtype, cache, seed=38 + n))
+    _check(vq, _case(vq, news, lens, 1, GQ, 16, dtype, cache, seed=39 + n, window=200, sinks=7))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("news", [[20, 7, 32], [50, 64, 20], [3, 4, 1]])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_rows_of_very_different_sizes_over_codes(vq, dtype, news, zeros):  # noqa: F811
+    """Tiles whose exponents lie far apart, zero value rows among them (bounds: as in
+    test_paged_exponents_gpu; a chain sees what the same tokens see in order)."""
+    def rows(b, gen):
+        n = 900 - 100 * b
+        k, v = (torch.randn(n, 2, D, generator=gen).double() * torch.exp2(torch.randint(lo, 3, (n, 2, 1), generator=gen)) for lo in (-4, -14))
+        k[:, :, 0] *= 0.05
+        if zeros:
+            v[torch.rand(n, generator=gen) < 0.2] = 0.0
+        return k, v
+    a = exponents._case(rows, news, 4, 2, 16, dtype, seed=sum(news))
+    a["parents"] = torch.tensor([i - 1 for m in news for i in range(m)], dtype=torch.int32)
+    c = {k: v.cuda() for k, v in a["c"].items()}
+    for x in "kv":
+        c[x + "_pages"] = c[x + "_pages"].view(E4M3)
+    got = _run(vq, dict(a, c=c))
+    _clean(vq)
+    o, bound = exponents._reference(a, 2.0 ** -24)
+    err = (got.cpu().double() - o).abs()
+    tol = bound + ref.U16[dtype] * (o.abs() + bound) + (2.0 ** -25 if dtype == F16 else 0.0)
+    assert bool((err <= tol).all()), "error %.2f times the bound" % float((err / tol).nan_to_num(0.0).max())
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
