@@ -39,7 +39,7 @@ constexpr float NEG_INF = -__builtin_huge_valf();
 // the SM's path to L2 carries.)
 //
 // Roles (one CTA per SM): a warp that finds the CTA's units and copies keys and
-// queries by TMA, one that issues the products, two that bring the rows' -lse, two
+// queries by TMA, two that issue the products, one that brings the rows' -lse, two
 // groups of 4 softmax warps, one for each key tile, with two score tiles each in
 // tensor memory; with an 8-bit cache four more warps turn a unit's codes into
 // operands of the queries' type (exact in both).  The keys' exponents act on the
@@ -77,7 +77,7 @@ template <bool Q8> struct WgBars {
         }
         for (int s = 0; s < C::QST; ++s) {
             mbar_init(&q_full[s], 1);
-            mbar_init(&q_empty[s], 1);
+            mbar_init(&q_empty[s], 2);
         }
         for (int s = 0; s < C::LST; ++s) {
             mbar_init(&l_full[s], 1);
@@ -91,7 +91,7 @@ template <bool Q8> struct WgBars {
             mbar_init(&s_full[s], 1);
             mbar_init(&s_empty[s], 4);
         }
-        mbar_init(drain, 1);
+        mbar_init(drain, 2);
         for (int s = 0; s < C::RAW; ++s) {
             mbar_init(&raw_full[s], 1);
             mbar_init(&raw_empty[s], C::CONV);
@@ -313,53 +313,54 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
             (void)mbar_wait_bounded(&kb[j % KR], (uint32_t)(j / KR) & 1u);
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------ products
+    } else if (warp == 1 || warp == 3) {
+        // ------------------------------------------------ products, a warp a key tile (one
+        // for both was busy with waits and issues half of the time)
         constexpr uint32_t ID = ck_idesc(std::is_same<T, __nv_bfloat16>::value, false);
         const uint64_t dk = qt_desc(smem_u32(sk)), dq = qt_desc(smem_u32(sq));
         const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0);
+        const int g = warp >> 1;
         PgRing<C::KST> ks;
         PgRing<C::QST> qs;
-        uint32_t done[2] = {0u, 0u};  // tiles of each softmax group
+        PgRing<2> ss;  // its score tiles
         WgItem w;
         while (next(w)) {
             if (w.qa >= w.qz) continue;
-            const int two = w.k1 < 0 ? 1 : 2;
-            PgRing<C::KST> k2 = ks;
-            if (two == 2) k2.step();
-            await(&bar.k_full[ks.s], ks.par);
-            await(&bar.k_full[k2.s], k2.par);
+            const bool two = w.k1 >= 0;
+            if (g == 1 && two) ks.step();
+            const bool mine = g == 0 || two;
+            if (mine) await(&bar.k_full[ks.s], ks.par);
             for (int j = w.qa; j < w.qz && ok; ++j) {
                 await(&bar.q_full[qs.s], qs.par);
-                for (int g = 0; g < two; ++g) {
-                    const int slot = 2 * g + (int)(done[g] & 1u);
-                    await(&bar.s_empty[slot], ((done[g] >> 1) & 1u) ^ 1u);
+                if (mine) {
+                    await(&bar.s_empty[2 * g + ss.s], ss.par ^ 1u);
                     if (!ok) break;
                     qt_fence_after();
-                    ck_mma_ss(tm + 128 * slot, dk + (g ? k2.s : ks.s) * (TILE_B >> 4), dq + qs.s * (TILE_B >> 4), ID,
-                              smem_u32(&bar.s_full[slot]));
-                    ++done[g];
+                    ck_mma_ss(tm + 128 * (2 * g + ss.s), dk + ks.s * (TILE_B >> 4), dq + qs.s * (TILE_B >> 4), ID,
+                              smem_u32(&bar.s_full[2 * g + ss.s]));
+                    ss.step();
+                    ck_commit(&bar.q_empty[qs.s]);
+                } else if (ok && elect_lane()) {
+                    mbar_arrive(&bar.q_empty[qs.s]);
                 }
-                if (!ok) break;
-                ck_commit(&bar.q_empty[qs.s]);
+                __syncwarp();
                 qs.step();
             }
             if (!ok) break;
-            ck_commit(&bar.k_empty[ks.s]);
-            if (two == 2) ck_commit(&bar.k_empty[k2.s]);
-            ks = k2;
+            if (mine) ck_commit(&bar.k_empty[ks.s]);
             ks.step();
+            if (g == 0 && two) ks.step();
         }
         // every product is done before shared and tensor memory are given up
         ck_commit(bar.drain);
         (void)mbar_wait_bounded(bar.drain, 0u);
         __syncwarp();
-    } else if (warp < 4) {
-        // ------------------------------------------------ the rows' -lse: two warps in turn
+    } else if (warp == 2) {
+        // ------------------------------------------------ the rows' -lse
         uint32_t run = 0u;  // tiles of all units so far
         WgItem w;
         while (next(w)) {
-            const int cnt = max(w.qz - w.qa, 0), j0 = (int)((run ^ (uint32_t)warp) & 1u);  // its first tile of the unit
+            const int cnt = max(w.qz - w.qa, 0);
             const float *rows = p.lse + ((size_t)w.h * p.T + w.start + w.i0) * p.GQ;
             auto load = [&](int j, float (&x)[4]) {  // (the next tile's while this one waits for its place)
                 const int c0 = (w.qa + j) * cols, end = j < cnt ? min(cols, (w.n - w.i0) * p.GQ - c0) : 0;
@@ -367,9 +368,9 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
                 for (int i = 0; i < 4; ++i) x[i] = 32 * i + lane < end ? -rows[c0 + 32 * i + lane] : NEG_INF;
             };
             float x[4], y[4];
-            load(j0, x);
-            for (int j = j0; j < cnt; j += 2) {
-                load(j + 2, y);
+            load(0, x);
+            for (int j = 0; j < cnt; ++j) {
+                load(j + 1, y);
                 const uint32_t at = run + (uint32_t)j;
                 const int ls = (int)(at % C::LST);
                 await(&bar.l_empty[ls], ((at / C::LST) & 1u) ^ 1u);
