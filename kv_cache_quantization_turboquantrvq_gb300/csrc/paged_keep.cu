@@ -33,9 +33,14 @@ namespace cg = cooperative_groups;
 // it; they read one another's histograms and counts.  Weights are handled four
 // tokens at a time (a page holds whole fours), those of tokens outside the middle
 // as 0, which no weight is.
+//
+// 2048 of up to 16384 tokens, 512 rows: 27 us, where reading the weights takes 3; 8192
+// of 131072, 8 rows in clusters of 8: 23 us.  A block's chain (page, weights, three
+// digits with a scan each, counts, list) bounds it: token by token it took 48 us,
+// with 256 threads and two blocks a row 35.
 constexpr int SEL_THREADS = 512, SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_BINS = 2048;
-constexpr int SEL_MAX = 10240;  // fours of a CTA that stay in shared memory
+constexpr int SEL_MAX = 10240, SEL_PAIR = 6000;  // fours of a CTA that stay in shared memory: of one on an SM, of two
 constexpr int SEL_OWN = SEL_BINS / SEL_THREADS;  // bins of a thread
 static_assert(SEL_OWN * SEL_THREADS == SEL_BINS && SEL_OWN % 4 == 0, "whole fours of bins a thread");
 
@@ -281,8 +286,8 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
 // to shared memory, where the lane that asked for them takes them) while this
 // round waits for the cluster and writes.  A row's list entry, its pages and its
 // data come one after another, each a round ahead of its use (all in the round of
-// the copy: evict_16x16k_bf16 177 us; without copies ahead 138).  Bound by HBM: a
-// row read and written.
+// the copy: 4096 tokens of 16 x 8 rows 177 us; without copies ahead 138).  Bound by
+// HBM: rows of 256 bytes picked at random, each read and written, 114 us or 4.8 TB/s.
 constexpr int MOVE_THREADS = 256, MOVE_R = 4, MOVE_ROWS = MOVE_THREADS / 16 * MOVE_R, MOVE_STAGES = 3;
 constexpr int MOVE_AHEAD = MOVE_STAGES - 1;  // rounds that are copied ahead
 constexpr int MOVE_SLOTS = 8;                // rounds whose rows are known
@@ -446,11 +451,16 @@ cudaError_t launch_paged_select(const PagedSelectParams &p0, cudaStream_t stream
     PagedSelectParams p = p0;
     const unsigned rows = (unsigned)p.B * (unsigned)p.Hkv;
     const long long cap = (long long)p.max_pages << p.page_shift;
-    // CTAs a row: as many as keep its weights at hand, and more where there are few rows
+    // CTAs a row: more than one where there are few rows (8 rows of 131072 tokens with 1,
+    // 2, 4 and 8: 145, 72, 31 and 27 us; 512 rows of up to 16384: 31, 41, 74 and 227).
+    // Not by the block table's width: that says little about the lengths (those 512 rows
+    // in a table for 131072, with as many CTAs a row as could keep all of that: 115 us).
     int cs = 1;
-    while (cs < 8 && cap / cs > SEL_BINS && ((long long)rows * cs < sm_count() || cap / 4 / cs > SEL_MAX)) cs *= 2;
-    const long long held = (cap / 4 + 1 + cs) / cs;
-    p.held = (int)(held < SEL_MAX ? held : SEL_MAX);
+    while (cs < 8 && cap / cs > SEL_BINS && (long long)rows * cs < sm_count()) cs *= 2;
+    // what is kept at hand leaves room for two CTAs an SM where there are many rows (the
+    // wide table 39 us with SEL_MAX, 33 so; 512 rows of 131072 tokens 449 and 365)
+    const long long most = (long long)rows * cs > 2 * sm_count() ? SEL_PAIR : SEL_MAX, held = (cap / 4 + 1 + cs) / cs;
+    p.held = (int)(held < most ? held : most);
     constexpr size_t fixed = (sizeof(SelShared) + 15) / 16 * 16;
     const size_t smem = fixed + sizeof(uint4) * (size_t)p.held;
     cudaError_t e = cudaFuncSetAttribute(paged_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -463,6 +473,8 @@ cudaError_t launch_paged_compact(const PagedCompactParams &p, int cache_dtype, c
 {
     const unsigned rows = (unsigned)p.B * (unsigned)p.c.Hkv;
     const int chunks = (p.K + MOVE_ROWS - 1) / MOVE_ROWS;
+    // CTAs a row: as many as fill the SMs twice (4096 tokens of 8 rows with 1, 2, 4 and
+    // 8: 109, 61, 35 and 23 us; of 128 rows 135, 115, 119 and 123)
     int cs = 1;
     while (cs < 8 && cs < chunks && (long long)rows * cs < 2 * sm_count()) cs *= 2;
     const bool q8 = cache_dtype == VQ_E4M3;

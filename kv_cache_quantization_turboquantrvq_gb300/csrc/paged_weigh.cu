@@ -38,6 +38,11 @@ constexpr float NEG_INF = -__builtin_huge_valf();
 // groups in turn, asked L2 for 32 KB a product, which takes 512 cycles: as much as
 // the SM's path to L2 carries.)
 //
+// 2048 tokens over 8192, 32 query and 8 kv heads, bf16: 112 us (235 with one key tile a
+// unit), 0.95 us for two key tiles against 128 query rows, whose products take 0.54.
+// What bounds it is each group's chain of a tile (waits, columns out of tensor memory,
+// exponentials), with one warp of a group on a scheduler; a unit costs 1 us besides.
+//
 // Roles (one CTA per SM): a warp that finds the CTA's units and copies keys and
 // queries by TMA, two that issue the products, one that brings the rows' -lse, two
 // groups of 4 softmax warps, one for each key tile, with two score tiles each in
@@ -552,8 +557,9 @@ template <class T, bool Q8> cudaError_t launch_weigh(const PagedAttendParams &p,
 //
 // Each CTA takes an even share of the units (sequence, head, 8 tiles of keys) in
 // their order; a thread has four keys, whose scores, rows' lse and weights it reads
-// with all loads in flight.  Bound by HBM: 4 bytes a row and key and 8 for the
-// weight.
+// with all loads in flight, while it finds the next unit's.  Bound by memory: 4 bytes
+// a row and key (of which most are still in L2) and 8 for the weight; 64 sequences of
+// up to 16384 tokens, 8 kv heads of 4: 20 us, 107 MB.
 constexpr int UPD_THREADS = 256, UPD_TILES = UPD_THREADS / 32;
 constexpr int UPD_ROWS = 4;  // rows' scores in flight
 
