@@ -499,6 +499,9 @@ vq_status vq_paged_attend_tree(const void *q, long long q_stride_t, long long q_
  *   softmax weight that j has in their output.
  * The new tokens' weights are set, whatever was there, and with decay 0 all are;
  * weights of tokens that no new token sees stay as they are.  0 <= decay <= 1.
+ * Tokens that come into the cache in another way (accepted drafts) have the weights
+ * that their places held: the caller sets those.  Where outputs are unspecified, the
+ * weights of the sequence's tokens are too.
  * The sums are held in 32 bits, in an order that is the same on every call.  Where
  * sequences of one call share a page, its weights are unspecified.
  *   workspace: of vq_paged_attend_weigh_workspace, which also depends on the block

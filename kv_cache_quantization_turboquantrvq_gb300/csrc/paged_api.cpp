@@ -76,7 +76,7 @@ vq_status attend_plan(int T, int B, int Hq, int Hkv, int max_q, PgMode mode, lon
     pl.bytes = pl.depth + (mode == PG_TREE && large ? up((size_t)T * 4) : 0);
     if (mode == PG_WEIGH) {
         // scores of the small kernel's rows, or the parts of a chunk's sums
-        pl.srows = small ? (pl.small_rows < max_q * gq ? pl.small_rows : max_q * gq) : 0;
+        pl.srows = !small ? 0 : pl.small_rows < (long long)max_q * gq ? pl.small_rows : max_q * gq;
         if (large && pl.srows < PG_PARTS) pl.srows = PG_PARTS;
         if ((double)B * Hkv * pl.srows * (double)keys >= 1e15) return VQ_ERR_UNSUPPORTED;
         pl.wbase = pl.bytes;

@@ -91,9 +91,9 @@ template <class F> __device__ __forceinline__ int parts_at(F &&first, int g, int
 }
 
 // The masks and depths of the tokens of sequence b, a thread each: up its ancestors
-// twice, for its depth and for the bits.  (Beside the plan, in its launch, and
-// done before it: it takes 7 to 9 us with 64 trees of 16 and without.)  A parent that does not come before its
-// token is reported and taken for the last cached token.
+// twice, for its depth and for the bits.  A parent that does not come before its
+// token is reported and taken for the last cached token.  (Beside the plan, in its
+// launch, and done before it: that takes 8 us with 64 trees of 16, as without.)
 __device__ __forceinline__ void tree_masks(const PagedAttendParams &p, int b, int *parent, uint32_t *rows)
 {
     int start = 0, n = 0, len = 0;

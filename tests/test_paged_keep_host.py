@@ -223,3 +223,15 @@ def test_bound_attention_refusals(binding, call, name, bad):  # noqa: F811
     with pytest.raises(ValueError):
         call(binding, **{name: bad})
     assert not binding.log
+
+
+@pytest.mark.parametrize("max_q", [1 << 27, 1 << 28, (1 << 28) + 1, (1 << 31) - 1])
+def test_weigh_workspace_of_any_max_q(api, max_q):  # noqa: F811
+    """max_q times the query heads passes 32 bits: as much room as for chunks of 100 tokens."""
+    f = api.lib().vq_paged_attend_weigh_workspace
+    sizes = []
+    for m in (100, max_q):
+        n = ctypes.c_size_t(0)
+        assert f(150, 2, 16, 1, m, 4, 16, ctypes.byref(n)) == api.VQ_OK
+        sizes.append(n.value)
+    assert sizes[0] == sizes[1]
