@@ -892,10 +892,16 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     if (part == 0 ? u == r.tn : u == r.t0) continue;
                     const int k0 = pg_tile_key(r.e, part ? u - 1 : u);
                     const bool edge = k0 + PG_TILE > view.hi || (k0 < view.lo && k0 + PG_TILE > view.sink);
-                    ok = __all_sync(FULL_MASK, wait(&bar.raw_full[raw.s], raw.par));
-                    if (ok && tiles >= STAGES) ok = __all_sync(FULL_MASK, wait(&bar.kv_empty[kv.s], kv.par ^ 1u));
-                    if (ok && part == 0 && keys >= C::META) ok = __all_sync(FULL_MASK, wait(&bar.meta_empty[mt.s], mt.par ^ 1u));
-                    if (!ok) break;
+                    // (asked together first: one after another three answers take 300 cycles)
+                    const bool r1 = mbar_try_wait(&bar.raw_full[raw.s], raw.par);
+                    const bool r2 = mbar_try_wait(&bar.kv_empty[kv.s], kv.par ^ 1u);
+                    const bool r3 = part != 0 || mbar_try_wait(&bar.meta_empty[mt.s], mt.par ^ 1u);
+                    if (!__all_sync(FULL_MASK, r1 && r2 && r3)) {
+                        ok = __all_sync(FULL_MASK, wait(&bar.raw_full[raw.s], raw.par));
+                        if (ok) ok = __all_sync(FULL_MASK, wait(&bar.kv_empty[kv.s], kv.par ^ 1u));
+                        if (ok && part == 0) ok = __all_sync(FULL_MASK, wait(&bar.meta_empty[mt.s], mt.par ^ 1u));
+                        if (!ok) break;
+                    }
                     // rows of this thread: j / 8 + 4 CONV i
                     int top;              // the tile's largest exponent; 0: codes are taken as they are
                     uint32_t rows = 0;    // this thread's rows' exponents, a byte each
