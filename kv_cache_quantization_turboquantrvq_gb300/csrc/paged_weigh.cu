@@ -38,8 +38,8 @@ constexpr float NEG_INF = -__builtin_huge_valf();
 // groups in turn, asked L2 for 32 KB a product, which takes 512 cycles: as much as
 // the SM's path to L2 carries.)
 //
-// 2048 tokens over 8192, 32 query and 8 kv heads, bf16: 112 us (235 with one key tile a
-// unit), 0.95 us for two key tiles against 128 query rows, whose products take 0.54.
+// 2048 tokens over 8192, 32 query and 8 kv heads, bf16: 109 us (235 with one key tile a
+// unit), 0.92 us for two key tiles against 128 query rows, whose products take 0.54.
 // What bounds it is each group's chain of a tile (waits, columns out of tensor memory,
 // exponentials), with one warp of a group on a scheduler; a unit costs 1 us besides.
 //
