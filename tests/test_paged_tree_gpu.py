@@ -319,3 +319,10 @@ def test_verify_a_tree_and_keep_the_accepted_path(vq):  # noqa: F811
         k2, v2 = vq.vq_paged_gather(ordered, table, lens, 160)
         assert torch.equal(k, k2) and torch.equal(v, v2)
     _clean(vq)
+
+
+def test_more_trees_than_a_block_has_threads(vq):  # noqa: F811
+    news = [17 + i % 5 if i % 9 else 40 for i in range(1100)]
+    news[3::50] = [1] * len(news[3::50])
+    _check(vq, _case(vq, news, [n + i % 37 for i, n in enumerate(news)], 1, 1, 16, F16, F16, seed=56))
+    _check(vq, _case(vq, [1 + i % 4 for i in range(1300)], [5 + i % 60 for i in range(1300)], 1, 4, 16, F16, F16, seed=57))

@@ -308,3 +308,12 @@ def test_a_bounded_cache(vq, cache):  # noqa: F811
             length = counts.tolist()
             assert all(len(kept[b][h]) == length[b] for b in range(B) for h in range(H))
     _clean(vq)
+
+
+def test_more_sequences_than_a_block_has_threads(vq):  # noqa: F811
+    """Over a thousand chunks and single tokens: units of weighing are found among
+    sequences that the plan goes through in several steps."""
+    news = [17 + i % 5 if i % 9 else 40 for i in range(1100)]
+    news[3::50] = [1] * len(news[3::50])
+    lens = [n + i % 37 for i, n in enumerate(news)]
+    _check(vq, _case(vq, news, lens, 1, 1, 16, F16, F16, seed=55), observe=9, decay=0.5)
