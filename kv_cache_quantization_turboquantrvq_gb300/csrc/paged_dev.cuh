@@ -7,6 +7,7 @@
 
 #include "device_common.cuh"
 #include "paged.h"
+#include "paged_rings.h"
 
 namespace vq {
 namespace {
@@ -226,19 +227,6 @@ struct PgRun {
     __device__ __forceinline__ bool next(const PgPlan &pl, int Hkv)
     {
         return next(Hkv, [&](PgRun &r) { r.e = pg_entry(pl.ent + ++r.ei); });
-    }
-};
-
-// Position in a ring of N barriers: slot and the parity of its current pass.
-template <int N> struct PgRing {
-    int s = 0;
-    uint32_t par = 0;
-    __device__ __forceinline__ void step()
-    {
-        if (++s == N) {
-            s = 0;
-            par ^= 1u;
-        }
     }
 };
 

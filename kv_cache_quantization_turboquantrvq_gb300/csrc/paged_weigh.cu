@@ -49,13 +49,9 @@ constexpr float NEG_INF = -__builtin_huge_valf();
 // tensor memory; with an 8-bit cache four more warps turn a unit's codes into
 // operands of the queries' type (exact in both).  The keys' exponents act on the
 // scores, a factor a thread.
-template <bool Q8> struct WgShape {
-    static constexpr int KST = Q8 ? 3 : 4;     // key tiles
-    static constexpr int QST = 3;              // query tiles
-    static constexpr int RAW = Q8 ? 2 : 0;     // tiles of codes
-    static constexpr int LST = 2;              // rows' -lse
-    static constexpr int IST = 4;              // units known ahead
-    static constexpr int CONV = Q8 ? 4 : 0;
+template <bool Q8> struct WgShape : WgRings<Q8> {
+    using R = WgRings<Q8>;
+    using R::KST, R::QST, R::RAW, R::LST, R::IST, R::CONV;
     static constexpr int WARPS = 12 + CONV;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int BARS = 2 * KST + 2 * QST + 2 * RAW + 2 * LST + 2 * IST + 2 * 4 + 1;
@@ -78,11 +74,11 @@ template <bool Q8> struct WgBars {
     {
         for (int s = 0; s < C::KST; ++s) {
             mbar_init(&k_full[s], Q8 ? C::CONV : 1);
-            mbar_init(&k_empty[s], 1);
+            mbar_init(&k_empty[s], C::READERS);
         }
         for (int s = 0; s < C::QST; ++s) {
             mbar_init(&q_full[s], 1);
-            mbar_init(&q_empty[s], 2);
+            mbar_init(&q_empty[s], C::READERS);
         }
         for (int s = 0; s < C::LST; ++s) {
             mbar_init(&l_full[s], 1);
@@ -335,34 +331,56 @@ __global__ void __launch_bounds__(WgShape<Q8>::THREADS, 1) paged_weigh_kernel(co
         const int g = warp >> 1;
         PgRing<C::KST> ks;
         PgRing<C::QST> qs;
-        PgRing<2> ss;  // its score tiles
+        PgRing<C::SST> ss;  // its score tiles
+        struct Ops {
+            decltype(await) &wait_;
+            decltype(await2) &wait2;
+            const bool &ok;
+            const WgBars<Q8> &bar;
+            const uint32_t tm;
+            const uint64_t dk, dq;
+            const int g;
+            __device__ __forceinline__ bool keys(const PgRing<C::KST> &k) const
+            {
+                wait_(&bar.k_full[k.s], k.par);
+                return ok;
+            }
+            __device__ __forceinline__ bool queries(const PgRing<C::QST> &q) const
+            {
+                wait_(&bar.q_full[q.s], q.par);
+                return ok;
+            }
+            __device__ __forceinline__ bool both(const PgRing<C::QST> &q, const PgRing<C::SST> &s) const
+            {
+                wait2(&bar.q_full[q.s], q.par, &bar.s_empty[C::SST * g + s.s], s.par ^ 1u);
+                return ok;
+            }
+            __device__ __forceinline__ void product(const PgRing<C::KST> &k, const PgRing<C::QST> &q, const PgRing<C::SST> &s) const
+            {
+                qt_fence_after();
+                ck_mma_ss(tm + 128 * (C::SST * g + s.s), dk + k.s * (TILE_B >> 4), dq + q.s * (TILE_B >> 4), ID,
+                          smem_u32(&bar.s_full[C::SST * g + s.s]));
+            }
+            __device__ __forceinline__ void used(uint64_t *empty) const
+            {
+                ck_commit(empty);
+                __syncwarp();
+            }
+            __device__ __forceinline__ void passed(uint64_t *empty) const
+            {
+                if (elect_lane()) mbar_arrive(empty);
+                __syncwarp();
+            }
+            __device__ __forceinline__ void keys_used(const PgRing<C::KST> &k) const { used(&bar.k_empty[k.s]); }
+            __device__ __forceinline__ void keys_passed(const PgRing<C::KST> &k) const { passed(&bar.k_empty[k.s]); }
+            __device__ __forceinline__ void queries_used(const PgRing<C::QST> &q) const { used(&bar.q_empty[q.s]); }
+            __device__ __forceinline__ void queries_passed(const PgRing<C::QST> &q) const { passed(&bar.q_empty[q.s]); }
+        };
+        const Ops ops{await, await2, ok, bar, tm, dk, dq, g};
         WgItem w;
         while (next(w)) {
             if (w.qa >= w.qz) continue;
-            const bool two = w.k1 >= 0;
-            if (g == 1 && two) ks.step();
-            const bool mine = g == 0 || two;
-            if (mine) await(&bar.k_full[ks.s], ks.par);
-            for (int j = w.qa; j < w.qz && ok; ++j) {
-                if (mine) {
-                    await2(&bar.q_full[qs.s], qs.par, &bar.s_empty[2 * g + ss.s], ss.par ^ 1u);
-                    if (!ok) break;
-                    qt_fence_after();
-                    ck_mma_ss(tm + 128 * (2 * g + ss.s), dk + ks.s * (TILE_B >> 4), dq + qs.s * (TILE_B >> 4), ID,
-                              smem_u32(&bar.s_full[2 * g + ss.s]));
-                    ss.step();
-                    ck_commit(&bar.q_empty[qs.s]);
-                } else {
-                    await(&bar.q_full[qs.s], qs.par);
-                    if (ok && elect_lane()) mbar_arrive(&bar.q_empty[qs.s]);
-                }
-                __syncwarp();
-                qs.step();
-            }
-            if (!ok) break;
-            if (mine) ck_commit(&bar.k_empty[ks.s]);
-            ks.step();
-            if (g == 0 && two) ks.step();
+            if (!wg_products(ops, ks, qs, ss, g, w.k1 >= 0, w.qz - w.qa)) break;
         }
         // every product is done before shared and tensor memory are given up
         ck_commit(bar.drain);
