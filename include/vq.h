@@ -527,11 +527,12 @@ vq_status vq_paged_attend_tree(const void *q, long long q_stride_t, long long q_
  * first[b] + counts[b] tokens.
  *   keep [B, Hkv, K] int32, device, with strides of sequence and head in elements
  *     (a head stride of 0: one list for all heads); ascending, and no token may come
- *     before the place it goes to.  A token that breaks this, or whose page or place
- *     is not in the pool, is left out and sets VQ_DEVERR_BAD_OFFSET; so do counts
- *     outside [0, K] (cut to it) and a `first` outside the block table (nothing
- *     moves).  Where the list does not ascend, what the moved places hold is
- *     unspecified.
+ *     before the place it goes to.  A token that breaks this, or that moves and
+ *     whose page or place is not in the pool, is left out and sets
+ *     VQ_DEVERR_BAD_OFFSET; so do counts outside [0, K] (cut to it) and a `first`
+ *     outside the block table (nothing moves).  Where the list does not ascend,
+ *     what the moved places hold is unspecified.  Pages of tokens that are at their
+ *     places already are not asked for: a sequence may have given them back.
  * vq_paged_select and vq_paged_compact: B * Hkv at most 2^24, at most 2^30 positions
  * a sequence; one kernel launch; nothing is allocated.
  */

@@ -333,13 +333,13 @@ __global__ void __launch_bounds__(MOVE_THREADS) paged_compact_kernel(const __gri
     auto ends = [&](int round, Entry e) {
         const int i = round * step + i0;
         Ends x = {-1, -1, -1};
-        if (round >= rounds || i >= n || (e.t == at + i && e.t < cap)) return x;  // (stays where it is)
-        if (e.t > e.before && e.t > at + i && e.t < cap) {
+        if (round >= rounds || i >= n) return x;
+        if (e.t <= e.before || e.t < at + i || e.t >= cap) {
+            atomicOr(&g_pe_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
+        } else if (e.t > at + i) {  // (else it stays where it is)
             x.t = e.t;
             x.from = __ldg(table + (e.t >> p.c.page_shift));
             x.to = __ldg(table + ((at + i) >> p.c.page_shift));
-        } else {
-            atomicOr(&g_pe_err, (unsigned)VQ_DEVERR_BAD_OFFSET);
         }
         return x;
     };

@@ -19,6 +19,10 @@ def vq():
     return api
 
 
+def _cuda(c):
+    return {k: None if x is None else x.cuda() for k, x in c.items()}
+
+
 def _clean(vq, code=0):
     torch.cuda.synchronize()
     assert vq.vq_device_error() == code
@@ -285,6 +289,36 @@ def test_compact_leaves_out_and_reports_what_makes_no_sense(vq):
     _clean(vq, vq.VQ_DEVERR_BAD_OFFSET)
     want = _compact_ref(c, None, table, keep, [4, 0, 2, 0, 4, 0, 4], None)
     assert torch.equal(_bits(g["k_pages"]).cpu(), want["k_pages"])
+
+
+def test_compact_reports_a_list_that_goes_back_to_a_token_in_its_place(vq):
+    """The order is asked of every token of a list, those that stay where they are among
+    them; a sequence beside it moves as it should.  Pages of tokens that stay are not
+    asked for."""
+    gen = torch.Generator().manual_seed(13)
+    table, NP = _table(gen, [64, 64], 16, extra=0)
+    c = _pool(vq, NP, 2, 16, F16, gen)
+    i32 = torch.int32
+    good = [5, 9, 20, 63]
+    for back, first in (([0, 5, 2, 40], 0), ([0, 1, 9, 3], 0), ([16, 30, 18, 19], 16), ([0, 0, 2, 3], 0)):
+        keep = torch.tensor([back, good], dtype=i32)[:, None]
+        g = _cuda(c)
+        vq.vq_paged_compact(g, table.cuda(), keep.cuda(), torch.tensor([4, 4], dtype=i32).cuda(),
+                            first=torch.tensor([first, 0], dtype=i32).cuda())
+        _clean(vq, vq.VQ_DEVERR_BAD_OFFSET)
+        want = _compact_ref(c, None, table, keep, [0, 4], [0, 0])
+        mine = table[1].long()
+        for x in ("k_pages", "v_pages"):
+            assert torch.equal(_bits(g[x]).cpu()[mine], want[x][mine])
+    # the first two pages were given back; their tokens and the next ones stay, then others move
+    hole = table.clone()
+    hole[:, :2] = torch.tensor([-1, NP + 3], dtype=i32)
+    keep = torch.tensor(list(range(40)) + [44, 50], dtype=i32).repeat(2, 1)[:, None]
+    g = _cuda(c)
+    vq.vq_paged_compact(g, hole.cuda(), keep.cuda(), torch.tensor([42, 40], dtype=i32).cuda())
+    _clean(vq)
+    want = _compact_ref(c, None, table, keep, [42, 40], None)
+    assert all(torch.equal(_bits(g[x]).cpu(), want[x]) for x in ("k_pages", "v_pages"))
 
 
 def test_select_and_compact_on_a_stream_and_in_a_graph(vq):
