@@ -173,6 +173,18 @@ __device__ __forceinline__ void ck_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         : "memory");
 }
 
+__device__ __forceinline__ void ck_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void ck_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // 16 consecutive fp32 columns of this thread's tensor-memory lane.
 __device__ __forceinline__ void ck_ld16(uint32_t taddr, uint32_t (&r)[16])
 {
@@ -878,7 +890,6 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
         PgRing<C::RAW ? C::RAW : 1> raw;
         PgRing<STAGES> kv;
         PgRing<C::META ? C::META : 1> mt;
-        int tiles = 0, keys = 0;
         const int box = min(1 << p.c.page_shift, PG_TILE);
         uint32_t far = 0u;  // exponents of this lane's keys too far below the tile's largest
         int vtop0 = 0, vtop1 = 0;  // exponents of the values to come: of tile u - 1, of tile u
@@ -990,10 +1001,8 @@ __global__ void __launch_bounds__(CkShape<Q8>::THREADS, 1) paged_chunk_kernel(co
                     }
                     raw.step();
                     kv.step();
-                    ++tiles;
                     if (part == 0) {
                         mt.step();
-                        ++keys;
                         // (exponent 0, or more: there may be zero rows)
                         if (!BY_KEY && (__any_sync(FULL_MASK, far != 0u) || vtop1 >= 127)) {
                             *abort_flag = CK_BY_KEY;

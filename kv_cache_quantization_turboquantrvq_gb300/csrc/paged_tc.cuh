@@ -55,32 +55,6 @@ __device__ __forceinline__ void ck_mma_ss(uint32_t d, uint64_t a, uint64_t b, ui
         : "memory");
 }
 
-// D = A B with A (16-bit pairs) in tensor memory, 8 columns a step, and B's rows of 64
-// entries as above.
-__device__ __forceinline__ void ck_mma_tk(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t bar)
-{
-    asm volatile(
-        "{\n\t.reg .pred q, f, t;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
-        ".reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "setp.ne.b32 t, 1, 0;\n\tsetp.ne.b32 f, 0, 0;\n\t"
-        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\tadd.s32 a4, %1, 32;\n\t"
-        "add.s32 a5, %1, 40;\n\tadd.s32 a6, %1, 48;\n\tadd.s32 a7, %1, 56;\n\t"
-        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\tadd.s64 b4, %2, 1024;\n\t"
-        "add.s64 b5, %2, 1026;\n\tadd.s64 b6, %2, 1028;\n\tadd.s64 b7, %2, 1030;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(bar)
-        : "memory");
-}
-
 // An arrival on `bar` when every product that this warp's elected thread issued
 // is done.
 __device__ __forceinline__ void ck_commit(uint64_t *bar)
@@ -90,18 +64,6 @@ __device__ __forceinline__ void ck_commit(uint64_t *bar)
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
-
-__device__ __forceinline__ void ck_st16(uint32_t taddr, const uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-__device__ __forceinline__ void ck_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // L2 policy of the cache's tiles: other CTAs read them too.
 __device__ __forceinline__ uint64_t ck_policy()
@@ -113,10 +75,8 @@ __device__ __forceinline__ uint64_t ck_policy()
 
 __device__ __forceinline__ float2 ck_f2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
 
-
 // A word with its n lowest bits set (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t ck_below(int n) { return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u; }
-
 
 template <class T> __device__ __forceinline__ uint32_t ck_pack(float a, float b);
 template <> __device__ __forceinline__ uint32_t ck_pack<__half>(float a, float b)
