@@ -499,6 +499,9 @@ vq_status vq_paged_attend_tree(const void *q, long long q_stride_t, long long q_
  *   softmax weight that j has in their output.
  * The new tokens' weights are set, whatever was there, and with decay 0 all are;
  * weights of tokens that no new token sees stay as they are.  0 <= decay <= 1.
+ * Weights fade once a call, however many tokens it has: with decay below 1 a prompt
+ * given in four chunks leaves other weights than in one (those of the first chunk
+ * have faded three times).
  * Tokens that come into the cache in another way (accepted drafts) have the weights
  * that their places held: the caller sets those.  Where outputs are unspecified, the
  * weights of the sequence's tokens are too.

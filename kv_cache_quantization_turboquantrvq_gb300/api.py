@@ -723,9 +723,9 @@ def vq_paged_attend_weigh(q, cache: dict, weights, block_table, cu_q, lens, scal
     gets: weights [num_pages, Hkv, page_size] (float32, updated in place) of every
     token that some new token sees become decay times what they were (of the new
     tokens: 0) plus the sum over the last `observe` new tokens of the sequence (0:
-    all) and the query heads of the kv head.  Sequences must not share pages.  The
-    workspace grows with the block table's width
-    (vq_paged_attend_weigh_workspace)."""
+    all) and the query heads of the kv head.  decay acts once a call, however many
+    tokens it has.  Sequences must not share pages.  The workspace grows with the
+    block table's width (vq_paged_attend_weigh_workspace)."""
     import torch
     if observe > _INT_MAX:
         raise ValueError("observe: less than 2^31")

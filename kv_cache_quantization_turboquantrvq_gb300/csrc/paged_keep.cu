@@ -286,8 +286,11 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) paged_select_kernel(const __gr
 // to shared memory, where the lane that asked for them takes them) while this
 // round waits for the cluster and writes.  A row's list entry, its pages and its
 // data come one after another, each a round ahead of its use (all in the round of
-// the copy: 4096 tokens of 16 x 8 rows 177 us; without copies ahead 138).  Bound by
-// HBM: rows of 256 bytes picked at random, each read and written, 114 us or 4.8 TB/s.
+// the copy: 4096 tokens of 16 x 8 rows 177 us; without copies ahead 138).
+//
+// 4096 tokens of 16 x 8 rows, bf16: 114 us, 4.8 TB/s.  The rounds and their barrier
+// bound it: the same rows copied from and to the same kind of places, but in another
+// pool and each for itself, take 84 us (6.4 TB/s).
 constexpr int MOVE_THREADS = 256, MOVE_R = 4, MOVE_ROWS = MOVE_THREADS / 16 * MOVE_R, MOVE_STAGES = 3;
 constexpr int MOVE_AHEAD = MOVE_STAGES - 1;  // rounds that are copied ahead
 constexpr int MOVE_SLOTS = 8;                // rounds whose rows are known
@@ -452,13 +455,15 @@ cudaError_t launch_paged_select(const PagedSelectParams &p0, cudaStream_t stream
     const unsigned rows = (unsigned)p.B * (unsigned)p.Hkv;
     const long long cap = (long long)p.max_pages << p.page_shift;
     // CTAs a row: more than one where there are few rows (8 rows of 131072 tokens with 1,
-    // 2, 4 and 8: 145, 72, 31 and 27 us; 512 rows of up to 16384: 31, 41, 74 and 227).
-    // Not by the block table's width: that says little about the lengths (those 512 rows
-    // in a table for 131072, with as many CTAs a row as could keep all of that: 115 us).
+    // 2, 4 and 8: 132, 65, 26 and 22 us; 512 rows of up to 16384: 29, 39, 72 and 230;
+    // each over several pools in turn).  Not by the block table's width, which says
+    // little about the lengths: those 512 rows in a table for 131072 take 29 us with
+    // one and 71 with the four that could keep all of that (512 rows that do have 131072
+    // tokens 389 with one, 303 with two).
     int cs = 1;
     while (cs < 8 && cap / cs > SEL_BINS && (long long)rows * cs < sm_count()) cs *= 2;
     // what is kept at hand leaves room for two CTAs an SM where there are many rows (the
-    // wide table 39 us with SEL_MAX, 33 so; 512 rows of 131072 tokens 449 and 365)
+    // wide table 36 us with SEL_MAX, 29 so; 512 rows of 131072 tokens 485 and 389)
     const long long most = (long long)rows * cs > 2 * sm_count() ? SEL_PAIR : SEL_MAX, held = (cap / 4 + 1 + cs) / cs;
     p.held = (int)(held < most ? held : most);
     constexpr size_t fixed = (sizeof(SelShared) + 15) / 16 * 16;
@@ -474,7 +479,7 @@ cudaError_t launch_paged_compact(const PagedCompactParams &p, int cache_dtype, c
     const unsigned rows = (unsigned)p.B * (unsigned)p.c.Hkv;
     const int chunks = (p.K + MOVE_ROWS - 1) / MOVE_ROWS;
     // CTAs a row: as many as fill the SMs twice (4096 tokens of 8 rows with 1, 2, 4 and
-    // 8: 109, 61, 35 and 23 us; of 128 rows 135, 115, 119 and 123)
+    // 8: 107, 60, 33 and 21 us; of 128 rows 134, 113, 115 and 120)
     int cs = 1;
     while (cs < 8 && cs < chunks && (long long)rows * cs < 2 * sm_count()) cs *= 2;
     const bool q8 = cache_dtype == VQ_E4M3;
